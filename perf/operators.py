@@ -137,15 +137,16 @@ def prepare(case, seed):
         s["lengths"] = torch.tensor(s["lens"], dtype=torch.int32, device="cuda")
         s["prefix"] = torch.tensor(s["prompts"], dtype=torch.int32, device="cuda") if case["prefix"] else None
         s["qkv"] = normal(T, (H + 2 * kv) * d).half()
-        s["index"] = torch.empty(5, T, dtype=torch.int32, device="cuda")
         s["o"] = torch.empty(T, H * d, dtype=torch.float16, device="cuda")
         s["lse"] = torch.empty(H, T, device="cuda")
+        if own:
+            from layer_streamed_qlora_nf4_b200 import lib
+            s["index"] = lib.PackedIndex(T, len(s["lens"]))
         if case["op"] == "attn_train":
             # gradients of a mean loss: small, and of different size from token to token
             s["dout"] = (normal(T, H * d) * torch.exp(normal(T, 1)) * 1e-5).bfloat16()
             s["dqkv"] = torch.empty(T, (H + 2 * kv) * d, dtype=torch.bfloat16, device="cuda")
             if own:
-                from layer_streamed_qlora_nf4_b200 import lib
                 s["ws"] = torch.empty(lib.packed_attention_workspace_bytes(T, H, kv, d), dtype=torch.uint8, device="cuda")
     elif case["op"] == "loss":
         T, V = case["T"], case["V"]
