@@ -68,9 +68,12 @@ int lsq_version(void);
 /* Reads (and, if clear != 0, resets) the device status word of the current
  * device into *flags.  Synchronises the device.  Returns LSQ_OK or LSQ_ERR_CUDA.
  * Bits: LSQ_DEV_ERR_WAIT (a bounded in-kernel wait gave up), LSQ_DEV_ERR_NONFINITE
- * (a non-finite quantiser input, or a forward value beyond the fp16 range). */
+ * (a non-finite quantiser input, a forward value beyond the fp16 range, or a
+ * non-finite optimiser moment), LSQ_DEV_ERR_INDEX (document lengths, a prompt or a
+ * target outside its range; see packed_index and packed_cross_entropy). */
 #define LSQ_DEV_ERR_WAIT 1
 #define LSQ_DEV_ERR_NONFINITE 2
+#define LSQ_DEV_ERR_INDEX 4
 int lsq_device_status(int* flags, int clear);
 
 /* ------------------------------------------------------------------- NF4 */
@@ -428,6 +431,88 @@ int stream_stack_shard(lsq_stack* stack, const void* nccl_id, int64_t id_bytes, 
 int stream_stack_reduce_grads(lsq_stack* stack, const void* nccl_id, int64_t id_bytes,
                               int32_t world, int32_t rank);
 
+/* ------------------------------------------------------- packed documents */
+/* A packed row holds several documents behind one another, so that short ones
+ * waste no tokens; attention, positions and targets stay inside each document.
+ * The pages fine-tune on single sequences; these operators are the library's own.
+ * Added in ABI 2.2. */
+
+/* int32 words of an index of T tokens and n_docs documents (0 for a size < 1). */
+int64_t packed_index_ints(int64_t T, int32_t n_docs);
+
+/* packed_index - the index of the documents in a row of T tokens, which the
+ * operators below read (build it once per batch; its layout is private).
+ *   lengths  device int32 [n_docs]: tokens of each document, in order; 0 is allowed.
+ *            Tokens behind the last document are padding.
+ *   prefix   device int32 [n_docs] or NULL: the first prefix[k] tokens of document k
+ *            are a prompt that is read in both directions (0: causal throughout).
+ *   T        1 .. 2^30 tokens;  n_docs  1 .. 2^24.
+ *   index    device int32 [packed_index_ints(T, n_docs)], 16-byte aligned (output).
+ * Token i of a document [s, e) with a prompt of p tokens sees the keys
+ * [s, max(i + 1, s + p)).  A negative length counts as 0, a prompt is cut to
+ * [0, length], documents are cut at T; each of these latches LSQ_DEV_ERR_INDEX.
+ * Asynchronous, deterministic. */
+int packed_index(const int32_t* lengths, const int32_t* prefix, int32_t n_docs, int64_t T,
+                 int32_t* index, void* stream);
+
+/* packed_attention_fwd - o = softmax(q k^T / sqrt(d)) v over the keys a token sees.
+ *   qkv    device fp16 [T, (H + 2 Hkv) d]: the q heads, then the k and v heads (RoPE
+ *          already applied); query head h reads kv head h / (H / Hkv).
+ *   H % Hkv == 0;  d is 64 or 128.
+ *   index, n_docs  of packed_index with this T and n_docs.
+ *   o      device fp16 [T, H d];  lse  device fp32 [H, T]: the log-sum-exp of the
+ *          scaled scores.  Padding rows get o = 0 and lse = -inf.
+ * Products of fp16 operands (the probabilities rounded to fp16), fp32 softmax and
+ * sums.  A document's values never reach another's rows, not even as 0 * inf.
+ * Asynchronous, deterministic. */
+int packed_attention_fwd(const uint16_t* qkv, const int32_t* index, int32_t n_docs, int64_t T,
+                         int32_t H, int32_t Hkv, int32_t d, uint16_t* o, float* lse, void* stream);
+
+/* Workspace of packed_attention_bwd (0 for a bad shape). */
+size_t packed_attention_workspace_bytes(int64_t T, int32_t H, int32_t Hkv, int32_t d);
+
+/* packed_attention_bwd - the gradient of packed_attention_fwd.
+ *   o, lse  its outputs;  dout  device bf16 [T, H d].
+ *   dqkv    device bf16 [T, (H + 2 Hkv) d] (overwritten; 0 in padding rows): dq, and dk
+ *           and dv summed in fp32 over the query heads of each kv head.
+ *   ws      device workspace of packed_attention_workspace_bytes(T, H, Hkv, d).
+ * The score gradients multiply in fp16 after each row of dout is scaled by the power
+ * of two that brings its norm to [8, 16), so their range does not matter; a row of v
+ * whose norm is above 2047 latches LSQ_DEV_ERR_NONFINITE (its score gradients may
+ * overflow).  Asynchronous, deterministic (fixed-order sums, no atomics). */
+int packed_attention_bwd(const uint16_t* qkv, const int32_t* index, int32_t n_docs,
+                         const uint16_t* o, const float* lse, const uint16_t* dout, int64_t T,
+                         int32_t H, int32_t Hkv, int32_t d, uint16_t* dqkv, void* ws,
+                         size_t ws_bytes, void* stream);
+
+/* packed_targets - the tokens that are trained on.
+ *   tokens     device int32 [T];  index, n_docs  of packed_index.
+ *   loss_mask  device uint8 [T] or NULL: nonzero where a token is to be predicted
+ *              (the answers of a chat); NULL: all.
+ *   targets    device int32 [T] (output): tokens[t + 1] where that token belongs to t's
+ *              document, is marked, and is not part of a prompt that t itself sees;
+ *              -1 elsewhere.
+ *   count      device int32: the number of targets, added to it (accumulate = 1, over
+ *              the micro-batches of a step) or written to it (0).
+ * Asynchronous, deterministic. */
+int packed_targets(const int32_t* tokens, const int32_t* index, int32_t n_docs, int64_t T,
+                   const uint8_t* loss_mask, int32_t* targets, int32_t* count, int32_t accumulate,
+                   void* stream);
+
+/* packed_cross_entropy - loss and logit gradient of the rows that have a target.
+ *   logits   device fp32 [T, V];  targets  device int32 [T], negative: no target.
+ *   weight   device fp32 [T] or NULL (1);  count  device int32 or NULL (1).
+ *   With c_t = weight[t] / max(count, 1):
+ *   row_loss device fp32 [T] = logsumexp(logits[t]) - logits[t, target];
+ *   loss     device fp32 [1] (+)= sum c_t row_loss[t]  (accumulate 0/1);
+ *   dlogits  device bf16 [T, V] or NULL = c_t (softmax(logits[t]) - onehot(target)).
+ * Rows without a target get row_loss 0 and a zero gradient, whatever their logits; a
+ * target >= V counts as none and latches LSQ_DEV_ERR_INDEX.  Any V >= 1.
+ * Asynchronous, deterministic. */
+int packed_cross_entropy(const float* logits, int64_t T, int64_t V, const int32_t* targets,
+                         const float* weight, const int32_t* count, uint16_t* dlogits,
+                         float* row_loss, float* loss, int32_t accumulate, void* stream);
+
 /* ------------------------------------------------------------ optimiser */
 
 /* lora_adamw_step - one AdamW update of n LoRA parameters (fp32, any layout
@@ -437,6 +522,53 @@ int stream_stack_reduce_grads(lsq_stack* stack, const void* nccl_id, int64_t id_
  * callers can reduce gradients across ranks between the step and the update.
  * Asynchronous. */
 int lora_adamw_step(float* lora, const float* grad, const lsq_adamw* opt, int64_t n, void* stream);
+
+/* adamw_multi_step - one AdamW update of many tensors at once (the formula of
+ * lora_adamw_step), with the moments in fp32 or in 8 bits.  Added in ABI 2.2.
+ *   tensors   host array of n_tensors (read during the call; a captured graph keeps
+ *             its own copy).  p, g, m and v are 16-byte aligned, scales 4-byte; an
+ *             empty tensor (n = 0) is skipped.  The tensors must not overlap.
+ *   state_bits  32: m, v fp32.  8: m int8, v uint8, with one fp32 scale per 256
+ *             elements (adamw_scale_floats(n) of them), the block's largest
+ *             magnitude a: m = a fl32(c |c| / 127^2), v = a fl32(q^4 / 255^4),
+ *             the codes those of the nearest root, a v > 0 never stored as 0; a
+ *             block whose largest magnitude is below 2^-126 is stored as zeros.
+ *             All-zero codes and scales are the initial state.
+ *   grad_bits  32: g fp32;  16: g bf16.
+ *   step_dev  device int32 or NULL: read instead of step, so that a captured update
+ *             can be replayed as the count advances (below 1 counts as 1).
+ * An element whose new moment is not finite keeps its parameter and moments and
+ * latches LSQ_DEV_ERR_NONFINITE.  Asynchronous, deterministic. */
+typedef struct lsq_adamw_tensor {
+  float* p;
+  const void* g;
+  void* m;
+  void* v;
+  float* m_scale;
+  float* v_scale;
+  int64_t n;
+  float lr, weight_decay;
+} lsq_adamw_tensor;
+typedef struct lsq_adamw_hyper {
+  float beta1, beta2, eps;
+  int32_t step;
+  int32_t state_bits;
+  int32_t grad_bits;
+  const int32_t* step_dev;
+} lsq_adamw_hyper;
+int64_t adamw_scale_floats(int64_t n);
+int adamw_multi_step(const lsq_adamw_tensor* tensors, int32_t n_tensors,
+                     const lsq_adamw_hyper* opt, void* stream);
+
+/* adamw_state_dequantize / adamw_state_quantize - an 8-bit moment to fp32 values and
+ * back (to save, load or convert a state).  is_signed 1: m (int8 codes), 0: v (uint8
+ * codes).  codes and values device [n], 16-byte aligned; scale device fp32
+ * [adamw_scale_floats(n)].  A value that is not finite, or negative for v, is stored
+ * as 0 and latches LSQ_DEV_ERR_NONFINITE.  Asynchronous, deterministic. */
+int adamw_state_dequantize(const void* codes, const float* scale, int64_t n, int32_t is_signed,
+                           float* out, void* stream);
+int adamw_state_quantize(const float* x, int64_t n, int32_t is_signed, void* codes, float* scale,
+                         void* stream);
 
 /* ------------------------------------------------------------ measurement */
 

@@ -49,7 +49,7 @@ void prof_release(std::vector<ProfRec>& recs);
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Device status word bits (latched by kernels, read by lsq_device_status).
-enum { DEV_ERR_WAIT_GEMM = 1, DEV_ERR_NONFINITE = 2 };
+enum { DEV_ERR_WAIT_GEMM = 1, DEV_ERR_NONFINITE = 2, DEV_ERR_INDEX = 4 };
 int* device_status_ptr();  // device address of the status word (current device)
 
 // NF4 levels and fp32 decision midpoints, derived on the host from the
@@ -266,6 +266,38 @@ int launch_attention_fwd(const uint16_t* qkv, int64_t T, int seq, int H, int Hkv
 int launch_attention_bwd(const uint16_t* qkv, const uint16_t* o, const uint16_t* dout,
                          const float* lse, int64_t T, int seq, int H, int Hkv, int d, float* delta,
                          float* dq, float* dk, float* dv, cudaStream_t st);
+
+// ---------------------------------------------------------------- packed documents
+// (the index's layout: packed.cuh)
+int check_packed(int64_t T, int64_t n_docs, const void* index, const char* who);
+int launch_packed_index(const int32_t* lengths, const int32_t* prefix, int n_docs, int64_t T,
+                        int32_t* index, cudaStream_t st);
+// targets of T tokens and their number, added to *count (or, without accumulate, set)
+int launch_packed_targets(const int32_t* tokens, const int32_t* index, int n_docs, int64_t T,
+                          const uint8_t* loss_mask, int32_t* targets, int32_t* count,
+                          int accumulate, cudaStream_t st);
+// row losses and, when dlogits is given, c_t (softmax - onehot) in bf16 with
+// c_t = weight[t] / max(*count, 1) (1 for a null weight or count); rows whose target is
+// negative get zeros
+int launch_packed_ce(const float* logits, int64_t T, int64_t V, const int32_t* targets,
+                     const float* weight, const int32_t* count, uint16_t* dlogits,
+                     float* row_loss, cudaStream_t st);
+int launch_packed_loss(const float* row_loss, const int32_t* targets, int64_t T, int64_t V,
+                       const float* weight, const int32_t* count, int accumulate, float* loss,
+                       cudaStream_t st);
+// attention inside the documents of an index: as launch_attention_fwd / _bwd, with o
+// and the gradients 0 and lse -inf in the padding
+int launch_packed_attention_fwd(const uint16_t* qkv, const int32_t* index, int n_docs, int64_t T,
+                                int H, int Hkv, int d, uint16_t* o, float* lse, cudaStream_t st);
+size_t packed_attention_ws_bytes(int64_t T, int H, int Hkv, int d);
+// cs (nullable): the RoPE table of the positions, whose rotation of q and k is undone
+// in their gradients
+int launch_packed_attention_bwd(const uint16_t* qkv, const int32_t* index, int n_docs,
+                                const uint16_t* o, const float* lse, const uint16_t* dout,
+                                int64_t T, int H, int Hkv, int d, const float2* cs, uint16_t* dqkv,
+                                void* ws, size_t ws_bytes, cudaStream_t st);
+int launch_adamw_multi(const lsq_adamw_tensor* t, int n, const lsq_adamw_hyper* o,
+                       cudaStream_t st);
 
 // ---------------------------------------------------------------- layer internals
 struct LayerShapes {

@@ -1,0 +1,392 @@
+// Operators of a packed fine-tuning step that are not attention: the index of the
+// documents in a row of tokens, the targets of the tokens that are trained on, and
+// the cross-entropy over the vocabulary with its gradient.
+#include <math.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "packed.cuh"
+
+namespace lsq {
+
+namespace {
+
+constexpr int kIdxThreads = 1024;
+
+// Inclusive sum over the CTA's 1024 threads (in thread order); sh holds 32 values.
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* sh) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t u = __shfl_up_sync(0xFFFFFFFFu, v, o);
+    if (lane >= o) v += u;
+  }
+  __syncthreads();  // sh is free
+  if (lane == 31) sh[warp] = v;
+  __syncthreads();
+  if (warp == 0) {
+    int64_t w = sh[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t u = __shfl_up_sync(0xFFFFFFFFu, w, o);
+      if (lane >= o) w += u;
+    }
+    sh[lane] = w;
+  }
+  __syncthreads();
+  return v + (warp > 0 ? sh[warp - 1] : 0);
+}
+
+// Index of the last entry of a[0, n) that is <= x (a ascending, a[0] <= x).
+__device__ __forceinline__ int find_last(const int* a, int n, int x) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (a[mid] <= x)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  return lo;
+}
+
+// Every CTA scans all lengths, 1024 documents at a time (a few microseconds for the
+// thousands of documents a row holds), and writes its own share of the tokens and
+// tiles, each found by a binary search over the 1024 starts in shared memory: a
+// single long document costs no more than many short ones.
+__global__ void __launch_bounds__(kIdxThreads)
+    packed_index_kernel(const int32_t* __restrict__ lengths, const int32_t* __restrict__ prefix,
+                        int n_docs, int T, PackedIndex x, int* dev_err) {
+  __shared__ int64_t sh[32];
+  __shared__ int tok0[kIdxThreads], t1[kIdxThreads], t2[kIdxThreads], doc_e[kIdxThreads],
+      doc_p[kIdxThreads];
+  pdl_trigger();
+  pdl_wait();
+  const int tid = threadIdx.x;
+  const int gtid = blockIdx.x * kIdxThreads + tid, gsize = gridDim.x * kIdxThreads;
+  int64_t base = 0;          // tokens, tiles of 128 and tiles of 256 before this chunk
+  int base1 = 0, base2 = 0;
+  bool bad = false;
+  for (int d0 = 0; d0 < n_docs; d0 += kIdxThreads) {
+    const int d = d0 + tid;
+    int len = d < n_docs ? lengths[d] : 0;
+    int pre = d < n_docs && prefix ? prefix[d] : 0;
+    if (len < 0 || pre < 0 || pre > len) bad = true;  // such a length counts as 0
+    len = max(len, 0);
+    const int64_t end = base + block_scan(len, sh);
+    const int64_t total = base + sh[31];
+    if (end > T) bad = true;  // documents are cut where the row ends
+    const int s = (int)min((int64_t)T, end - len), e = (int)min((int64_t)T, end);
+    pre = min(max(pre, 0), e - s);
+    const int n1 = (e - s + kPackedTile - 1) / kPackedTile;
+    const int n2 = (e - s + 2 * kPackedTile - 1) / (2 * kPackedTile);
+    const int64_t i12 = block_scan(((int64_t)n1 << 32) | (int64_t)n2, sh);
+    const int64_t all12 = sh[31];
+    tok0[tid] = s;
+    doc_e[tid] = e;
+    doc_p[tid] = s + pre;
+    t1[tid] = base1 + (int)(i12 >> 32) - n1;
+    t2[tid] = base2 + (int)(i12 & 0xFFFFFFFF) - n2;
+    __syncthreads();
+    // documents of no tokens share their start with the next one: the last at or
+    // before a token is the one that holds it
+    const int c1 = (int)(all12 >> 32), c2 = (int)(all12 & 0xFFFFFFFF);
+    const int hi = (int)min((int64_t)T, total);
+    for (int t = (int)base + gtid; t < hi; t += gsize) {
+      const int k = find_last(tok0, kIdxThreads, t);
+      x.pos[t] = t - tok0[k];
+      x.key_end[t] = max(t + 1, doc_p[k]);
+      x.doc_end[t] = doc_e[k];
+    }
+    for (int i = gtid; i < c1; i += gsize) {
+      const int k = find_last(t1, kIdxThreads, base1 + i);
+      if (base1 + i < x.cap)
+        x.tiles[base1 + i] = {tok0[k] + (base1 + i - t1[k]) * kPackedTile, tok0[k], doc_e[k],
+                              doc_p[k]};
+    }
+    for (int i = gtid; i < c2; i += gsize) {
+      const int k = find_last(t2, kIdxThreads, base2 + i);
+      if (base2 + i < x.cap2)
+        x.tiles2[base2 + i] = {tok0[k] + (base2 + i - t2[k]) * 2 * kPackedTile, tok0[k], doc_e[k],
+                               doc_p[k]};
+    }
+    base = hi;
+    base1 += c1;
+    base2 += c2;
+    if (total > T) bad = true;
+    __syncthreads();
+  }
+  // padding belongs to no document
+  for (int t = (int)base + gtid; t < T; t += gsize) {
+    x.pos[t] = 0;
+    x.key_end[t] = (int)base;
+    x.doc_end[t] = (int)base;
+  }
+  if (gtid == 0) {
+    x.head[0] = min(base1, x.cap);
+    x.head[1] = min(base2, x.cap2);
+    x.head[2] = (int)base;
+    for (int i = 3; i < 8; ++i) x.head[i] = 0;
+  }
+  if (bad) atomicOr(dev_err, DEV_ERR_INDEX);
+}
+
+// Target of token t: the next token, where that belongs to the same document, is not
+// seen by t itself (a prompt read in both directions is not predicted), and is marked
+// in loss_mask (if given); -1 elsewhere.  count: the integer sum over CTAs, the same
+// in any order.
+__global__ void __launch_bounds__(256)
+    packed_targets_kernel(const int32_t* __restrict__ tokens, const int* __restrict__ key_end,
+                          const int* __restrict__ doc_end, const uint8_t* __restrict__ loss_mask,
+                          int T, int32_t* __restrict__ targets, int32_t* __restrict__ count) {
+  pdl_trigger();
+  pdl_wait();
+  int n = 0;
+  for (int t = blockIdx.x * 256 + threadIdx.x; t < T; t += gridDim.x * 256) {
+    const bool on = t + 1 < doc_end[t] && key_end[t] == t + 1 && (!loss_mask || loss_mask[t + 1]);
+    targets[t] = on ? tokens[t + 1] : -1;
+    n += on;
+  }
+  n = __reduce_add_sync(0xFFFFFFFFu, n);
+  if ((threadIdx.x & 31) == 0 && n) atomicAdd(count, n);
+}
+
+// ------------------------------------------------------------------ cross-entropy
+constexpr float kLog2e = 1.4426950408889634f;
+
+// (max, sum of exp relative to it) of two sets; (-inf, 0) is the empty set.
+__device__ __forceinline__ void join(float& m, float& s, float mo, float so) {
+  const float mn = fmaxf(m, mo);
+  if (mn == -INFINITY) return;
+  s = s * exp2f((m - mn) * kLog2e) + so * exp2f((mo - mn) * kLog2e);
+  m = mn;
+}
+
+// One CTA per row.  A row is read twice (maximum and sum of exponentials in one pass,
+// then the gradient), the second time from L2 while it still holds it.  Elements are
+// taken eight at a time from the first whose index in the whole array is a multiple of
+// eight, so that any V is read and written in aligned 16-byte pieces.
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS)
+    packed_ce_kernel(const float* __restrict__ logits, const int32_t* __restrict__ targets,
+                     int64_t V, const float* __restrict__ weight, const int32_t* __restrict__ count,
+                     uint16_t* __restrict__ dlogits, float* __restrict__ row_loss, int* dev_err) {
+  __shared__ float red_m[32], red_s[32];
+  pdl_trigger();
+  pdl_wait();
+  const int64_t row = blockIdx.x;
+  const float* __restrict__ x = logits + row * V;
+  uint16_t* __restrict__ dx = dlogits ? dlogits + row * V : nullptr;
+  const int head = (int)min(V, (int64_t)((8 - (int)((row * V) & 7)) & 7));
+  const int64_t n8 = (V - head) / 8;
+  const int64_t tail = head + n8 * 8;
+  const int64_t y = targets[row];
+  const int tid = threadIdx.x;
+  if (y < 0 || y >= V) {
+    if (dx) {
+      for (int64_t i = tid; i < n8; i += THREADS)
+        reinterpret_cast<uint4*>(dx + head)[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (tid < head) dx[tid] = 0;
+      if (tail + tid < V && tid < 8) dx[tail + tid] = 0;
+    }
+    if (tid == 0) {
+      row_loss[row] = 0.f;
+      if (y >= V) atomicOr(dev_err, DEV_ERR_INDEX);
+    }
+    return;
+  }
+  float m = -INFINITY, s = 0.f;
+  auto add = [&](float v) { join(m, s, v, 1.f); };
+  if (tid < head) add(x[tid]);
+  if (tid < 8 && tail + tid < V) add(x[tail + tid]);
+  const float4* x4 = reinterpret_cast<const float4*>(x + head);
+  for (int64_t i = tid; i < n8; i += THREADS) {
+    const float4 a = x4[2 * i], b = x4[2 * i + 1];
+    const float t = fmaxf(fmaxf(fmaxf(a.x, a.y), fmaxf(a.z, a.w)),
+                          fmaxf(fmaxf(b.x, b.y), fmaxf(b.z, b.w)));
+    if (t > m) {
+      s *= exp2f((m - t) * kLog2e);
+      m = t;
+    }
+    const float c = m == -INFINITY ? 0.f : -m * kLog2e;
+    s += ((exp2f(fmaf(a.x, kLog2e, c)) + exp2f(fmaf(a.y, kLog2e, c))) +
+          (exp2f(fmaf(a.z, kLog2e, c)) + exp2f(fmaf(a.w, kLog2e, c)))) +
+         ((exp2f(fmaf(b.x, kLog2e, c)) + exp2f(fmaf(b.y, kLog2e, c))) +
+          (exp2f(fmaf(b.z, kLog2e, c)) + exp2f(fmaf(b.w, kLog2e, c))));
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float mo = __shfl_xor_sync(0xFFFFFFFFu, m, o);
+    const float so = __shfl_xor_sync(0xFFFFFFFFu, s, o);
+    join(m, s, mo, so);
+  }
+  if ((tid & 31) == 0) {
+    red_m[tid >> 5] = m;
+    red_s[tid >> 5] = s;
+  }
+  __syncthreads();
+  m = red_m[0];
+  s = red_s[0];
+  for (int w = 1; w < THREADS / 32; ++w) join(m, s, red_m[w], red_s[w]);
+  if (tid == 0) row_loss[row] = m + logf(s) - x[y];
+  if (!dx) return;
+  float c = weight ? weight[row] : 1.f;
+  if (count) c /= (float)max(1, *count);
+  const float k = c / s, off = -m * kLog2e;
+  auto grad = [&](float v, int64_t j) { return k * exp2f(fmaf(v, kLog2e, off)) - (j == y ? c : 0.f); };
+  if (tid < head) dx[tid] = float_to_bf16_bits(grad(x[tid], tid));
+  if (tid < 8 && tail + tid < V) dx[tail + tid] = float_to_bf16_bits(grad(x[tail + tid], tail + tid));
+  for (int64_t i = tid; i < n8; i += THREADS) {
+    const float4 a = x4[2 * i], b = x4[2 * i + 1];
+    const int64_t j = head + 8 * i;
+    reinterpret_cast<uint4*>(dx + head)[i] =
+        make_uint4(pack_bf16x2(grad(a.x, j), grad(a.y, j + 1)),
+                   pack_bf16x2(grad(a.z, j + 2), grad(a.w, j + 3)),
+                   pack_bf16x2(grad(b.x, j + 4), grad(b.y, j + 5)),
+                   pack_bf16x2(grad(b.z, j + 6), grad(b.w, j + 7)));
+  }
+}
+
+// loss (+)= sum over rows with a target of c_t row_loss[t], in a fixed order.
+__global__ void __launch_bounds__(1024)
+    packed_loss_kernel(const float* __restrict__ row_loss, const int32_t* __restrict__ targets,
+                       int64_t T, int64_t V, const float* __restrict__ weight,
+                       const int32_t* __restrict__ count, int accumulate, float* __restrict__ loss) {
+  __shared__ float red[32];
+  pdl_trigger();
+  pdl_wait();
+  float s = 0.f;
+  for (int64_t t = threadIdx.x; t < T; t += 1024)
+    if (targets[t] >= 0 && targets[t] < V) s += (weight ? weight[t] : 1.f) * row_loss[t];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s;
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    s = red[threadIdx.x];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+    if (threadIdx.x == 0) {
+      if (count) s /= (float)max(1, *count);
+      *loss = (accumulate ? *loss : 0.f) + s;
+    }
+  }
+}
+
+template <class... P, class... A>
+cudaError_t launch_dep(void (*k)(P...), unsigned grid, unsigned threads, cudaStream_t st, A... a) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return ::lsq::launched(cudaLaunchKernelEx(&cfg, k, P(a)...));
+}
+
+}  // namespace
+
+int launch_packed_index(const int32_t* lengths, const int32_t* prefix, int n_docs, int64_t T,
+                        int32_t* index, cudaStream_t st) {
+  int* err = device_status_ptr();
+  if (!err) return set_error(LSQ_ERR_CUDA, "device status word unavailable");
+  const unsigned grid = (unsigned)std::min<int64_t>(64, (T + kIdxThreads - 1) / kIdxThreads);
+  LSQ_CUDA(launch_dep(packed_index_kernel, grid, kIdxThreads, st, lengths, prefix, n_docs, (int)T,
+                      packed_index_view(index, T, n_docs), err));
+  return LSQ_OK;
+}
+
+int launch_packed_targets(const int32_t* tokens, const int32_t* index, int n_docs, int64_t T,
+                          const uint8_t* loss_mask, int32_t* targets, int32_t* count,
+                          int accumulate, cudaStream_t st) {
+  const PackedIndex x = packed_index_view(index, T, n_docs);
+  if (!accumulate) LSQ_CUDA(cudaMemsetAsync(count, 0, sizeof(int32_t), st));
+  const unsigned grid = (unsigned)std::min<int64_t>(512, (T + 255) / 256);
+  LSQ_CUDA(launch_dep(packed_targets_kernel, grid, 256, st, tokens, x.key_end, x.doc_end, loss_mask,
+                      (int)T, targets, count));
+  return LSQ_OK;
+}
+
+int launch_packed_ce(const float* logits, int64_t T, int64_t V, const int32_t* targets,
+                     const float* weight, const int32_t* count, uint16_t* dlogits,
+                     float* row_loss, cudaStream_t st) {
+  int* err = device_status_ptr();
+  if (!err) return set_error(LSQ_ERR_CUDA, "device status word unavailable");
+  const int prof = prof_begin(st);
+  if (V >= 4096)
+    LSQ_CUDA(launch_dep(packed_ce_kernel<512>, (unsigned)T, 512, st, logits, targets, V, weight,
+                        count, dlogits, row_loss, err));
+  else
+    LSQ_CUDA(launch_dep(packed_ce_kernel<128>, (unsigned)T, 128, st, logits, targets, V, weight,
+                        count, dlogits, row_loss, err));
+  if (prof >= 0) prof_end(prof, st, "packed_ce", 0.0, (dlogits ? 6.0 : 4.0) * T * V);
+  return LSQ_OK;
+}
+
+int launch_packed_loss(const float* row_loss, const int32_t* targets, int64_t T, int64_t V,
+                       const float* weight, const int32_t* count, int accumulate, float* loss,
+                       cudaStream_t st) {
+  LSQ_CUDA(launch_dep(packed_loss_kernel, 1, 1024, st, row_loss, targets, T, V, weight, count,
+                      accumulate, loss));
+  return LSQ_OK;
+}
+
+int check_packed(int64_t T, int64_t n_docs, const void* index, const char* who) {
+  if (T <= 0 || T > (int64_t(1) << 30))
+    return set_error(LSQ_ERR_SHAPE, "%s: T must be in [1, 2^30]", who);
+  if (n_docs <= 0 || n_docs > (int64_t(1) << 24))
+    return set_error(LSQ_ERR_SHAPE, "%s: n_docs must be in [1, 2^24]", who);
+  if (!index) return set_error(LSQ_ERR_INVALID, "%s: null index", who);
+  if (!aligned16(index)) return set_error(LSQ_ERR_ALIGN, "%s: the index must be 16-byte aligned", who);
+  return LSQ_OK;
+}
+
+}  // namespace lsq
+
+using namespace lsq;
+
+extern "C" int64_t packed_index_ints(int64_t T, int32_t n_docs) {
+  if (T <= 0 || n_docs <= 0) return 0;
+  return packed_index_words(T, n_docs);
+}
+
+extern "C" int packed_index(const int32_t* lengths, const int32_t* prefix, int32_t n_docs,
+                            int64_t T, int32_t* index, void* stream) {
+  LSQ_TRY(check_packed(T, n_docs, index, "packed_index"));
+  if (!lengths) return set_error(LSQ_ERR_INVALID, "packed_index: null lengths");
+  return launch_packed_index(lengths, prefix, n_docs, T, index, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" int packed_targets(const int32_t* tokens, const int32_t* index, int32_t n_docs,
+                              int64_t T, const uint8_t* loss_mask, int32_t* targets,
+                              int32_t* count, int32_t accumulate, void* stream) {
+  LSQ_TRY(check_packed(T, n_docs, index, "packed_targets"));
+  if (!tokens || !targets || !count)
+    return set_error(LSQ_ERR_INVALID, "packed_targets: null pointer");
+  if (accumulate != 0 && accumulate != 1)
+    return set_error(LSQ_ERR_INVALID, "packed_targets: accumulate must be 0 or 1");
+  return launch_packed_targets(tokens, index, n_docs, T, loss_mask, targets, count, accumulate,
+                               static_cast<cudaStream_t>(stream));
+}
+
+extern "C" int packed_cross_entropy(const float* logits, int64_t T, int64_t V,
+                                    const int32_t* targets, const float* weight,
+                                    const int32_t* count, uint16_t* dlogits, float* row_loss,
+                                    float* loss, int32_t accumulate, void* stream) {
+  if (T <= 0 || T > INT32_MAX || V <= 0 || V > INT32_MAX)
+    return set_error(LSQ_ERR_SHAPE, "packed_cross_entropy: T and V must be in [1, 2^31)");
+  if (!logits || !targets || !row_loss || !loss)
+    return set_error(LSQ_ERR_INVALID, "packed_cross_entropy: null pointer");
+  if (accumulate != 0 && accumulate != 1)
+    return set_error(LSQ_ERR_INVALID, "packed_cross_entropy: accumulate must be 0 or 1");
+  if (!aligned16(logits) || (dlogits && !aligned16(dlogits)))
+    return set_error(LSQ_ERR_ALIGN,
+                     "packed_cross_entropy: logits and dlogits must be 16-byte aligned");
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  LSQ_TRY(launch_packed_ce(logits, T, V, targets, weight, count, dlogits, row_loss, st));
+  return launch_packed_loss(row_loss, targets, T, V, weight, count, accumulate, loss, st);
+}

@@ -15,6 +15,9 @@ LIB_PATH = os.path.join(HERE, "liblsq.so")
 LSQ_OK, LSQ_ERR_INVALID, LSQ_ERR_SHAPE, LSQ_ERR_CUDA = 0, 1, 2, 3
 LSQ_ERR_TIMEOUT, LSQ_ERR_WORKSPACE, LSQ_ERR_ALIGN, LSQ_ERR_DEVICE = 4, 5, 6, 7
 
+# device status word bits (lsq_device_status)
+LSQ_DEV_ERR_WAIT, LSQ_DEV_ERR_NONFINITE, LSQ_DEV_ERR_INDEX = 1, 2, 4
+
 # Every symbol include/lsq.h declares (checked by tests/test_abi.py).
 EXPORTS = (
     "lsq_last_error", "lsq_version", "lsq_device_status", "lsq_nf4_codebook",
@@ -28,6 +31,9 @@ EXPORTS = (
     "stream_stack_dpo_workspace_bytes", "stream_stack_dpo_step", "lsq_bf16_from_f32",
     "lsq_shard_bytes", "lsq_nccl_unique_id", "stream_stack_shard", "lsq_stream_plan",
     "stream_stack_reduce_grads", "lsq_gemm_plan_get", "lsq_lora_plan_get",
+    "packed_index_ints", "packed_index", "packed_targets", "packed_cross_entropy",
+    "packed_attention_fwd", "packed_attention_bwd", "packed_attention_workspace_bytes",
+    "adamw_scale_floats", "adamw_multi_step", "adamw_state_dequantize", "adamw_state_quantize",
 )
 LSQ_NCCL_ID_BYTES = 128
 
@@ -65,6 +71,17 @@ class lsq_adamw(ctypes.Structure):
     _fields_ = [("lr", ctypes.c_float), ("beta1", ctypes.c_float), ("beta2", ctypes.c_float),
                 ("eps", ctypes.c_float), ("weight_decay", ctypes.c_float),
                 ("step", ctypes.c_int32), ("m", ctypes.c_void_p), ("v", ctypes.c_void_p)]
+
+
+class lsq_adamw_tensor(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("p", "g", "m", "v", "m_scale", "v_scale")] + [
+        ("n", ctypes.c_int64), ("lr", ctypes.c_float), ("weight_decay", ctypes.c_float)]
+
+
+class lsq_adamw_hyper(ctypes.Structure):
+    _fields_ = [("beta1", ctypes.c_float), ("beta2", ctypes.c_float), ("eps", ctypes.c_float),
+                ("step", ctypes.c_int32), ("state_bits", ctypes.c_int32),
+                ("grad_bits", ctypes.c_int32), ("step_dev", ctypes.c_void_p)]
 
 
 class lsq_prof_entry(ctypes.Structure):
@@ -150,6 +167,19 @@ _PROTOS = {
     "lsq_lora_plan_get": (ctypes.c_int, [_I64, _I64, _I64, _I32, ctypes.POINTER(lsq_lora_plan)]),
     "nf4_lora_linear_fwd_noalloc": (ctypes.c_int, [_P, _I64, _I64, _I64, _P, _P, _I32, _P, _P, _I32,
                                                    _F, _P, _P, _I32, _P, _P]),
+    "packed_index_ints": (_I64, [_I64, _I32]),
+    "packed_index": (ctypes.c_int, [_P, _P, _I32, _I64, _P, _P]),
+    "packed_attention_fwd": (ctypes.c_int, [_P, _P, _I32, _I64, _I32, _I32, _I32, _P, _P, _P]),
+    "packed_attention_workspace_bytes": (_SZ, [_I64, _I32, _I32, _I32]),
+    "packed_attention_bwd": (ctypes.c_int, [_P, _P, _I32, _P, _P, _P, _I64, _I32, _I32, _I32, _P,
+                                            _P, _SZ, _P]),
+    "packed_targets": (ctypes.c_int, [_P, _P, _I32, _I64, _P, _P, _P, _I32, _P]),
+    "packed_cross_entropy": (ctypes.c_int, [_P, _I64, _I64, _P, _P, _P, _P, _P, _P, _I32, _P]),
+    "adamw_scale_floats": (_I64, [_I64]),
+    "adamw_multi_step": (ctypes.c_int, [ctypes.POINTER(lsq_adamw_tensor), _I32,
+                                        ctypes.POINTER(lsq_adamw_hyper), _P]),
+    "adamw_state_dequantize": (ctypes.c_int, [_P, _P, _I64, _I32, _P, _P]),
+    "adamw_state_quantize": (ctypes.c_int, [_P, _I64, _I32, _P, _P, _P]),
     "lsq_profile_enable": (ctypes.c_int, [ctypes.c_int]),
     "lsq_profile_read": (ctypes.c_int, [ctypes.POINTER(lsq_prof_entry), _I32,
                                         ctypes.POINTER(ctypes.c_int32)]),
@@ -488,3 +518,257 @@ def nf4_lora_linear_fwd_noalloc(x, codes, absmax, A, B, scale, y, residual=None,
     _check(load().nf4_lora_linear_fwd_noalloc(_ptr(x), T, K, N, _ptr(codes), _ptr(absmax), block,
                                               _ptr(A), _ptr(B), r, scale, _ptr(residual), _ptr(y),
                                               _y_fp32(y), _ptr(u_out), _stream(stream)))
+
+
+# ------------------------------------------------------------ packed documents, AdamW
+class _On:
+    """The tensors of one call: all on one CUDA device, which is made current for the call."""
+
+    def __init__(self, stream, **tensors):
+        import torch
+        dev = None
+        for name, t in tensors.items():
+            if t is None:
+                continue
+            if not t.is_cuda:
+                raise ValueError("%s must be a CUDA tensor" % name)
+            if dev is not None and t.device != dev:
+                raise ValueError("%s is on %s, the other tensors on %s" % (name, t.device, dev))
+            dev = t.device
+        self.dev, self.prev, self.cuda = dev.index, None, torch.cuda
+        self.given = stream
+
+    def __enter__(self):
+        if self.cuda.current_device() != self.dev:
+            self.prev = self.cuda.current_device()
+            self.cuda.set_device(self.dev)
+        if self.given is not None:
+            return ctypes.c_void_p(self.given)
+        return ctypes.c_void_p(self.cuda.current_stream().cuda_stream)
+
+    def __exit__(self, *exc):
+        if self.prev is not None:
+            self.cuda.set_device(self.prev)
+
+
+def _need(name, t, dtype, shape=None, numel=None, optional=False):
+    """Checks one tensor argument: its type, that it is contiguous, its shape or length."""
+    import torch
+    if t is None and optional:
+        return
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch tensor" % name)
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, not %s" % (name, dtype, t.dtype))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must have shape %s, not %s" % (name, tuple(shape), tuple(t.shape)))
+    if numel is not None and t.numel() != numel:
+        raise ValueError("%s must have %d elements, not %d" % (name, numel, t.numel()))
+
+
+def packed_index_ints(T, n_docs):
+    return int(load().packed_index_ints(int(T), int(n_docs)))
+
+
+class PackedIndex:
+    """The buffer of a packed row's index: n_tokens tokens holding n_docs documents
+    (filled by packed_index, once per batch)."""
+
+    def __init__(self, n_tokens, n_docs, device="cuda"):
+        import torch
+        words = packed_index_ints(n_tokens, n_docs)
+        if words <= 0:
+            raise ValueError("a packed row has at least one token and one document")
+        self.n_tokens, self.n_docs = int(n_tokens), int(n_docs)
+        self.buf = torch.empty(words, dtype=torch.int32, device=device)
+
+
+def packed_index(lengths, index, prefix=None, stream=None):
+    """lengths, prefix: int32 [n_docs] on the device; index: PackedIndex (filled)."""
+    import torch
+    _need("lengths", lengths, torch.int32, (index.n_docs,))
+    _need("prefix", prefix, torch.int32, (index.n_docs,), optional=True)
+    with _On(stream, lengths=lengths, prefix=prefix, index=index.buf) as st:
+        _check(load().packed_index(_ptr(lengths), _ptr(prefix), index.n_docs, index.n_tokens,
+                                   _ptr(index.buf), st))
+
+
+def _packed_heads(qkv, index, n_heads, n_kv_heads):
+    import torch
+    n = n_heads + 2 * n_kv_heads
+    if n_heads <= 0 or n_kv_heads <= 0 or qkv.dim() != 2 or qkv.shape[1] % n:
+        raise ValueError("qkv must be [T, (n_heads + 2 n_kv_heads) d]")
+    _need("qkv", qkv, torch.float16, (index.n_tokens, qkv.shape[1]))
+    return qkv.shape[1] // n
+
+
+def packed_attention_fwd(qkv, index, n_heads, n_kv_heads, o, lse, stream=None):
+    """qkv: fp16 [T, (H + 2 Hkv) d]; o: fp16 [T, H d]; lse: fp32 [H, T]."""
+    import torch
+    d, T = _packed_heads(qkv, index, n_heads, n_kv_heads), index.n_tokens
+    _need("o", o, torch.float16, (T, n_heads * d))
+    _need("lse", lse, torch.float32, (n_heads, T))
+    with _On(stream, qkv=qkv, index=index.buf, o=o, lse=lse) as st:
+        _check(load().packed_attention_fwd(_ptr(qkv), _ptr(index.buf), index.n_docs, T, n_heads,
+                                           n_kv_heads, d, _ptr(o), _ptr(lse), st))
+
+
+def packed_attention_workspace_bytes(T, n_heads, n_kv_heads, d):
+    return int(load().packed_attention_workspace_bytes(int(T), n_heads, n_kv_heads, d))
+
+
+def packed_attention_bwd(qkv, index, o, lse, dout, n_heads, n_kv_heads, dqkv, ws, stream=None):
+    """dout: bf16 [T, H d]; dqkv: bf16, the shape of qkv (overwritten); ws: uint8 of
+    packed_attention_workspace_bytes."""
+    import torch
+    d, T = _packed_heads(qkv, index, n_heads, n_kv_heads), index.n_tokens
+    _need("o", o, torch.float16, (T, n_heads * d))
+    _need("lse", lse, torch.float32, (n_heads, T))
+    _need("dout", dout, torch.bfloat16, (T, n_heads * d))
+    _need("dqkv", dqkv, torch.bfloat16, qkv.shape)
+    _need("ws", ws, torch.uint8)
+    with _On(stream, qkv=qkv, index=index.buf, o=o, lse=lse, dout=dout, dqkv=dqkv, ws=ws) as st:
+        _check(load().packed_attention_bwd(_ptr(qkv), _ptr(index.buf), index.n_docs, _ptr(o),
+                                           _ptr(lse), _ptr(dout), T, n_heads, n_kv_heads, d,
+                                           _ptr(dqkv), _ptr(ws), ws.numel(), st))
+
+
+def packed_targets(tokens, index, targets, count, loss_mask=None, accumulate=False, stream=None):
+    """tokens, targets: int32 [T]; count: int32 [1]; loss_mask: uint8 or bool [T]."""
+    import torch
+    T = index.n_tokens
+    _need("tokens", tokens, torch.int32, numel=T)
+    _need("targets", targets, torch.int32, numel=T)
+    _need("count", count, torch.int32, numel=1)
+    if loss_mask is not None and loss_mask.dtype == torch.bool:
+        loss_mask = loss_mask.view(torch.uint8)
+    _need("loss_mask", loss_mask, torch.uint8, numel=T, optional=True)
+    with _On(stream, tokens=tokens, index=index.buf, targets=targets, count=count,
+             loss_mask=loss_mask) as st:
+        _check(load().packed_targets(_ptr(tokens), _ptr(index.buf), index.n_docs, T,
+                                     _ptr(loss_mask), _ptr(targets), _ptr(count),
+                                     1 if accumulate else 0, st))
+
+
+def packed_cross_entropy(logits, targets, row_loss, loss, dlogits=None, weight=None, count=None,
+                         accumulate=False, stream=None):
+    """logits: fp32 [T, V]; targets: int32 [T]; row_loss: fp32 [T]; loss: fp32 [1];
+    dlogits: bf16 [T, V]; weight: fp32 [T]; count: int32 [1]."""
+    import torch
+    if logits.dim() != 2:
+        raise ValueError("logits must be [T, V]")
+    T, V = logits.shape
+    _need("logits", logits, torch.float32, (T, V))
+    _need("targets", targets, torch.int32, numel=T)
+    _need("row_loss", row_loss, torch.float32, numel=T)
+    _need("loss", loss, torch.float32, numel=1)
+    _need("dlogits", dlogits, torch.bfloat16, (T, V), optional=True)
+    _need("weight", weight, torch.float32, numel=T, optional=True)
+    _need("count", count, torch.int32, numel=1, optional=True)
+    with _On(stream, logits=logits, targets=targets, row_loss=row_loss, loss=loss, dlogits=dlogits,
+             weight=weight, count=count) as st:
+        _check(load().packed_cross_entropy(_ptr(logits), T, V, _ptr(targets), _ptr(weight),
+                                           _ptr(count), _ptr(dlogits), _ptr(row_loss), _ptr(loss),
+                                           1 if accumulate else 0, st))
+
+
+def adamw_scale_floats(n):
+    return int(load().adamw_scale_floats(int(n)))
+
+
+def _state_signed(codes):
+    import torch
+    if codes.dtype not in (torch.int8, torch.uint8):
+        raise TypeError("codes must be int8 (m) or uint8 (v)")
+    return 1 if codes.dtype == torch.int8 else 0
+
+
+def adamw_state_dequantize(codes, scale, out, stream=None):
+    """codes: int8 (m) or uint8 (v); scale: fp32 per 256 codes; out: fp32."""
+    import torch
+    signed, n = _state_signed(codes), codes.numel()
+    _need("codes", codes, codes.dtype)
+    _need("scale", scale, torch.float32, numel=adamw_scale_floats(n))
+    _need("out", out, torch.float32, numel=n)
+    with _On(stream, codes=codes, scale=scale, out=out) as st:
+        _check(load().adamw_state_dequantize(_ptr(codes), _ptr(scale), n, signed, _ptr(out), st))
+
+
+def adamw_state_quantize(x, codes, scale, stream=None):
+    """The inverse: x fp32 to int8 (m) or uint8 (v) codes and their scales."""
+    import torch
+    signed, n = _state_signed(codes), codes.numel()
+    _need("codes", codes, codes.dtype)
+    _need("x", x, torch.float32, numel=n)
+    _need("scale", scale, torch.float32, numel=adamw_scale_floats(n))
+    with _On(stream, x=x, codes=codes, scale=scale) as st:
+        _check(load().adamw_state_quantize(_ptr(x), n, signed, _ptr(codes), _ptr(scale), st))
+
+
+class AdamWMulti:
+    """AdamW over lists of tensors, one adamw_multi_step per step.
+
+    params: fp32; grads: all fp32 or all bf16; m, v: fp32 (32-bit state), or int8 and
+    uint8 with m_scale, v_scale (8-bit state, fp32 scales of adamw_scale_floats(numel)).
+    lr, weight_decay: one number or one per tensor.  The tensors are checked and their
+    addresses taken here; they must stay allocated while the object is used."""
+
+    def __init__(self, params, grads, m, v, lr, weight_decay=0.0, m_scale=None, v_scale=None,
+                 betas=(0.9, 0.999), eps=1e-8):
+        import torch
+        n = len(params)
+        bits = 8 if n and m[0].dtype == torch.int8 else 32
+        gdt = grads[0].dtype if n else torch.float32
+        if gdt not in (torch.float32, torch.bfloat16):
+            raise TypeError("gradients must be float32 or bfloat16")
+        lists = [params, grads, m, v] + ([m_scale, v_scale] if bits == 8 else [])
+        if any(x is None or len(x) != n for x in lists):
+            raise ValueError("params, grads, m, v%s need one tensor each per parameter"
+                             % (", m_scale, v_scale" if bits == 8 else ""))
+        lrs = list(lr) if hasattr(lr, "__len__") else [lr] * n
+        wds = list(weight_decay) if hasattr(weight_decay, "__len__") else [weight_decay] * n
+        if len(lrs) != n or len(wds) != n:
+            raise ValueError("lr and weight_decay need one number per parameter")
+        self._table = (lsq_adamw_tensor * max(n, 1))()
+        self._n, self._keep, self._dev = n, lists, None
+        for i in range(n):
+            k = params[i].numel()
+            _need("params[%d]" % i, params[i], torch.float32)
+            _need("grads[%d]" % i, grads[i], gdt, numel=k)
+            _need("m[%d]" % i, m[i], torch.int8 if bits == 8 else torch.float32, numel=k)
+            _need("v[%d]" % i, v[i], torch.uint8 if bits == 8 else torch.float32, numel=k)
+            if bits == 8:
+                _need("m_scale[%d]" % i, m_scale[i], torch.float32, numel=adamw_scale_floats(k))
+                _need("v_scale[%d]" % i, v_scale[i], torch.float32, numel=adamw_scale_floats(k))
+            ts = [x[i] for x in lists]
+            for t in ts:
+                if not t.is_cuda:
+                    raise ValueError("tensor %d is not on a CUDA device" % i)
+                if self._dev is None:
+                    self._dev = t
+                if t.device != self._dev.device:
+                    raise ValueError("tensor %d is on %s, the first on %s"
+                                     % (i, t.device, self._dev.device))
+            ptrs = [t.data_ptr() for t in ts] + [None] * (6 - len(ts))
+            self._table[i] = lsq_adamw_tensor(*ptrs, k, lrs[i], wds[i])
+        self._hyper = lsq_adamw_hyper(beta1=betas[0], beta2=betas[1], eps=eps, step=1,
+                                      state_bits=bits,
+                                      grad_bits=32 if gdt == torch.float32 else 16)
+
+    def step(self, step, stream=None):
+        """One update; step: the count from 1, or an int32 device tensor that holds it
+        (for a captured update that is replayed as the count advances)."""
+        import torch
+        h = self._hyper
+        if isinstance(step, torch.Tensor):
+            _need("step", step, torch.int32, numel=1)
+            h.step, h.step_dev = 1, step.data_ptr()
+        else:
+            h.step, h.step_dev = int(step), None
+        if self._n == 0:
+            return
+        with _On(stream, params=self._dev,
+                 step=step if isinstance(step, torch.Tensor) else None) as st:
+            _check(load().adamw_multi_step(self._table, self._n, ctypes.byref(h), st))

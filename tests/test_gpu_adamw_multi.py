@@ -1,0 +1,219 @@
+"""GPU parity of AdamW over many tensors: the 8-bit codes and scales bit for bit, the
+fp32 moments bit for bit, and the parameters within a few fp32 roundings of the oracle.
+"""
+import numpy as np
+import pytest
+
+from oracle import packed as op
+
+pytestmark = pytest.mark.gpu
+
+SIZES = [1, 3, 4, 255, 256, 257, 0, 2048, 2049, 5000, 64 * 256]
+
+
+@pytest.fixture(scope="module")
+def L():
+    from layer_streamed_qlora_nf4_b200 import lib
+    lib.load()
+    return lib
+
+
+def _problem(sizes, bits, gbf16, seed):
+    """Tensors with a running state, every one in its own allocation."""
+    import torch
+    rng = np.random.default_rng(seed)
+    out = dict(p=[], g=[], m=[], v=[], ms=[], vs=[])
+    for n in sizes:
+        s = np.exp(rng.standard_normal()) * 1e-4
+        g = (rng.standard_normal(n) * s).astype(np.float32)
+        if gbf16:
+            g = torch.from_numpy(g).bfloat16().float().numpy()
+        m = (rng.standard_normal(n) * s * 0.3).astype(np.float32)
+        v = ((0.1 + rng.standard_normal(n) ** 2) * s * s).astype(np.float32)
+        v[rng.random(n) < 0.05] = 0
+        if bits == 8:
+            mc, ms = op.encode(m, True)
+            vc, vs = op.encode(v, False)
+            out["m"].append(mc), out["v"].append(vc), out["ms"].append(ms), out["vs"].append(vs)
+        else:
+            out["m"].append(m), out["v"].append(v), out["ms"].append(None), out["vs"].append(None)
+        out["p"].append((rng.standard_normal(n) * 0.02 * (rng.random() < 0.7)).astype(np.float32))
+        out["g"].append(g)
+    return out
+
+
+def _device(x, gbf16):
+    import torch
+    d = {k: [None if a is None else torch.from_numpy(a.copy()).cuda() for a in x[k]] for k in x}
+    if gbf16:
+        d["g"] = [a.bfloat16() for a in d["g"]]
+    return d
+
+
+def _opt(L, d, lr, wd, bits):
+    return L.AdamWMulti(d["p"], d["g"], d["m"], d["v"], lr=lr, weight_decay=wd,
+                        m_scale=d["ms"] if bits == 8 else None,
+                        v_scale=d["vs"] if bits == 8 else None)
+
+
+def _reference(x, step, lr, wd, bits):
+    """One oracle step of every tensor, in place."""
+    for i in range(len(x["p"])):
+        m, v = x["m"][i], x["v"][i]
+        if bits == 8:
+            m, v = op.decode(m, x["ms"][i]), op.decode(v, x["vs"][i])
+        p, m, v = op.adamw(x["p"][i], x["g"][i], m, v, step, lr[i], wd[i])
+        x["p"][i] = p
+        if bits == 8:
+            x["m"][i], x["ms"][i] = op.encode(m, True)
+            x["v"][i], x["vs"][i] = op.encode(v, False)
+        else:
+            x["m"][i], x["v"][i] = m, v
+
+
+def _check(x, d, lr, bits, steps=1):
+    for i in range(len(x["p"])):
+        for k in ("m", "v") + (("ms", "vs") if bits == 8 else ()):
+            assert np.array_equal(d[k][i].cpu().numpy(), x[k][i]), (k, i)
+        # p is rounded twice a step (2^-24 each), and the update of at most a few lr is
+        # off by 2^-20 relative
+        tol = steps * (2.0 ** -23 * np.abs(x["p"][i]) + 2.0 ** -20 * 10 * lr[i])
+        assert (np.abs(d["p"][i].cpu().numpy() - x["p"][i]) <= tol).all(), i
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+@pytest.mark.parametrize("gbf16", [False, True])
+@pytest.mark.parametrize("copies", [1, 50])
+def test_steps(L, bits, gbf16, copies):
+    """copies = 50: more tensors than one launch takes."""
+    import torch
+    sizes = SIZES * copies if copies == 1 else [s for s in SIZES if s < 300] * copies + [700]
+    sizes = sizes if copies == 1 else sizes * 2
+    x = _problem(sizes, bits, gbf16, seed=bits + copies)
+    d = _device(x, gbf16)
+    n = len(sizes)
+    lr = [2e-4 * (1 + i % 3) for i in range(n)]
+    wd = [0.01 * (i % 2) for i in range(n)]
+    o = _opt(L, d, lr, wd, bits)
+    for step in (3, 4):
+        o.step(step)
+        _reference(x, step, lr, wd, bits)
+    torch.cuda.synchronize()
+    assert L.lsq_device_status(clear=True) == 0
+    _check(x, d, lr, bits, steps=2)
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_from_nothing(L, bits):
+    """Zero state and zero parameters: the first step is lr times the gradient's sign."""
+    import torch
+    n = 1000
+    g = np.random.default_rng(0).standard_normal(n).astype(np.float32) * np.float32(1e-6)
+    g[::7] = 0
+    x = dict(p=[np.zeros(n, np.float32)], g=[g],
+             m=[np.zeros(n, np.int8 if bits == 8 else np.float32)],
+             v=[np.zeros(n, np.uint8 if bits == 8 else np.float32)],
+             ms=[np.zeros(4, np.float32)], vs=[np.zeros(4, np.float32)])
+    d = _device(x, False)
+    _opt(L, d, 1e-3, 0.0, bits).step(1)
+    _reference(x, 1, [1e-3], [0.0], bits)
+    torch.cuda.synchronize()
+    _check(x, d, [1e-3], bits)
+    assert not d["p"][0][::7].any()
+
+
+def test_tiny_and_huge_moments(L):
+    """Blocks whose largest magnitude is below the normal range are stored as zeros; very
+    large ones stay finite."""
+    import torch
+    g = np.concatenate([np.full(256, 1e-39), np.full(256, 1e-22), np.full(256, 1e15)]).astype(np.float32)
+    x = dict(p=[np.zeros(768, np.float32)], g=[g], m=[np.zeros(768, np.int8)],
+             v=[np.zeros(768, np.uint8)], ms=[np.zeros(3, np.float32)], vs=[np.zeros(3, np.float32)])
+    d = _device(x, False)
+    _opt(L, d, 1e-3, 0.0, 8).step(1)
+    _reference(x, 1, [1e-3], [0.0], 8)
+    torch.cuda.synchronize()
+    _check(x, d, [1e-3], 8)
+    assert d["ms"][0][0].item() == 0 and d["vs"][0][1].item() == 0
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_not_finite_gradients_are_left_out(L, bits):
+    import torch
+    sizes = [600]
+    x = _problem(sizes, bits, False, 7)
+    bad = [0, 5, 256, 599]
+    clean = {k: [a.copy() if a is not None else None for a in v] for k, v in x.items()}
+    for i, val in zip(bad, (np.nan, np.inf, -np.inf, 1e30)):  # 1e30: its square overflows
+        x["g"][0][i] = val
+    d = _device(x, False)
+    _opt(L, d, 1e-3, 0.01, bits).step(2)
+    torch.cuda.synchronize()
+    assert L.lsq_device_status(clear=True) == L.LSQ_DEV_ERR_NONFINITE
+    p = d["p"][0].cpu().numpy()
+    assert np.array_equal(p[bad], clean["p"][0][bad]) and np.isfinite(p).all()
+    m0 = clean["m"][0] if bits == 32 else op.decode(clean["m"][0], clean["ms"][0])
+    v0 = clean["v"][0] if bits == 32 else op.decode(clean["v"][0], clean["vs"][0])
+    g = clean["g"][0].copy()
+    rp, m1, v1 = op.adamw(clean["p"][0], g, m0, v0, 2, 1e-3, 0.01)
+    m1[bad], v1[bad], rp[bad] = m0[bad], v0[bad], clean["p"][0][bad]
+    if bits == 32:
+        assert np.array_equal(d["m"][0].cpu().numpy(), m1)
+        assert np.array_equal(d["v"][0].cpu().numpy(), v1)
+    else:
+        for k, s, ref, signed in (("m", "ms", m1, True), ("v", "vs", v1, False)):
+            c, sc = op.encode(ref, signed)
+            assert np.array_equal(d[k][0].cpu().numpy(), c)
+            assert np.array_equal(d[s][0].cpu().numpy(), sc)
+
+
+def test_replayed_graph_follows_the_count(L):
+    import torch
+    x = _problem([700, 300], 8, False, 9)
+    d = _device(x, False)
+    count = torch.zeros(1, dtype=torch.int32, device="cuda")
+    o = _opt(L, d, 1e-3, 0.0, 8)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        count += 1
+        o.step(count)
+    for step in (1, 2, 3):
+        g.replay()
+        _reference(x, step, [1e-3] * 2, [0.0] * 2, 8)
+    torch.cuda.synchronize()
+    _check(x, d, [1e-3] * 2, 8, steps=3)
+
+
+@pytest.mark.parametrize("n", [1, 15, 16, 257, 4096, 70001])
+@pytest.mark.parametrize("signed", [True, False])
+def test_state_round_trip(L, n, signed):
+    import torch
+    rng = np.random.default_rng(n)
+    v = (rng.standard_normal(n) * np.exp(3 * rng.standard_normal(n))).astype(np.float32)
+    v = v if signed else np.abs(v)
+    codes, scale = op.encode(v, signed)
+    c = torch.full((n,), 3, dtype=torch.int8 if signed else torch.uint8, device="cuda")
+    s = torch.full((len(scale),), 9.0, device="cuda")
+    L.adamw_state_quantize(torch.from_numpy(v).cuda(), c, s)
+    assert np.array_equal(c.cpu().numpy(), codes) and np.array_equal(s.cpu().numpy(), scale)
+    out = torch.empty(n, device="cuda")
+    L.adamw_state_dequantize(c, s, out)
+    assert np.array_equal(out.cpu().numpy(), op.decode(codes, scale))
+
+
+def test_every_code_and_its_borders(L):
+    """Values at, one step below and one step above every border between two codes."""
+    import torch
+    for signed, top, pw in ((True, 127, 2), (False, 255, 4)):
+        edge = (((2 * np.arange(top) + 1) / (2.0 * top)) ** pw).astype(np.float32)
+        vals = np.concatenate([edge, np.nextafter(edge, np.float32(0)),
+                               np.nextafter(edge, np.float32(2))])
+        for a in (1.0, 3e-7, 12345.678):
+            x = (vals * np.float32(a)).astype(np.float32)
+            x = np.resize(x, (len(x) + 254) // 255 * 255).reshape(-1, 255)
+            x = np.concatenate([np.full((len(x), 1), a, np.float32), x], 1).reshape(-1)
+            codes, scale = op.encode(x, signed)
+            c = torch.empty(len(x), dtype=torch.int8 if signed else torch.uint8, device="cuda")
+            s = torch.empty(len(scale), device="cuda")
+            L.adamw_state_quantize(torch.from_numpy(x).cuda(), c, s)
+            assert np.array_equal(c.cpu().numpy(), codes)

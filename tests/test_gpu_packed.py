@@ -1,0 +1,345 @@
+"""GPU parity of the packed operators (index, targets, attention inside documents,
+cross-entropy) against the fp64 oracle.
+
+Tolerances count roundings.  A rounding is off by at most half a step: 2^-11 relative
+in fp16, 2^-9 in bf16 (8 significant bits, so half a step is 2^-9 of the power of two
+above and 2^-8 of the value at worst: 2^-8 is used), 2^-24 in fp32.
+Scores: |q||k| sums in fp32 by the tensor cores (each of d products, steps of 2^-23),
+times log2 e: below 2^-15 for the values here, so p = exp2(s - m) is off by at most
+2^-15 relative from fp32 work.
+"""
+import numpy as np
+import pytest
+
+from oracle import packed as op
+
+pytestmark = pytest.mark.gpu
+
+F32 = 2.0 ** -15     # fp32 work on scores and sums, as above
+HALF = 2.0 ** -11    # half a step of fp16
+BF = 2.0 ** -8       # half a step of bf16
+
+HEADS = [(8, 2, 64), (4, 4, 128), (6, 2, 128), (5, 1, 64), (4, 1, 128)]
+ROWS = [
+    # lengths, prompts, tokens
+    ([1], None, 1),
+    ([1], None, 3),
+    ([128], None, 128),
+    ([129], [129], 129),
+    ([127, 1, 0, 129, 200], None, 500),
+    ([64, 64, 0, 0, 65, 63], [64, 1, 0, 0, 0, 30], 256),
+    ([3] * 41, [2] * 41, 140),
+    ([700], None, 701),
+    ([300, 280], [140, 200], 600),
+    ([0, 0, 5], None, 9),
+    ([0], None, 4),
+]
+
+
+@pytest.fixture(scope="module")
+def L():
+    from layer_streamed_qlora_nf4_b200 import lib
+    lib.load()
+    return lib
+
+
+def _index(L, lengths, prefix, T):
+    import torch
+    idx = L.PackedIndex(T, len(lengths))
+    idx.buf.fill_(-7)
+    L.packed_index(torch.tensor(lengths, dtype=torch.int32, device="cuda"), idx,
+                   prefix=None if prefix is None else torch.tensor(prefix, dtype=torch.int32,
+                                                                   device="cuda"))
+    return idx
+
+
+def _inputs(T, H, Hkv, d, seed, grad=1e-5):
+    import torch
+    g = torch.Generator().manual_seed(seed)
+    qkv = torch.randn(T, (H + 2 * Hkv) * d, generator=g).half()
+    dout = (torch.randn(T, H * d, generator=g) * torch.exp(torch.randn(T, 1, generator=g)) *
+            grad).bfloat16()
+    return qkv, dout
+
+
+def _run(L, qkv, dout, idx, H, Hkv, ws_fill=255):
+    import torch
+    T, d = qkv.shape[0], qkv.shape[1] // (H + 2 * Hkv)
+    nan = float("nan")
+    o = torch.full((T, H * d), nan, dtype=torch.float16, device="cuda")
+    lse = torch.full((H, T), nan, device="cuda")
+    dqkv = torch.full((T, (H + 2 * Hkv) * d), nan, dtype=torch.bfloat16, device="cuda")
+    ws = torch.full((L.packed_attention_workspace_bytes(T, H, Hkv, d),), ws_fill, dtype=torch.uint8,
+                    device="cuda")
+    L.packed_attention_fwd(qkv, idx, H, Hkv, o, lse)
+    L.packed_attention_bwd(qkv, idx, o, lse, dout, H, Hkv, dqkv, ws)
+    torch.cuda.synchronize()
+    assert L.lsq_device_status(clear=True) == 0
+    return o, lse, dqkv
+
+
+def _check(qkv, dout, docs, H, Hkv, o, lse, dqkv):
+    x = qkv.float().numpy().astype(np.float64)
+    T, d = x.shape[0], x.shape[1] // (H + 2 * Hkv)
+    q, k, v = op.split_heads(x, H, Hkv)
+    ro, rlse, p = op.attention_fwd(x, H, Hkv, docs)
+    rg = op.attention_bwd(x, H, Hkv, docs, dout.float().numpy())
+    do = dout.float().numpy().astype(np.float64).reshape(T, H, d)
+    o = o.float().cpu().numpy().astype(np.float64).reshape(T, H, d)
+    lse = lse.cpu().numpy()
+    got = dqkv.float().cpu().numpy().astype(np.float64).reshape(T, H + 2 * Hkv, d)
+    rg = rg.reshape(T, H + 2 * Hkv, d)
+    dead = ~np.isfinite(rlse)
+    assert np.array_equal(np.isneginf(lse), dead)
+    assert (np.abs(lse - rlse)[~dead] <= F32 * (1 + np.abs(rlse[~dead]))).all()
+    tol_k, tol_v = np.zeros((T, Hkv, d)), np.zeros((T, Hkv, d))
+    grad_top = np.abs(do).max() * np.sqrt(d)
+    for h in range(H):
+        g = h // (H // Hkv)
+        # o: each probability rounded to fp16 (at least 2^-25 absolute, relative to a
+        # largest one of 1 or more), then the result
+        a = p[h] @ np.abs(v[:, g])
+        tol_o = (HALF + F32) * (a + np.abs(ro[:, h])) + T * 2.0 ** -25 * np.abs(v).max()
+        assert (np.abs(o[:, h] - ro[:, h]) <= tol_o).all(), ("o", h)
+        # delta takes the rounded o; p and ds are rounded to fp16, the result to bf16
+        dp = np.abs(do[:, h]) @ np.abs(v[:, g]).T
+        ds = np.abs(p[h] * (do[:, h] @ v[:, g].T - (do[:, h] * ro[:, h]).sum(1)[:, None]))
+        e = (HALF + F32) * ds + p[h] * (F32 * dp + (np.abs(do[:, h]) * tol_o).sum(1)[:, None])
+        e = e / np.sqrt(d)
+        # codes below fp16's normal range: half a step of 2^-24 against rows of norm 8
+        low = 2.0 ** -28 * grad_top / np.sqrt(d)
+        tq = e @ np.abs(k[:, g]) + T * low * np.abs(k).max() + BF * np.abs(rg[:, h])
+        assert (np.abs(got[:, h] - rg[:, h]) <= tq).all(), ("dq", h)
+        tol_k[:, g] += e.T @ np.abs(q[:, h]) + T * low * np.abs(q).max()
+        tol_v[:, g] += (HALF + F32) * (p[h].T @ np.abs(do[:, h])) + T * 2.0 ** -28 * grad_top
+    assert (np.abs(got[:, H:H + Hkv] - rg[:, H:H + Hkv])
+            <= tol_k + BF * np.abs(rg[:, H:H + Hkv])).all(), "dk"
+    assert (np.abs(got[:, H + Hkv:] - rg[:, H + Hkv:])
+            <= tol_v + BF * np.abs(rg[:, H + Hkv:])).all(), "dv"
+    pad = ~op.visible(T, docs).any(1)
+    assert not o[pad].any() and not got[pad].any()
+
+
+@pytest.mark.parametrize("lengths,prefix,T", ROWS)
+def test_index_and_targets(L, lengths, prefix, T):
+    import torch
+    idx = _index(L, lengths, prefix, T)
+    docs = op.documents(lengths, prefix)
+    words = idx.buf.cpu().numpy()
+    cap = min(T, T // 128 + len(lengths))
+    cap2 = min(T, T // 256 + len(lengths))
+    for n, size, base, room in ((words[0], 128, 8, cap), (words[1], 256, 8 + 4 * cap, cap2)):
+        want = [(r, s, e, pe) for s, e, pe in docs for r in range(s, e, size)]
+        assert n == len(want) <= room
+        assert sorted(map(tuple, words[base:base + 4 * n].reshape(n, 4))) == sorted(want)
+    assert words[2] == sum(lengths)
+    pos, key_end, doc_end = words[8 + 4 * (cap + cap2):].reshape(3, T)
+    for s, e, pe in docs:
+        for t in range(s, e):
+            assert (pos[t], key_end[t], doc_end[t]) == (t - s, max(t + 1, pe), e)
+    rng = np.random.default_rng(T)
+    tok = rng.integers(0, 1000, T).astype(np.int32)
+    for mask in (None, rng.integers(0, 2, T).astype(np.uint8)):
+        want = op.targets(tok, docs, mask)
+        y = torch.full((T,), -9, dtype=torch.int32, device="cuda")
+        n = torch.full((1,), 5, dtype=torch.int32, device="cuda")
+        m = None if mask is None else torch.from_numpy(mask).cuda()
+        L.packed_targets(torch.from_numpy(tok).cuda(), idx, y, n, loss_mask=m)
+        assert np.array_equal(y.cpu().numpy(), want) and n.item() == (want >= 0).sum()
+        L.packed_targets(torch.from_numpy(tok).cuda(), idx, y, n,
+                         loss_mask=None if m is None else m.bool(), accumulate=True)
+        assert n.item() == 2 * (want >= 0).sum()
+    assert L.lsq_device_status(clear=True) == 0
+
+
+def test_index_of_many_documents(L):
+    """More documents than a pass of the scan takes, and a long row."""
+    rng = np.random.default_rng(0)
+    lengths = rng.integers(0, 40, 3000)
+    T = int(lengths.sum()) + 11
+    idx = _index(L, lengths.tolist(), None, T)
+    words = idx.buf.cpu().numpy()
+    ends = np.cumsum(lengths)
+    starts = ends - lengths
+    own = np.repeat(np.arange(3000), lengths)
+    pos, key_end, doc_end = words[-3 * T:].reshape(3, T)
+    n = T - 11
+    assert np.array_equal(pos[:n], np.arange(n) - starts[own])
+    assert np.array_equal(doc_end[:n], ends[own]) and (doc_end[n:] == n).all()
+    assert words[0] == (lengths > 0).sum()
+
+
+def test_index_bad_lengths_are_cut_and_latched(L):
+    bad = L.LSQ_DEV_ERR_INDEX
+    for lengths, prefix, T, total in (([5, -3, 4], None, 12, 9), ([5, 9], None, 10, 10),
+                                      ([4, 4], [5, 0], 8, 8), ([4, 4], [-1, 0], 8, 8),
+                                      ([8, 3], None, 8, 8)):
+        idx = _index(L, lengths, prefix, T)
+        assert idx.buf[2].item() == total
+        assert L.lsq_device_status(clear=True) == bad
+
+
+@pytest.mark.parametrize("H,Hkv,d", HEADS)
+@pytest.mark.parametrize("lengths,prefix,T", ROWS)
+def test_attention(L, lengths, prefix, T, H, Hkv, d):
+    qkv, dout = _inputs(T, H, Hkv, d, seed=T + H)
+    idx = _index(L, lengths, prefix, T)
+    r = _run(L, qkv.cuda(), dout.cuda(), idx, H, Hkv)
+    _check(qkv, dout, op.documents(lengths, prefix), H, Hkv, *r)
+
+
+@pytest.mark.parametrize("H,Hkv,d", [(4, 2, 128), (3, 1, 64)])
+def test_attention_large_scores_and_extreme_gradients(L, H, Hkv, d):
+    """Scores of some hundreds (one key takes all), and gradients far below and above
+    what fp16 holds, of different size from row to row."""
+    import torch
+    T, lengths = 300, [260, 40]
+    idx = _index(L, lengths, None, T)
+    docs = op.documents(lengths)
+    qkv, dout = _inputs(T, H, Hkv, d, 3, grad=1.0)
+    qkv[:, :(H + Hkv) * d] *= 6
+    for scale in (1e-30, 1e30):
+        g = (dout.float() * scale).bfloat16()
+        o, lse, dqkv = _run(L, qkv.cuda(), g.cuda(), idx, H, Hkv)
+        ref = op.attention_bwd(qkv.float().numpy(), H, Hkv, docs, g.float().numpy())
+        got = dqkv.float().cpu().numpy()
+        # scores of size s carry an error of s 2^-22 or so; q k / sqrt d is below 2^10
+        assert np.abs(got - ref).max() <= 2.0 ** -7 * np.abs(ref).max()
+    zero = torch.zeros_like(dout)
+    assert not _run(L, qkv.cuda(), zero.cuda(), idx, H, Hkv)[2].any()
+
+
+@pytest.mark.parametrize("H,Hkv,d", [(4, 2, 64), (3, 3, 128)])
+def test_nothing_crosses_a_document(L, H, Hkv, d):
+    """Infinities and NaN in one document and in the padding leave the others' results
+    bit for bit as they are."""
+    import torch
+    lengths, prefix, T = [70, 130, 90, 20], [10, 60, 0, 20], 330
+    idx = _index(L, lengths, prefix, T)
+    qkv, dout = _inputs(T, H, Hkv, d, 5)
+    clean = _run(L, qkv.cuda(), dout.cuda(), idx, H, Hkv)
+    for bad in (float("nan"), float("inf")):
+        q2, g2 = qkv.clone(), dout.clone()
+        for a, e in ((70, 200), (310, 330)):
+            q2[a:e] = bad
+            g2[a:e] = bad
+        qc, gc = q2.cuda(), g2.cuda()
+        o = torch.empty_like(clean[0])
+        lse, dqkv = torch.empty_like(clean[1]), torch.empty_like(clean[2])
+        ws = torch.empty(L.packed_attention_workspace_bytes(T, H, Hkv, d), dtype=torch.uint8,
+                         device="cuda")
+        L.packed_attention_fwd(qc, idx, H, Hkv, o, lse)
+        L.packed_attention_bwd(qc, idx, o, lse, gc, H, Hkv, dqkv, ws)
+        torch.cuda.synchronize()
+        assert L.lsq_device_status(clear=True) == L.LSQ_DEV_ERR_NONFINITE
+        keep = torch.ones(T, dtype=torch.bool)
+        keep[70:200] = False
+        keep = keep.cuda()
+        assert torch.equal(o[keep], clean[0][keep])
+        assert torch.equal(lse[:, keep], clean[1][:, keep])
+        assert torch.equal(dqkv[keep], clean[2][keep])
+
+
+def test_attention_is_deterministic_on_any_stream_and_in_a_graph(L):
+    import torch
+    H, Hkv, d, T, lengths = 8, 2, 64, 500, [300, 190]
+    idx = _index(L, lengths, None, T)
+    qkv, dout = (x.cuda() for x in _inputs(T, H, Hkv, d, 8))
+    a = _run(L, qkv, dout, idx, H, Hkv)
+    b = _run(L, qkv, dout, idx, H, Hkv, ws_fill=0)
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        c = _run(L, qkv, dout, idx, H, Hkv)
+    assert all(torch.equal(x, y) for x, y in zip(a, c))
+    # captured with its index, replayed on other documents and other values
+    lens = torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    out = [torch.empty_like(x) for x in a]
+    ws = torch.empty(L.packed_attention_workspace_bytes(T, H, Hkv, d), dtype=torch.uint8,
+                     device="cuda")
+
+    def step():
+        L.packed_index(lens, idx)
+        L.packed_attention_fwd(qkv, idx, H, Hkv, out[0], out[1])
+        L.packed_attention_bwd(qkv, idx, out[0], out[1], dout, H, Hkv, out[2], ws)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(a, out))
+    q2, g2 = (x.cuda() for x in _inputs(T, H, Hkv, d, 9))
+    qkv.copy_(q2)
+    dout.copy_(g2)
+    lens.copy_(torch.tensor([0, 450], dtype=torch.int32))
+    g.replay()
+    torch.cuda.synchronize()
+    _check(q2.cpu(), g2.cpu(), op.documents([0, 450]), H, Hkv, *out)
+
+
+LOSS = [(1, 1), (1, 2), (3, 7), (5, 8), (4, 1001), (6, 4096), (2, 5003), (3, 40000), (2, 131075)]
+
+
+@pytest.mark.parametrize("T,V", LOSS)
+@pytest.mark.parametrize("form", ["plain", "weighted", "none"])
+def test_cross_entropy(L, T, V, form):
+    import torch
+    rng = np.random.default_rng(T * V)
+    x = (rng.standard_normal((T, V)) * 3).astype(np.float32)
+    y = rng.integers(0, V, T).astype(np.int32)
+    y[rng.random(T) < 0.3] = -1
+    y[0] = -100 if form == "none" else V - 1
+    if form == "none":
+        y[:] = -1
+    w = rng.random(T).astype(np.float32) if form == "weighted" else None
+    n = int((y >= 0).sum()) if form != "weighted" else None
+    if V > 20:
+        x[0, 3:9] = -np.inf         # excluded words
+        x[y < 0] = np.nan           # rows without a target are not read
+    row, loss, grad = op.cross_entropy(np.nan_to_num(x, nan=0.0, neginf=-1e30), y, w, n)
+    dl = torch.full((T, V), float("nan"), dtype=torch.bfloat16, device="cuda")
+    rl = torch.full((T,), float("nan"), device="cuda")
+    tot = torch.full((1,), 2.5, device="cuda")
+    kw = dict(weight=None if w is None else torch.from_numpy(w).cuda(),
+              count=None if n is None else torch.tensor([n], dtype=torch.int32, device="cuda"))
+    xd, yd = torch.from_numpy(x).cuda(), torch.from_numpy(y).cuda()
+    L.packed_cross_entropy(xd, yd, rl, tot, dlogits=dl, **kw)
+    # arguments of exp2 below 64 in magnitude: 2^-17 relative; sums of V terms, V / 128
+    # of them in a row
+    tol = 2.0 ** -16 + V / 128 * 2.0 ** -24
+    assert (np.abs(rl.cpu().numpy() - row) <= tol * (1 + np.abs(row))).all()
+    c = np.zeros(T)
+    c[y >= 0] = (1.0 if w is None else w[y >= 0]) / (1 if n is None else max(n, 1))
+    assert abs(tot.item() - loss) <= 2 * tol * (1 + abs(loss))
+    err = np.abs(dl.float().cpu().numpy() - grad)
+    assert (err <= BF * np.abs(grad) + tol * c[:, None]).all()
+    only = torch.empty_like(rl)
+    L.packed_cross_entropy(xd, yd, only, tot, accumulate=True, **kw)
+    assert torch.equal(only, rl)
+    assert abs(tot.item() - 2 * loss) <= 4 * tol * (1 + abs(loss))
+    assert L.lsq_device_status(clear=True) == 0
+
+
+def test_cross_entropy_target_beyond_the_vocabulary(L):
+    import torch
+    x = torch.randn(3, 50, device="cuda")
+    y = torch.tensor([1, 50, 7], dtype=torch.int32, device="cuda")
+    rl, tot = torch.empty(3, device="cuda"), torch.empty(1, device="cuda")
+    dl = torch.empty(3, 50, dtype=torch.bfloat16, device="cuda")
+    L.packed_cross_entropy(x, y, rl, tot, dlogits=dl)
+    assert rl[1].item() == 0 and not dl[1].any() and dl[0].any()
+    assert abs(tot.item() - (rl[0] + rl[2]).item()) < 1e-5
+    assert L.lsq_device_status(clear=True) == L.LSQ_DEV_ERR_INDEX
+
+
+def test_cross_entropy_not_finite_rows_are_the_formulas(L):
+    import torch
+    x = torch.randn(3, 300, device="cuda")
+    x[0] = -float("inf")
+    x[1, 5] = float("inf")
+    x[2, 9] = -float("inf")
+    y = torch.tensor([4, 5, 9], dtype=torch.int32, device="cuda")
+    rl, tot = torch.empty(3, device="cuda"), torch.empty(1, device="cuda")
+    L.packed_cross_entropy(x, y, rl, tot)
+    assert torch.isnan(rl[0]) and torch.isnan(rl[1]) and rl[2].item() == float("inf")

@@ -1,0 +1,177 @@
+"""What the packed operators and the many-tensor AdamW refuse, before any CUDA call:
+sizes, null and unaligned pointers through the C entries, and the binding's own checks
+of types, shapes and devices."""
+import ctypes
+
+import numpy as np
+import pytest
+
+
+@pytest.fixture(scope="module")
+def L():
+    import os
+    from layer_streamed_qlora_nf4_b200 import build, lib
+    if not os.path.exists(lib.LIB_PATH):
+        build.build()
+    lib.load()
+    return lib
+
+
+_raw = np.zeros(4096 + 64, np.uint8)
+P = ctypes.c_void_p((_raw.ctypes.data + 63) // 64 * 64)    # aligned; never dereferenced
+ODD = ctypes.c_void_p(P.value + 4)
+
+
+def _rc(L, name, *args):
+    return getattr(L.load(), name)(*args)
+
+
+def test_index_sizes(L):
+    assert L.packed_index_ints(512, 5) == 8 + 4 * (9 + 7) + 3 * 512
+    assert L.packed_index_ints(1, 1) == 8 + 4 * 2 + 3
+    assert L.packed_index_ints(0, 1) == 0 and L.packed_index_ints(4, 0) == 0
+    with pytest.raises(ValueError):
+        L.PackedIndex(0, 1, device="cpu")
+
+
+def test_packed_entries(L):
+    bad = L.LSQ_ERR_INVALID, L.LSQ_ERR_SHAPE, L.LSQ_ERR_ALIGN, L.LSQ_ERR_WORKSPACE
+    inval, shape, align, work = bad
+    for rc, args in (
+            (shape, (P, None, 1, 0, P, None)), (shape, (P, None, 0, 4, P, None)),
+            (shape, (P, None, 1, (1 << 30) + 1, P, None)), (inval, (None, None, 1, 4, P, None)),
+            (inval, (P, None, 1, 4, None, None)), (align, (P, None, 1, 4, ODD, None))):
+        assert _rc(L, "packed_index", *args) == rc
+    ok = [P, P, 1, 4, 4, 2, 64, P, P, None]
+    for at, val, rc in ((0, None, inval), (1, None, inval), (2, 0, shape), (3, 0, shape),
+                        (4, 3, shape), (4, 0, shape), (5, 0, shape), (6, 96, shape),
+                        (7, None, inval), (8, None, inval), (0, ODD, align), (1, ODD, align),
+                        (7, ODD, align), (8, ODD, align), (3, 1 << 30, shape)):
+        args = list(ok)
+        args[at] = val
+        if (at, val) == (3, 1 << 30):
+            args[4] = 64
+        assert _rc(L, "packed_attention_fwd", *args) == rc, (at, val)
+    need = L.packed_attention_workspace_bytes(4, 4, 2, 64)
+    assert need > 0
+    for bad_shape in ((0, 4, 2, 64), (4, 3, 2, 64), (4, 4, 2, 32), (4, 0, 2, 64), (4, 4, 0, 64)):
+        assert L.packed_attention_workspace_bytes(*bad_shape) == 0
+    ok = [P, P, 1, P, P, P, 4, 4, 2, 64, P, P, need, None]
+    for at, val, rc in ((0, None, inval), (3, None, inval), (4, None, inval), (5, None, inval),
+                        (10, None, inval), (11, None, work), (12, need - 1, work),
+                        (11, ODD, align), (5, ODD, align), (10, ODD, align), (9, 80, shape),
+                        (7, 5, shape)):
+        args = list(ok)
+        args[at] = val
+        assert _rc(L, "packed_attention_bwd", *args) == rc, (at, val)
+    ok = [P, P, 1, 4, None, P, P, 0, None]
+    for at, val, rc in ((0, None, inval), (1, None, inval), (5, None, inval), (6, None, inval),
+                        (7, 2, inval), (3, 0, shape)):
+        args = list(ok)
+        args[at] = val
+        assert _rc(L, "packed_targets", *args) == rc, (at, val)
+    ok = [P, 4, 9, P, None, None, P, P, P, 0, None]
+    for at, val, rc in ((0, None, inval), (3, None, inval), (7, None, inval), (8, None, inval),
+                        (1, 0, shape), (2, 0, shape), (9, 3, inval), (0, ODD, align),
+                        (6, ODD, align), (1, 1 << 31, shape)):
+        args = list(ok)
+        args[at] = val
+        assert _rc(L, "packed_cross_entropy", *args) == rc, (at, val)
+
+
+def _table(L, *rows):
+    t = (L.lsq_adamw_tensor * max(1, len(rows)))()
+    for i, r in enumerate(rows):
+        for k, v in dict(dict(p=P.value, g=P.value + 512, m=P.value + 1024, v=P.value + 1536,
+                              m_scale=P.value + 2048, v_scale=P.value + 2112, n=16, lr=1e-3,
+                              weight_decay=0.0), **r).items():
+            setattr(t[i], k, v)
+    return t
+
+
+def _hyper(L, **kw):
+    return L.lsq_adamw_hyper(**dict(dict(beta1=0.9, beta2=0.999, eps=1e-8, step=1, state_bits=8,
+                                         grad_bits=32, step_dev=None), **kw))
+
+
+def test_adamw_entries(L):
+    inval, shape, align = L.LSQ_ERR_INVALID, L.LSQ_ERR_SHAPE, L.LSQ_ERR_ALIGN
+
+    def rc(table, n, **kw):
+        return _rc(L, "adamw_multi_step", table, n, ctypes.byref(_hyper(L, **kw)), None)
+    for row, want in ((dict(p=None), inval), (dict(g=None), inval), (dict(m=None), inval),
+                      (dict(v=None), inval), (dict(m_scale=None), inval), (dict(n=-1), shape),
+                      (dict(p=P.value + 4), align), (dict(g=P.value + 8), align),
+                      (dict(m=P.value + 1), align), (dict(v=P.value + 2), align),
+                      (dict(v_scale=P.value + 2), align), (dict(lr=-1.0), inval),
+                      (dict(lr=float("nan")), inval), (dict(weight_decay=float("inf")), inval)):
+        assert rc(_table(L, row), 1) == want, row
+    # the same tensor twice, one inside another, in and out of address order
+    for a, b in ((0, 0), (0, 48), (48, 0)):
+        assert rc(_table(L, dict(p=P.value + a), dict(p=P.value + b)), 2) == inval
+    t = _table(L, {})
+    for kw, want in ((dict(state_bits=16), inval), (dict(grad_bits=8), inval), (dict(step=0), shape),
+                     (dict(beta1=1.0), inval), (dict(beta2=-0.1), inval), (dict(eps=0.0), inval),
+                     (dict(eps=float("nan")), inval), (dict(beta1=float("nan")), inval)):
+        assert rc(t, 1, **kw) == want, kw
+    assert rc(t, -1) == shape
+    assert _rc(L, "adamw_multi_step", t, 1, None, None) == inval
+    assert _rc(L, "adamw_multi_step", None, 1, ctypes.byref(_hyper(L)), None) == inval
+    assert [L.adamw_scale_floats(n) for n in (-1, 0, 1, 256, 257)] == [0, 0, 1, 1, 2]
+    for name in ("adamw_state_dequantize", "adamw_state_quantize"):
+        a = [P, P, 4, 1, P, None] if name.endswith("dequantize") else [P, 4, 1, P, P, None]
+        sizes = (2, 3) if name.endswith("dequantize") else (1, 2)
+        for at, val, want in ((0, None, inval), (sizes[0], 0, shape), (sizes[1], 2, inval),
+                              (0, ODD, align)):
+            args = list(a)
+            args[at] = val
+            assert _rc(L, name, *args) == want, (name, at, val)
+
+
+def test_binding_checks(L):
+    import torch
+    i32 = torch.zeros(2, dtype=torch.int32)
+    idx = L.PackedIndex(8, 2, device="cpu")
+    with pytest.raises(ValueError, match="CUDA"):
+        L.packed_index(i32, idx)
+    with pytest.raises(TypeError):
+        L.packed_index(i32.long(), idx)
+    with pytest.raises(ValueError):
+        L.packed_index(torch.zeros(3, dtype=torch.int32), idx)
+    with pytest.raises(ValueError):
+        L.packed_index(i32, idx, prefix=torch.zeros(4, dtype=torch.int32)[::2][:1])
+    qkv = torch.zeros(8, 8 * 64, dtype=torch.float16)
+    o, lse = torch.zeros(8, 4 * 64, dtype=torch.float16), torch.zeros(4, 8)
+    for a in ((qkv.float(), 4, 2, o, lse), (qkv, 4, 3, o, lse), (qkv, 0, 2, o, lse),
+              (qkv[:4], 4, 2, o, lse), (qkv.t(), 4, 2, o, lse), (qkv, 4, 2, o[:, :64], lse),
+              (qkv, 4, 2, o, lse.t()), (qkv, 4, 2, o.bfloat16(), lse)):
+        with pytest.raises((TypeError, ValueError)):
+            L.packed_attention_fwd(a[0], idx, *a[1:])
+    with pytest.raises(ValueError, match="CUDA"):
+        L.packed_attention_fwd(qkv, idx, 4, 2, o, lse)
+    x = torch.zeros(3, 5)
+    y, r, t = torch.zeros(3, dtype=torch.int32), torch.zeros(3), torch.zeros(1)
+    for kw in (dict(dlogits=x), dict(weight=torch.zeros(2)), dict(count=t)):
+        with pytest.raises((TypeError, ValueError)):
+            L.packed_cross_entropy(x, y, r, t, **kw)
+    with pytest.raises(ValueError):
+        L.packed_cross_entropy(x[0], y, r, t)
+    with pytest.raises(ValueError, match="CUDA"):
+        L.packed_cross_entropy(x, y, r, t)
+    p = [torch.zeros(300)]
+    with pytest.raises(ValueError, match="CUDA"):
+        L.AdamWMulti(p, p, p, p, lr=1.0)
+    with pytest.raises(TypeError):
+        L.AdamWMulti(p, [p[0].half()], p, p, lr=1.0)
+    with pytest.raises(ValueError):
+        L.AdamWMulti(p, p, p, [], lr=1.0)
+    with pytest.raises(ValueError):
+        L.AdamWMulti(p, p, p, p, lr=[1.0, 2.0])
+    c = [torch.zeros(300, dtype=torch.int8)], [torch.zeros(300, dtype=torch.uint8)]
+    with pytest.raises(ValueError):
+        L.AdamWMulti(p, p, *c, lr=1.0, m_scale=[torch.zeros(1)], v_scale=[torch.zeros(2)])
+    with pytest.raises(ValueError):
+        L.AdamWMulti(p, p, *c, lr=1.0)
+    with pytest.raises(TypeError):
+        L.adamw_state_dequantize(p[0], p[0], p[0])
+    assert L.AdamWMulti([], [], [], [], lr=1.0).step(1) is None
