@@ -31,29 +31,93 @@ __device__ __forceinline__ uint8_t* align1024_p(uint8_t* p) {
   return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023));
 }
 
-constexpr int kAQ = 128;   // queries per CTA (UMMA M)
+// ------------------------------------------------------------------ forward
+// A persistent CTA per SM takes work items in turn.  An item is two streams of 128
+// query rows of one document that read the same K and V tiles: two query heads of a kv
+// head on the same rows where the group has an even number of heads, else two
+// neighbouring row tiles of one head.  While the tensor cores work for one stream the
+// softmax of the other runs:
+//   S_s = Q_s K_j^T (TMEM) -> softmax warps of stream s: P = exp2(S c - m) as fp16 over
+//   the same TMEM columns -> O_s += P V_j (A operand from TMEM), S_s of tile j + 1.
+// The reference maximum m of a row moves only when a tile's maximum exceeds it by more
+// than 2^8 (then O and the running sum are rescaled): the result is exact for any
+// reference, and P stays below 2^8, well inside fp16.
+//   warps 0-3, 4-7: softmax and epilogue of streams 0 and 1, a query row per thread
+//   warp 8 : TMA producer (Q of each stream; a ring of K and V tiles)
+//   warp 9 : TMEM allocation and the MMA issuer (lane 0)
+//   warp 10: clears the rows of a document's last V tile that lie behind its end
+constexpr int kAQ = 128;   // queries per stream (UMMA M)
 constexpr int kAK = 128;   // keys per tile (UMMA N of S, K of P V)
-constexpr int kAThreads = 320;
-constexpr int kWarpTma = 8, kWarpMma = 9;
+constexpr int kFThreads = 352;
+constexpr int kWarpTma = 8, kWarpMma = 9, kWarpTail = 10;
 constexpr float kRescaleLog2 = 8.f;
 
 template <int D>
-struct PaSmem {
-  static constexpr int DA = D / 64;                   // 64-element swizzle atoms along d
-  static constexpr uint32_t kQ = kAQ * D * 2;         // Q: DA boxes of [128 rows x 64]
-  static constexpr uint32_t kKV = kAK * D * 2;        // one K or V tile
-  static constexpr uint32_t kP = kAQ * kAK * 2;       // P: 2 atoms of [128 rows x 64 keys]
-  static constexpr uint32_t kBytes = 1024 + kQ + 4 * kKV + kP;  // Q, 2 x (K, V), P
+struct FwdSmem {
+  static constexpr int DA = D / 64;                  // 64-element swizzle atoms along d
+  static constexpr uint32_t kTile = 128 * D * 2;     // a tile of 128 rows of Q, K or V
+  static constexpr int kRing = D == 128 ? 5 : 8;     // K and V tiles in flight
+  static constexpr uint32_t kBytes = 1024 + (2 + kRing) * kTile;
 };
+
+// The two streams of an item: first row, head and number of key tiles (0: unused).
+struct FwdItem {
+  int begin, end, prompt;
+  int row[2], head[2], n[2];
+};
+__device__ __forceinline__ int key_tiles(const PackedTile& t, int row) {
+  return (min(t.end, max(row + kAQ, t.prompt)) - t.begin + kAK - 1) / kAK;
+}
+__device__ __forceinline__ FwdItem fwd_item(const PackedIndex& x, int w, int H, bool heads) {
+  FwdItem it;
+  const int per = heads ? H / 2 : H;
+  const PackedTile t = heads ? x.tiles[w / per] : x.tiles2[w / per];
+  it.begin = t.begin;
+  it.end = t.end;
+  it.prompt = t.prompt;
+  it.row[0] = t.row0;
+  it.n[0] = key_tiles(t, t.row0);
+  if (heads) {
+    it.head[0] = 2 * (w % per);
+    it.head[1] = it.head[0] + 1;
+    it.row[1] = t.row0;
+    it.n[1] = it.n[0];
+  } else {
+    it.head[0] = it.head[1] = w % per;
+    it.row[1] = t.row0 + kAQ;
+    it.n[1] = it.row[1] < t.end ? key_tiles(t, it.row[1]) : 0;
+  }
+  return it;
+}
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+      "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+// D[tmem] (+)= A[tmem] * B[smem]^T: A holds two 16-bit elements per 32-bit column.
+__device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
+                                          uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
 
 // Padding rows (behind the last document) hold no document: o = 0, lse = -inf.  The
 // whole grid shares them.
 template <int D>
 __device__ __forceinline__ void fill_padding(int first, int64_t T, int H, uint16_t* out,
                                              float* lse_out) {
-  const int64_t cta = blockIdx.x + (int64_t)blockIdx.y * gridDim.x;
-  const int64_t step = (int64_t)gridDim.x * gridDim.y * blockDim.x;
-  const int64_t i0 = cta * blockDim.x + threadIdx.x;
+  const int64_t step = (int64_t)gridDim.x * blockDim.x;
+  const int64_t i0 = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   const int64_t n = (T - first) * H * (D / 8);
   uint4* o = reinterpret_cast<uint4*>(out + (int64_t)first * H * D);
   for (int64_t i = i0; i < n; i += step) o[i] = make_uint4(0u, 0u, 0u, 0u);
@@ -61,71 +125,52 @@ __device__ __forceinline__ void fill_padding(int first, int64_t T, int H, uint16
     lse_out[(i % H) * T + first + i / H] = -INFINITY;
 }
 
-// Clears rows [rows, all) of a K-major swizzled tile of D columns (one warp) once its
-// load has landed, and arrives on `done`; a whole tile only arrives.
+// Clears rows [rows, all) of a swizzled tile of D columns (one warp).
 template <int D>
-__device__ __forceinline__ void zero_tail(uint8_t* tile, int rows, int all, uint32_t bar,
-                                          uint32_t parity, int lane, uint32_t done,
-                                          volatile int* abort_flag, int* dev_err) {
-  if (rows < all) {
-    bool ok = mbar_wait_bounded(bar, parity, abort_flag, dev_err, DEV_ERR_WAIT_GEMM);
-    ok = __all_sync(0xFFFFFFFFu, ok);
-    if (ok)
-      for (int a = 0; a < D / 64; ++a)
-        for (uint32_t o = (uint32_t)rows * 128u + (uint32_t)lane * 16u; o < (uint32_t)all * 128u;
-             o += 512u)
-          *reinterpret_cast<uint4*>(tile + (uint32_t)a * all * 128u + o) = make_uint4(0u, 0u, 0u, 0u);
-    fence_proxy_async_smem();
-  }
-  __syncwarp();
-  if (lane == 0) mbar_arrive(done);
+__device__ __forceinline__ void zero_rows(uint8_t* tile, int rows, int all, int lane) {
+  for (int a = 0; a < D / 64; ++a)
+    for (uint32_t o = (uint32_t)rows * 128u + (uint32_t)lane * 16u; o < (uint32_t)all * 128u;
+         o += 512u)
+      *reinterpret_cast<uint4*>(tile + (uint32_t)a * all * 128u + o) = make_uint4(0u, 0u, 0u, 0u);
 }
 
 template <int D>
-__global__ void __launch_bounds__(kAThreads, 1)
-    packed_attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_qkv, PackedIndex idx, int64_t T, int H,
-                           int Hkv, uint16_t* __restrict__ out, float* __restrict__ lse_out, float sl2,
-                       int* __restrict__ dev_err) {
-  using SM = PaSmem<D>;
-  constexpr int DA = SM::DA;
+__global__ void __launch_bounds__(kFThreads, 1)
+    packed_attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_qkv, PackedIndex idx, int64_t T,
+                           int H, int Hkv, uint16_t* __restrict__ out,
+                           float* __restrict__ lse_out, float sl2, int* __restrict__ dev_err) {
+  using SM = FwdSmem<D>;
+  constexpr int DA = SM::DA, NR = SM::kRing;
   extern __shared__ uint8_t attn_raw[];
-  __shared__ __align__(8) uint64_t bar_q, bar_kv[2], bar_kv_free[2], bar_s[2], bar_s_free[2];
-  __shared__ __align__(8) uint64_t bar_p, bar_pv, bar_tail;
-  __shared__ __align__(8) uint64_t bar_sm;  // the eight softmax warps meet here
+  __shared__ __align__(8) uint64_t q_full[2], q_free[2], kv_full[NR], kv_free[NR];
+  __shared__ __align__(8) uint64_t s_full[2], p_full[2], o_full[2], o_free[2];
+  __shared__ __align__(8) uint64_t tail_done[NR];
   __shared__ uint32_t tmem_sh;
   __shared__ int abort_sh;
-  __shared__ float xch[2][kAQ];  // the two halves of a row exchange its maximum, then its sum
   volatile int* abort_flag = &abort_sh;
   pdl_trigger();  // the next kernel may launch once all CTAs of this one run
 
-  uint8_t* Qs = align1024_p(attn_raw);
-  uint8_t* Ks = Qs + SM::kQ;            // [2] K tiles
-  uint8_t* Vs = Ks + 2 * SM::kKV;       // [2] V tiles
-  uint8_t* Ps = Vs + 2 * SM::kKV;
+  uint8_t* Qs = align1024_p(attn_raw);   // [2] Q tiles
+  uint8_t* KV = Qs + 2 * SM::kTile;      // ring: K and V tiles in turn
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int h = blockIdx.y;
-  const int g = h / (H / Hkv);
-  pdl_wait();  // the index and q, k, v come from the kernels before
-  fill_padding<D>(idx.head[2], T, H, out, lse_out);
-  if ((int)blockIdx.x >= idx.head[0]) return;
-  const PackedTile tile = idx.tiles[blockIdx.x];
-  const int q0 = tile.row0;
-  const int kv_end = min(tile.end, max(q0 + kAQ, tile.prompt));  // keys this block sees
-  const int n_kv = (kv_end - tile.begin + kAK - 1) / kAK;
-  constexpr uint32_t kColS = 0, kColO = 2 * kAK;  // TMEM: S buffers at 0 and 128, O at 256
+  constexpr uint32_t kColS = 0, kColO = 2 * kAK;  // TMEM: S at 0 and 128, O at 256 and 384
+  const int G = H / Hkv;
+  const bool heads = G % 2 == 0;
 
   if (threadIdx.x == 0) {
-    mbar_init(smem_u32(&bar_q), 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&bar_kv[i]), 1);
-      mbar_init(smem_u32(&bar_kv_free[i]), 1);
-      mbar_init(smem_u32(&bar_s[i]), 1);
-      mbar_init(smem_u32(&bar_s_free[i]), 8);
+      mbar_init(smem_u32(&q_full[i]), 1);
+      mbar_init(smem_u32(&q_free[i]), 1);
+      mbar_init(smem_u32(&s_full[i]), 1);
+      mbar_init(smem_u32(&p_full[i]), 4);
+      mbar_init(smem_u32(&o_full[i]), 1);
+      mbar_init(smem_u32(&o_free[i]), 4);
     }
-    mbar_init(smem_u32(&bar_p), 8);
-    mbar_init(smem_u32(&bar_pv), 1);
-    mbar_init(smem_u32(&bar_tail), 1);
-    mbar_init(smem_u32(&bar_sm), 8);
+    for (int i = 0; i < NR; ++i) {
+      mbar_init(smem_u32(&kv_full[i]), 1);
+      mbar_init(smem_u32(&kv_free[i]), 2);  // the products and the tail warp
+      mbar_init(smem_u32(&tail_done[i]), 1);
+    }
     abort_sh = 0;
     fence_mbar_init();
     fence_proxy_async_smem();
@@ -139,235 +184,255 @@ __global__ void __launch_bounds__(kAThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_sh;
+  pdl_wait();  // the index and q, k, v come from the kernels before
+  const int items = heads ? idx.head[0] * (H / 2) : idx.head[1] * H;
+  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+    return mbar_wait_bounded(smem_u32(bar), parity & 1u, abort_flag, dev_err, DEV_ERR_WAIT_GEMM);
+  };
 
   if (warp == kWarpTma) {
     // ---------------------------------------------------------------- TMA producer
     if (lane == 0) {
-      mbar_arrive_expect_tx(smem_u32(&bar_q), SM::kQ);
-      for (int a = 0; a < DA; ++a)
-        tma_load_2d(smem_u32(Qs + a * kAQ * 128), &tm_qkv, smem_u32(&bar_q), h * D + 64 * a,
-                    q0);
-      for (int j = 0; j < n_kv; ++j) {
-        const int buf = j & 1;
-        if (j >= 2 && !mbar_wait_bounded(smem_u32(&bar_kv_free[buf]), (uint32_t)(((j - 2) >> 1) & 1),
-                                         abort_flag, dev_err, DEV_ERR_WAIT_GEMM))
-          break;
-        const uint32_t fb = smem_u32(&bar_kv[buf]);
-        mbar_arrive_expect_tx(fb, 2 * SM::kKV);
-        for (int a = 0; a < DA; ++a) {
-          tma_load_2d(smem_u32(Ks + buf * SM::kKV + a * kAK * 128), &tm_qkv, fb,
-                      (H + g) * D + 64 * a, tile.begin + j * kAK);
-          tma_load_2d(smem_u32(Vs + buf * SM::kKV + a * kAK * 128), &tm_qkv, fb,
-                      (H + Hkv + g) * D + 64 * a, tile.begin + j * kAK);
+      uint32_t c = 0, nq[2] = {0, 0};  // ring tiles and Q tiles issued
+      bool ok = true;
+      auto load_kv = [&](int col, int row) -> bool {
+        const uint32_t slot = c % NR;
+        if (c >= NR && !wait(&kv_free[slot], c / NR - 1)) return false;
+        const uint32_t fb = smem_u32(&kv_full[slot]);
+        mbar_arrive_expect_tx(fb, SM::kTile);
+        for (int a = 0; a < DA; ++a)
+          tma_load_2d(smem_u32(KV + slot * SM::kTile + a * kAK * 128), &tm_qkv, fb, col + 64 * a, row);
+        ++c;
+        return true;
+      };
+      for (int w = blockIdx.x; w < items && ok; w += gridDim.x) {
+        const FwdItem it = fwd_item(idx, w, H, heads);
+        const int g = it.head[0] / G;
+        const int kc = (H + g) * D, vc = (H + Hkv + g) * D;
+        const int n = max(it.n[0], it.n[1]);
+        ok = load_kv(kc, it.begin) && load_kv(vc, it.begin);
+        for (int s = 0; s < 2 && ok; ++s) {
+          if (it.n[s] == 0) continue;
+          if (nq[s] > 0) ok = wait(&q_free[s], nq[s] - 1);
+          if (!ok) break;
+          ++nq[s];
+          const uint32_t fb = smem_u32(&q_full[s]);
+          mbar_arrive_expect_tx(fb, SM::kTile);
+          for (int a = 0; a < DA; ++a)
+            tma_load_2d(smem_u32(Qs + s * SM::kTile + a * kAQ * 128), &tm_qkv, fb,
+                        it.head[s] * D + 64 * a, it.row[s]);
         }
+        for (int j = 1; j < n && ok; ++j)
+          ok = load_kv(kc, it.begin + j * kAK) && load_kv(vc, it.begin + j * kAK);
       }
     }
     __syncwarp();
-    // rows of the last V tile behind the keys belong to another document or to the
-    // padding: cleared, since 0 * inf would reach this document's rows
-    zero_tail<D>(Vs + ((n_kv - 1) & 1) * SM::kKV, kv_end - tile.begin - (n_kv - 1) * kAK, kAK,
-                 smem_u32(&bar_kv[(n_kv - 1) & 1]), (uint32_t)(((n_kv - 1) >> 1) & 1), lane,
-                 smem_u32(&bar_tail), abort_flag, dev_err);
   } else if (warp == kWarpMma) {
     // ---------------------------------------------------------------- MMA issuer
     if (lane == 0) {
       const uint32_t idesc_s = umma_idesc_f16(kAQ, kAK);
       const uint32_t idesc_o = umma_idesc_f16(kAQ, D) | (1u << 16);  // B (V) MN-major
-      bool ok = mbar_wait_bounded(smem_u32(&bar_q), 0u, abort_flag, dev_err, DEV_ERR_WAIT_GEMM);
-      auto issue_s = [&](int j) -> bool {
-        const int buf = j & 1;
-        if (!mbar_wait_bounded(smem_u32(&bar_kv[buf]), (uint32_t)((j >> 1) & 1), abort_flag,
-                               dev_err, DEV_ERR_WAIT_GEMM))
-          return false;
-        if (j >= 2 && !mbar_wait_bounded(smem_u32(&bar_s_free[buf]), (uint32_t)(((j - 2) >> 1) & 1),
-                                         abort_flag, dev_err, DEV_ERR_WAIT_GEMM))
-          return false;
-        tc_fence_after();
+      uint32_t c = 0, tails = 0;                       // ring tiles; phase of each slot's tail_done
+      uint32_t nq[2] = {0, 0}, np[2] = {0, 0};         // items, P tiles of each stream
+      bool ok = true;
+      auto issue_s = [&](int s, uint32_t ck) {  // S_s = Q_s K^T with the K tile at ring count ck
+        const uint32_t kt = smem_u32(KV + (ck % NR) * SM::kTile), qt = smem_u32(Qs + s * SM::kTile);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (uint32_t)((kk >> 2) * kAQ * 128 + (kk & 3) * 32);
-          const uint64_t ad = umma_desc_k_sw128(smem_u32(Qs) + off);
-          const uint64_t bd = umma_desc_k_sw128(smem_u32(Ks + buf * SM::kKV) + off);
-          tc_mma_bf16(tmem + kColS + (uint32_t)buf * kAK, ad, bd, idesc_s, kk > 0 ? 1u : 0u);
+          const uint32_t off = (uint32_t)((kk >> 2) * 128 * 128 + (kk & 3) * 32);
+          tc_mma_bf16(tmem + kColS + (uint32_t)s * kAK, umma_desc_k_sw128(qt + off),
+                      umma_desc_k_sw128(kt + off), idesc_s, kk > 0 ? 1u : 0u);
         }
-        tc_commit(smem_u32(&bar_s[buf]));
-        return true;
+        tc_commit(smem_u32(&s_full[s]));
       };
-      ok = ok && issue_s(0);
-      for (int j = 0; j < n_kv && ok; ++j) {
-        const int buf = j & 1;
-        if (j + 1 < n_kv) ok = issue_s(j + 1);
-        if (!ok) break;
-        // P_j written (and O rescaled if its reference maximum moved)
-        ok = mbar_wait_bounded(smem_u32(&bar_p), (uint32_t)(j & 1), abort_flag, dev_err,
-                               DEV_ERR_WAIT_GEMM);
-        if (j == n_kv - 1)
-          ok = ok && mbar_wait_bounded(smem_u32(&bar_tail), 0u, abort_flag, dev_err,
-                                       DEV_ERR_WAIT_GEMM);
-        if (!ok) break;
-        tc_fence_after();
-#pragma unroll
-        for (int kk = 0; kk < kAK / 16; ++kk) {
-          const uint64_t ad = umma_desc_k_sw128(smem_u32(Ps) + (uint32_t)((kk >> 2) * kAQ * 128 +
-                                                                          (kk & 3) * 32));
-          const uint64_t bd = umma_desc_mn_sw128(smem_u32(Vs + buf * SM::kKV) + (uint32_t)kk * 16 * 128,
-                                                 (uint32_t)(kAK * 128), 1024u);
-          tc_mma_bf16(tmem + kColO, ad, bd, idesc_o, (j > 0 || kk > 0) ? 1u : 0u);
+      for (int w = blockIdx.x; w < items && ok; w += gridDim.x) {
+        const FwdItem it = fwd_item(idx, w, H, heads);
+        const int n = max(it.n[0], it.n[1]);
+        const bool tail = it.begin + n * kAK > it.end;
+        ok = wait(&kv_full[c % NR], c / NR);
+        for (int s = 0; s < 2 && ok; ++s) {
+          if (it.n[s] == 0) continue;
+          ok = wait(&q_full[s], nq[s]);
+          if (!ok) break;
+          tc_fence_after();
+          issue_s(s, c);
+          if (it.n[s] == 1) tc_commit(smem_u32(&q_free[s]));
         }
-        tc_commit(smem_u32(&bar_pv));           // P free, O updated
-        tc_commit(smem_u32(&bar_kv_free[buf]));  // K_j and V_j read
+        if (ok) tc_commit(smem_u32(&kv_free[c % NR]));
+        for (int j = 0; j < n && ok; ++j) {
+          const uint32_t cv = c + 2 * j + 1, ck = cv + 1;
+          const uint32_t vt = smem_u32(KV + (cv % NR) * SM::kTile);
+          for (int s = 0; s < 2 && ok; ++s) {
+            if (j >= it.n[s]) continue;
+            ok = wait(&kv_full[cv % NR], cv / NR);
+            if (ok && tail && j == n - 1) ok = wait(&tail_done[cv % NR], tails >> (cv % NR));
+            // O of the stream's previous item has been read
+            if (ok && j == 0 && nq[s] > 0) ok = wait(&o_free[s], nq[s] - 1);
+            // P_j written (and O rescaled if its reference maximum moved)
+            if (ok) ok = wait(&p_full[s], np[s]);
+            if (!ok) break;
+            ++np[s];
+            tc_fence_after();
+#pragma unroll
+            for (int kk = 0; kk < kAK / 16; ++kk)
+              tc_mma_ts(tmem + kColO + (uint32_t)s * 128, tmem + kColS + (uint32_t)(s * kAK + kk * 8),
+                        umma_desc_mn_sw128(vt + (uint32_t)kk * 16 * 128, (uint32_t)(kAK * 128), 1024u),
+                        idesc_o, (j > 0 || kk > 0) ? 1u : 0u);
+            if (j + 1 < it.n[s]) {
+              ok = wait(&kv_full[ck % NR], ck / NR);
+              if (!ok) break;
+              tc_fence_after();
+              issue_s(s, ck);  // (its completion also says that this P V has run)
+              if (j + 2 == it.n[s]) tc_commit(smem_u32(&q_free[s]));
+            } else {
+              tc_commit(smem_u32(&o_full[s]));
+              ++nq[s];
+            }
+          }
+          if (!ok) break;
+          tc_commit(smem_u32(&kv_free[cv % NR]));
+          if (j + 1 < n) tc_commit(smem_u32(&kv_free[ck % NR]));
+        }
+        if (tail) tails ^= 1u << ((c + 2 * n - 1) % NR);
+        c += 2 * n;
       }
     }
     __syncwarp();
+  } else if (warp == kWarpTail) {
+    // It follows every tile of the ring (so that it never falls a phase behind) and
+    // gives each slot free again together with the products.
+    uint32_t c = 0;
+    bool ok = true;
+    for (int w = blockIdx.x; w < items && ok; w += gridDim.x) {
+      const FwdItem it = fwd_item(idx, w, H, heads);
+      const int n = max(it.n[0], it.n[1]);
+      for (int k = 0; k < 2 * n && ok; ++k, ++c) {
+        const uint32_t slot = c % NR;
+        ok = __all_sync(0xFFFFFFFFu, wait(&kv_full[slot], c / NR));
+        if (ok && k == 2 * n - 1 && it.begin + n * kAK > it.end) {
+          // V rows behind the document belong to another one or to the padding:
+          // cleared, since 0 * inf would reach this document's rows
+          zero_rows<D>(KV + slot * SM::kTile, it.end - it.begin - (n - 1) * kAK, kAK, lane);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&tail_done[slot]));
+        }
+        if (lane == 0) mbar_arrive(smem_u32(&kv_free[slot]));
+      }
+    }
   } else {
     // ---------------------------------------------------------------- softmax (warps 0-7)
-    const int r = (warp & 3) * 32 + lane;  // query row of the block = TMEM lane
-    const int hf = warp >> 2;               // half: keys (and O columns) 64 hf ..
-    const int q = q0 + r;                   // the row's token
-    const int kmax = min(max(q, tile.prompt - 1), tile.end - 1);  // its last key
+    const int s = warp >> 2;
+    const int r = (warp & 3) * 32 + lane;  // query row of the stream = TMEM lane
     const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    constexpr int KH = kAK / 2, DH = D / 2;  // keys and O columns per half
-    float m_ref = -INFINITY, l_run = 0.f;    // l_run: this half's share of the row sum
+    const uint32_t ts = trow + kColS + (uint32_t)s * kAK, to = trow + kColO + (uint32_t)s * 128;
+    uint32_t ns = 0, no = 0;  // S tiles and items of this stream
     bool ok = true;
-    // the eight softmax warps meet at a bounded barrier (one arrival per warp),
-    // so that an abort in one of them cannot strand the others
-    int sm_phase = 0;
-    auto sm_sync = [&]() -> bool {
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&bar_sm));
-      const bool rr = mbar_wait_bounded(smem_u32(&bar_sm), (uint32_t)(sm_phase & 1), abort_flag,
-                                        dev_err, DEV_ERR_WAIT_GEMM);
-      ++sm_phase;
-      return __all_sync(0xFFFFFFFFu, rr);
-    };
-    for (int j = 0; j < n_kv && ok; ++j) {
-      const int buf = j & 1;
-      ok = mbar_wait_bounded(smem_u32(&bar_s[buf]), (uint32_t)((j >> 1) & 1), abort_flag, dev_err,
-                             DEV_ERR_WAIT_GEMM);
-      ok = __all_sync(0xFFFFFFFFu, ok);
-      if (!ok) break;
-      tc_fence_after();
-      const int k0 = tile.begin + j * kAK + hf * KH;  // first key of this half
-      const bool full = k0 + KH - 1 <= kmax;  // no key of this half is masked for the row
-      // this half of the row's scores, all loads in flight at once
-      uint32_t sv[KH / 16][16];
-#pragma unroll
-      for (int c = 0; c < KH / 16; ++c)
-        tmem_ld16(trow + kColS + (uint32_t)buf * kAK + (uint32_t)(hf * KH + 16 * c), sv[c]);
-      tmem_ld_wait();
-      float mt = -INFINITY;
-      if (full) {
-#pragma unroll
-        for (int c = 0; c < KH / 16; ++c)
-#pragma unroll
-          for (int e = 0; e < 16; ++e) mt = fmaxf(mt, __uint_as_float(sv[c][e]));
-      } else {
-#pragma unroll
-        for (int c = 0; c < KH / 16; ++c)
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            if (k0 + 16 * c + e > kmax) sv[c][e] = __float_as_uint(-INFINITY);
-            mt = fmaxf(mt, __uint_as_float(sv[c][e]));
-          }
-      }
-      // the row's maximum over both halves, in the log2 domain
-      xch[hf][r] = mt;
-      ok = sm_sync();
-      mt = fmaxf(mt, xch[hf ^ 1][r]) * sl2;
-      ok = sm_sync() && ok;  // xch is free again
-      if (!ok) break;
-      float corr = 1.f;
-      bool moved = false;
-      if (j == 0) {
-        m_ref = mt;  // (finite: every row sees the document's first key)
-      } else if (mt > m_ref + kRescaleLog2) {
-        corr = exp2f(m_ref - mt);
-        m_ref = mt;
-        l_run *= corr;
-        moved = true;
-      }
-      // the previous P V has read P and written O
-      if (j > 0) {
-        ok = mbar_wait_bounded(smem_u32(&bar_pv), (uint32_t)((j - 1) & 1), abort_flag, dev_err,
-                               DEV_ERR_WAIT_GEMM);
-        ok = __all_sync(0xFFFFFFFFu, ok);
+    for (int w = blockIdx.x; w < items && ok; w += gridDim.x) {
+      const FwdItem it = fwd_item(idx, w, H, heads);
+      const int n = it.n[s];
+      if (n == 0) continue;
+      const int q = it.row[s] + r;
+      const int kmax = min(max(q, it.prompt - 1), it.end - 1);  // the row's last key
+      const int kall = min(max(it.row[s] + (warp & 3) * 32, it.prompt - 1), it.end - 1);
+      float m_ref = -INFINITY, l_run = 0.f;
+      for (int j = 0; j < n && ok; ++j) {
+        ok = __all_sync(0xFFFFFFFFu, wait(&s_full[s], ns));
         if (!ok) break;
+        ++ns;
         tc_fence_after();
-      }
-      if (__any_sync(0xFFFFFFFFu, moved)) {
+        uint32_t sv[kAK];
+#pragma unroll
+        for (int c = 0; c < kAK / 32; ++c) tmem_ld32(ts + 32 * c, sv + 32 * c);
+        tmem_ld_wait();
+        const int k0 = it.begin + j * kAK;
+        if (k0 + kAK - 1 > kall) {  // (uniform in the warp)
+          const int last = kmax - k0;
+#pragma unroll
+          for (int e = 0; e < kAK; ++e)
+            if (e > last) sv[e] = 0xFF800000u;  // -inf
+        }
+        float mt = -INFINITY, mt1 = -INFINITY;
+#pragma unroll
+        for (int e = 0; e < kAK; e += 4) {
+          mt = fmaxf(fmaxf(mt, __uint_as_float(sv[e])), __uint_as_float(sv[e + 1]));
+          mt1 = fmaxf(fmaxf(mt1, __uint_as_float(sv[e + 2])), __uint_as_float(sv[e + 3]));
+        }
+        mt = fmaxf(mt, mt1) * sl2;
+        float corr = 1.f;
+        bool moved = false;
+        if (j == 0) {
+          m_ref = mt;  // (finite for finite scores: every row sees its document's first key)
+        } else if (mt > m_ref + kRescaleLog2) {
+          corr = exp2f(m_ref - mt);
+          m_ref = mt;
+          l_run *= corr;
+          moved = true;
+        }
+        if (__any_sync(0xFFFFFFFFu, moved)) {
 #pragma unroll 1
-        for (int c = 0; c < DH / 16; ++c) {
-          uint32_t v[16];
-          tmem_ld16(trow + kColO + (uint32_t)(hf * DH + 16 * c), v);
-          tmem_ld_wait();
+          for (int c = 0; c < D / 16; ++c) {
+            uint32_t v[16];
+            tmem_ld16(to + 16 * c, v);
+            tmem_ld_wait();
 #pragma unroll
-          for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * corr);
-          tmem_st16(trow + kColO + (uint32_t)(hf * DH + 16 * c), v);
+            for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * corr);
+            tmem_st16(to + 16 * c, v);
+          }
         }
+        // P = exp2(s sl2 - m_ref) in fp16 (masked scores are -inf, so their p is 0) over
+        // the scores' own columns, and the row sum
+        const float nm = -m_ref;
+        float rs0 = 0.f, rs1 = 0.f;
+#pragma unroll
+        for (int c = 0; c < kAK / 32; ++c) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const float p0 = exp2f(fmaf(__uint_as_float(sv[32 * c + e]), sl2, nm));
+            const float p1 = exp2f(fmaf(__uint_as_float(sv[32 * c + e + 1]), sl2, nm));
+            rs0 += p0;
+            rs1 += p1;
+            pk[e >> 1] = pack_f16x2(p0, p1);
+          }
+          tmem_st16(ts + 16 * c, pk);
+        }
+        l_run += rs0 + rs1;
         tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&p_full[s]));
       }
-      // P = exp2(s sl2 - m_ref) in fp16 into this half's 64-key atom of the P
-      // tile (masked scores are -inf, so their p is 0), and this half's row sum
-      const float nm = -m_ref;
-      float rs = 0.f;
-      uint8_t* atom = Ps + hf * kAQ * 128;
+      // -------------------------------------------------------------- epilogue
+      ok = ok && __all_sync(0xFFFFFFFFu, wait(&o_full[s], no));
+      if (!ok) break;
+      ++no;
+      tc_fence_after();
+      const float inv = 1.f / l_run;
+      const bool live = q < it.end;
+      uint16_t* orow = out + (int64_t)q * H * D + (int64_t)it.head[s] * D;
+      uint32_t ov[D];
 #pragma unroll
-      for (int c = 0; c < KH / 16; ++c) {
-        uint32_t pk[8];
-#pragma unroll
-        for (int e = 0; e < 16; e += 2) {
-          const float p0 = exp2f(fmaf(__uint_as_float(sv[c][e]), sl2, nm));
-          const float p1 = exp2f(fmaf(__uint_as_float(sv[c][e + 1]), sl2, nm));
-          rs += p0 + p1;
-          pk[e >> 1] = pack_f16x2(p0, p1);
-        }
-        *reinterpret_cast<uint4*>(atom + sw128_offset((uint32_t)r, (uint32_t)(2 * c))) =
-            make_uint4(pk[0], pk[1], pk[2], pk[3]);
-        *reinterpret_cast<uint4*>(atom + sw128_offset((uint32_t)r, (uint32_t)(2 * c + 1))) =
-            make_uint4(pk[4], pk[5], pk[6], pk[7]);
-      }
-      l_run += rs;
-      fence_proxy_async_smem();  // P visible to the tensor core
+      for (int c = 0; c < D / 32; ++c) tmem_ld32(to + 32 * c, ov + 32 * c);
+      tmem_ld_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(smem_u32(&bar_s_free[buf]));
-        mbar_arrive(smem_u32(&bar_p));
-      }
-    }
-    // ---------------------------------------------------------------- epilogue
-    if (ok) ok = mbar_wait_bounded(smem_u32(&bar_pv), (uint32_t)((n_kv - 1) & 1), abort_flag,
-                                   dev_err, DEV_ERR_WAIT_GEMM);
-    ok = __all_sync(0xFFFFFFFFu, ok);
-    // the row sum over both halves (every softmax thread reaches the barrier)
-    xch[hf][r] = l_run;
-    ok = sm_sync() && ok;
-    const float l_row = l_run + xch[hf ^ 1][r];
-    if (ok) {
-      tc_fence_after();
-      const float inv = 1.f / l_row;
-      const bool live = q < tile.end;
-      uint16_t* orow = out + (int64_t)q * (int64_t)H * D + (int64_t)h * D + hf * DH;
-      uint32_t ov[DH / 16][16];
+      if (lane == 0) mbar_arrive(smem_u32(&o_free[s]));
+      if (live) {
 #pragma unroll
-      for (int c = 0; c < DH / 16; ++c) tmem_ld16(trow + kColO + (uint32_t)(hf * DH + 16 * c), ov[c]);
-      tmem_ld_wait();
+        for (int c = 0; c < D / 8; ++c) {
+          uint32_t pk[4];
 #pragma unroll
-      for (int c = 0; c < DH / 16; ++c) {
-        uint32_t pk[8];
-#pragma unroll
-        for (int e = 0; e < 16; e += 2)
-          pk[e >> 1] =
-              pack_f16x2(__uint_as_float(ov[c][e]) * inv, __uint_as_float(ov[c][e + 1]) * inv);
-        if (live) {
-          *reinterpret_cast<uint4*>(orow + 16 * c) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-          *reinterpret_cast<uint4*>(orow + 16 * c + 8) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+          for (int e = 0; e < 4; ++e)
+            pk[e] = pack_f16x2(__uint_as_float(ov[8 * c + 2 * e]) * inv,
+                               __uint_as_float(ov[8 * c + 2 * e + 1]) * inv);
+          *reinterpret_cast<uint4*>(orow + 8 * c) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
         }
+        lse_out[(int64_t)it.head[s] * T + q] = (m_ref + log2f(l_run)) * 0.69314718055994531f;
       }
-      if (live && hf == 0)
-        lse_out[(int64_t)h * T + q] = (m_ref + log2f(l_row)) * 0.69314718055994531f;
     }
   }
+  fill_padding<D>(idx.head[2], T, H, out, lse_out);
 
   // ------------------------------------------------------------------ teardown
   tc_fence_before();
@@ -380,9 +445,11 @@ __global__ void __launch_bounds__(kAThreads, 1)
 }
 
 // ------------------------------------------------------------------ backward
+constexpr int kBThreads = 320;
 constexpr int kBC = 64;  // columns of a chunk (queries for dK/dV, keys for dQ)
 
-// zero_tail for two tiles that share a barrier.
+// Clears rows [rows, all) of two tiles that share a barrier (one warp) once their load has
+// landed, and arrives on `done`; whole tiles only arrive.
 template <int D>
 __device__ __forceinline__ void zero_tail2(uint8_t* a, uint8_t* b, int rows, int all, uint32_t bar,
                                            uint32_t parity, int lane, uint32_t done,
@@ -500,7 +567,7 @@ struct PaDkvSmem {
 // after the key block (causal), accumulating dV += P^T dO and dK += dS^T Q in
 // TMEM; writes dk = scale dK and dv per query head.
 template <int D>
-__global__ void __launch_bounds__(kAThreads, 1)
+__global__ void __launch_bounds__(kBThreads, 1)
     packed_attn_dkdv_kernel(const __grid_constant__ CUtensorMap tm_kv,   // qkv, boxes of 128 rows
                             const __grid_constant__ CUtensorMap tm_q,    // qkv, boxes of 64 rows
                             const __grid_constant__ CUtensorMap tm_do,   // dO', boxes of 64 rows
@@ -784,7 +851,7 @@ struct PaDqSmem {
 // dQ of 128 queries for one query head: loops over the 64-key chunks up to the
 // queries (causal), accumulating dQ += dS K in TMEM; writes dq = scale dQ.
 template <int D>
-__global__ void __launch_bounds__(kAThreads, 1)
+__global__ void __launch_bounds__(kBThreads, 1)
     packed_attn_dq_kernel(const __grid_constant__ CUtensorMap tm_q,    // qkv, boxes of 128 rows
                           const __grid_constant__ CUtensorMap tm_kv,   // qkv, boxes of 64 rows
                           const __grid_constant__ CUtensorMap tm_do,   // dO', boxes of 128 rows
@@ -1095,7 +1162,7 @@ cudaError_t launch_dep(void (*k)(P...), dim3 grid, unsigned threads, size_t smem
 template <int D>
 int fwd_t(const uint16_t* qkv, const PackedIndex& x, int64_t T, int H, int Hkv, uint16_t* o,
           float* lse, cudaStream_t st) {
-  using SM = PaSmem<D>;
+  using SM = FwdSmem<D>;
   static bool attr[64] = {false};
   LSQ_TRY(allow_smem(packed_attn_fwd_kernel<D>, (int)SM::kBytes, attr));
   const int64_t row = (int64_t)(H + 2 * Hkv) * D;
@@ -1105,8 +1172,10 @@ int fwd_t(const uint16_t* qkv, const PackedIndex& x, int64_t T, int H, int Hkv, 
   int* err = device_status_ptr();
   if (!err) return set_error(LSQ_ERR_CUDA, "device status word unavailable");
   const float sl2 = 1.4426950408889634f / sqrtf((float)D);
-  LSQ_CUDA(launch_dep(packed_attn_fwd_kernel<D>, dim3((unsigned)x.cap, (unsigned)H), kAThreads,
-                      SM::kBytes, st, tm, x, T, H, Hkv, o, lse, sl2, err));
+  const int64_t items = (H / Hkv) % 2 == 0 ? (int64_t)x.cap * (H / 2) : (int64_t)x.cap2 * H;
+  const unsigned grid = (unsigned)std::min<int64_t>(items, gemm_num_sms());
+  LSQ_CUDA(launch_dep(packed_attn_fwd_kernel<D>, dim3(grid), kFThreads, SM::kBytes, st, tm, x, T, H,
+                      Hkv, o, lse, sl2, err));
   return LSQ_OK;
 }
 
@@ -1157,10 +1226,10 @@ int bwd_t(const uint16_t* qkv, const PackedIndex& x, const uint16_t* o, const fl
   LSQ_TRY(make_tmap_2d(&do64, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, w.dos, (uint64_t)hd, (uint64_t)T,
                        (uint64_t)hd, 64, kBC, CU_TENSOR_MAP_SWIZZLE_128B));
   const dim3 grid((unsigned)x.cap, (unsigned)H);
-  LSQ_CUDA(launch_dep(packed_attn_dkdv_kernel<D>, grid, kAThreads, PaDkvSmem<D>::kBytes, st, qkv128,
+  LSQ_CUDA(launch_dep(packed_attn_dkdv_kernel<D>, grid, kBThreads, PaDkvSmem<D>::kBytes, st, qkv128,
                       qkv64, do64, x, lse, w.delta, w.rowexp, T, H, Hkv, sl2, scale, w.dk, w.dv,
                       err));
-  LSQ_CUDA(launch_dep(packed_attn_dq_kernel<D>, grid, kAThreads, PaDqSmem<D>::kBytes, st, qkv128,
+  LSQ_CUDA(launch_dep(packed_attn_dq_kernel<D>, grid, kBThreads, PaDqSmem<D>::kBytes, st, qkv128,
                       qkv64, do128, x, lse, w.delta, w.rowexp, T, H, Hkv, sl2, scale, w.dq, err));
   const int64_t items = T * (H + 2 * Hkv) * (D / 8);
   LSQ_CUDA(launch_dep(packed_grad_kernel,
