@@ -51,6 +51,25 @@ __device__ __forceinline__ int find_last(const int* a, int n, int x) {
   return lo;
 }
 
+// How many tiles of a document of nt tiles, pt of which hold some of its prompt, have
+// more work than w.  Query tiles of 128: tile i sees max(i + 1, pt) key tiles; of 256:
+// taken as max(2 i + 2, pt); key tiles: tile i is seen by nt - i query tiles, by all nt
+// where it holds some of the prompt.
+enum ListKind { LIST_Q = 0, LIST_Q2 = 1, LIST_K = 2 };
+__device__ __forceinline__ int work_of(int kind, int i, int nt, int pt) {
+  return kind == LIST_Q ? max(i + 1, pt) : kind == LIST_Q2 ? max(2 * i + 2, pt) : i < pt ? nt : nt - i;
+}
+__device__ __forceinline__ int count_above(int kind, int nt, int pt, int w) {
+  if (kind == LIST_K) return nt <= w ? 0 : pt + max(0, nt - w - pt);
+  if (pt > w) return nt;
+  return max(0, nt - (kind == LIST_Q ? w : w / 2));
+}
+// Tiles before tile i of the same document with the same work.
+__device__ __forceinline__ int ties_before(int kind, int i, int pt) {
+  const bool flat = kind == LIST_Q ? i + 1 <= pt : kind == LIST_Q2 ? 2 * i + 2 <= pt : i < pt;
+  return flat ? i : 0;
+}
+
 // Every CTA scans all lengths, 1024 documents at a time (a few microseconds for the
 // thousands of documents a row holds), and writes its own share of the tokens and
 // tiles, each found by a binary search over the 1024 starts in shared memory: a
@@ -61,6 +80,7 @@ __global__ void __launch_bounds__(kIdxThreads)
   __shared__ int64_t sh[32];
   __shared__ int tok0[kIdxThreads], t1[kIdxThreads], t2[kIdxThreads], doc_e[kIdxThreads],
       doc_p[kIdxThreads];
+  const bool sorted = n_docs <= kIdxThreads;
   pdl_trigger();
   pdl_wait();
   const int tid = threadIdx.x;
@@ -99,18 +119,34 @@ __global__ void __launch_bounds__(kIdxThreads)
       x.key_end[t] = max(t + 1, doc_p[k]);
       x.doc_end[t] = doc_e[k];
     }
-    for (int i = gtid; i < c1; i += gsize) {
-      const int k = find_last(t1, kIdxThreads, base1 + i);
-      if (base1 + i < x.cap)
-        x.tiles[base1 + i] = {tok0[k] + (base1 + i - t1[k]) * kPackedTile, tok0[k], doc_e[k],
-                              doc_p[k]};
-    }
-    for (int i = gtid; i < c2; i += gsize) {
-      const int k = find_last(t2, kIdxThreads, base2 + i);
-      if (base2 + i < x.cap2)
-        x.tiles2[base2 + i] = {tok0[k] + (base2 + i - t2[k]) * 2 * kPackedTile, tok0[k], doc_e[k],
-                               doc_p[k]};
-    }
+    // a tile's place: by its work, or (with more documents than one chunk) in order
+    auto emit = [&](int kind, const int* first, int n, int before, int size, PackedTile* list,
+                    int cap) {
+      for (int i = gtid >> 5; i < n; i += gsize >> 5) {
+        const int k = find_last(first, kIdxThreads, before + i);
+        const int at = before + i - first[k];  // tile of its document
+        int place = before + i;
+        if (sorted) {
+          const int lane = tid & 31;
+          auto tiles_of = [&](int len) { return (len + size - 1) / size; };
+          const int pt = (doc_p[k] - tok0[k] + kPackedTile - 1) / kPackedTile;
+          const int w = work_of(kind, at, tiles_of(doc_e[k] - tok0[k]), pt);
+          place = 0;
+          for (int d = lane; d < n_docs; d += 32) {
+            const int nt = tiles_of(doc_e[d] - tok0[d]);
+            const int dpt = (doc_p[d] - tok0[d] + kPackedTile - 1) / kPackedTile;
+            const int above = count_above(kind, nt, dpt, w);
+            place += d < k ? count_above(kind, nt, dpt, w - 1) : above;
+          }
+          place = __reduce_add_sync(0xFFFFFFFFu, place) + ties_before(kind, at, pt);
+        }
+        if ((tid & 31) == 0 && place < cap)
+          list[place] = {tok0[k] + at * size, tok0[k], doc_e[k], doc_p[k]};
+      }
+    };
+    emit(LIST_Q, t1, c1, base1, kPackedTile, x.tiles, x.cap);
+    emit(LIST_K, t1, c1, base1, kPackedTile, x.ktiles, x.cap);
+    emit(LIST_Q2, t2, c2, base2, 2 * kPackedTile, x.tiles2, x.cap2);
     base = hi;
     base1 += c1;
     base2 += c2;

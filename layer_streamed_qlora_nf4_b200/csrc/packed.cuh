@@ -22,16 +22,19 @@ struct PackedTile {
 constexpr int kPackedTile = 128;
 
 // int32 words: a header of 8 (tiles of 128, tiles of 256, tokens in documents), the
-// two tile lists, then per token its position in its document, the end of the keys
-// it sees and the end of its document.
+// tile lists, then per token its position in its document, the end of the keys it sees
+// and the end of its document.  The lists are in order of falling work (with more than
+// 1024 documents: in token order), so that persistent CTAs that take items in turn end
+// together: query tiles by the keys they see, key tiles by the queries that see them.
 struct PackedIndex {
   int* head;
-  PackedTile* tiles;   // tiles of 128 tokens
-  PackedTile* tiles2;  // tiles of 256 tokens
+  PackedTile* tiles;    // query tiles of 128 tokens
+  PackedTile* ktiles;   // the same tiles in the key tiles' order
+  PackedTile* tiles2;   // query tiles of 256 tokens
   int* pos;
   int* key_end;
   int* doc_end;
-  int cap, cap2;       // room in the lists
+  int cap, cap2;        // room in the lists
 };
 
 inline int64_t packed_tile_cap(int64_t T, int64_t n_docs, int size) {
@@ -39,7 +42,7 @@ inline int64_t packed_tile_cap(int64_t T, int64_t n_docs, int size) {
   return c < T ? c : T;
 }
 inline int64_t packed_index_words(int64_t T, int64_t n_docs) {
-  return 8 + 4 * (packed_tile_cap(T, n_docs, kPackedTile) +
+  return 8 + 4 * (2 * packed_tile_cap(T, n_docs, kPackedTile) +
                   packed_tile_cap(T, n_docs, 2 * kPackedTile)) + 3 * T;
 }
 inline PackedIndex packed_index_view(const int32_t* base, int64_t T, int64_t n_docs) {
@@ -48,7 +51,8 @@ inline PackedIndex packed_index_view(const int32_t* base, int64_t T, int64_t n_d
   x.cap = (int)packed_tile_cap(T, n_docs, kPackedTile);
   x.cap2 = (int)packed_tile_cap(T, n_docs, 2 * kPackedTile);
   x.tiles = reinterpret_cast<PackedTile*>(x.head + 8);
-  x.tiles2 = x.tiles + x.cap;
+  x.ktiles = x.tiles + x.cap;
+  x.tiles2 = x.ktiles + x.cap;
   x.pos = reinterpret_cast<int*>(x.tiles2 + x.cap2);
   x.key_end = x.pos + T;
   x.doc_end = x.key_end + T;

@@ -68,6 +68,13 @@ struct FwdItem {
 __device__ __forceinline__ int key_tiles(const PackedTile& t, int row) {
   return (min(t.end, max(row + kAQ, t.prompt)) - t.begin + kAK - 1) / kAK;
 }
+// Item of this CTA in round k: the items, heaviest first, are dealt forth and back, so
+// that no CTA gets the heavier one every time; -1 behind the last.
+__device__ __forceinline__ int deal(int k, int items) {
+  const int w = k * (int)gridDim.x +
+                ((k & 1) ? (int)(gridDim.x - 1 - blockIdx.x) : (int)blockIdx.x);
+  return w < items ? w : -1;
+}
 __device__ __forceinline__ FwdItem fwd_item(const PackedIndex& x, int w, int H, bool heads) {
   FwdItem it;
   const int per = heads ? H / 2 : H;
@@ -205,7 +212,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
         ++c;
         return true;
       };
-      for (int w = blockIdx.x; w < items && ok; w += gridDim.x) {
+      for (int k = 0, w; ok && (w = deal(k, items)) >= 0; ++k) {
         const FwdItem it = fwd_item(idx, w, H, heads);
         const int g = it.head[0] / G;
         const int kc = (H + g) * D, vc = (H + Hkv + g) * D;
@@ -245,7 +252,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
         }
         tc_commit(smem_u32(&s_full[s]));
       };
-      for (int w = blockIdx.x; w < items && ok; w += gridDim.x) {
+      for (int k = 0, w; ok && (w = deal(k, items)) >= 0; ++k) {
         const FwdItem it = fwd_item(idx, w, H, heads);
         const int n = max(it.n[0], it.n[1]);
         const bool tail = it.begin + n * kAK > it.end;
@@ -303,13 +310,13 @@ __global__ void __launch_bounds__(kFThreads, 1)
     // gives each slot free again together with the products.
     uint32_t c = 0;
     bool ok = true;
-    for (int w = blockIdx.x; w < items && ok; w += gridDim.x) {
+    for (int k = 0, w; ok && (w = deal(k, items)) >= 0; ++k) {
       const FwdItem it = fwd_item(idx, w, H, heads);
       const int n = max(it.n[0], it.n[1]);
-      for (int k = 0; k < 2 * n && ok; ++k, ++c) {
+      for (int i = 0; i < 2 * n && ok; ++i, ++c) {
         const uint32_t slot = c % NR;
         ok = __all_sync(0xFFFFFFFFu, wait(&kv_full[slot], c / NR));
-        if (ok && k == 2 * n - 1 && it.begin + n * kAK > it.end) {
+        if (ok && i == 2 * n - 1 && it.begin + n * kAK > it.end) {
           // V rows behind the document belong to another one or to the padding:
           // cleared, since 0 * inf would reach this document's rows
           zero_rows<D>(KV + slot * SM::kTile, it.end - it.begin - (n - 1) * kAK, kAK, lane);
@@ -328,7 +335,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
     const uint32_t ts = trow + kColS + (uint32_t)s * kAK, to = trow + kColO + (uint32_t)s * 128;
     uint32_t ns = 0, no = 0;  // S tiles and items of this stream
     bool ok = true;
-    for (int w = blockIdx.x; w < items && ok; w += gridDim.x) {
+    for (int k = 0, w; ok && (w = deal(k, items)) >= 0; ++k) {
       const FwdItem it = fwd_item(idx, w, H, heads);
       const int n = it.n[s];
       if (n == 0) continue;

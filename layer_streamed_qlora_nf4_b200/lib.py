@@ -521,51 +521,56 @@ def nf4_lora_linear_fwd_noalloc(x, codes, absmax, A, B, scale, y, residual=None,
 
 
 # ------------------------------------------------------------ packed documents, AdamW
-class _On:
-    """The tensors of one call: all on one CUDA device, which is made current for the call."""
-
-    def __init__(self, stream, **tensors):
-        import torch
-        dev = None
-        for name, t in tensors.items():
-            if t is None:
-                continue
-            if not t.is_cuda:
-                raise ValueError("%s must be a CUDA tensor" % name)
-            if dev is not None and t.device != dev:
-                raise ValueError("%s is on %s, the other tensors on %s" % (name, t.device, dev))
-            dev = t.device
-        self.dev, self.prev, self.cuda = dev.index, None, torch.cuda
-        self.given = stream
-
-    def __enter__(self):
-        if self.cuda.current_device() != self.dev:
-            self.prev = self.cuda.current_device()
-            self.cuda.set_device(self.dev)
-        if self.given is not None:
-            return ctypes.c_void_p(self.given)
-        return ctypes.c_void_p(self.cuda.current_stream().cuda_stream)
-
-    def __exit__(self, *exc):
-        if self.prev is not None:
-            self.cuda.set_device(self.prev)
-
-
-def _need(name, t, dtype, shape=None, numel=None, optional=False):
+def _need(name, t, dtype, shape=None, numel=None):
     """Checks one tensor argument: its type, that it is contiguous, its shape or length."""
     import torch
-    if t is None and optional:
-        return
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch tensor" % name)
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError("%s must be %s, not %s" % (name, dtype, t.dtype))
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError("%s must have shape %s, not %s" % (name, tuple(shape), tuple(t.shape)))
     if numel is not None and t.numel() != numel:
         raise ValueError("%s must have %d elements, not %d" % (name, numel, t.numel()))
+
+
+_current = None   # (current device, its current stream): looked up once, a call of each is cheap
+
+
+def _call(name, stream, tensors, *args):
+    """Runs one entry point on the device that holds all the tensors (made current for
+    the call) and on its current stream, or the given one.  args: all but the stream."""
+    global _current
+    if _current is None:
+        import torch
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        _current = (torch.cuda.current_device,
+                    raw or (lambda d: torch.cuda.current_stream(d).cuda_stream))
+    dev = -2
+    for t in tensors:
+        if t is not None:
+            d = t.get_device()
+            if d < 0:
+                raise ValueError("%s: every tensor must be a CUDA tensor" % name)
+            if d != dev:
+                if dev != -2:
+                    raise ValueError("%s: tensors on cuda:%d and cuda:%d" % (name, dev, d))
+                dev = d
+    fn = getattr(load(), name)
+    if dev == _current[0]():
+        rc = fn(*args, _current[1](dev) if stream is None else stream)
+    else:
+        import torch
+        with torch.cuda.device(dev):
+            rc = fn(*args, _current[1](dev) if stream is None else stream)
+    if rc != LSQ_OK:
+        _check(rc)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 def packed_index_ints(T, n_docs):
@@ -589,10 +594,10 @@ def packed_index(lengths, index, prefix=None, stream=None):
     """lengths, prefix: int32 [n_docs] on the device; index: PackedIndex (filled)."""
     import torch
     _need("lengths", lengths, torch.int32, (index.n_docs,))
-    _need("prefix", prefix, torch.int32, (index.n_docs,), optional=True)
-    with _On(stream, lengths=lengths, prefix=prefix, index=index.buf) as st:
-        _check(load().packed_index(_ptr(lengths), _ptr(prefix), index.n_docs, index.n_tokens,
-                                   _ptr(index.buf), st))
+    if prefix is not None:
+        _need("prefix", prefix, torch.int32, (index.n_docs,))
+    _call("packed_index", stream, (lengths, prefix, index.buf), lengths.data_ptr(), _addr(prefix),
+          index.n_docs, index.n_tokens, index.buf.data_ptr())
 
 
 def _packed_heads(qkv, index, n_heads, n_kv_heads):
@@ -610,9 +615,9 @@ def packed_attention_fwd(qkv, index, n_heads, n_kv_heads, o, lse, stream=None):
     d, T = _packed_heads(qkv, index, n_heads, n_kv_heads), index.n_tokens
     _need("o", o, torch.float16, (T, n_heads * d))
     _need("lse", lse, torch.float32, (n_heads, T))
-    with _On(stream, qkv=qkv, index=index.buf, o=o, lse=lse) as st:
-        _check(load().packed_attention_fwd(_ptr(qkv), _ptr(index.buf), index.n_docs, T, n_heads,
-                                           n_kv_heads, d, _ptr(o), _ptr(lse), st))
+    _call("packed_attention_fwd", stream, (qkv, index.buf, o, lse), qkv.data_ptr(),
+          index.buf.data_ptr(), index.n_docs, T, n_heads, n_kv_heads, d, o.data_ptr(),
+          lse.data_ptr())
 
 
 def packed_attention_workspace_bytes(T, n_heads, n_kv_heads, d):
@@ -629,10 +634,9 @@ def packed_attention_bwd(qkv, index, o, lse, dout, n_heads, n_kv_heads, dqkv, ws
     _need("dout", dout, torch.bfloat16, (T, n_heads * d))
     _need("dqkv", dqkv, torch.bfloat16, qkv.shape)
     _need("ws", ws, torch.uint8)
-    with _On(stream, qkv=qkv, index=index.buf, o=o, lse=lse, dout=dout, dqkv=dqkv, ws=ws) as st:
-        _check(load().packed_attention_bwd(_ptr(qkv), _ptr(index.buf), index.n_docs, _ptr(o),
-                                           _ptr(lse), _ptr(dout), T, n_heads, n_kv_heads, d,
-                                           _ptr(dqkv), _ptr(ws), ws.numel(), st))
+    _call("packed_attention_bwd", stream, (qkv, index.buf, o, lse, dout, dqkv, ws),
+          qkv.data_ptr(), index.buf.data_ptr(), index.n_docs, o.data_ptr(), lse.data_ptr(),
+          dout.data_ptr(), T, n_heads, n_kv_heads, d, dqkv.data_ptr(), ws.data_ptr(), ws.numel())
 
 
 def packed_targets(tokens, index, targets, count, loss_mask=None, accumulate=False, stream=None):
@@ -644,12 +648,11 @@ def packed_targets(tokens, index, targets, count, loss_mask=None, accumulate=Fal
     _need("count", count, torch.int32, numel=1)
     if loss_mask is not None and loss_mask.dtype == torch.bool:
         loss_mask = loss_mask.view(torch.uint8)
-    _need("loss_mask", loss_mask, torch.uint8, numel=T, optional=True)
-    with _On(stream, tokens=tokens, index=index.buf, targets=targets, count=count,
-             loss_mask=loss_mask) as st:
-        _check(load().packed_targets(_ptr(tokens), _ptr(index.buf), index.n_docs, T,
-                                     _ptr(loss_mask), _ptr(targets), _ptr(count),
-                                     1 if accumulate else 0, st))
+    if loss_mask is not None:
+        _need("loss_mask", loss_mask, torch.uint8, numel=T)
+    _call("packed_targets", stream, (tokens, index.buf, targets, count, loss_mask),
+          tokens.data_ptr(), index.buf.data_ptr(), index.n_docs, T, _addr(loss_mask),
+          targets.data_ptr(), count.data_ptr(), 1 if accumulate else 0)
 
 
 def packed_cross_entropy(logits, targets, row_loss, loss, dlogits=None, weight=None, count=None,
@@ -664,14 +667,15 @@ def packed_cross_entropy(logits, targets, row_loss, loss, dlogits=None, weight=N
     _need("targets", targets, torch.int32, numel=T)
     _need("row_loss", row_loss, torch.float32, numel=T)
     _need("loss", loss, torch.float32, numel=1)
-    _need("dlogits", dlogits, torch.bfloat16, (T, V), optional=True)
-    _need("weight", weight, torch.float32, numel=T, optional=True)
-    _need("count", count, torch.int32, numel=1, optional=True)
-    with _On(stream, logits=logits, targets=targets, row_loss=row_loss, loss=loss, dlogits=dlogits,
-             weight=weight, count=count) as st:
-        _check(load().packed_cross_entropy(_ptr(logits), T, V, _ptr(targets), _ptr(weight),
-                                           _ptr(count), _ptr(dlogits), _ptr(row_loss), _ptr(loss),
-                                           1 if accumulate else 0, st))
+    if dlogits is not None:
+        _need("dlogits", dlogits, torch.bfloat16, (T, V))
+    if weight is not None:
+        _need("weight", weight, torch.float32, numel=T)
+    if count is not None:
+        _need("count", count, torch.int32, numel=1)
+    _call("packed_cross_entropy", stream, (logits, targets, row_loss, loss, dlogits, weight, count),
+          logits.data_ptr(), T, V, targets.data_ptr(), _addr(weight), _addr(count),
+          _addr(dlogits), row_loss.data_ptr(), loss.data_ptr(), 1 if accumulate else 0)
 
 
 def adamw_scale_floats(n):
@@ -692,8 +696,8 @@ def adamw_state_dequantize(codes, scale, out, stream=None):
     _need("codes", codes, codes.dtype)
     _need("scale", scale, torch.float32, numel=adamw_scale_floats(n))
     _need("out", out, torch.float32, numel=n)
-    with _On(stream, codes=codes, scale=scale, out=out) as st:
-        _check(load().adamw_state_dequantize(_ptr(codes), _ptr(scale), n, signed, _ptr(out), st))
+    _call("adamw_state_dequantize", stream, (codes, scale, out), codes.data_ptr(),
+          scale.data_ptr(), n, signed, out.data_ptr())
 
 
 def adamw_state_quantize(x, codes, scale, stream=None):
@@ -703,8 +707,8 @@ def adamw_state_quantize(x, codes, scale, stream=None):
     _need("codes", codes, codes.dtype)
     _need("x", x, torch.float32, numel=n)
     _need("scale", scale, torch.float32, numel=adamw_scale_floats(n))
-    with _On(stream, x=x, codes=codes, scale=scale) as st:
-        _check(load().adamw_state_quantize(_ptr(x), n, signed, _ptr(codes), _ptr(scale), st))
+    _call("adamw_state_quantize", stream, (x, codes, scale), x.data_ptr(), n, signed,
+          codes.data_ptr(), scale.data_ptr())
 
 
 class AdamWMulti:
@@ -769,6 +773,6 @@ class AdamWMulti:
             h.step, h.step_dev = int(step), None
         if self._n == 0:
             return
-        with _On(stream, params=self._dev,
-                 step=step if isinstance(step, torch.Tensor) else None) as st:
-            _check(load().adamw_multi_step(self._table, self._n, ctypes.byref(h), st))
+        _call("adamw_multi_step", stream,
+              (self._dev, step if isinstance(step, torch.Tensor) else None), self._table, self._n,
+              ctypes.byref(h))

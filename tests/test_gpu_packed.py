@@ -128,12 +128,20 @@ def test_index_and_targets(L, lengths, prefix, T):
     words = idx.buf.cpu().numpy()
     cap = min(T, T // 128 + len(lengths))
     cap2 = min(T, T // 256 + len(lengths))
-    for n, size, base, room in ((words[0], 128, 8, cap), (words[1], 256, 8 + 4 * cap, cap2)):
+    for n, size, base, room in ((words[0], 128, 8, cap), (words[0], 128, 8 + 4 * cap, cap),
+                                (words[1], 256, 8 + 8 * cap, cap2)):
         want = [(r, s, e, pe) for s, e, pe in docs for r in range(s, e, size)]
         assert n == len(want) <= room
         assert sorted(map(tuple, words[base:base + 4 * n].reshape(n, 4))) == sorted(want)
+    # in order of falling work: the keys a query tile sees, the queries a key tile is seen by
+    tiles = words[8:8 + 4 * words[0]].reshape(-1, 4)
+    seen = np.minimum(tiles[:, 2], np.maximum(tiles[:, 0] + 128, tiles[:, 3])) - tiles[:, 1]
+    assert (np.diff((seen + 127) // 128) <= 0).all()
+    tiles = words[8 + 4 * cap:8 + 4 * (cap + words[0])].reshape(-1, 4)
+    first = np.where(tiles[:, 0] < tiles[:, 3], tiles[:, 1], tiles[:, 0])
+    assert (np.diff((tiles[:, 2] - first + 127) // 128) <= 0).all()
     assert words[2] == sum(lengths)
-    pos, key_end, doc_end = words[8 + 4 * (cap + cap2):].reshape(3, T)
+    pos, key_end, doc_end = words[8 + 4 * (2 * cap + cap2):].reshape(3, T)
     for s, e, pe in docs:
         for t in range(s, e):
             assert (pos[t], key_end[t], doc_end[t]) == (t - s, max(t + 1, pe), e)

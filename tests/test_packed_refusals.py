@@ -27,8 +27,8 @@ def _rc(L, name, *args):
 
 
 def test_index_sizes(L):
-    assert L.packed_index_ints(512, 5) == 8 + 4 * (9 + 7) + 3 * 512
-    assert L.packed_index_ints(1, 1) == 8 + 4 * 2 + 3
+    assert L.packed_index_ints(512, 5) == 8 + 4 * (9 + 9 + 7) + 3 * 512
+    assert L.packed_index_ints(1, 1) == 8 + 4 * 3 + 3
     assert L.packed_index_ints(0, 1) == 0 and L.packed_index_ints(4, 0) == 0
     with pytest.raises(ValueError):
         L.PackedIndex(0, 1, device="cpu")
