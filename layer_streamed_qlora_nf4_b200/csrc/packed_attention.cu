@@ -31,14 +31,22 @@ __device__ __forceinline__ uint8_t* align1024_p(uint8_t* p) {
   return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023));
 }
 
+// 2^x (relative error 2^-22; results below 2^-126 are 0)
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 // ------------------------------------------------------------------ forward
 // A persistent CTA per SM takes work items in turn.  An item is two streams of 128
 // query rows of one document that read the same K and V tiles: two query heads of a kv
 // head on the same rows where the group has an even number of heads, else two
-// neighbouring row tiles of one head.  While the tensor cores work for one stream the
-// softmax of the other runs:
-//   S_s = Q_s K_j^T (TMEM) -> softmax warps of stream s: P = exp2(S c - m) as fp16 over
-//   the same TMEM columns -> O_s += P V_j (A operand from TMEM), S_s of tile j + 1.
+// neighbouring row tiles of one head.  A stream goes through its keys in steps of 64:
+//   S = Q_s K^T (TMEM) -> softmax warps of the stream: P = exp2(S c - m) as fp16 over
+//   the same TMEM columns -> O_s += P V (A operand from TMEM).
+// Two score buffers a stream let the products of step u + 2 and P V of step u run while
+// the softmax of step u + 1 does, so that neither waits for the other's latency.
 // The reference maximum m of a row moves only when a tile's maximum exceeds it by more
 // than 2^8 (then O and the running sum are rescaled): the result is exact for any
 // reference, and P stays below 2^8, well inside fp16.
@@ -47,7 +55,8 @@ __device__ __forceinline__ uint8_t* align1024_p(uint8_t* p) {
 //   warp 9 : TMEM allocation and the MMA issuer (lane 0)
 //   warp 10: clears the rows of a document's last V tile that lie behind its end
 constexpr int kAQ = 128;   // queries per stream (UMMA M)
-constexpr int kAK = 128;   // keys per tile (UMMA N of S, K of P V)
+constexpr int kAK = 128;   // keys per K or V tile
+constexpr int kStep = 64;  // keys per step (UMMA N of S, K of P V)
 constexpr int kFThreads = 352;
 constexpr int kWarpTma = 8, kWarpMma = 9, kWarpTail = 10;
 constexpr float kRescaleLog2 = 8.f;
@@ -60,13 +69,13 @@ struct FwdSmem {
   static constexpr uint32_t kBytes = 1024 + (2 + kRing) * kTile;
 };
 
-// The two streams of an item: first row, head and number of key tiles (0: unused).
+// The two streams of an item: first row, head and number of key steps (0: unused).
 struct FwdItem {
   int begin, end, prompt;
   int row[2], head[2], n[2];
 };
-__device__ __forceinline__ int key_tiles(const PackedTile& t, int row) {
-  return (min(t.end, max(row + kAQ, t.prompt)) - t.begin + kAK - 1) / kAK;
+__device__ __forceinline__ int key_steps(const PackedTile& t, int row) {
+  return (min(t.end, max(row + kAQ, t.prompt)) - t.begin + kStep - 1) / kStep;
 }
 // Item of this CTA in round k: the items, heaviest first, are dealt forth and back, so
 // that no CTA gets the heavier one every time; -1 behind the last.
@@ -83,7 +92,7 @@ __device__ __forceinline__ FwdItem fwd_item(const PackedIndex& x, int w, int H, 
   it.end = t.end;
   it.prompt = t.prompt;
   it.row[0] = t.row0;
-  it.n[0] = key_tiles(t, t.row0);
+  it.n[0] = key_steps(t, t.row0);
   if (heads) {
     it.head[0] = 2 * (w % per);
     it.head[1] = it.head[0] + 1;
@@ -92,7 +101,7 @@ __device__ __forceinline__ FwdItem fwd_item(const PackedIndex& x, int w, int H, 
   } else {
     it.head[0] = it.head[1] = w % per;
     it.row[1] = t.row0 + kAQ;
-    it.n[1] = it.row[1] < t.end ? key_tiles(t, it.row[1]) : 0;
+    it.n[1] = it.row[1] < t.end ? key_steps(t, it.row[1]) : 0;
   }
   return it;
 }
@@ -108,13 +117,41 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
         "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr));
 }
-// D[tmem] (+)= A[tmem] * B[smem]^T: A holds two 16-bit elements per 32-bit column.
-__device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
-                                          uint32_t idesc, uint32_t accumulate) {
+// The MMA warp runs its loop as a whole, so that the compiler sees uniform values and
+// keeps descriptors in uniform registers; `lead` is nonzero in the one lane that issues.
+// (With the loop inside a one-lane branch each product cost a dozen dependent
+// instructions, and the issuing lane, not the tensor cores, set the pace.)
+__device__ __forceinline__ uint32_t elect_lane() {
+  uint32_t r;
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r;
+}
+// D[tmem] (+)= A[smem] * B[smem]^T
+__device__ __forceinline__ void mma_ss(uint32_t lead, uint32_t d_tmem, uint64_t adesc,
+                                       uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(lead)
+      : "memory");
+}
+// D[tmem] (+)= A[tmem] * B[smem]^T: A holds two 16-bit elements per 32-bit column.
+__device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d_tmem, uint32_t a_tmem,
+                                       uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint32_t lead, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+          bar),
+      "r"(lead)
       : "memory");
 }
 
@@ -150,7 +187,8 @@ __global__ void __launch_bounds__(kFThreads, 1)
   constexpr int DA = SM::DA, NR = SM::kRing;
   extern __shared__ uint8_t attn_raw[];
   __shared__ __align__(8) uint64_t q_full[2], q_free[2], kv_full[NR], kv_free[NR];
-  __shared__ __align__(8) uint64_t s_full[2], p_full[2], o_full[2], o_free[2];
+  __shared__ __align__(8) uint64_t s_full[2][2], p_full[2][2], pv_done[2];
+  __shared__ __align__(8) uint64_t o_full[2], o_free[2];
   __shared__ __align__(8) uint64_t tail_done[NR];
   __shared__ uint32_t tmem_sh;
   __shared__ int abort_sh;
@@ -160,7 +198,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
   uint8_t* Qs = align1024_p(attn_raw);   // [2] Q tiles
   uint8_t* KV = Qs + 2 * SM::kTile;      // ring: K and V tiles in turn
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  constexpr uint32_t kColS = 0, kColO = 2 * kAK;  // TMEM: S at 0 and 128, O at 256 and 384
+  constexpr uint32_t kColS = 0, kColO = 256;  // TMEM: S[stream][buffer] from 0, O at 256 and 384
   const int G = H / Hkv;
   const bool heads = G % 2 == 0;
 
@@ -168,8 +206,11 @@ __global__ void __launch_bounds__(kFThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&q_full[i]), 1);
       mbar_init(smem_u32(&q_free[i]), 1);
-      mbar_init(smem_u32(&s_full[i]), 1);
-      mbar_init(smem_u32(&p_full[i]), 4);
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(smem_u32(&s_full[i][b]), 1);
+        mbar_init(smem_u32(&p_full[i][b]), 4);
+      }
+      mbar_init(smem_u32(&pv_done[i]), 1);
       mbar_init(smem_u32(&o_full[i]), 1);
       mbar_init(smem_u32(&o_free[i]), 4);
     }
@@ -197,6 +238,12 @@ __global__ void __launch_bounds__(kFThreads, 1)
     return mbar_wait_bounded(smem_u32(bar), parity & 1u, abort_flag, dev_err, DEV_ERR_WAIT_GEMM);
   };
 
+  // the same by a whole warp, which leaves it together: a lane that fell behind could
+  // miss a phase
+  auto wait_all = [&](uint64_t* bar, uint32_t parity) -> bool {
+    return __all_sync(0xFFFFFFFFu, wait(bar, parity));
+  };
+
   if (warp == kWarpTma) {
     // ---------------------------------------------------------------- TMA producer
     if (lane == 0) {
@@ -216,7 +263,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
         const FwdItem it = fwd_item(idx, w, H, heads);
         const int g = it.head[0] / G;
         const int kc = (H + g) * D, vc = (H + Hkv + g) * D;
-        const int n = max(it.n[0], it.n[1]);
+        const int n = (max(it.n[0], it.n[1]) + 1) / 2;  // K and V tiles
         ok = load_kv(kc, it.begin) && load_kv(vc, it.begin);
         for (int s = 0; s < 2 && ok; ++s) {
           if (it.n[s] == 0) continue;
@@ -236,69 +283,79 @@ __global__ void __launch_bounds__(kFThreads, 1)
     __syncwarp();
   } else if (warp == kWarpMma) {
     // ---------------------------------------------------------------- MMA issuer
-    if (lane == 0) {
-      const uint32_t idesc_s = umma_idesc_f16(kAQ, kAK);
+    {
+      const uint32_t lead = elect_lane();
+      const uint32_t idesc_s = umma_idesc_f16(kAQ, kStep);
       const uint32_t idesc_o = umma_idesc_f16(kAQ, D) | (1u << 16);  // B (V) MN-major
-      uint32_t c = 0, tails = 0;                       // ring tiles; phase of each slot's tail_done
-      uint32_t nq[2] = {0, 0}, np[2] = {0, 0};         // items, P tiles of each stream
+      uint32_t c = 0, tails = 0;                // ring tiles; phase of each slot's tail_done
+      uint32_t items_of[2] = {0, 0};            // items of each stream
+      uint32_t ns[2][2] = {{0, 0}, {0, 0}};     // steps of each stream and buffer
       bool ok = true;
-      auto issue_s = [&](int s, uint32_t ck) {  // S_s = Q_s K^T with the K tile at ring count ck
-        const uint32_t kt = smem_u32(KV + (ck % NR) * SM::kTile), qt = smem_u32(Qs + s * SM::kTile);
+      auto issue_s = [&](int s, int u, uint32_t ck) {  // step u, its K tile at ring count ck
+        const uint64_t kd = umma_desc_k_sw128(smem_u32(KV + (ck % NR) * SM::kTile) +
+                                              (uint32_t)(u & 1) * kStep * 128u);
+        const uint64_t qd = umma_desc_k_sw128(smem_u32(Qs + s * SM::kTile));
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (uint32_t)((kk >> 2) * 128 * 128 + (kk & 3) * 32);
-          tc_mma_bf16(tmem + kColS + (uint32_t)s * kAK, umma_desc_k_sw128(qt + off),
-                      umma_desc_k_sw128(kt + off), idesc_s, kk > 0 ? 1u : 0u);
+          constexpr uint32_t kAtom = 128 * 128 / 16;
+          const uint32_t off = (uint32_t)(kk >> 2) * kAtom + (uint32_t)(kk & 3) * 2;
+          mma_ss(lead, tmem + kColS + (uint32_t)(s * 128 + (u & 1) * kStep), qd + off, kd + off,
+                 idesc_s, kk > 0 ? 1u : 0u);
         }
-        tc_commit(smem_u32(&s_full[s]));
+        mma_commit(lead, smem_u32(&s_full[s][u & 1]));
       };
       for (int k = 0, w; ok && (w = deal(k, items)) >= 0; ++k) {
         const FwdItem it = fwd_item(idx, w, H, heads);
-        const int n = max(it.n[0], it.n[1]);
+        const int nu = max(it.n[0], it.n[1]), n = (nu + 1) / 2;
         const bool tail = it.begin + n * kAK > it.end;
-        ok = wait(&kv_full[c % NR], c / NR);
+        ok = wait_all(&kv_full[c % NR], c / NR);
         for (int s = 0; s < 2 && ok; ++s) {
           if (it.n[s] == 0) continue;
-          ok = wait(&q_full[s], nq[s]);
+          ok = wait_all(&q_full[s], items_of[s]);
           if (!ok) break;
           tc_fence_after();
-          issue_s(s, c);
-          if (it.n[s] == 1) tc_commit(smem_u32(&q_free[s]));
+          issue_s(s, 0, c);
+          if (it.n[s] > 1) issue_s(s, 1, c);
+          if (it.n[s] <= 2) mma_commit(lead, smem_u32(&q_free[s]));
         }
-        if (ok) tc_commit(smem_u32(&kv_free[c % NR]));
-        for (int j = 0; j < n && ok; ++j) {
-          const uint32_t cv = c + 2 * j + 1, ck = cv + 1;
-          const uint32_t vt = smem_u32(KV + (cv % NR) * SM::kTile);
+        if (ok) mma_commit(lead, smem_u32(&kv_free[c % NR]));
+        for (int u = 0; u < nu && ok; ++u) {
+          const uint32_t cv = c + 2 * (u >> 1) + 1, ck = cv + 1;
+          const uint64_t vd =
+              umma_desc_mn_sw128(smem_u32(KV + (cv % NR) * SM::kTile) +
+                                     (uint32_t)(u & 1) * kStep * 128u,
+                                 (uint32_t)(kAK * 128), 1024u);
+          if ((u & 1) == 0) {
+            ok = wait_all(&kv_full[cv % NR], cv / NR);
+            if (ok && tail && (u >> 1) == n - 1) ok = wait_all(&tail_done[cv % NR], tails >> (cv % NR));
+            if (ok && u + 2 < nu) ok = wait_all(&kv_full[ck % NR], ck / NR);
+          }
           for (int s = 0; s < 2 && ok; ++s) {
-            if (j >= it.n[s]) continue;
-            ok = wait(&kv_full[cv % NR], cv / NR);
-            if (ok && tail && j == n - 1) ok = wait(&tail_done[cv % NR], tails >> (cv % NR));
+            if (u >= it.n[s]) continue;
             // O of the stream's previous item has been read
-            if (ok && j == 0 && nq[s] > 0) ok = wait(&o_free[s], nq[s] - 1);
-            // P_j written (and O rescaled if its reference maximum moved)
-            if (ok) ok = wait(&p_full[s], np[s]);
+            if (u == 0 && items_of[s] > 0) ok = wait_all(&o_free[s], items_of[s] - 1);
+            // P written (and O rescaled if its reference maximum moved)
+            if (ok) ok = wait_all(&p_full[s][u & 1], ns[s][u & 1]);
             if (!ok) break;
-            ++np[s];
+            ++ns[s][u & 1];
             tc_fence_after();
 #pragma unroll
-            for (int kk = 0; kk < kAK / 16; ++kk)
-              tc_mma_ts(tmem + kColO + (uint32_t)s * 128, tmem + kColS + (uint32_t)(s * kAK + kk * 8),
-                        umma_desc_mn_sw128(vt + (uint32_t)kk * 16 * 128, (uint32_t)(kAK * 128), 1024u),
-                        idesc_o, (j > 0 || kk > 0) ? 1u : 0u);
-            if (j + 1 < it.n[s]) {
-              ok = wait(&kv_full[ck % NR], ck / NR);
-              if (!ok) break;
-              tc_fence_after();
-              issue_s(s, ck);  // (its completion also says that this P V has run)
-              if (j + 2 == it.n[s]) tc_commit(smem_u32(&q_free[s]));
-            } else {
-              tc_commit(smem_u32(&o_full[s]));
-              ++nq[s];
+            for (int kk = 0; kk < kStep / 16; ++kk)
+              mma_ts(lead, tmem + kColO + (uint32_t)s * 128,
+                     tmem + kColS + (uint32_t)(s * 128 + (u & 1) * kStep + kk * 8),
+                     vd + (uint32_t)kk * 128u, idesc_o, (u > 0 || kk > 0) ? 1u : 0u);
+            mma_commit(lead, smem_u32(&pv_done[s]));
+            if (u + 2 < it.n[s]) issue_s(s, u + 2, ck);
+            // Q is free behind the stream's last scores
+            if (u + 3 == it.n[s]) mma_commit(lead, smem_u32(&q_free[s]));
+            if (u + 1 == it.n[s]) {
+              mma_commit(lead, smem_u32(&o_full[s]));
+              ++items_of[s];
             }
           }
           if (!ok) break;
-          tc_commit(smem_u32(&kv_free[cv % NR]));
-          if (j + 1 < n) tc_commit(smem_u32(&kv_free[ck % NR]));
+          if ((u & 1) || u + 1 == nu) mma_commit(lead, smem_u32(&kv_free[cv % NR]));
+          if (u + 2 < nu && ((u & 1) || u + 3 == nu)) mma_commit(lead, smem_u32(&kv_free[ck % NR]));
         }
         if (tail) tails ^= 1u << ((c + 2 * n - 1) % NR);
         c += 2 * n;
@@ -312,10 +369,10 @@ __global__ void __launch_bounds__(kFThreads, 1)
     bool ok = true;
     for (int k = 0, w; ok && (w = deal(k, items)) >= 0; ++k) {
       const FwdItem it = fwd_item(idx, w, H, heads);
-      const int n = max(it.n[0], it.n[1]);
+      const int n = (max(it.n[0], it.n[1]) + 1) / 2;
       for (int i = 0; i < 2 * n && ok; ++i, ++c) {
         const uint32_t slot = c % NR;
-        ok = __all_sync(0xFFFFFFFFu, wait(&kv_full[slot], c / NR));
+        ok = wait_all(&kv_full[slot], c / NR);
         if (ok && i == 2 * n - 1 && it.begin + n * kAK > it.end) {
           // V rows behind the document belong to another one or to the padding:
           // cleared, since 0 * inf would reach this document's rows
@@ -332,8 +389,8 @@ __global__ void __launch_bounds__(kFThreads, 1)
     const int s = warp >> 2;
     const int r = (warp & 3) * 32 + lane;  // query row of the stream = TMEM lane
     const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t ts = trow + kColS + (uint32_t)s * kAK, to = trow + kColO + (uint32_t)s * 128;
-    uint32_t ns = 0, no = 0;  // S tiles and items of this stream
+    const uint32_t to = trow + kColO + (uint32_t)s * 128;
+    uint32_t ns[2] = {0, 0}, nv = 0, no = 0;  // steps of each buffer, P V products, items
     bool ok = true;
     for (int k = 0, w; ok && (w = deal(k, items)) >= 0; ++k) {
       const FwdItem it = fwd_item(idx, w, H, heads);
@@ -343,32 +400,34 @@ __global__ void __launch_bounds__(kFThreads, 1)
       const int kmax = min(max(q, it.prompt - 1), it.end - 1);  // the row's last key
       const int kall = min(max(it.row[s] + (warp & 3) * 32, it.prompt - 1), it.end - 1);
       float m_ref = -INFINITY, l_run = 0.f;
-      for (int j = 0; j < n && ok; ++j) {
-        ok = __all_sync(0xFFFFFFFFu, wait(&s_full[s], ns));
+#pragma unroll 2
+      for (int u = 0; u < n; ++u) {
+        const uint32_t ts = trow + kColS + (uint32_t)(s * 128 + (u & 1) * kStep);
+        ok = wait_all(&s_full[s][u & 1], ns[u & 1]);
         if (!ok) break;
-        ++ns;
+        ++ns[u & 1];
         tc_fence_after();
-        uint32_t sv[kAK];
-#pragma unroll
-        for (int c = 0; c < kAK / 32; ++c) tmem_ld32(ts + 32 * c, sv + 32 * c);
+        uint32_t sv[kStep];
+        tmem_ld32(ts, sv);
+        tmem_ld32(ts + 32, sv + 32);
         tmem_ld_wait();
-        const int k0 = it.begin + j * kAK;
-        if (k0 + kAK - 1 > kall) {  // (uniform in the warp)
+        const int k0 = it.begin + u * kStep;
+        if (k0 + kStep - 1 > kall) {  // (uniform in the warp)
           const int last = kmax - k0;
 #pragma unroll
-          for (int e = 0; e < kAK; ++e)
+          for (int e = 0; e < kStep; ++e)
             if (e > last) sv[e] = 0xFF800000u;  // -inf
         }
         float mt = -INFINITY, mt1 = -INFINITY;
 #pragma unroll
-        for (int e = 0; e < kAK; e += 4) {
+        for (int e = 0; e < kStep; e += 4) {
           mt = fmaxf(fmaxf(mt, __uint_as_float(sv[e])), __uint_as_float(sv[e + 1]));
           mt1 = fmaxf(fmaxf(mt1, __uint_as_float(sv[e + 2])), __uint_as_float(sv[e + 3]));
         }
         mt = fmaxf(mt, mt1) * sl2;
         float corr = 1.f;
         bool moved = false;
-        if (j == 0) {
+        if (u == 0) {
           m_ref = mt;  // (finite for finite scores: every row sees its document's first key)
         } else if (mt > m_ref + kRescaleLog2) {
           corr = exp2f(m_ref - mt);
@@ -377,6 +436,11 @@ __global__ void __launch_bounds__(kFThreads, 1)
           moved = true;
         }
         if (__any_sync(0xFFFFFFFFu, moved)) {
+          // the product before this step has written O (the one before that has, since
+          // this step's scores were computed behind it)
+          ok = wait_all(&pv_done[s], nv + u - 1);
+          if (!ok) break;
+          tc_fence_after();
 #pragma unroll 1
           for (int c = 0; c < D / 16; ++c) {
             uint32_t v[16];
@@ -392,12 +456,12 @@ __global__ void __launch_bounds__(kFThreads, 1)
         const float nm = -m_ref;
         float rs0 = 0.f, rs1 = 0.f;
 #pragma unroll
-        for (int c = 0; c < kAK / 32; ++c) {
+        for (int c = 0; c < kStep / 32; ++c) {
           uint32_t pk[16];
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
-            const float p0 = exp2f(fmaf(__uint_as_float(sv[32 * c + e]), sl2, nm));
-            const float p1 = exp2f(fmaf(__uint_as_float(sv[32 * c + e + 1]), sl2, nm));
+            const float p0 = ex2(fmaf(__uint_as_float(sv[32 * c + e]), sl2, nm));
+            const float p1 = ex2(fmaf(__uint_as_float(sv[32 * c + e + 1]), sl2, nm));
             rs0 += p0;
             rs1 += p1;
             pk[e >> 1] = pack_f16x2(p0, p1);
@@ -408,12 +472,15 @@ __global__ void __launch_bounds__(kFThreads, 1)
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&p_full[s]));
+        if (lane == 0) mbar_arrive(smem_u32(&p_full[s][u & 1]));
       }
       // -------------------------------------------------------------- epilogue
-      ok = ok && __all_sync(0xFFFFFFFFu, wait(&o_full[s], no));
+      // (a barrier of its own: pv_done may be two phases on, where a wait for the
+      // phase before the last would not return)
+      ok = ok && wait_all(&o_full[s], no);
       if (!ok) break;
       ++no;
+      nv += n;
       tc_fence_after();
       const float inv = 1.f / l_run;
       const bool live = q < it.end;
@@ -781,7 +848,7 @@ __global__ void __launch_bounds__(kBThreads, 1)
           const float dp = __uint_as_float(pv[(e + u) >> 4][(e + u) & 15]);
           const float l2 = __shfl_sync(0xFFFFFFFFu, l2_own, e + u);
           const float dl = __shfl_sync(0xFFFFFFFFu, dl_own, e + u);
-          p[u] = live ? exp2f(fmaf(s, sl2, -l2)) : 0.f;
+          p[u] = live ? ex2(fmaf(s, sl2, -l2)) : 0.f;
           d[u] = live ? p[u] * (dp - dl) : 0.f;
         }
         ppk[e >> 1] = pack_f16x2(p[0], p[1]);
@@ -1035,7 +1102,7 @@ __global__ void __launch_bounds__(kBThreads, 1)
           const bool live = key <= kmax;
           const float s = __uint_as_float(sv[(e + u) >> 4][(e + u) & 15]);
           const float dp = __uint_as_float(pv[(e + u) >> 4][(e + u) & 15]);
-          const float p = live ? exp2f(fmaf(s, sl2, -l2)) : 0.f;
+          const float p = live ? ex2(fmaf(s, sl2, -l2)) : 0.f;
           d[u] = live ? p * (dp - dl) : 0.f;
         }
         dpk[e >> 1] = pack_f16x2(d[0], d[1]);

@@ -362,3 +362,38 @@ def test_attention_of_many_short_documents(L):
     idx = _index(L, lengths, None, T)
     r = _run(L, qkv.cuda(), dout.cuda(), idx, H, Hkv)
     _check(qkv, dout, op.documents(lengths), H, Hkv, *r)
+
+
+@pytest.mark.parametrize("prefix", [False, True])
+def test_attention_of_a_long_row(L, prefix):
+    """Many items of many steps a CTA: against plain torch in fp32, document by document."""
+    import torch
+    rng = np.random.default_rng(1)
+    H, Hkv, d, lengths = 16, 2, 128, []
+    while sum(lengths) < 9000:
+        lengths.append(int(np.exp(rng.uniform(np.log(32), np.log(2048)))))
+    T = sum(lengths) + 100
+    pre = [int(rng.integers(0, n + 1)) for n in lengths] if prefix else None
+    qkv, dout = (x.cuda() for x in _inputs(T, H, Hkv, d, 4))
+    idx = _index(L, lengths, pre, T)
+    o, lse, dqkv = _run(L, qkv, dout, idx, H, Hkv)
+    # error of a row of n terms against its largest value: roundings of 2^-11 (p) and
+    # 2^-8 (bf16) relative to sums that are never larger than ~sqrt(n) times the result
+    for k, (s, e, pe) in enumerate(op.documents(lengths, pre)):
+        x = qkv[s:e].float().view(e - s, H + 2 * Hkv, d).permute(1, 0, 2)
+        q, kk, v = x[:H], x[H:H + Hkv].repeat_interleave(8, 0), x[H + Hkv:].repeat_interleave(8, 0)
+        at = torch.arange(e - s, device="cuda")
+        see = (at[None] <= at[:, None]) | (at[None] < pe - s)
+        sc = (q @ kk.transpose(1, 2) / d ** 0.5).masked_fill(~see, -float("inf"))
+        p = sc.softmax(-1)
+        ro = p @ v
+        do = dout[s:e].float().view(e - s, H, d).permute(1, 0, 2)
+        ds = p * (do @ v.transpose(1, 2) - (do * ro).sum(-1, keepdim=True)) / d ** 0.5
+        dq, dk = ds @ kk, (ds.transpose(1, 2) @ q).view(Hkv, 8, e - s, d).sum(1)
+        dv = (p.transpose(1, 2) @ do).view(Hkv, 8, e - s, d).sum(1)
+        ref = torch.cat([dq, dk, dv]).permute(1, 0, 2).reshape(e - s, -1)
+        assert (lse[:, s:e] - sc.logsumexp(-1)).abs().max() <= 1e-4, k
+        for got, want, tol in ((o[s:e].float(), ro.permute(1, 0, 2).reshape(e - s, -1), 2.0 ** -9),
+                               (dqkv[s:e].float(), ref, 2.0 ** -7)):
+            assert (got - want).norm() <= tol * want.norm(), k
+            assert (got - want).abs().max() <= 4 * tol * want.abs().max(), k
