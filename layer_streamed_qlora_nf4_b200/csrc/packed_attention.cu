@@ -52,13 +52,15 @@ __device__ __forceinline__ float ex2(float x) {
 // reference, and P stays below 2^8, well inside fp16.
 //   warps 0-3, 4-7: softmax and epilogue of streams 0 and 1, a query row per thread
 //   warp 8 : TMA producer (Q of each stream; a ring of K and V tiles)
-//   warp 9 : TMEM allocation and the MMA issuer (lane 0)
-//   warp 10: clears the rows of a document's last V tile that lie behind its end
+//   warps 9, 10: the MMA issuers of streams 0 and 1 (warp 9 also allocates TMEM); one
+//            warp for both left the tensor cores idle for the 300 to 800 cycles that its
+//            waits took between the products of one stream and the other's
+//   warp 11: clears the rows of a document's last V tile that lie behind its end
 constexpr int kAQ = 128;   // queries per stream (UMMA M)
 constexpr int kAK = 128;   // keys per K or V tile
 constexpr int kStep = 64;  // keys per step (UMMA N of S, K of P V)
-constexpr int kFThreads = 352;
-constexpr int kWarpTma = 8, kWarpMma = 9, kWarpTail = 10;
+constexpr int kFThreads = 384;
+constexpr int kWarpTma = 8, kWarpMma = 9, kWarpTail = 11;
 constexpr float kRescaleLog2 = 8.f;
 
 template <int D>
@@ -69,12 +71,9 @@ struct FwdSmem {
   static constexpr uint32_t kBytes = 1024 + (2 + kRing) * kTile;
 };
 
-// The two streams of an item: first row, head and number of key steps (0: unused).
-struct FwdItem {
-  int begin, end, prompt;
-  int row[2], head[2], n[2];
-};
+// Key steps of the rows [row, row + 128) of a tile's document (0: no such rows).
 __device__ __forceinline__ int key_steps(const PackedTile& t, int row) {
+  if (row >= t.end) return 0;
   return (min(t.end, max(row + kAQ, t.prompt)) - t.begin + kStep - 1) / kStep;
 }
 // Item of this CTA in round k: the items, heaviest first, are dealt forth and back, so
@@ -84,25 +83,23 @@ __device__ __forceinline__ int deal(int k, int items) {
                 ((k & 1) ? (int)(gridDim.x - 1 - blockIdx.x) : (int)blockIdx.x);
   return w < items ? w : -1;
 }
-__device__ __forceinline__ FwdItem fwd_item(const PackedIndex& x, int w, int H, bool heads) {
+// An item as stream s sees it: its first row, head and number of steps (0: none), and
+// the steps of the longer stream.
+struct FwdItem {
+  int begin, end, prompt;
+  int row, head, n, nu;
+};
+__device__ __forceinline__ FwdItem fwd_item(const PackedIndex& x, int w, int H, bool heads, int s) {
   FwdItem it;
   const int per = heads ? H / 2 : H;
   const PackedTile t = heads ? x.tiles[w / per] : x.tiles2[w / per];
   it.begin = t.begin;
   it.end = t.end;
   it.prompt = t.prompt;
-  it.row[0] = t.row0;
-  it.n[0] = key_steps(t, t.row0);
-  if (heads) {
-    it.head[0] = 2 * (w % per);
-    it.head[1] = it.head[0] + 1;
-    it.row[1] = t.row0;
-    it.n[1] = it.n[0];
-  } else {
-    it.head[0] = it.head[1] = w % per;
-    it.row[1] = t.row0 + kAQ;
-    it.n[1] = it.row[1] < t.end ? key_steps(t, it.row[1]) : 0;
-  }
+  it.head = heads ? 2 * (w % per) + s : w % per;
+  it.row = heads ? t.row0 : t.row0 + s * kAQ;
+  it.n = key_steps(t, it.row);
+  it.nu = heads ? it.n : max(key_steps(t, t.row0), key_steps(t, t.row0 + kAQ));
   return it;
 }
 
@@ -216,7 +213,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
     }
     for (int i = 0; i < NR; ++i) {
       mbar_init(smem_u32(&kv_full[i]), 1);
-      mbar_init(smem_u32(&kv_free[i]), 2);  // the products and the tail warp
+      mbar_init(smem_u32(&kv_free[i]), 3);  // the two streams' products and the tail warp
       mbar_init(smem_u32(&tail_done[i]), 1);
     }
     abort_sh = 0;
@@ -260,116 +257,109 @@ __global__ void __launch_bounds__(kFThreads, 1)
         return true;
       };
       for (int k = 0, w; ok && (w = deal(k, items)) >= 0; ++k) {
-        const FwdItem it = fwd_item(idx, w, H, heads);
-        const int g = it.head[0] / G;
+        const FwdItem it = fwd_item(idx, w, H, heads, 0), it1 = fwd_item(idx, w, H, heads, 1);
+        const int g = it.head / G;
         const int kc = (H + g) * D, vc = (H + Hkv + g) * D;
-        const int n = (max(it.n[0], it.n[1]) + 1) / 2;  // K and V tiles
+        const int n = (it.nu + 1) / 2;  // K and V tiles
         ok = load_kv(kc, it.begin) && load_kv(vc, it.begin);
-        for (int s = 0; s < 2 && ok; ++s) {
-          if (it.n[s] == 0) continue;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          if (!ok || (s == 1 && it1.n == 0)) continue;
           if (nq[s] > 0) ok = wait(&q_free[s], nq[s] - 1);
-          if (!ok) break;
+          if (!ok) continue;
           ++nq[s];
           const uint32_t fb = smem_u32(&q_full[s]);
           mbar_arrive_expect_tx(fb, SM::kTile);
           for (int a = 0; a < DA; ++a)
             tma_load_2d(smem_u32(Qs + s * SM::kTile + a * kAQ * 128), &tm_qkv, fb,
-                        it.head[s] * D + 64 * a, it.row[s]);
+                        (s ? it1.head : it.head) * D + 64 * a, s ? it1.row : it.row);
         }
         for (int j = 1; j < n && ok; ++j)
           ok = load_kv(kc, it.begin + j * kAK) && load_kv(vc, it.begin + j * kAK);
       }
     }
     __syncwarp();
-  } else if (warp == kWarpMma) {
-    // ---------------------------------------------------------------- MMA issuer
-    {
-      const uint32_t lead = elect_lane();
-      const uint32_t idesc_s = umma_idesc_f16(kAQ, kStep);
-      const uint32_t idesc_o = umma_idesc_f16(kAQ, D) | (1u << 16);  // B (V) MN-major
-      uint32_t c = 0, tails = 0;                // ring tiles; phase of each slot's tail_done
-      uint32_t items_of[2] = {0, 0};            // items of each stream
-      uint32_t ns[2][2] = {{0, 0}, {0, 0}};     // steps of each stream and buffer
-      bool ok = true;
-      auto issue_s = [&](int s, int u, uint32_t ck) {  // step u, its K tile at ring count ck
-        const uint64_t kd = umma_desc_k_sw128(smem_u32(KV + (ck % NR) * SM::kTile) +
-                                              (uint32_t)(u & 1) * kStep * 128u);
-        const uint64_t qd = umma_desc_k_sw128(smem_u32(Qs + s * SM::kTile));
+  } else if (warp == kWarpMma || warp == kWarpMma + 1) {
+    // ---------------------------------------------------------------- MMA issuers
+    const int s = warp - kWarpMma;
+    const uint32_t lead = elect_lane();
+    const uint32_t idesc_s = umma_idesc_f16(kAQ, kStep);
+    const uint32_t idesc_o = umma_idesc_f16(kAQ, D) | (1u << 16);  // B (V) MN-major
+    const uint32_t ts = tmem + kColS + (uint32_t)s * 128, to = tmem + kColO + (uint32_t)s * 128;
+    const uint64_t qd = umma_desc_k_sw128(smem_u32(Qs + s * SM::kTile));
+    uint32_t c = 0, tails = 0;     // ring tiles; phase of each slot's tail_done
+    uint32_t ni = 0;               // items of this stream
+    uint32_t ns[2] = {0, 0};       // steps of each buffer
+    bool ok = true;
+    auto issue_s = [&](int b, uint32_t ck) {  // buffer b = the half of the K tile at ring count ck
+      const uint64_t kd = umma_desc_k_sw128(smem_u32(KV + (ck % NR) * SM::kTile) +
+                                            (uint32_t)b * kStep * 128u);
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          constexpr uint32_t kAtom = 128 * 128 / 16;
-          const uint32_t off = (uint32_t)(kk >> 2) * kAtom + (uint32_t)(kk & 3) * 2;
-          mma_ss(lead, tmem + kColS + (uint32_t)(s * 128 + (u & 1) * kStep), qd + off, kd + off,
-                 idesc_s, kk > 0 ? 1u : 0u);
-        }
-        mma_commit(lead, smem_u32(&s_full[s][u & 1]));
-      };
-      for (int k = 0, w; ok && (w = deal(k, items)) >= 0; ++k) {
-        const FwdItem it = fwd_item(idx, w, H, heads);
-        const int nu = max(it.n[0], it.n[1]), n = (nu + 1) / 2;
-        const bool tail = it.begin + n * kAK > it.end;
-        ok = wait_all(&kv_full[c % NR], c / NR);
-        for (int s = 0; s < 2 && ok; ++s) {
-          if (it.n[s] == 0) continue;
-          ok = wait_all(&q_full[s], items_of[s]);
-          if (!ok) break;
-          tc_fence_after();
-          issue_s(s, 0, c);
-          if (it.n[s] > 1) issue_s(s, 1, c);
-          if (it.n[s] <= 2) mma_commit(lead, smem_u32(&q_free[s]));
-        }
-        if (ok) mma_commit(lead, smem_u32(&kv_free[c % NR]));
-        for (int u = 0; u < nu && ok; ++u) {
-          const uint32_t cv = c + 2 * (u >> 1) + 1, ck = cv + 1;
-          const uint64_t vd =
-              umma_desc_mn_sw128(smem_u32(KV + (cv % NR) * SM::kTile) +
-                                     (uint32_t)(u & 1) * kStep * 128u,
-                                 (uint32_t)(kAK * 128), 1024u);
-          if ((u & 1) == 0) {
-            ok = wait_all(&kv_full[cv % NR], cv / NR);
-            if (ok && tail && (u >> 1) == n - 1) ok = wait_all(&tail_done[cv % NR], tails >> (cv % NR));
-            if (ok && u + 2 < nu) ok = wait_all(&kv_full[ck % NR], ck / NR);
-          }
-          for (int s = 0; s < 2 && ok; ++s) {
-            if (u >= it.n[s]) continue;
-            // O of the stream's previous item has been read
-            if (u == 0 && items_of[s] > 0) ok = wait_all(&o_free[s], items_of[s] - 1);
-            // P written (and O rescaled if its reference maximum moved)
-            if (ok) ok = wait_all(&p_full[s][u & 1], ns[s][u & 1]);
-            if (!ok) break;
-            ++ns[s][u & 1];
-            tc_fence_after();
-#pragma unroll
-            for (int kk = 0; kk < kStep / 16; ++kk)
-              mma_ts(lead, tmem + kColO + (uint32_t)s * 128,
-                     tmem + kColS + (uint32_t)(s * 128 + (u & 1) * kStep + kk * 8),
-                     vd + (uint32_t)kk * 128u, idesc_o, (u > 0 || kk > 0) ? 1u : 0u);
-            mma_commit(lead, smem_u32(&pv_done[s]));
-            if (u + 2 < it.n[s]) issue_s(s, u + 2, ck);
-            // Q is free behind the stream's last scores
-            if (u + 3 == it.n[s]) mma_commit(lead, smem_u32(&q_free[s]));
-            if (u + 1 == it.n[s]) {
-              mma_commit(lead, smem_u32(&o_full[s]));
-              ++items_of[s];
-            }
-          }
-          if (!ok) break;
-          if ((u & 1) || u + 1 == nu) mma_commit(lead, smem_u32(&kv_free[cv % NR]));
-          if (u + 2 < nu && ((u & 1) || u + 3 == nu)) mma_commit(lead, smem_u32(&kv_free[ck % NR]));
-        }
-        if (tail) tails ^= 1u << ((c + 2 * n - 1) % NR);
-        c += 2 * n;
+      for (int kk = 0; kk < D / 16; ++kk) {
+        constexpr uint32_t kAtom = 128 * 128 / 16;
+        const uint32_t off = (uint32_t)(kk >> 2) * kAtom + (uint32_t)(kk & 3) * 2;
+        mma_ss(lead, ts + (uint32_t)(b * kStep), qd + off, kd + off, idesc_s, kk > 0 ? 1u : 0u);
       }
+      mma_commit(lead, smem_u32(&s_full[s][b]));
+    };
+    for (int k = 0, w; ok && (w = deal(k, items)) >= 0; ++k) {
+      const FwdItem it = fwd_item(idx, w, H, heads, s);
+      const int n = (it.nu + 1) / 2;
+      const bool tail = it.begin + n * kAK > it.end;
+      ok = wait_all(&kv_full[c % NR], c / NR);
+      if (ok && it.n > 0) {
+        ok = wait_all(&q_full[s], ni);
+        if (!ok) break;
+        tc_fence_after();
+        issue_s(0, c);
+        if (it.n > 1) issue_s(1, c);
+        if (it.n <= 2) mma_commit(lead, smem_u32(&q_free[s]));
+        // O of the stream's previous item has been read
+        if (ni > 0) ok = wait_all(&o_free[s], ni - 1);
+        ++ni;
+      }
+      if (ok) mma_commit(lead, smem_u32(&kv_free[c % NR]));
+      for (int j = 0; j < n && ok; ++j) {
+        const uint32_t cv = c + 2 * j + 1, ck = cv + 1;
+        const uint64_t vd = umma_desc_mn_sw128(smem_u32(KV + (cv % NR) * SM::kTile),
+                                               (uint32_t)(kAK * 128), 1024u);
+        ok = wait_all(&kv_full[cv % NR], cv / NR);
+        if (ok && tail && j == n - 1) ok = wait_all(&tail_done[cv % NR], tails >> (cv % NR));
+        if (ok && j + 1 < n) ok = wait_all(&kv_full[ck % NR], ck / NR);
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          const int u = 2 * j + b;
+          if (!ok || u >= it.n) continue;
+          // P written (and O rescaled if its reference maximum moved)
+          ok = wait_all(&p_full[s][b], ns[b]);
+          if (!ok) continue;
+          ++ns[b];
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < kStep / 16; ++kk)
+            mma_ts(lead, to, ts + (uint32_t)(b * kStep + kk * 8),
+                   vd + (uint32_t)((b * kStep + kk * 16) * 128 / 16), idesc_o,
+                   (u > 0 || kk > 0) ? 1u : 0u);
+          mma_commit(lead, smem_u32(&pv_done[s]));
+          if (u + 2 < it.n) issue_s(b, ck);
+          if (u + 3 == it.n) mma_commit(lead, smem_u32(&q_free[s]));  // the last scores
+          if (u + 1 == it.n) mma_commit(lead, smem_u32(&o_full[s]));
+        }
+        if (!ok) break;
+        mma_commit(lead, smem_u32(&kv_free[cv % NR]));
+        if (j + 1 < n) mma_commit(lead, smem_u32(&kv_free[ck % NR]));
+      }
+      if (tail) tails ^= 1u << ((c + 2 * n - 1) % NR);
+      c += 2 * n;
     }
-    __syncwarp();
   } else if (warp == kWarpTail) {
     // It follows every tile of the ring (so that it never falls a phase behind) and
     // gives each slot free again together with the products.
     uint32_t c = 0;
     bool ok = true;
     for (int k = 0, w; ok && (w = deal(k, items)) >= 0; ++k) {
-      const FwdItem it = fwd_item(idx, w, H, heads);
-      const int n = (max(it.n[0], it.n[1]) + 1) / 2;
+      const FwdItem it = fwd_item(idx, w, H, heads, 0);
+      const int n = (it.nu + 1) / 2;
       for (int i = 0; i < 2 * n && ok; ++i, ++c) {
         const uint32_t slot = c % NR;
         ok = wait_all(&kv_full[slot], c / NR);
@@ -393,12 +383,12 @@ __global__ void __launch_bounds__(kFThreads, 1)
     uint32_t ns[2] = {0, 0}, nv = 0, no = 0;  // steps of each buffer, P V products, items
     bool ok = true;
     for (int k = 0, w; ok && (w = deal(k, items)) >= 0; ++k) {
-      const FwdItem it = fwd_item(idx, w, H, heads);
-      const int n = it.n[s];
+      const FwdItem it = fwd_item(idx, w, H, heads, s);
+      const int n = it.n;
       if (n == 0) continue;
-      const int q = it.row[s] + r;
+      const int q = it.row + r;
       const int kmax = min(max(q, it.prompt - 1), it.end - 1);  // the row's last key
-      const int kall = min(max(it.row[s] + (warp & 3) * 32, it.prompt - 1), it.end - 1);
+      const int kall = min(max(it.row + (warp & 3) * 32, it.prompt - 1), it.end - 1);
       float m_ref = -INFINITY, l_run = 0.f;
 #pragma unroll 2
       for (int u = 0; u < n; ++u) {
@@ -484,7 +474,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
       tc_fence_after();
       const float inv = 1.f / l_run;
       const bool live = q < it.end;
-      uint16_t* orow = out + (int64_t)q * H * D + (int64_t)it.head[s] * D;
+      uint16_t* orow = out + (int64_t)q * H * D + (int64_t)it.head * D;
       uint32_t ov[D];
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) tmem_ld32(to + 32 * c, ov + 32 * c);
@@ -502,7 +492,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
                                __uint_as_float(ov[8 * c + 2 * e + 1]) * inv);
           *reinterpret_cast<uint4*>(orow + 8 * c) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
         }
-        lse_out[(int64_t)it.head[s] * T + q] = (m_ref + log2f(l_run)) * 0.69314718055994531f;
+        lse_out[(int64_t)it.head * T + q] = (m_ref + log2f(l_run)) * 0.69314718055994531f;
       }
     }
   }
