@@ -27,6 +27,8 @@ namespace lsq {
 
 namespace {
 
+constexpr float kLog2e = 1.4426950408889634f;
+
 __device__ __forceinline__ uint8_t* align1024_p(uint8_t* p) {
   return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023));
 }
@@ -509,176 +511,238 @@ __global__ void __launch_bounds__(kFThreads, 1)
 }
 
 // ------------------------------------------------------------------ backward
-constexpr int kBThreads = 320;
-constexpr int kBC = 64;  // columns of a chunk (queries for dK/dV, keys for dQ)
+// Two kernels recompute the probabilities, p = exp2(s c - lse log2 e), and form
+// ds = p (dp - delta) with delta = rowsum(dO o O): one owns the keys (dK, dV), one the
+// queries (dQ), so that no sum is shared between CTAs and none depends on their order.
+// Both are persistent, go through the other side in chunks of 64, keep P and dS in TMEM
+// as fp16 A operands over the columns they come from, and split the issuing of products
+// between two warps.
+//   warps 0-3, 4-7: the gradient warps (a TMEM lane per thread)
+//   warp 8 : TMA producer;  warps 9, 10: MMA issuers (warp 9 also allocates TMEM)
+//   warp 11: clears rows behind a document's end, and (dK, dV) stages the queries' values
+// The prepared values of a query and head: dO' = 2^e dO in fp16 with a norm in [8, 16),
+// e, delta' = 2^e delta and l = lse log2 e + e.
+constexpr int kBC = 64;        // columns of a chunk (queries for dK/dV, keys for dQ)
+constexpr int kWindow = 64;    // tokens of a window of the exponents' minima
 
-// Clears rows [rows, all) of two tiles that share a barrier (one warp) once their load has
-// landed, and arrives on `done`; whole tiles only arrive.
-template <int D>
-__device__ __forceinline__ void zero_tail2(uint8_t* a, uint8_t* b, int rows, int all, uint32_t bar,
-                                           uint32_t parity, int lane, uint32_t done,
-                                           volatile int* abort_flag, int* dev_err) {
-  if (rows < all) {
-    bool ok = mbar_wait_bounded(bar, parity, abort_flag, dev_err, DEV_ERR_WAIT_GEMM);
-    ok = __all_sync(0xFFFFFFFFu, ok);
-    if (ok)
-      for (int k = 0; k < D / 64; ++k)
-        for (uint32_t o = (uint32_t)rows * 128u + (uint32_t)lane * 16u; o < (uint32_t)all * 128u;
-             o += 512u) {
-          *reinterpret_cast<uint4*>(a + (uint32_t)k * all * 128u + o) = make_uint4(0u, 0u, 0u, 0u);
-          *reinterpret_cast<uint4*>(b + (uint32_t)k * all * 128u + o) = make_uint4(0u, 0u, 0u, 0u);
-        }
-    fence_proxy_async_smem();
-  }
-  __syncwarp();
-  if (lane == 0) mbar_arrive(done);
+__device__ __forceinline__ float warp_min(float x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x = fminf(x, __shfl_xor_sync(0xFFFFFFFFu, x, o));
+  return x;
 }
 
-// One warp per token and query head: dO' = fp16(2^e dO) with e such that the row's norm
-// is in [8, 16), delta' = 2^e rowsum(dO o O), and e.  A zero row takes e = 127 (it must
-// not lower the least exponent of a tile); a row that is not finite e = 0, and its
-// gradients come out not finite.  Warps T H .. check the norms of the v rows.
+// One CTA per window of 64 tokens and head (a warp per token, eight tokens each), or,
+// for blockIdx.y >= H, the norms of the v rows of kv head blockIdx.y - H.  A zero row
+// takes e = 127 (it must not lower the least exponent of a tile); a row that is not
+// finite takes e = 0, and its gradients come out not finite.
 template <int D>
 __global__ void __launch_bounds__(256)
     packed_attn_prep_kernel(const uint16_t* __restrict__ qkv, const uint16_t* __restrict__ o,
-                            const uint16_t* __restrict__ dout, const int* __restrict__ head,
-                            int64_t T, int H, int Hkv, uint16_t* __restrict__ dos,
-                            float* __restrict__ delta, float* __restrict__ rowexp, int* dev_err) {
+                            const uint16_t* __restrict__ dout, const float* __restrict__ lse,
+                            const int* __restrict__ head, int64_t T, int H, int Hkv,
+                            uint16_t* __restrict__ dos, float2* __restrict__ stats,
+                            float* __restrict__ rowexp, float* __restrict__ winexp, int* dev_err) {
   constexpr int E = D / 32;  // elements per lane
+  __shared__ float low[8];
   pdl_trigger();
   pdl_wait();
-  const int64_t w = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-  const int lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int h = blockIdx.y;
   const int64_t live = head[2];
-  if (w >= T * H) {
-    const int64_t t = (w - T * H) / Hkv;
-    if (t >= live) return;
-    const uint16_t* v = qkv + t * (int64_t)(H + 2 * Hkv) * D +
-                        (int64_t)(H + Hkv + (w - T * H) % Hkv) * D + lane * E;
-    float n = 0.f;
+  const int64_t t0 = (int64_t)blockIdx.x * kWindow + warp * (kWindow / 8);
+  if (h >= H) {
+    bool big = false;
+    for (int64_t t = t0; t < min(live, t0 + kWindow / 8); ++t) {
+      const uint16_t* v = qkv + t * (int64_t)(H + 2 * Hkv) * D + (int64_t)(Hkv + h) * D + lane * E;
+      float n = 0.f;
 #pragma unroll
-    for (int i = 0; i < E; i += 2) {
-      const float2 x = unpack_f16x2(*reinterpret_cast<const uint32_t*>(v + i));
-      n += x.x * x.x + x.y * x.y;
+      for (int i = 0; i < E; i += 2) {
+        const float2 x = unpack_f16x2(*reinterpret_cast<const uint32_t*>(v + i));
+        n += x.x * x.x + x.y * x.y;
+      }
+#pragma unroll
+      for (int k = 16; k > 0; k >>= 1) n += __shfl_xor_sync(0xFFFFFFFFu, n, k);
+      big |= !(n <= 2047.f * 2047.f);
     }
-#pragma unroll
-    for (int k = 16; k > 0; k >>= 1) n += __shfl_xor_sync(0xFFFFFFFFu, n, k);
-    if (lane == 0 && !(n <= 2047.f * 2047.f)) atomicOr(dev_err, DEV_ERR_NONFINITE);
+    if (big && lane == 0) atomicOr(dev_err, DEV_ERR_NONFINITE);
     return;
   }
-  const int64_t t = w / H;
-  const int h = (int)(w % H);
-  const int64_t at = w * D + lane * E;
-  float g[E];
-  float n = 0.f, dl = 0.f;
+  float emin = 127.f;
+#pragma unroll 4
+  for (int i = 0; i < kWindow / 8; ++i) {
+    const int64_t t = t0 + i;
+    if (t >= T) break;
+    const int64_t at = (t * H + h) * D + lane * E;
+    uint32_t gr[E / 2], orow[E / 2];
+    if (E == 4) {
+      const uint2 a = *reinterpret_cast<const uint2*>(dout + at);
+      const uint2 b = *reinterpret_cast<const uint2*>(o + at);
+      gr[0] = a.x; gr[E / 2 - 1] = a.y;
+      orow[0] = b.x; orow[E / 2 - 1] = b.y;
+    } else {
+      gr[0] = *reinterpret_cast<const uint32_t*>(dout + at);
+      orow[0] = *reinterpret_cast<const uint32_t*>(o + at);
+    }
+    float g[E], n = 0.f;
+    bool bad = false;
 #pragma unroll
-  for (int i = 0; i < E; i += 2) {
-    const float2 x = unpack_bf16x2(*reinterpret_cast<const uint32_t*>(dout + at + i));
-    const float2 y = unpack_f16x2(*reinterpret_cast<const uint32_t*>(o + at + i));
-    g[i] = t < live ? x.x : 0.f;
-    g[i + 1] = t < live ? x.y : 0.f;
-    dl += g[i] * y.x + g[i + 1] * y.y;
-    n = fmaxf(n, fmaxf(fabsf(g[i]), fabsf(g[i + 1])));
-    if (!(fabsf(g[i]) <= 3.4e38f && fabsf(g[i + 1]) <= 3.4e38f)) n = INFINITY;
-  }
+    for (int k = 0; k < E; k += 2) {
+      const float2 x = unpack_bf16x2(gr[k / 2]);
+      g[k] = t < live ? x.x : 0.f;
+      g[k + 1] = t < live ? x.y : 0.f;
+      n = fmaxf(n, fmaxf(fabsf(g[k]), fabsf(g[k + 1])));
+      bad |= !(fabsf(g[k]) <= 3.4e38f) || !(fabsf(g[k + 1]) <= 3.4e38f);
+    }
+    n = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(n)));
+    bad = __any_sync(0xFFFFFFFFu, bad);
+    // the norm from values near 1, so that its squares neither overflow nor vanish
+    int e = n == 0.f ? 127 : 0;
+    if (n > 0.f && !bad) {
+      const int x = max(1, (int)(__float_as_uint(n) >> 23)) - 126;  // n < 2^x
+      const float s = ldexpf(1.f, -x);
+      float sq = 0.f;
 #pragma unroll
-  for (int k = 16; k > 0; k >>= 1) {
-    dl += __shfl_xor_sync(0xFFFFFFFFu, dl, k);
-    n = fmaxf(n, __shfl_xor_sync(0xFFFFFFFFu, n, k));
-  }
-  // the norm from values near 1, so that its squares neither overflow nor vanish
-  int e = 0;
-  if (n > 0.f && n <= 3.4e38f) {
-    int x;
-    frexpf(n, &x);
-    float s = 0.f;
+      for (int k = 0; k < E; ++k) sq += (g[k] * s) * (g[k] * s);
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-      const float y = ldexpf(g[i], -x);
-      s += y * y;
+      for (int k = 16; k > 0; k >>= 1) sq += __shfl_xor_sync(0xFFFFFFFFu, sq, k);
+      const int z = (int)(__float_as_uint(sqrtf(sq)) >> 23) - 126;  // the norm is below 2^(x + z)
+      e = min(127, 4 - x - z);
+    }
+    const float up = ldexpf(1.f, e);
+    float dl = 0.f;
+    uint32_t p[E / 2];
+#pragma unroll
+    for (int k = 0; k < E; k += 2) {
+      const float2 y = unpack_f16x2(orow[k / 2]);
+      g[k] *= up;
+      g[k + 1] *= up;
+      dl += g[k] * y.x + g[k + 1] * y.y;
+      p[k / 2] = pack_f16x2(g[k], g[k + 1]);
     }
 #pragma unroll
-    for (int k = 16; k > 0; k >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, k);
-    int z;
-    frexpf(sqrtf(s), &z);  // the norm is in [2^(x + z - 1), 2^(x + z))
-    e = 4 - x - z;
-  } else if (n == 0.f) {
-    e = 127;
+    for (int k = 16; k > 0; k >>= 1) dl += __shfl_xor_sync(0xFFFFFFFFu, dl, k);
+    if (E == 4)
+      *reinterpret_cast<uint2*>(dos + at) = make_uint2(p[0], p[E / 2 - 1]);
+    else
+      *reinterpret_cast<uint32_t*>(dos + at) = p[0];
+    if (lane == 0) {
+      const int64_t r = (int64_t)h * T + t;
+      stats[r] = t < live ? make_float2(fmaf(lse[r], kLog2e, (float)e), dl) : make_float2(0.f, 0.f);
+      rowexp[r] = (float)e;
+    }
+    emin = fminf(emin, (float)e);
   }
-  e = min(e, 127);
-  uint32_t p[E / 2];
-#pragma unroll
-  for (int i = 0; i < E; i += 2) p[i / 2] = pack_f16x2(ldexpf(g[i], e), ldexpf(g[i + 1], e));
-  if (E == 4)
-    *reinterpret_cast<uint2*>(dos + at) = make_uint2(p[0], p[E / 2 - 1]);
-  else
-    *reinterpret_cast<uint32_t*>(dos + at) = p[0];
-  if (lane == 0) {
-    delta[(int64_t)h * T + t] = t < live ? ldexpf(dl, e) : 0.f;
-    rowexp[(int64_t)h * T + t] = (float)e;
+  if (lane == 0) low[warp] = emin;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int i = 1; i < 8; ++i) emin = fminf(emin, low[i]);
+    winexp[(int64_t)h * gridDim.x + blockIdx.x] = emin;
   }
 }
 
+// Two consecutive fp32 rows' halves to bf16 and out: v[0, D) of one row, scaled, with cs
+// (nullable) the rotation by the row's position undone in the pairs (i, i + D/2).
 template <int D>
-struct PaDkvSmem {
-  static constexpr uint32_t kKV = kAK * D * 2;   // K (fp16) or V (bf16): 128 keys
-  static constexpr uint32_t kQc = kBC * D * 2;   // a chunk of Q or dO: 64 queries
-  static constexpr uint32_t kPc = kAK * kBC * 2; // P^T or dS^T: 128 keys x 64 queries
-  static constexpr uint32_t kBytes = 1024 + 2 * kKV + 4 * kQc + 2 * kPc;
+__device__ __forceinline__ void store_grad_row(const uint32_t (&raw)[D], float scale,
+                                               const float2* cs, uint16_t* out) {
+#pragma unroll
+  for (int c = 0; c < D / 16; ++c) {
+    float a[8], b[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      a[e] = __uint_as_float(raw[8 * c + e]) * scale;
+      b[e] = __uint_as_float(raw[D / 2 + 8 * c + e]) * scale;
+    }
+    if (cs) {
+#pragma unroll
+      for (int e = 0; e < 8; e += 2) {
+        const float4 f = __ldg(reinterpret_cast<const float4*>(cs + 8 * c + e));
+        const float x0 = a[e], y0 = b[e], x1 = a[e + 1], y1 = b[e + 1];
+        a[e] = x0 * f.x + y0 * f.y;
+        b[e] = y0 * f.x - x0 * f.y;
+        a[e + 1] = x1 * f.z + y1 * f.w;
+        b[e + 1] = y1 * f.z - x1 * f.w;
+      }
+    }
+    *reinterpret_cast<uint4*>(out + 8 * c) =
+        make_uint4(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]), pack_bf16x2(a[4], a[5]),
+                   pack_bf16x2(a[6], a[7]));
+    *reinterpret_cast<uint4*>(out + D / 2 + 8 * c) =
+        make_uint4(pack_bf16x2(b[0], b[1]), pack_bf16x2(b[2], b[3]), pack_bf16x2(b[4], b[5]),
+                   pack_bf16x2(b[6], b[7]));
+  }
+}
+
+// ------------------------------------------------------------------ dK, dV
+// An item: 128 keys of a document, a kv head and `nh` of its query heads.  For each of
+// those heads the chunks of 64 queries that see some of the keys go by; chunk c is the
+// gradient warps' set c % 2, so that one set's arithmetic runs while the products of the
+// other's chunk do:
+//   warp 9 : S^T = K Q^T, dP'^T = V dO'^T          (buffers c % 2, 64 columns each)
+//   sets   : P' = exp2(S^T c - l + emin) -> TMEM;  dS' = P' (dP' - delta') -> TMEM
+//   warp 10: dV' += P' dO', dK' += dS' Q           (in order, so the sums are fixed)
+// emin is the least exponent of the item's queries: P' = 2^(emin - e) P <= 1, so all
+// products carry the same factor 2^emin, taken out at the end.  With all heads of the
+// group in one item (nh = G) the sums are the gradients, written in bf16; otherwise
+// fp32 parts are left for the kernel below.
+template <int D>
+struct DkvSmem {
+  static constexpr uint32_t kTile = 128 * D * 2;  // K or V
+  static constexpr uint32_t kQc = kBC * D * 2;    // a chunk of Q or dO'
+  static constexpr int kRing = D == 128 ? 4 : 6;  // chunks in flight
+  static constexpr uint32_t kBytes = 1024 + 2 * kTile + 2 * kRing * kQc + kRing * kBC * 8;
 };
 
-// dK, dV of 128 keys for one query head: loops over the 64-query chunks at and
-// after the key block (causal), accumulating dV += P^T dO and dK += dS^T Q in
-// TMEM; writes dk = scale dK and dv per query head.
 template <int D>
-__global__ void __launch_bounds__(kBThreads, 1)
+__global__ void __launch_bounds__(kFThreads, 1)
     packed_attn_dkdv_kernel(const __grid_constant__ CUtensorMap tm_kv,   // qkv, boxes of 128 rows
                             const __grid_constant__ CUtensorMap tm_q,    // qkv, boxes of 64 rows
                             const __grid_constant__ CUtensorMap tm_do,   // dO', boxes of 64 rows
-                            PackedIndex idx, const float* __restrict__ lse,
-                            const float* __restrict__ delta, const float* __restrict__ rowexp,
-                            int64_t T, int H, int Hkv, float sl2, float scale,
-                            float* __restrict__ dk, float* __restrict__ dv, int* __restrict__ dev_err) {
-  using SM = PaDkvSmem<D>;
-  constexpr int DA = D / 64;
+                            PackedIndex idx, const float2* __restrict__ stats,
+                            const float* __restrict__ rowexp, const float* __restrict__ winexp,
+                            int64_t T, int H, int Hkv, int nh, float sl2, float scale,
+                            const float2* __restrict__ cs, uint16_t* __restrict__ dqkv,
+                            float* __restrict__ dk, float* __restrict__ dv,
+                            int* __restrict__ dev_err) {
+  using SM = DkvSmem<D>;
+  constexpr int DA = D / 64, NR = SM::kRing, kItems = 8;
+  static_assert(NR % 2 == 0 && kItems > NR, "a ring slot always serves the same set of warps");
   extern __shared__ uint8_t dkv_raw[];
-  __shared__ __align__(8) uint64_t bar_kv, bar_tail, bar_q[2], bar_qfree[2], bar_sdp[2],
-      bar_tfree[2], bar_ds, bar_pds;
+  __shared__ __align__(8) uint64_t kv_full, kv_free, r_full[NR], r_free[NR], st_full[NR];
+  __shared__ __align__(8) uint64_t s_full[2], dp_full[2], p_full[2], ds_full[2], s_free[2], dp_free[2];
+  __shared__ __align__(8) uint64_t acc_full, acc_free;
+  __shared__ float emin_sh[kItems];
   __shared__ uint32_t tmem_sh;
   __shared__ int abort_sh;
   volatile int* abort_flag = &abort_sh;
   pdl_trigger();
 
   uint8_t* Ks = align1024_p(dkv_raw);
-  uint8_t* Vs = Ks + SM::kKV;
-  uint8_t* Qb = Vs + SM::kKV;       // [2] Q chunks (fp16, then bf16)
-  uint8_t* dOb = Qb + 2 * SM::kQc;  // [2] dO chunks (bf16)
-  uint8_t* Pt = dOb + 2 * SM::kQc;  // P^T (bf16, K-major over queries)
-  uint8_t* dSt = Pt + SM::kPc;      // dS^T
+  uint8_t* Vs = Ks + SM::kTile;
+  uint8_t* Qb = Vs + SM::kTile;             // [NR] chunks of Q
+  uint8_t* dOb = Qb + NR * SM::kQc;         // [NR] chunks of dO'
+  float2* st = reinterpret_cast<float2*>(dOb + NR * SM::kQc);  // [NR][64] (emin - l, delta')
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int h = blockIdx.y;
-  const int g = h / (H / Hkv);
-  pdl_wait();
-  if ((int)blockIdx.x >= idx.head[0]) return;
-  const PackedTile tile = idx.tiles[blockIdx.x];
-  const int k0 = tile.row0;
-  // the queries that see some of these keys: from the first key on, or, where the
-  // tile reaches into the prompt, the whole document
-  const int qs = k0 < tile.prompt ? tile.begin : k0;
-  const int nc = (tile.end - qs + kBC - 1) / kBC;
   constexpr uint32_t kColS = 0, kColP = 2 * kBC, kColV = 4 * kBC, kColK = 4 * kBC + 128;
 
   if (threadIdx.x == 0) {
-    mbar_init(smem_u32(&bar_kv), 1);
-    mbar_init(smem_u32(&bar_tail), 1);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&bar_q[i]), 1);
-      mbar_init(smem_u32(&bar_qfree[i]), 1);
-      mbar_init(smem_u32(&bar_sdp[i]), 1);
-      mbar_init(smem_u32(&bar_tfree[i]), 8);
+    mbar_init(smem_u32(&kv_full), 1);
+    mbar_init(smem_u32(&kv_free), 1);
+    for (int i = 0; i < NR; ++i) {
+      mbar_init(smem_u32(&r_full[i]), 1);
+      mbar_init(smem_u32(&r_free[i]), 1);
+      mbar_init(smem_u32(&st_full[i]), 1);
     }
-    mbar_init(smem_u32(&bar_ds), 8);
-    mbar_init(smem_u32(&bar_pds), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&s_full[i]), 1);
+      mbar_init(smem_u32(&dp_full[i]), 1);
+      mbar_init(smem_u32(&p_full[i]), 4);
+      mbar_init(smem_u32(&ds_full[i]), 4);
+      mbar_init(smem_u32(&s_free[i]), 1);
+      mbar_init(smem_u32(&dp_free[i]), 1);
+    }
+    mbar_init(smem_u32(&acc_full), 1);
+    mbar_init(smem_u32(&acc_free), 8);
     abort_sh = 0;
     fence_mbar_init();
     fence_proxy_async_smem();
@@ -691,206 +755,297 @@ __global__ void __launch_bounds__(kBThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_sh;
+  pdl_wait();
+  const int G = H / Hkv, parts = G / nh;
+  const int per = Hkv * parts;              // items of a tile
+  const int items = idx.head[0] * per;
+  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+    return mbar_wait_bounded(smem_u32(bar), parity & 1u, abort_flag, dev_err, DEV_ERR_WAIT_GEMM);
+  };
+  auto wait_all = [&](uint64_t* bar, uint32_t parity) -> bool {
+    return __all_sync(0xFFFFFFFFu, wait(bar, parity));
+  };
+  // an item's tile, first query head, first query and chunks of a head
+  struct Item {
+    PackedTile t;
+    int g, h0, qs, nc;
+  };
+  auto item = [&](int w) {
+    Item it;
+    it.t = idx.ktiles[w / per];
+    it.g = (w % per) / parts;
+    it.h0 = it.g * G + (w % per) % parts * nh;
+    // the queries that see some of these keys: from the first key on, or, where the
+    // tile reaches into the prompt, the whole document
+    it.qs = it.t.row0 < it.t.prompt ? it.t.begin : it.t.row0;
+    it.nc = (it.t.end - it.qs + kBC - 1) / kBC;
+    return it;
+  };
 
   if (warp == kWarpTma) {
     if (lane == 0) {
-      mbar_arrive_expect_tx(smem_u32(&bar_kv), 2 * SM::kKV);
-      for (int a = 0; a < DA; ++a) {
-        tma_load_2d(smem_u32(Ks + a * kAK * 128), &tm_kv, smem_u32(&bar_kv), (H + g) * D + 64 * a,
-                    k0);
-        tma_load_2d(smem_u32(Vs + a * kAK * 128), &tm_kv, smem_u32(&bar_kv),
-                    (H + Hkv + g) * D + 64 * a, k0);
-      }
-      for (int c = 0; c < nc; ++c) {
-        const int qb = c & 1;
-        if (c >= 2 && !mbar_wait_bounded(smem_u32(&bar_qfree[qb]), (uint32_t)(((c - 2) >> 1) & 1),
-                                         abort_flag, dev_err, DEV_ERR_WAIT_GEMM))
-          break;
-        const int row = qs + c * kBC;
-        const uint32_t fb = smem_u32(&bar_q[qb]);
-        mbar_arrive_expect_tx(fb, 2 * SM::kQc);
+      uint32_t c = 0, ni = 0;
+      bool ok = true;
+      for (int k = 0, w; ok && (w = deal(k, items)) >= 0; ++k) {
+        const Item it = item(w);
+        if (ni > 0) ok = wait(&kv_free, ni - 1);
+        if (!ok) break;
+        ++ni;
+        mbar_arrive_expect_tx(smem_u32(&kv_full), 2 * SM::kTile);
         for (int a = 0; a < DA; ++a) {
-          tma_load_2d(smem_u32(Qb + qb * SM::kQc + a * kBC * 128), &tm_q, fb, h * D + 64 * a, row);
-          tma_load_2d(smem_u32(dOb + qb * SM::kQc + a * kBC * 128), &tm_do, fb, h * D + 64 * a, row);
+          tma_load_2d(smem_u32(Ks + a * 128 * 128), &tm_kv, smem_u32(&kv_full),
+                      (H + it.g) * D + 64 * a, it.t.row0);
+          tma_load_2d(smem_u32(Vs + a * 128 * 128), &tm_kv, smem_u32(&kv_full),
+                      (H + Hkv + it.g) * D + 64 * a, it.t.row0);
         }
+        for (int hh = 0; hh < nh && ok; ++hh)
+          for (int j = 0; j < it.nc; ++j, ++c) {
+            const uint32_t slot = c % NR;
+            if (c >= NR) ok = wait(&r_free[slot], c / NR - 1);
+            if (!ok) break;
+            const uint32_t fb = smem_u32(&r_full[slot]);
+            mbar_arrive_expect_tx(fb, 2 * SM::kQc);
+            for (int a = 0; a < DA; ++a) {
+              tma_load_2d(smem_u32(Qb + slot * SM::kQc + a * kBC * 128), &tm_q, fb,
+                          (it.h0 + hh) * D + 64 * a, it.qs + j * kBC);
+              tma_load_2d(smem_u32(dOb + slot * SM::kQc + a * kBC * 128), &tm_do, fb,
+                          (it.h0 + hh) * D + 64 * a, it.qs + j * kBC);
+            }
+          }
       }
     }
     __syncwarp();
-    // rows of the last chunk behind the document are cleared: their P and dS are 0,
-    // and 0 * inf would reach this document's gradients
-    const int lb = (nc - 1) & 1;
-    zero_tail2<D>(Qb + lb * SM::kQc, dOb + lb * SM::kQc, tile.end - qs - (nc - 1) * kBC, kBC,
-                  smem_u32(&bar_q[lb]), (uint32_t)(((nc - 1) >> 1) & 1), lane, smem_u32(&bar_tail),
-                  abort_flag, dev_err);
   } else if (warp == kWarpMma) {
-    if (lane == 0) {
-      const uint32_t id_s = umma_idesc_f16(kAK, kBC);            // S^T = K Q^T (fp16)
-      const uint32_t id_dp = id_s;                                // dP'^T = V dO'^T
-      const uint32_t id_acc = umma_idesc_f16(kAK, D) | (1u << 16);  // dV, dK: B MN-major
-      bool ok = mbar_wait_bounded(smem_u32(&bar_kv), 0u, abort_flag, dev_err, DEV_ERR_WAIT_GEMM);
-      auto issue_sdp = [&](int c) -> bool {
-        const int qb = c & 1;
-        if (!mbar_wait_bounded(smem_u32(&bar_q[qb]), (uint32_t)((c >> 1) & 1), abort_flag, dev_err,
-                               DEV_ERR_WAIT_GEMM))
-          return false;
-        if (c >= 2 && !mbar_wait_bounded(smem_u32(&bar_tfree[qb]), (uint32_t)(((c - 2) >> 1) & 1),
-                                         abort_flag, dev_err, DEV_ERR_WAIT_GEMM))
-          return false;
-        // (the last chunk's tail is cleared before any product reads it)
-        if (c == nc - 1 && !mbar_wait_bounded(smem_u32(&bar_tail), 0u, abort_flag, dev_err,
-                                              DEV_ERR_WAIT_GEMM))
-          return false;
-        tc_fence_after();
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t ka = (uint32_t)((kk >> 2) * kAK * 128 + (kk & 3) * 32);
-          const uint32_t kq = (uint32_t)((kk >> 2) * kBC * 128 + (kk & 3) * 32);
-          tc_mma_bf16(tmem + kColS + (uint32_t)qb * kBC, umma_desc_k_sw128(smem_u32(Ks) + ka),
-                      umma_desc_k_sw128(smem_u32(Qb + qb * SM::kQc) + kq), id_s, kk > 0 ? 1u : 0u);
-          tc_mma_bf16(tmem + kColP + (uint32_t)qb * kBC, umma_desc_k_sw128(smem_u32(Vs) + ka),
-                      umma_desc_k_sw128(smem_u32(dOb + qb * SM::kQc) + kq), id_dp, kk > 0 ? 1u : 0u);
-        }
-        tc_commit(smem_u32(&bar_sdp[qb]));
-        return true;
-      };
-      ok = ok && issue_sdp(0);
-      for (int c = 0; c < nc && ok; ++c) {
-        const int qb = c & 1;
-        if (c + 1 < nc) ok = issue_sdp(c + 1);
-        if (!ok) break;
-        ok = mbar_wait_bounded(smem_u32(&bar_ds), (uint32_t)(c & 1), abort_flag, dev_err,
-                               DEV_ERR_WAIT_GEMM);
+    // ---------------------------------------------------------------- S^T and dP'^T
+    const uint32_t lead = elect_lane();
+    const uint32_t id = umma_idesc_f16(128, kBC);
+    const uint64_t kd = umma_desc_k_sw128(smem_u32(Ks)), vd = umma_desc_k_sw128(smem_u32(Vs));
+    uint32_t c = 0, ni = 0;
+    bool ok = true;
+    for (int k = 0, w; ok && (w = deal(k, items)) >= 0; ++k) {
+      const Item it = item(w);
+      ok = wait_all(&kv_full, ni);
+      ++ni;
+      const int n = nh * it.nc;
+      for (int j = 0; j < n && ok; ++j, ++c) {
+        const uint32_t slot = c % NR, b = c & 1;
+        const uint64_t qd = umma_desc_k_sw128(smem_u32(Qb + slot * SM::kQc));
+        const uint64_t dd = umma_desc_k_sw128(smem_u32(dOb + slot * SM::kQc));
+        ok = wait_all(&r_full[slot], c / NR);
+        // dV of the chunk before the last has read the P in this buffer
+        if (ok && c >= 2) ok = wait_all(&s_free[b], c / 2 - 1);
         if (!ok) break;
         tc_fence_after();
 #pragma unroll
-        for (int kk = 0; kk < kBC / 16; ++kk) {
-          const uint32_t pa = (uint32_t)(kk * 32);
-          const uint32_t bo = (uint32_t)kk * 16 * 128;
-          const uint32_t acc = (c > 0 || kk > 0) ? 1u : 0u;
-          tc_mma_bf16(tmem + kColV, umma_desc_k_sw128(smem_u32(Pt) + pa),
-                      umma_desc_mn_sw128(smem_u32(dOb + qb * SM::kQc) + bo, kBC * 128, 1024u), id_acc,
-                      acc);
-          tc_mma_bf16(tmem + kColK, umma_desc_k_sw128(smem_u32(dSt) + pa),
-                      umma_desc_mn_sw128(smem_u32(Qb + qb * SM::kQc) + bo, kBC * 128, 1024u), id_acc,
-                      acc);
+        for (int kk = 0; kk < D / 16; ++kk)
+          mma_ss(lead, tmem + kColS + b * kBC,
+                 kd + (uint32_t)((kk >> 2) * (128 * 128 / 16) + (kk & 3) * 2),
+                 qd + (uint32_t)((kk >> 2) * (kBC * 128 / 16) + (kk & 3) * 2), id, kk > 0 ? 1u : 0u);
+        mma_commit(lead, smem_u32(&s_full[b]));
+        if (c >= 2) ok = wait_all(&dp_free[b], c / 2 - 1);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          mma_ss(lead, tmem + kColP + b * kBC,
+                 vd + (uint32_t)((kk >> 2) * (128 * 128 / 16) + (kk & 3) * 2),
+                 dd + (uint32_t)((kk >> 2) * (kBC * 128 / 16) + (kk & 3) * 2), id, kk > 0 ? 1u : 0u);
+        mma_commit(lead, smem_u32(&dp_full[b]));
+      }
+      if (ok) mma_commit(lead, smem_u32(&kv_free));
+    }
+  } else if (warp == kWarpMma + 1) {
+    // ---------------------------------------------------------------- dV' and dK'
+    const uint32_t lead = elect_lane();
+    const uint32_t id = umma_idesc_f16(128, D) | (1u << 16);  // B MN-major
+    uint32_t c = 0, ni = 0;
+    bool ok = true;
+    for (int k = 0, w; ok && (w = deal(k, items)) >= 0; ++k) {
+      const Item it = item(w);
+      if (ni > 0) ok = wait_all(&acc_free, ni - 1);
+      ++ni;
+      const int n = nh * it.nc;
+      for (int j = 0; j < n && ok; ++j, ++c) {
+        const uint32_t slot = c % NR, b = c & 1;
+        const uint64_t qd = umma_desc_mn_sw128(smem_u32(Qb + slot * SM::kQc), kBC * 128, 1024u);
+        const uint64_t dd = umma_desc_mn_sw128(smem_u32(dOb + slot * SM::kQc), kBC * 128, 1024u);
+        ok = wait_all(&p_full[b], c / 2);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < kBC / 16; ++kk)
+          mma_ts(lead, tmem + kColV, tmem + kColS + b * kBC + kk * 8, dd + (uint32_t)(kk * 128), id,
+                 (j > 0 || kk > 0) ? 1u : 0u);
+        mma_commit(lead, smem_u32(&s_free[b]));
+        ok = wait_all(&ds_full[b], c / 2);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < kBC / 16; ++kk)
+          mma_ts(lead, tmem + kColK, tmem + kColP + b * kBC + kk * 8, qd + (uint32_t)(kk * 128), id,
+                 (j > 0 || kk > 0) ? 1u : 0u);
+        mma_commit(lead, smem_u32(&dp_free[b]));
+        mma_commit(lead, smem_u32(&r_free[slot]));
+      }
+      if (ok) mma_commit(lead, smem_u32(&acc_full));
+    }
+  } else if (warp == kWarpTail) {
+    // ---------------------------------------------------------------- the queries' values
+    uint32_t c = 0, ni = 0;
+    bool ok = true;
+    const int64_t nw = (T + kWindow - 1) / kWindow;
+    for (int k = 0, w; ok && (w = deal(k, items)) >= 0; ++k, ++ni) {
+      const Item it = item(w);
+      // the least exponent: whole windows by their minima, the edges token by token (a
+      // window that reaches into another document must not count)
+      float emin = 127.f;
+      const int w0 = (it.qs + kWindow - 1) / kWindow, w1 = it.t.end / kWindow;
+      for (int hh = 0; hh < nh; ++hh) {
+        const float* we = winexp + (int64_t)(it.h0 + hh) * nw;
+        const float* re = rowexp + (int64_t)(it.h0 + hh) * T;
+        for (int i = w0 + lane; i < w1; i += 32) emin = fminf(emin, __ldg(we + i));
+        const int e0 = w0 < w1 ? w0 * kWindow : it.t.end;  // [qs, e0) and [w1 .., end)
+        for (int q = it.qs + lane; q < e0; q += 32) emin = fminf(emin, __ldg(re + q));
+        if (w0 < w1)
+          for (int q = w1 * kWindow + lane; q < it.t.end; q += 32) emin = fminf(emin, __ldg(re + q));
+      }
+      emin = warp_min(emin);
+      if (lane == 0) emin_sh[ni % kItems] = emin;
+      for (int hh = 0; hh < nh && ok; ++hh) {
+        const float2* sh = stats + (int64_t)(it.h0 + hh) * T;
+        for (int j = 0; j < it.nc; ++j, ++c) {
+          const uint32_t slot = c % NR;
+          const int q0 = it.qs + j * kBC;
+          float2 v[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int q = q0 + lane + 32 * i;
+            v[i] = q < it.t.end ? __ldg(sh + q) : make_float2(INFINITY, 0.f);
+            v[i].x = emin - v[i].x;
+          }
+          ok = wait_all(&r_full[slot], c / NR);
+          if (!ok) break;
+          st[slot * kBC + lane] = v[0];
+          st[slot * kBC + 32 + lane] = v[1];
+          if (q0 + kBC > it.t.end) {
+            // queries behind the document: their P and dS are 0, and so must the rows be
+            // that those multiply (0 * inf)
+            zero_rows<D>(Qb + slot * SM::kQc, it.t.end - q0, kBC, lane);
+            zero_rows<D>(dOb + slot * SM::kQc, it.t.end - q0, kBC, lane);
+            fence_proxy_async_smem();
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&st_full[slot]));
         }
-        tc_commit(smem_u32(&bar_pds));       // P^T, dS^T read; dK, dV updated
-        tc_commit(smem_u32(&bar_qfree[qb]));  // the Q and dO chunk read
       }
     }
-    __syncwarp();
   } else {
     // ---------------------------------------------------------------- gradient warps
-    const int r = (warp & 3) * 32 + lane;      // key row of the block = TMEM lane
-    const int hf = warp >> 2;                  // queries 32 hf .. of each chunk
-    const int kpos = k0 + r;
-    // the queries that see this key
-    const int qlo = kpos < tile.prompt ? tile.begin : kpos;
-    const int qhi = kpos < tile.end ? tile.end : 0;
+    const uint32_t b = warp >> 2;              // set: chunks c with c % 2 == b
+    const int r = (warp & 3) * 32 + lane;      // key of the tile = TMEM lane
     const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const float* lse_h = lse + (int64_t)h * T;
-    const float* delta_h = delta + (int64_t)h * T;
-    const float* exp_h = rowexp + (int64_t)h * T;
-    // the least of the queries' exponents: P is scaled by 2^(emin - e) <= 1, so that
-    // the products with dO' = 2^e dO all carry the factor 2^emin
-    float emin = INFINITY;
-    for (int q = qs + lane; q < tile.end; q += 32) emin = fminf(emin, __ldg(exp_h + q));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) emin = fminf(emin, __shfl_xor_sync(0xFFFFFFFFu, emin, o));
+    uint32_t c = 0, ni = 0;
     bool ok = true;
-    // lse (log2 units, with the scale) and delta of the warp's 32 queries of a chunk:
-    // lane i holds query i's, fetched one chunk ahead, and the lanes read them by shuffle
-    auto fetch = [&](int c, float* l2v, float* dlv) {
-      const int qq = min(qs + c * kBC + 32 * hf + lane, tile.end - 1);
-      *l2v = __ldg(lse_h + qq) * 1.4426950408889634f + (__ldg(exp_h + qq) - emin);
-      *dlv = __ldg(delta_h + qq);
-    };
-    float l2_own = 0.f, dl_own = 0.f;
-    fetch(0, &l2_own, &dl_own);
-    for (int c = 0; c < nc && ok; ++c) {
-      const int qb = c & 1;
-      const int q0 = qs + c * kBC + 32 * hf;  // this thread's first query
-      float l2_next = 0.f, dl_next = 0.f;
-      if (c + 1 < nc) fetch(c + 1, &l2_next, &dl_next);
-      ok = mbar_wait_bounded(smem_u32(&bar_sdp[qb]), (uint32_t)((c >> 1) & 1), abort_flag, dev_err,
-                             DEV_ERR_WAIT_GEMM);
-      ok = __all_sync(0xFFFFFFFFu, ok);
+    for (int k = 0, w; ok && (w = deal(k, items)) >= 0; ++k) {
+      const Item it = item(w);
+      const int kpos = it.t.row0 + r;
+      // the queries [qlo, end) see this key; all of the warp's keys from qall on
+      const int qlo = kpos < it.t.prompt ? it.t.begin : kpos;
+      const int klast = it.t.row0 + (warp & 3) * 32 + 31;
+      const int qall = klast < it.t.prompt ? it.t.begin : klast;
+      const int n = nh * it.nc;
+      for (int j = 0; j < n; ++j, ++c) {
+        if ((c & 1) != b) continue;
+        const uint32_t slot = c % NR, ph = c / 2;
+        const int q0 = it.qs + (j % it.nc) * kBC;
+        const float4* sv4 = reinterpret_cast<const float4*>(st + slot * kBC);
+        ok = wait_all(&st_full[slot], c / NR) && wait_all(&s_full[b], ph);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t p[kBC];
+        tmem_ld32(trow + kColS + b * kBC, p);
+        tmem_ld32(trow + kColS + b * kBC + 32, p + 32);
+        tmem_ld_wait();
+        const bool whole = q0 >= qall && q0 + kBC <= it.t.end;  // (uniform in the warp)
+#pragma unroll
+        for (int e = 0; e < kBC; e += 2) {
+          const float4 v = sv4[e / 2];
+          p[e] = __float_as_uint(ex2(fmaf(__uint_as_float(p[e]), sl2, v.x)));
+          p[e + 1] = __float_as_uint(ex2(fmaf(__uint_as_float(p[e + 1]), sl2, v.z)));
+        }
+        if (!whole) {
+          const int lo = qlo - q0, hi = it.t.end - q0;
+#pragma unroll
+          for (int e = 0; e < kBC; ++e)
+            if (e < lo || e >= hi) p[e] = 0u;
+        }
+#pragma unroll
+        for (int e = 0; e < kBC; e += 32) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            pk[i] = pack_f16x2(__uint_as_float(p[e + 2 * i]), __uint_as_float(p[e + 2 * i + 1]));
+          tmem_st16(trow + kColS + b * kBC + e / 2, pk);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&p_full[b]));
+        ok = wait_all(&dp_full[b], ph);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t dsk[kBC / 2];
+#pragma unroll
+        for (int e = 0; e < kBC; e += 32) {
+          uint32_t d[32];
+          tmem_ld32(trow + kColP + b * kBC + e, d);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            const float4 v = sv4[(e + i) / 2];
+            float x = __uint_as_float(p[e + i]) * (__uint_as_float(d[i]) - v.y);
+            float y = __uint_as_float(p[e + i + 1]) * (__uint_as_float(d[i + 1]) - v.w);
+            if (!whole) {  // (dp behind the document may be anything)
+              x = p[e + i] ? x : 0.f;
+              y = p[e + i + 1] ? y : 0.f;
+            }
+            dsk[(e + i) / 2] = pack_f16x2(x, y);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < kBC / 2; e += 16)
+          tmem_st16(trow + kColP + b * kBC + e, *reinterpret_cast<uint32_t(*)[16]>(dsk + e));
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ds_full[b]));
+      }
+      // -------------------------------------------------------------- epilogue: set 0
+      // takes dV, set 1 dK
+      ok = ok && wait_all(&acc_full, ni);
       if (!ok) break;
       tc_fence_after();
-      uint32_t sv[2][16], pv[2][16];
-      tmem_ld16(trow + kColS + (uint32_t)(qb * kBC + 32 * hf), sv[0]);
-      tmem_ld16(trow + kColS + (uint32_t)(qb * kBC + 32 * hf + 16), sv[1]);
-      tmem_ld16(trow + kColP + (uint32_t)(qb * kBC + 32 * hf), pv[0]);
-      tmem_ld16(trow + kColP + (uint32_t)(qb * kBC + 32 * hf + 16), pv[1]);
+      uint32_t acc[D];
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) tmem_ld32(trow + (b ? kColK : kColV) + 32 * i, acc + 32 * i);
       tmem_ld_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&bar_tfree[qb]));
-      uint32_t ppk[16], dpk[16];
+      if (lane == 0) mbar_arrive(smem_u32(&acc_free));
+      const float f = ex2(-emin_sh[ni % kItems]) * (b ? scale : 1.f);
+      ++ni;
+      if (kpos < it.t.end) {
+        if (parts == 1) {
+          const int col = (b ? H + it.g : H + Hkv + it.g) * D;
+          store_grad_row<D>(acc, f, b && cs ? cs + (int64_t)idx.pos[kpos] * (D / 2) : nullptr,
+                            dqkv + (int64_t)kpos * (H + 2 * Hkv) * D + col);
+        } else {
+          float* out = (b ? dk : dv) + ((int64_t)kpos * Hkv * parts + it.h0 / nh) * D;
 #pragma unroll
-      for (int e = 0; e < 32; e += 2) {
-        float p[2], d[2];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int qq = q0 + e + u;
-          const bool live = qlo <= qq && qq < qhi;
-          const float s = __uint_as_float(sv[(e + u) >> 4][(e + u) & 15]);
-          const float dp = __uint_as_float(pv[(e + u) >> 4][(e + u) & 15]);
-          const float l2 = __shfl_sync(0xFFFFFFFFu, l2_own, e + u);
-          const float dl = __shfl_sync(0xFFFFFFFFu, dl_own, e + u);
-          p[u] = live ? ex2(fmaf(s, sl2, -l2)) : 0.f;
-          d[u] = live ? p[u] * (dp - dl) : 0.f;
-        }
-        ppk[e >> 1] = pack_f16x2(p[0], p[1]);
-        dpk[e >> 1] = pack_f16x2(d[0], d[1]);
-      }
-      // the previous chunk's dV, dK products have read P^T and dS^T
-      if (c > 0) {
-        ok = mbar_wait_bounded(smem_u32(&bar_pds), (uint32_t)((c - 1) & 1), abort_flag, dev_err,
-                               DEV_ERR_WAIT_GEMM);
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        if (!ok) break;
-      }
-#pragma unroll
-      for (int cc = 0; cc < 4; ++cc) {
-        const uint32_t off = sw128_offset((uint32_t)r, (uint32_t)(hf * 4 + cc));
-        *reinterpret_cast<uint4*>(Pt + off) =
-            make_uint4(ppk[4 * cc], ppk[4 * cc + 1], ppk[4 * cc + 2], ppk[4 * cc + 3]);
-        *reinterpret_cast<uint4*>(dSt + off) =
-            make_uint4(dpk[4 * cc], dpk[4 * cc + 1], dpk[4 * cc + 2], dpk[4 * cc + 3]);
-      }
-      fence_proxy_async_smem();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&bar_ds));
-      l2_own = l2_next;
-      dl_own = dl_next;
-    }
-    // ---------------------------------------------------------------- epilogue
-    if (ok) ok = mbar_wait_bounded(smem_u32(&bar_pds), (uint32_t)((nc - 1) & 1), abort_flag,
-                                   dev_err, DEV_ERR_WAIT_GEMM);
-    ok = __all_sync(0xFFFFFFFFu, ok);
-    if (ok) {
-      tc_fence_after();
-      const bool live = kpos < tile.end;
-      const float unscale = exp2f(-emin), ks = scale * unscale;
-      const int64_t o = (int64_t)kpos * (int64_t)H * D + (int64_t)h * D + hf * (D / 2);
-#pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t kv[16], vv[16];
-        tmem_ld16(trow + kColK + (uint32_t)(hf * (D / 2) + 16 * c), kv);
-        tmem_ld16(trow + kColV + (uint32_t)(hf * (D / 2) + 16 * c), vv);
-        tmem_ld_wait();
-        if (live) {
-#pragma unroll
-          for (int e = 0; e < 16; e += 4) {
-            *reinterpret_cast<float4*>(dk + o + 16 * c + e) =
-                make_float4(__uint_as_float(kv[e]) * ks, __uint_as_float(kv[e + 1]) * ks,
-                            __uint_as_float(kv[e + 2]) * ks, __uint_as_float(kv[e + 3]) * ks);
-            *reinterpret_cast<float4*>(dv + o + 16 * c + e) =
-                make_float4(__uint_as_float(vv[e]) * unscale, __uint_as_float(vv[e + 1]) * unscale,
-                            __uint_as_float(vv[e + 2]) * unscale, __uint_as_float(vv[e + 3]) * unscale);
-          }
+          for (int e = 0; e < D; e += 4)
+            *reinterpret_cast<float4*>(out + e) =
+                make_float4(__uint_as_float(acc[e]) * f, __uint_as_float(acc[e + 1]) * f,
+                            __uint_as_float(acc[e + 2]) * f, __uint_as_float(acc[e + 3]) * f);
         }
       }
     }
@@ -904,62 +1059,61 @@ __global__ void __launch_bounds__(kBThreads, 1)
   }
 }
 
+// ------------------------------------------------------------------ dQ
+// Items and streams as in the forward; a stream's chunk of 64 keys:
+//   its MMA warp: S = Q K^T, dP' = dO' V^T;  its gradient warps: P = exp2(S c - lse log2 e),
+//   dS' = P (dP' - delta') as fp16 over dP' in TMEM;  the MMA warp: dQ' += dS' K.
+// S of the next chunk is computed while dS of this one is formed.
 template <int D>
-struct PaDqSmem {
-  static constexpr uint32_t kQ = kAQ * D * 2;    // Q (fp16) or dO (bf16): 128 queries
-  static constexpr uint32_t kKc = kBC * D * 2;   // a chunk of K or V: 64 keys
-  static constexpr uint32_t kSc = kAQ * kBC * 2; // dS: 128 queries x 64 keys
-  static constexpr uint32_t kBytes = 1024 + 2 * kQ + 4 * kKc + kSc;
+struct DqSmem {
+  static constexpr uint32_t kTile = 128 * D * 2;  // Q or dO' of a stream
+  static constexpr uint32_t kKc = kBC * D * 2;    // a chunk of K or V
+  static constexpr int kRing = D == 128 ? 3 : 6;
+  static constexpr uint32_t kBytes = 1024 + 4 * kTile + 2 * kRing * kKc;
 };
 
-// dQ of 128 queries for one query head: loops over the 64-key chunks up to the
-// queries (causal), accumulating dQ += dS K in TMEM; writes dq = scale dQ.
 template <int D>
-__global__ void __launch_bounds__(kBThreads, 1)
+__global__ void __launch_bounds__(kFThreads, 1)
     packed_attn_dq_kernel(const __grid_constant__ CUtensorMap tm_q,    // qkv, boxes of 128 rows
                           const __grid_constant__ CUtensorMap tm_kv,   // qkv, boxes of 64 rows
                           const __grid_constant__ CUtensorMap tm_do,   // dO', boxes of 128 rows
-                          PackedIndex idx, const float* __restrict__ lse,
-                          const float* __restrict__ delta, const float* __restrict__ rowexp,
-                          int64_t T, int H, int Hkv, float sl2, float scale,
-                          float* __restrict__ dq, int* __restrict__ dev_err) {
-  using SM = PaDqSmem<D>;
-  constexpr int DA = D / 64;
+                          PackedIndex idx, const float2* __restrict__ stats,
+                          const float* __restrict__ rowexp, int64_t T, int H, int Hkv, float sl2,
+                          float scale, const float2* __restrict__ cs, uint16_t* __restrict__ dqkv,
+                          int* __restrict__ dev_err) {
+  using SM = DqSmem<D>;
+  constexpr int DA = D / 64, NR = SM::kRing;
   extern __shared__ uint8_t dq_raw[];
-  __shared__ __align__(8) uint64_t bar_qd, bar_kv[2], bar_tail, bar_kvfree[2], bar_sdp[2],
-      bar_tfree[2], bar_ds, bar_dsfree;
+  __shared__ __align__(8) uint64_t q_full[2], q_free[2], r_full[NR], r_free[NR], k_clear[NR];
+  __shared__ __align__(8) uint64_t s_full[2], s_free[2], dp_full[2], ds_full[2], dq_full[2], dq_free[2];
   __shared__ uint32_t tmem_sh;
   __shared__ int abort_sh;
   volatile int* abort_flag = &abort_sh;
   pdl_trigger();
 
-  uint8_t* Qs = align1024_p(dq_raw);
-  uint8_t* dOs = Qs + SM::kQ;
-  uint8_t* Kb = dOs + SM::kQ;       // [2] K chunks (fp16, then bf16)
-  uint8_t* Vb = Kb + 2 * SM::kKc;   // [2] V chunks (bf16)
-  uint8_t* dSs = Vb + 2 * SM::kKc;  // dS (fp16, K-major over keys)
+  uint8_t* Qs = align1024_p(dq_raw);        // [2] Q of the streams
+  uint8_t* dOs = Qs + 2 * SM::kTile;        // [2] dO'
+  uint8_t* Kb = dOs + 2 * SM::kTile;        // [NR] chunks of K
+  uint8_t* Vb = Kb + NR * SM::kKc;          // [NR] chunks of V
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int h = blockIdx.y;
-  const int g = h / (H / Hkv);
-  pdl_wait();
-  if ((int)blockIdx.x >= idx.head[0]) return;
-  const PackedTile tile = idx.tiles[blockIdx.x];
-  const int q0 = tile.row0;
-  const int kv_end = min(tile.end, max(q0 + kAQ, tile.prompt));  // keys this block sees
-  const int nc = (kv_end - tile.begin + kBC - 1) / kBC;
-  constexpr uint32_t kColS = 0, kColP = 2 * kBC, kColQ = 4 * kBC;
+  constexpr uint32_t kColS = 0, kColP = kBC, kColQ = 256;  // S and dP' of stream s at 128 s
 
   if (threadIdx.x == 0) {
-    mbar_init(smem_u32(&bar_qd), 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&bar_kv[i]), 1);
-      mbar_init(smem_u32(&bar_kvfree[i]), 1);
-      mbar_init(smem_u32(&bar_sdp[i]), 1);
-      mbar_init(smem_u32(&bar_tfree[i]), 8);
+      mbar_init(smem_u32(&q_full[i]), 1);
+      mbar_init(smem_u32(&q_free[i]), 1);
+      mbar_init(smem_u32(&s_full[i]), 1);
+      mbar_init(smem_u32(&s_free[i]), 4);
+      mbar_init(smem_u32(&dp_full[i]), 1);
+      mbar_init(smem_u32(&ds_full[i]), 4);
+      mbar_init(smem_u32(&dq_full[i]), 1);
+      mbar_init(smem_u32(&dq_free[i]), 4);
     }
-    mbar_init(smem_u32(&bar_ds), 8);
-    mbar_init(smem_u32(&bar_dsfree), 1);
-    mbar_init(smem_u32(&bar_tail), 1);
+    for (int i = 0; i < NR; ++i) {
+      mbar_init(smem_u32(&r_full[i]), 1);
+      mbar_init(smem_u32(&r_free[i]), 3);  // the two streams' products and warp 11
+      mbar_init(smem_u32(&k_clear[i]), 1);
+    }
     abort_sh = 0;
     fence_mbar_init();
     fence_proxy_async_smem();
@@ -972,168 +1126,234 @@ __global__ void __launch_bounds__(kBThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_sh;
+  pdl_wait();
+  const int G = H / Hkv;
+  const bool heads = G % 2 == 0;
+  const int items = heads ? idx.head[0] * (H / 2) : idx.head[1] * H;
+  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+    return mbar_wait_bounded(smem_u32(bar), parity & 1u, abort_flag, dev_err, DEV_ERR_WAIT_GEMM);
+  };
+  auto wait_all = [&](uint64_t* bar, uint32_t parity) -> bool {
+    return __all_sync(0xFFFFFFFFu, wait(bar, parity));
+  };
 
   if (warp == kWarpTma) {
     if (lane == 0) {
-      mbar_arrive_expect_tx(smem_u32(&bar_qd), 2 * SM::kQ);
-      for (int a = 0; a < DA; ++a) {
-        tma_load_2d(smem_u32(Qs + a * kAQ * 128), &tm_q, smem_u32(&bar_qd), h * D + 64 * a,
-                    q0);
-        tma_load_2d(smem_u32(dOs + a * kAQ * 128), &tm_do, smem_u32(&bar_qd), h * D + 64 * a,
-                    q0);
-      }
-      for (int c = 0; c < nc; ++c) {
-        const int kb = c & 1;
-        if (c >= 2 && !mbar_wait_bounded(smem_u32(&bar_kvfree[kb]), (uint32_t)(((c - 2) >> 1) & 1),
-                                         abort_flag, dev_err, DEV_ERR_WAIT_GEMM))
-          break;
-        const int row = tile.begin + c * kBC;
-        const uint32_t fb = smem_u32(&bar_kv[kb]);
-        mbar_arrive_expect_tx(fb, 2 * SM::kKc);
-        for (int a = 0; a < DA; ++a) {
-          tma_load_2d(smem_u32(Kb + kb * SM::kKc + a * kBC * 128), &tm_kv, fb, (H + g) * D + 64 * a,
-                      row);
-          tma_load_2d(smem_u32(Vb + kb * SM::kKc + a * kBC * 128), &tm_kv, fb,
-                      (H + Hkv + g) * D + 64 * a, row);
+      uint32_t c = 0, nq[2] = {0, 0};
+      bool ok = true;
+      for (int k = 0, w; ok && (w = deal(k, items)) >= 0; ++k) {
+        const FwdItem it = fwd_item(idx, w, H, heads, 0), it1 = fwd_item(idx, w, H, heads, 1);
+        const int g = it.head / G;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          if (!ok || (s == 1 && it1.n == 0)) continue;
+          if (nq[s] > 0) ok = wait(&q_free[s], nq[s] - 1);
+          if (!ok) continue;
+          ++nq[s];
+          const uint32_t fb = smem_u32(&q_full[s]);
+          mbar_arrive_expect_tx(fb, 2 * SM::kTile);
+          const int h = s ? it1.head : it.head, row = s ? it1.row : it.row;
+          for (int a = 0; a < DA; ++a) {
+            tma_load_2d(smem_u32(Qs + s * SM::kTile + a * 128 * 128), &tm_q, fb, h * D + 64 * a, row);
+            tma_load_2d(smem_u32(dOs + s * SM::kTile + a * 128 * 128), &tm_do, fb, h * D + 64 * a,
+                        row);
+          }
+        }
+        for (int j = 0; j < it.nu && ok; ++j, ++c) {
+          const uint32_t slot = c % NR;
+          if (c >= NR) ok = wait(&r_free[slot], c / NR - 1);
+          if (!ok) break;
+          const uint32_t fb = smem_u32(&r_full[slot]);
+          mbar_arrive_expect_tx(fb, 2 * SM::kKc);
+          for (int a = 0; a < DA; ++a) {
+            tma_load_2d(smem_u32(Kb + slot * SM::kKc + a * kBC * 128), &tm_kv, fb,
+                        (H + g) * D + 64 * a, it.begin + j * kBC);
+            tma_load_2d(smem_u32(Vb + slot * SM::kKc + a * kBC * 128), &tm_kv, fb,
+                        (H + Hkv + g) * D + 64 * a, it.begin + j * kBC);
+          }
         }
       }
     }
     __syncwarp();
-    const int lb = (nc - 1) & 1;  // (as in the kernel above: keys behind the last one)
-    zero_tail2<D>(Kb + lb * SM::kKc, Vb + lb * SM::kKc, kv_end - tile.begin - (nc - 1) * kBC, kBC,
-                  smem_u32(&bar_kv[lb]), (uint32_t)(((nc - 1) >> 1) & 1), lane, smem_u32(&bar_tail),
-                  abort_flag, dev_err);
-  } else if (warp == kWarpMma) {
-    if (lane == 0) {
-      const uint32_t id_s = umma_idesc_f16(kAQ, kBC);            // S = Q K^T (fp16)
-      const uint32_t id_dp = id_s;                                // dP' = dO' V^T
-      const uint32_t id_acc = umma_idesc_f16(kAQ, D) | (1u << 16);  // dQ += dS K: B MN-major
-      bool ok = mbar_wait_bounded(smem_u32(&bar_qd), 0u, abort_flag, dev_err, DEV_ERR_WAIT_GEMM);
-      auto issue_sdp = [&](int c) -> bool {
-        const int kb = c & 1;
-        if (!mbar_wait_bounded(smem_u32(&bar_kv[kb]), (uint32_t)((c >> 1) & 1), abort_flag,
-                               dev_err, DEV_ERR_WAIT_GEMM))
-          return false;
-        if (c == nc - 1 && !mbar_wait_bounded(smem_u32(&bar_tail), 0u, abort_flag, dev_err,
-                                              DEV_ERR_WAIT_GEMM))
-          return false;
-        if (c >= 2 && !mbar_wait_bounded(smem_u32(&bar_tfree[kb]), (uint32_t)(((c - 2) >> 1) & 1),
-                                         abort_flag, dev_err, DEV_ERR_WAIT_GEMM))
-          return false;
-        tc_fence_after();
+  } else if (warp == kWarpMma || warp == kWarpMma + 1) {
+    // ---------------------------------------------------------------- MMA issuers
+    const int s = warp - kWarpMma;
+    const uint32_t lead = elect_lane();
+    const uint32_t id_s = umma_idesc_f16(128, kBC);
+    const uint32_t id_q = umma_idesc_f16(128, D) | (1u << 16);  // B (K) MN-major
+    const uint32_t ts = tmem + kColS + (uint32_t)s * 128, tp = tmem + kColP + (uint32_t)s * 128;
+    const uint32_t tq = tmem + kColQ + (uint32_t)s * 128;
+    const uint64_t qd = umma_desc_k_sw128(smem_u32(Qs + s * SM::kTile));
+    const uint64_t od = umma_desc_k_sw128(smem_u32(dOs + s * SM::kTile));
+    uint32_t c = 0, ni = 0, nc = 0;  // ring chunks, items and chunks of this stream
+    bool ok = true;
+    auto scores = [&](uint32_t d, uint64_t a, uint8_t* tile, uint64_t* bar) {
+      const uint64_t bd = umma_desc_k_sw128(smem_u32(tile));
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t qa = (uint32_t)((kk >> 2) * kAQ * 128 + (kk & 3) * 32);
-          const uint32_t ka = (uint32_t)((kk >> 2) * kBC * 128 + (kk & 3) * 32);
-          tc_mma_bf16(tmem + kColS + (uint32_t)kb * kBC, umma_desc_k_sw128(smem_u32(Qs) + qa),
-                      umma_desc_k_sw128(smem_u32(Kb + kb * SM::kKc) + ka), id_s, kk > 0 ? 1u : 0u);
-          tc_mma_bf16(tmem + kColP + (uint32_t)kb * kBC, umma_desc_k_sw128(smem_u32(dOs) + qa),
-                      umma_desc_k_sw128(smem_u32(Vb + kb * SM::kKc) + ka), id_dp, kk > 0 ? 1u : 0u);
+      for (int kk = 0; kk < D / 16; ++kk)
+        mma_ss(lead, d, a + (uint32_t)((kk >> 2) * (128 * 128 / 16) + (kk & 3) * 2),
+               bd + (uint32_t)((kk >> 2) * (kBC * 128 / 16) + (kk & 3) * 2), id_s, kk > 0 ? 1u : 0u);
+      mma_commit(lead, smem_u32(bar));
+    };
+    for (int k = 0, w; ok && (w = deal(k, items)) >= 0; ++k) {
+      const FwdItem it = fwd_item(idx, w, H, heads, s);
+      if (it.n > 0) {
+        ok = wait_all(&q_full[s], ni) && wait_all(&r_full[c % NR], c / NR);
+        // (the scores of the item before have been read: its dS came behind them)
+        if (!ok) break;
+        tc_fence_after();
+        scores(ts, qd, Kb + (c % NR) * SM::kKc, &s_full[s]);
+        scores(tp, od, Vb + (c % NR) * SM::kKc, &dp_full[s]);
+        if (ni > 0) ok = wait_all(&dq_free[s], ni - 1);  // dQ' of the item before has been read
+        ++ni;
+      }
+      for (int j = 0; j < it.nu && ok; ++j, ++c) {
+        const uint32_t slot = c % NR, next = (c + 1) % NR;
+        if (j < it.n) {
+          const bool more = j + 1 < it.n;
+          if (more) {
+            ok = wait_all(&r_full[next], (c + 1) / NR) && wait_all(&s_free[s], nc);
+            if (!ok) break;
+            tc_fence_after();
+            scores(ts, qd, Kb + next * SM::kKc, &s_full[s]);
+          }
+          if (j + 1 == it.nu && it.begin + it.nu * kBC > it.end)
+            ok = wait_all(&k_clear[slot], c / NR);
+          ok = ok && wait_all(&ds_full[s], nc);
+          if (!ok) break;
+          ++nc;
+          tc_fence_after();
+          const uint64_t kd = umma_desc_mn_sw128(smem_u32(Kb + slot * SM::kKc), kBC * 128, 1024u);
+#pragma unroll
+          for (int kk = 0; kk < kBC / 16; ++kk)
+            mma_ts(lead, tq, tp + kk * 8, kd + (uint32_t)(kk * 128), id_q,
+                   (j > 0 || kk > 0) ? 1u : 0u);
+          if (more)
+            scores(tp, od, Vb + next * SM::kKc, &dp_full[s]);
+          else
+            mma_commit(lead, smem_u32(&dq_full[s]));
+          // Q and dO' are free behind the stream's last scores
+          if (j + 2 == it.n || it.n == 1) mma_commit(lead, smem_u32(&q_free[s]));
+        } else {
+          ok = wait_all(&r_full[slot], c / NR);
+          if (!ok) break;
         }
-        tc_commit(smem_u32(&bar_sdp[kb]));
-        return true;
-      };
-      ok = ok && issue_sdp(0);
-      for (int c = 0; c < nc && ok; ++c) {
-        const int kb = c & 1;
-        if (c + 1 < nc) ok = issue_sdp(c + 1);
-        if (!ok) break;
-        ok = mbar_wait_bounded(smem_u32(&bar_ds), (uint32_t)(c & 1), abort_flag, dev_err,
-                               DEV_ERR_WAIT_GEMM);
-        if (!ok) break;
-        tc_fence_after();
-#pragma unroll
-        for (int kk = 0; kk < kBC / 16; ++kk)
-          tc_mma_bf16(tmem + kColQ, umma_desc_k_sw128(smem_u32(dSs) + (uint32_t)(kk * 32)),
-                      umma_desc_mn_sw128(smem_u32(Kb + kb * SM::kKc) + (uint32_t)kk * 16 * 128,
-                                         kBC * 128, 1024u),
-                      id_acc, (c > 0 || kk > 0) ? 1u : 0u);
-        tc_commit(smem_u32(&bar_dsfree));     // dS read; dQ updated
-        tc_commit(smem_u32(&bar_kvfree[kb]));  // the K and V chunk read
+        mma_commit(lead, smem_u32(&r_free[slot]));
       }
     }
-    __syncwarp();
+  } else if (warp == kWarpTail) {
+    // Follows every chunk of the ring; keys behind the document: their dS is 0, and so
+    // must the K rows be that those multiply (0 * inf).
+    uint32_t c = 0;
+    bool ok = true;
+    for (int k = 0, w; ok && (w = deal(k, items)) >= 0; ++k) {
+      const FwdItem it = fwd_item(idx, w, H, heads, 0);
+      for (int j = 0; j < it.nu && ok; ++j, ++c) {
+        const uint32_t slot = c % NR;
+        ok = wait_all(&r_full[slot], c / NR);
+        if (!ok) break;
+        const int rows = it.end - it.begin - j * kBC;
+        if (rows < kBC) {
+          zero_rows<D>(Kb + slot * SM::kKc, rows, kBC, lane);
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        if (lane == 0) {
+          mbar_arrive(smem_u32(&k_clear[slot]));  // (every chunk: a phase per use of the slot)
+          mbar_arrive(smem_u32(&r_free[slot]));
+        }
+      }
+    }
   } else {
     // ---------------------------------------------------------------- gradient warps
-    const int r = (warp & 3) * 32 + lane;  // query row of the block = TMEM lane
-    const int hf = warp >> 2;              // keys 32 hf .. of each chunk
-    const int q = q0 + r;
-    const int kmax = min(max(q, tile.prompt - 1), tile.end - 1);  // its last key
-    const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const int64_t qq = (int64_t)h * T + min(q, tile.end - 1);
-    const float l2 = __ldg(lse + qq) * 1.4426950408889634f;
-    const float dl = __ldg(delta + qq);
-    const float unscale = scale * exp2f(-__ldg(rowexp + qq));
+    const int s = warp >> 2;
+    const int r = (warp & 3) * 32 + lane;  // query of the tile = TMEM lane
+    const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)s * 128;
+    uint32_t nc = 0, ni = 0;
     bool ok = true;
-    for (int c = 0; c < nc && ok; ++c) {
-      const int kb = c & 1;
-      ok = mbar_wait_bounded(smem_u32(&bar_sdp[kb]), (uint32_t)((c >> 1) & 1), abort_flag, dev_err,
-                             DEV_ERR_WAIT_GEMM);
-      ok = __all_sync(0xFFFFFFFFu, ok);
+    for (int k = 0, w; ok && (w = deal(k, items)) >= 0; ++k) {
+      const FwdItem it = fwd_item(idx, w, H, heads, s);
+      const int n = it.n;
+      if (n == 0) continue;
+      const int q = it.row + r;
+      const int kmax = min(max(q, it.prompt - 1), it.end - 1);  // its last key
+      const int kall = min(max(it.row + (warp & 3) * 32, it.prompt - 1), it.end - 1);
+      const int64_t at = (int64_t)it.head * T + min(q, it.end - 1);
+      const float2 sq = __ldg(stats + at);
+      const float e = __ldg(rowexp + at);
+      const float nl2 = e - sq.x, dl = sq.y;
+      for (int j = 0; j < n; ++j, ++nc) {
+        ok = wait_all(&s_full[s], nc);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t p[kBC];
+        tmem_ld32(trow + kColS, p);
+        tmem_ld32(trow + kColS + 32, p + 32);
+        tmem_ld_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&s_free[s]));
+#pragma unroll
+        for (int i = 0; i < kBC; ++i)
+          p[i] = __float_as_uint(ex2(fmaf(__uint_as_float(p[i]), sl2, nl2)));
+        const int last = kmax - it.begin - j * kBC;
+        const bool whole = it.begin + (j + 1) * kBC - 1 <= kall;  // (uniform in the warp)
+        if (!whole) {
+#pragma unroll
+          for (int i = 0; i < kBC; ++i)
+            if (i > last) p[i] = 0u;
+        }
+        ok = wait_all(&dp_full[s], nc);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t dsk[kBC / 2];
+#pragma unroll
+        for (int i = 0; i < kBC; i += 32) {
+          uint32_t d[32];
+          tmem_ld32(trow + kColP + i, d);
+          tmem_ld_wait();
+#pragma unroll
+          for (int u = 0; u < 32; u += 2) {
+            float x = __uint_as_float(p[i + u]) * (__uint_as_float(d[u]) - dl);
+            float y = __uint_as_float(p[i + u + 1]) * (__uint_as_float(d[u + 1]) - dl);
+            if (!whole) {  // (dp behind the document may be anything)
+              x = i + u > last ? 0.f : x;
+              y = i + u + 1 > last ? 0.f : y;
+            }
+            dsk[(i + u) / 2] = pack_f16x2(x, y);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kBC / 2; i += 16)
+          tmem_st16(trow + kColP + i, *reinterpret_cast<uint32_t(*)[16]>(dsk + i));
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ds_full[s]));
+      }
+      // -------------------------------------------------------------- epilogue
+      ok = ok && wait_all(&dq_full[s], ni);
       if (!ok) break;
+      ++ni;
       tc_fence_after();
-      uint32_t sv[2][16], pv[2][16];
-      tmem_ld16(trow + kColS + (uint32_t)(kb * kBC + 32 * hf), sv[0]);
-      tmem_ld16(trow + kColS + (uint32_t)(kb * kBC + 32 * hf + 16), sv[1]);
-      tmem_ld16(trow + kColP + (uint32_t)(kb * kBC + 32 * hf), pv[0]);
-      tmem_ld16(trow + kColP + (uint32_t)(kb * kBC + 32 * hf + 16), pv[1]);
+      uint32_t acc[D];
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) tmem_ld32(trow + kColQ + 32 * i, acc + 32 * i);
       tmem_ld_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&bar_tfree[kb]));
-      const int kfirst = tile.begin + c * kBC + 32 * hf;  // this thread's first key
-      uint32_t dpk[16];
-#pragma unroll
-      for (int e = 0; e < 32; e += 2) {
-        float d[2];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int key = kfirst + e + u;
-          const bool live = key <= kmax;
-          const float s = __uint_as_float(sv[(e + u) >> 4][(e + u) & 15]);
-          const float dp = __uint_as_float(pv[(e + u) >> 4][(e + u) & 15]);
-          const float p = live ? ex2(fmaf(s, sl2, -l2)) : 0.f;
-          d[u] = live ? p * (dp - dl) : 0.f;
-        }
-        dpk[e >> 1] = pack_f16x2(d[0], d[1]);
-      }
-      // the previous chunk's dQ product has read dS
-      if (c > 0) {
-        ok = mbar_wait_bounded(smem_u32(&bar_dsfree), (uint32_t)((c - 1) & 1), abort_flag, dev_err,
-                               DEV_ERR_WAIT_GEMM);
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        if (!ok) break;
-      }
-#pragma unroll
-      for (int cc = 0; cc < 4; ++cc)
-        *reinterpret_cast<uint4*>(dSs + sw128_offset((uint32_t)r, (uint32_t)(hf * 4 + cc))) =
-            make_uint4(dpk[4 * cc], dpk[4 * cc + 1], dpk[4 * cc + 2], dpk[4 * cc + 3]);
-      fence_proxy_async_smem();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&bar_ds));
+      if (lane == 0) mbar_arrive(smem_u32(&dq_free[s]));
+      if (q < it.end)
+        store_grad_row<D>(acc, scale * ex2(-e), cs ? cs + (int64_t)idx.pos[q] * (D / 2) : nullptr,
+                          dqkv + (int64_t)q * (H + 2 * Hkv) * D + (int64_t)it.head * D);
     }
-    if (ok) ok = mbar_wait_bounded(smem_u32(&bar_dsfree), (uint32_t)((nc - 1) & 1), abort_flag,
-                                   dev_err, DEV_ERR_WAIT_GEMM);
-    ok = __all_sync(0xFFFFFFFFu, ok);
-    if (ok) {
-      tc_fence_after();
-      const bool live = q < tile.end;
-      const int64_t o = (int64_t)q * (int64_t)H * D + (int64_t)h * D + hf * (D / 2);
-#pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t v[16];
-        tmem_ld16(trow + kColQ + (uint32_t)(hf * (D / 2) + 16 * c), v);
-        tmem_ld_wait();
-        if (live) {
-#pragma unroll
-          for (int e = 0; e < 16; e += 4)
-            *reinterpret_cast<float4*>(dq + o + 16 * c + e) =
-                make_float4(__uint_as_float(v[e]) * unscale, __uint_as_float(v[e + 1]) * unscale,
-                            __uint_as_float(v[e + 2]) * unscale, __uint_as_float(v[e + 3]) * unscale);
-        }
-      }
-    }
+  }
+  {  // padding rows have no gradient
+    const int64_t row = (int64_t)(H + 2 * Hkv) * (D / 8), first = idx.head[2];
+    uint4* o = reinterpret_cast<uint4*>(dqkv) + first * row;
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < (T - first) * row;
+         i += (int64_t)gridDim.x * blockDim.x)
+      o[i] = make_uint4(0u, 0u, 0u, 0u);
   }
   tc_fence_before();
   __syncthreads();
@@ -1144,51 +1364,44 @@ __global__ void __launch_bounds__(kBThreads, 1)
   }
 }
 
-// dqkv (bf16) from dq and the query heads' dk and dv (fp32 [T, H d] each): k and v
-// summed over their kv head's query heads in order, with cs the rotation of q and k
-// by their position in the document undone, padding rows 0.  A thread takes 4 pairs
-// (i, i + d/2).
+// dk and dv (bf16, into dqkv) from the fp32 parts of `parts` shares of each kv head's
+// query heads, summed in order; with cs the rotation of k by its position undone.  A
+// thread takes 4 pairs (i, i + d/2).
 __global__ void __launch_bounds__(256)
-    packed_grad_kernel(const float* __restrict__ dq, const float* __restrict__ dk,
-                       const float* __restrict__ dv, const int* __restrict__ head,
-                       const int* __restrict__ pos, int64_t T, int H, int Hkv, int d,
-                       const float2* __restrict__ cs, uint16_t* __restrict__ dqkv) {
+    packed_grad_kernel(const float* __restrict__ dk, const float* __restrict__ dv,
+                       const int* __restrict__ head, const int* __restrict__ pos, int H, int Hkv,
+                       int parts, int d, const float2* __restrict__ cs,
+                       uint16_t* __restrict__ dqkv) {
   pdl_trigger();
   pdl_wait();
-  const int half = d / 2, chunks = half / 4, rep = H / Hkv;
-  const int64_t ld = (int64_t)(H + 2 * Hkv) * d, hd = (int64_t)H * d;
-  const int64_t n = T * (H + 2 * Hkv) * chunks;
-  const int64_t live = head[2];
+  const int half = d / 2, chunks = half / 4;
+  const int64_t ld = (int64_t)(H + 2 * Hkv) * d;
+  const int64_t n = (int64_t)head[2] * 2 * Hkv * chunks;
   for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n;
        i += (int64_t)gridDim.x * blockDim.x) {
     const int ch = (int)(i % chunks);
     const int64_t th = i / chunks;
-    const int hh = (int)(th % (H + 2 * Hkv));
-    const int64_t t = th / (H + 2 * Hkv);
-    uint16_t* out = dqkv + t * ld + (int64_t)hh * d + ch * 4;
+    const int hh = (int)(th % (2 * Hkv));
+    const int64_t t = th / (2 * Hkv);
+    const float* src = (hh < Hkv ? dk : dv) + ((t * Hkv + hh % Hkv) * parts) * d + ch * 4;
     float a[4] = {0.f, 0.f, 0.f, 0.f}, b[4] = {0.f, 0.f, 0.f, 0.f};
-    if (t < live) {
-      const float* src = hh < H ? dq : hh < H + Hkv ? dk : dv;
-      const int h0 = hh < H ? hh : ((hh - H) % Hkv) * rep;
-      const int nh = hh < H ? 1 : rep;
-      for (int k = 0; k < nh; ++k) {
-        const float* s = src + t * hd + (int64_t)(h0 + k) * d + ch * 4;
-        const float4 x = *reinterpret_cast<const float4*>(s);
-        const float4 y = *reinterpret_cast<const float4*>(s + half);
-        a[0] += x.x; a[1] += x.y; a[2] += x.z; a[3] += x.w;
-        b[0] += y.x; b[1] += y.y; b[2] += y.z; b[3] += y.w;
-      }
-      if (cs && hh < H + Hkv) {
-        const float2* c = cs + (int64_t)pos[t] * half + ch * 4;
+    for (int k = 0; k < parts; ++k) {
+      const float4 x = *reinterpret_cast<const float4*>(src + (int64_t)k * d);
+      const float4 y = *reinterpret_cast<const float4*>(src + (int64_t)k * d + half);
+      a[0] += x.x; a[1] += x.y; a[2] += x.z; a[3] += x.w;
+      b[0] += y.x; b[1] += y.y; b[2] += y.z; b[3] += y.w;
+    }
+    if (cs && hh < Hkv) {
+      const float2* c = cs + (int64_t)pos[t] * half + ch * 4;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float2 f = c[k];
-          const float x = a[k], y = b[k];
-          a[k] = x * f.x + y * f.y;
-          b[k] = y * f.x - x * f.y;
-        }
+      for (int k = 0; k < 4; ++k) {
+        const float2 f = c[k];
+        const float x = a[k], y = b[k];
+        a[k] = x * f.x + y * f.y;
+        b[k] = y * f.x - x * f.y;
       }
     }
+    uint16_t* out = dqkv + t * ld + (int64_t)(H + hh) * d + ch * 4;
     *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]));
     *reinterpret_cast<uint2*>(out + half) =
         make_uint2(pack_bf16x2(b[0], b[1]), pack_bf16x2(b[2], b[3]));
@@ -1235,7 +1448,7 @@ int fwd_t(const uint16_t* qkv, const PackedIndex& x, int64_t T, int H, int Hkv, 
                        (uint64_t)row, 64, kAQ, CU_TENSOR_MAP_SWIZZLE_128B));
   int* err = device_status_ptr();
   if (!err) return set_error(LSQ_ERR_CUDA, "device status word unavailable");
-  const float sl2 = 1.4426950408889634f / sqrtf((float)D);
+  const float sl2 = kLog2e / sqrtf((float)D);
   const int64_t items = (H / Hkv) % 2 == 0 ? (int64_t)x.cap * (H / 2) : (int64_t)x.cap2 * H;
   const unsigned grid = (unsigned)std::min<int64_t>(items, gemm_num_sms());
   LSQ_CUDA(launch_dep(packed_attn_fwd_kernel<D>, dim3(grid), kFThreads, SM::kBytes, st, tm, x, T, H,
@@ -1245,20 +1458,35 @@ int fwd_t(const uint16_t* qkv, const PackedIndex& x, int64_t T, int H, int Hkv, 
 
 struct BwdWs {
   uint16_t* dos;   // [T, H d] fp16 dO'
-  float* delta;    // [H, T] delta'
+  float2* stats;   // [H, T] (lse log2 e + e, delta')
   float* rowexp;   // [H, T] e
-  float *dq, *dk, *dv;  // [T, H d] fp32
+  float* winexp;   // [H, windows] the least e of 64 tokens
+  float *dk, *dv;  // [T, Hkv parts, d] fp32
 };
-size_t carve_bwd(int64_t T, int H, int d, void* base, BwdWs* w) {
+
+// Into how many shares a kv head's query heads are split for dK and dV.  One share
+// needs no partial sums (8 bytes written and read per token, share and dimension) but
+// leaves few items: at least four per SM are wanted, so that they even out.
+// 16,384 tokens, 16/2 heads: see the measured times at the launch.
+int dkv_parts(int64_t T, int H, int Hkv) {
+  const int G = H / Hkv;
+  const int64_t tiles = (T + kPackedTile - 1) / kPackedTile;
+  for (int p = 1; p < G; ++p)
+    if (G % p == 0 && tiles * Hkv * p >= 4 * (int64_t)gemm_num_sms()) return p;
+  return G;
+}
+
+size_t carve_bwd(int64_t T, int H, int Hkv, int d, void* base, BwdWs* w) {
   Arena a;
   a.base = static_cast<uint8_t*>(base);
   a.cap = SIZE_MAX;
   BwdWs x;
-  const size_t n = (size_t)T * H * d;
-  x.dos = a.take<uint16_t>(n);
-  x.delta = a.take<float>((size_t)T * H);
+  const int parts = dkv_parts(T, H, Hkv);
+  x.dos = a.take<uint16_t>((size_t)T * H * d);
+  x.stats = a.take<float2>((size_t)T * H);
   x.rowexp = a.take<float>((size_t)T * H);
-  x.dq = a.take<float>(n);
+  x.winexp = a.take<float>((size_t)((T + kWindow - 1) / kWindow) * H);
+  const size_t n = parts > 1 ? (size_t)T * Hkv * parts * d : 0;
   x.dk = a.take<float>(n);
   x.dv = a.take<float>(n);
   if (w) *w = x;
@@ -1270,35 +1498,41 @@ int bwd_t(const uint16_t* qkv, const PackedIndex& x, const uint16_t* o, const fl
           const uint16_t* dout, int64_t T, int H, int Hkv, const float2* cs, uint16_t* dqkv,
           const BwdWs& w, cudaStream_t st) {
   static bool attr_kv[64] = {false}, attr_q[64] = {false};
-  LSQ_TRY(allow_smem(packed_attn_dkdv_kernel<D>, (int)PaDkvSmem<D>::kBytes, attr_kv));
-  LSQ_TRY(allow_smem(packed_attn_dq_kernel<D>, (int)PaDqSmem<D>::kBytes, attr_q));
+  LSQ_TRY(allow_smem(packed_attn_dkdv_kernel<D>, (int)DkvSmem<D>::kBytes, attr_kv));
+  LSQ_TRY(allow_smem(packed_attn_dq_kernel<D>, (int)DqSmem<D>::kBytes, attr_q));
   int* err = device_status_ptr();
   if (!err) return set_error(LSQ_ERR_CUDA, "device status word unavailable");
   const float scale = 1.f / sqrtf((float)D);
-  const float sl2 = 1.4426950408889634f * scale;
-  const int64_t warps = T * (H + Hkv);
-  LSQ_CUDA(launch_dep(packed_attn_prep_kernel<D>, dim3((unsigned)((warps + 7) / 8)), 256, 0, st, qkv,
-                      o, dout, x.head, T, H, Hkv, w.dos, w.delta, w.rowexp, err));
+  const float sl2 = kLog2e * scale;
+  const unsigned windows = (unsigned)((T + kWindow - 1) / kWindow);
+  LSQ_CUDA(launch_dep(packed_attn_prep_kernel<D>, dim3(windows, (unsigned)(H + Hkv)), 256, 0, st,
+                      qkv, o, dout, lse, x.head, T, H, Hkv, w.dos, w.stats, w.rowexp, w.winexp,
+                      err));
   const int64_t row = (int64_t)(H + 2 * Hkv) * D, hd = (int64_t)H * D;
   CUtensorMap qkv128, qkv64, do128, do64;
   LSQ_TRY(make_tmap_2d(&qkv128, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, qkv, (uint64_t)row, (uint64_t)T,
-                       (uint64_t)row, 64, kAK, CU_TENSOR_MAP_SWIZZLE_128B));
+                       (uint64_t)row, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B));
   LSQ_TRY(make_tmap_2d(&qkv64, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, qkv, (uint64_t)row, (uint64_t)T,
                        (uint64_t)row, 64, kBC, CU_TENSOR_MAP_SWIZZLE_128B));
   LSQ_TRY(make_tmap_2d(&do128, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, w.dos, (uint64_t)hd, (uint64_t)T,
-                       (uint64_t)hd, 64, kAQ, CU_TENSOR_MAP_SWIZZLE_128B));
+                       (uint64_t)hd, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B));
   LSQ_TRY(make_tmap_2d(&do64, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, w.dos, (uint64_t)hd, (uint64_t)T,
                        (uint64_t)hd, 64, kBC, CU_TENSOR_MAP_SWIZZLE_128B));
-  const dim3 grid((unsigned)x.cap, (unsigned)H);
-  LSQ_CUDA(launch_dep(packed_attn_dkdv_kernel<D>, grid, kBThreads, PaDkvSmem<D>::kBytes, st, qkv128,
-                      qkv64, do64, x, lse, w.delta, w.rowexp, T, H, Hkv, sl2, scale, w.dk, w.dv,
-                      err));
-  LSQ_CUDA(launch_dep(packed_attn_dq_kernel<D>, grid, kBThreads, PaDqSmem<D>::kBytes, st, qkv128,
-                      qkv64, do128, x, lse, w.delta, w.rowexp, T, H, Hkv, sl2, scale, w.dq, err));
-  const int64_t items = T * (H + 2 * Hkv) * (D / 8);
-  LSQ_CUDA(launch_dep(packed_grad_kernel,
-                      dim3((unsigned)std::min<int64_t>((items + 255) / 256, gemm_num_sms() * 16)),
-                      256, 0, st, w.dq, w.dk, w.dv, x.head, x.pos, T, H, Hkv, D, cs, dqkv));
+  const int parts = dkv_parts(T, H, Hkv), sms = gemm_num_sms();
+  const int64_t kitems = (int64_t)x.cap * Hkv * parts;
+  LSQ_CUDA(launch_dep(packed_attn_dkdv_kernel<D>, dim3((unsigned)std::min<int64_t>(kitems, sms)),
+                      kFThreads, DkvSmem<D>::kBytes, st, qkv128, qkv64, do64, x, w.stats, w.rowexp,
+                      w.winexp, T, H, Hkv, H / Hkv / parts, sl2, scale, cs, dqkv, w.dk, w.dv, err));
+  const int64_t qitems = (H / Hkv) % 2 == 0 ? (int64_t)x.cap * (H / 2) : (int64_t)x.cap2 * H;
+  LSQ_CUDA(launch_dep(packed_attn_dq_kernel<D>, dim3((unsigned)std::min<int64_t>(qitems, sms)),
+                      kFThreads, DqSmem<D>::kBytes, st, qkv128, qkv64, do128, x, w.stats, w.rowexp,
+                      T, H, Hkv, sl2, scale, cs, dqkv, err));
+  if (parts > 1) {
+    const int64_t n = T * 2 * Hkv * (D / 8);
+    LSQ_CUDA(launch_dep(packed_grad_kernel,
+                        dim3((unsigned)std::min<int64_t>((n + 255) / 256, sms * 16)), 256, 0, st,
+                        w.dk, w.dv, x.head, x.pos, H, Hkv, parts, D, cs, dqkv));
+  }
   return LSQ_OK;
 }
 
@@ -1327,7 +1561,7 @@ int launch_packed_attention_fwd(const uint16_t* qkv, const int32_t* index, int n
 }
 
 size_t packed_attention_ws_bytes(int64_t T, int H, int Hkv, int d) {
-  return carve_bwd(T, H, d, nullptr, nullptr);
+  return carve_bwd(T, H, Hkv, d, nullptr, nullptr);
 }
 
 int launch_packed_attention_bwd(const uint16_t* qkv, const int32_t* index, int n_docs,
@@ -1336,7 +1570,7 @@ int launch_packed_attention_bwd(const uint16_t* qkv, const int32_t* index, int n
                                 void* ws, size_t ws_bytes, cudaStream_t st) {
   const PackedIndex x = packed_index_view(index, T, n_docs);
   BwdWs w;
-  if (carve_bwd(T, H, d, ws, &w) > ws_bytes)
+  if (carve_bwd(T, H, Hkv, d, ws, &w) > ws_bytes)
     return set_error(LSQ_ERR_WORKSPACE, "packed attention: workspace too small");
   const int prof = prof_begin(st);
   LSQ_TRY(d == 128 ? bwd_t<128>(qkv, x, o, lse, dout, T, H, Hkv, cs, dqkv, w, st)
