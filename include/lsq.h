@@ -477,8 +477,8 @@ size_t packed_attention_workspace_bytes(int64_t T, int32_t H, int32_t Hkv, int32
  *           and dv summed in fp32 over the query heads of each kv head.
  *   ws      device workspace of packed_attention_workspace_bytes(T, H, Hkv, d).
  * The score gradients multiply in fp16 after each row of dout is scaled by the power
- * of two that brings its norm to [8, 16), so their range does not matter; a row of v
- * whose norm is above 2047 latches LSQ_DEV_ERR_NONFINITE (its score gradients may
+ * of two that brings its largest magnitude to [1, 2), so their range does not matter; a
+ * row of v whose norm is above 1447 latches LSQ_DEV_ERR_NONFINITE (its score gradients may
  * overflow).  Asynchronous, deterministic (fixed-order sums, no atomics). */
 int packed_attention_bwd(const uint16_t* qkv, const int32_t* index, int32_t n_docs,
                          const uint16_t* o, const float* lse, const uint16_t* dout, int64_t T,

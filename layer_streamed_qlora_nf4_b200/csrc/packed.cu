@@ -109,12 +109,13 @@ __global__ void __launch_bounds__(kIdxThreads)
     t1[tid] = base1 + (int)(i12 >> 32) - n1;
     t2[tid] = base2 + (int)(i12 & 0xFFFFFFFF) - n2;
     __syncthreads();
+    const int nd = min(n_docs - d0, kIdxThreads);
     // documents of no tokens share their start with the next one: the last at or
     // before a token is the one that holds it
     const int c1 = (int)(all12 >> 32), c2 = (int)(all12 & 0xFFFFFFFF);
     const int hi = (int)min((int64_t)T, total);
     for (int t = (int)base + gtid; t < hi; t += gsize) {
-      const int k = find_last(tok0, kIdxThreads, t);
+      const int k = find_last(tok0, nd, t);
       x.pos[t] = t - tok0[k];
       x.key_end[t] = max(t + 1, doc_p[k]);
       x.doc_end[t] = doc_e[k];
@@ -123,7 +124,7 @@ __global__ void __launch_bounds__(kIdxThreads)
     auto emit = [&](int kind, const int* first, int n, int before, int size, PackedTile* list,
                     int cap) {
       for (int i = gtid >> 5; i < n; i += gsize >> 5) {
-        const int k = find_last(first, kIdxThreads, before + i);
+        const int k = find_last(first, nd, before + i);
         const int at = before + i - first[k];  // tile of its document
         int place = before + i;
         if (sorted) {

@@ -12,7 +12,7 @@
 // All products run as tcgen05.mma from 128-byte-swizzled shared-memory tiles (TMA)
 // into TMEM accumulators, fp16 operands and fp32 sums throughout.  The gradient of the
 // output arrives in bf16, whose range fp16 lacks: its rows are scaled by powers of two
-// first (dO' = 2^e dO with a norm in [8, 16)), which loses nothing of bf16's 8 bits,
+// first (dO' = 2^e dO with a largest magnitude in [1, 2)), which loses none of bf16's 8 bits,
 // and the factors are taken out again in fp32.  Every sum has a fixed order, so the
 // results are deterministic.
 #include <cuda.h>
@@ -520,10 +520,12 @@ __global__ void __launch_bounds__(kFThreads, 1)
 //   warps 0-3, 4-7: the gradient warps (a TMEM lane per thread)
 //   warp 8 : TMA producer;  warps 9, 10: MMA issuers (warp 9 also allocates TMEM)
 //   warp 11: clears rows behind a document's end, and (dK, dV) stages the queries' values
-// The prepared values of a query and head: dO' = 2^e dO in fp16 with a norm in [8, 16),
+// The prepared values of a query and head: dO' = 2^e dO in fp16, its largest in [1, 2),
 // e, delta' = 2^e delta and l = lse log2 e + e.
 constexpr int kBC = 64;        // columns of a chunk (queries for dK/dV, keys for dQ)
 constexpr int kWindow = 64;    // tokens of a window of the exponents' minima
+// |dS'| <= 2 |dO'| |v| with |dO'| < 2 sqrt(128): below fp16's 65504 for these norms of v
+constexpr float kMaxNormV = 1447.f;
 
 __device__ __forceinline__ float warp_min(float x) {
 #pragma unroll
@@ -531,10 +533,12 @@ __device__ __forceinline__ float warp_min(float x) {
   return x;
 }
 
-// One CTA per window of 64 tokens and head (a warp per token, eight tokens each), or,
-// for blockIdx.y >= H, the norms of the v rows of kv head blockIdx.y - H.  A zero row
-// takes e = 127 (it must not lower the least exponent of a tile); a row that is not
-// finite takes e = 0, and its gradients come out not finite.
+// One CTA per window of 64 tokens and head; D / 8 lanes take a row, 16 bytes each, and a
+// warp its eight tokens with all loads in flight (memory bound: 6 bytes per element).
+// blockIdx.y >= H: the norms of the v rows of kv head blockIdx.y - H.  e brings the row's
+// largest magnitude to [1, 2), so its norm is below 2 sqrt(d).  A zero row takes e = 127
+// (it must not lower the least exponent of a tile); a row that is not finite takes e = 0,
+// and its gradients come out not finite.
 template <int D>
 __global__ void __launch_bounds__(256)
     packed_attn_prep_kernel(const uint16_t* __restrict__ qkv, const uint16_t* __restrict__ o,
@@ -542,96 +546,87 @@ __global__ void __launch_bounds__(256)
                             const int* __restrict__ head, int64_t T, int H, int Hkv,
                             uint16_t* __restrict__ dos, float2* __restrict__ stats,
                             float* __restrict__ rowexp, float* __restrict__ winexp, int* dev_err) {
-  constexpr int E = D / 32;  // elements per lane
+  constexpr int LR = D / 8, RW = 32 / LR, IT = kWindow / 8 / RW;  // lanes a row, rows a warp, rounds
   __shared__ float low[8];
   pdl_trigger();
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int h = blockIdx.y;
+  const int h = blockIdx.y, col = (lane % LR) * 8;
   const int64_t live = head[2];
-  const int64_t t0 = (int64_t)blockIdx.x * kWindow + warp * (kWindow / 8);
+  const int64_t t0 = (int64_t)blockIdx.x * kWindow + warp * (kWindow / 8) + lane / LR;
   if (h >= H) {
     bool big = false;
-    for (int64_t t = t0; t < min(live, t0 + kWindow / 8); ++t) {
-      const uint16_t* v = qkv + t * (int64_t)(H + 2 * Hkv) * D + (int64_t)(Hkv + h) * D + lane * E;
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+      const int64_t t = t0 + i * RW;
+      uint4 x = make_uint4(0u, 0u, 0u, 0u);
+      if (t < live)
+        x = *reinterpret_cast<const uint4*>(qkv + t * (int64_t)(H + 2 * Hkv) * D +
+                                            (int64_t)(Hkv + h) * D + col);
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
       float n = 0.f;
 #pragma unroll
-      for (int i = 0; i < E; i += 2) {
-        const float2 x = unpack_f16x2(*reinterpret_cast<const uint32_t*>(v + i));
-        n += x.x * x.x + x.y * x.y;
+      for (int k = 0; k < 4; ++k) {
+        const float2 f = unpack_f16x2(w[k]);
+        n += f.x * f.x + f.y * f.y;
       }
 #pragma unroll
-      for (int k = 16; k > 0; k >>= 1) n += __shfl_xor_sync(0xFFFFFFFFu, n, k);
-      big |= !(n <= 2047.f * 2047.f);
+      for (int k = LR / 2; k > 0; k >>= 1) n += __shfl_xor_sync(0xFFFFFFFFu, n, k);
+      big |= !(n <= kMaxNormV * kMaxNormV);
     }
-    if (big && lane == 0) atomicOr(dev_err, DEV_ERR_NONFINITE);
+    if (big) atomicOr(dev_err, DEV_ERR_NONFINITE);
     return;
   }
+  uint4 gr[IT], orow[IT];
+  float ls[IT];
+#pragma unroll
+  for (int i = 0; i < IT; ++i) {
+    const int64_t t = t0 + i * RW;
+    const int64_t at = (t * H + h) * D + col;
+    const bool in = t < live;
+    gr[i] = in ? *reinterpret_cast<const uint4*>(dout + at) : make_uint4(0u, 0u, 0u, 0u);
+    orow[i] = in ? *reinterpret_cast<const uint4*>(o + at) : make_uint4(0u, 0u, 0u, 0u);
+    ls[i] = in ? lse[(int64_t)h * T + t] : 0.f;
+  }
   float emin = 127.f;
-#pragma unroll 4
-  for (int i = 0; i < kWindow / 8; ++i) {
-    const int64_t t = t0 + i;
-    if (t >= T) break;
-    const int64_t at = (t * H + h) * D + lane * E;
-    uint32_t gr[E / 2], orow[E / 2];
-    if (E == 4) {
-      const uint2 a = *reinterpret_cast<const uint2*>(dout + at);
-      const uint2 b = *reinterpret_cast<const uint2*>(o + at);
-      gr[0] = a.x; gr[E / 2 - 1] = a.y;
-      orow[0] = b.x; orow[E / 2 - 1] = b.y;
-    } else {
-      gr[0] = *reinterpret_cast<const uint32_t*>(dout + at);
-      orow[0] = *reinterpret_cast<const uint32_t*>(o + at);
-    }
-    float g[E], n = 0.f;
-    bool bad = false;
 #pragma unroll
-    for (int k = 0; k < E; k += 2) {
-      const float2 x = unpack_bf16x2(gr[k / 2]);
-      g[k] = t < live ? x.x : 0.f;
-      g[k + 1] = t < live ? x.y : 0.f;
-      n = fmaxf(n, fmaxf(fabsf(g[k]), fabsf(g[k + 1])));
-      bad |= !(fabsf(g[k]) <= 3.4e38f) || !(fabsf(g[k + 1]) <= 3.4e38f);
-    }
-    n = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(n)));
-    bad = __any_sync(0xFFFFFFFFu, bad);
-    // the norm from values near 1, so that its squares neither overflow nor vanish
-    int e = n == 0.f ? 127 : 0;
-    if (n > 0.f && !bad) {
-      const int x = max(1, (int)(__float_as_uint(n) >> 23)) - 126;  // n < 2^x
-      const float s = ldexpf(1.f, -x);
-      float sq = 0.f;
+  for (int i = 0; i < IT; ++i) {
+    const int64_t t = t0 + i * RW;
+    const uint32_t gw[4] = {gr[i].x, gr[i].y, gr[i].z, gr[i].w};
+    const uint32_t ow[4] = {orow[i].x, orow[i].y, orow[i].z, orow[i].w};
+    uint32_t n = 0;  // the largest magnitude's bits (those of NaN and infinity above all)
 #pragma unroll
-      for (int k = 0; k < E; ++k) sq += (g[k] * s) * (g[k] * s);
+    for (int k = 0; k < 4; ++k)
+      n = max(n, max((gw[k] & 0x7FFFu) << 16, gw[k] & 0x7FFF0000u));
 #pragma unroll
-      for (int k = 16; k > 0; k >>= 1) sq += __shfl_xor_sync(0xFFFFFFFFu, sq, k);
-      const int z = (int)(__float_as_uint(sqrtf(sq)) >> 23) - 126;  // the norm is below 2^(x + z)
-      e = min(127, 4 - x - z);
-    }
+    for (int k = LR / 2; k > 0; k >>= 1) n = max(n, __shfl_xor_sync(0xFFFFFFFFu, n, k));
+    const int x = (int)(n >> 23);  // biased exponent
+    const int e = n == 0 ? 127 : x == 255 ? 0 : 127 - max(1, x);
     const float up = ldexpf(1.f, e);
     float dl = 0.f;
-    uint32_t p[E / 2];
+    uint32_t p[4];
 #pragma unroll
-    for (int k = 0; k < E; k += 2) {
-      const float2 y = unpack_f16x2(orow[k / 2]);
-      g[k] *= up;
-      g[k + 1] *= up;
-      dl += g[k] * y.x + g[k + 1] * y.y;
-      p[k / 2] = pack_f16x2(g[k], g[k + 1]);
+    for (int k = 0; k < 4; ++k) {
+      float2 g = unpack_bf16x2(gw[k]);
+      const float2 y = unpack_f16x2(ow[k]);
+      g.x *= up;
+      g.y *= up;
+      dl += g.x * y.x + g.y * y.y;
+      p[k] = pack_f16x2(g.x, g.y);
     }
 #pragma unroll
-    for (int k = 16; k > 0; k >>= 1) dl += __shfl_xor_sync(0xFFFFFFFFu, dl, k);
-    if (E == 4)
-      *reinterpret_cast<uint2*>(dos + at) = make_uint2(p[0], p[E / 2 - 1]);
-    else
-      *reinterpret_cast<uint32_t*>(dos + at) = p[0];
-    if (lane == 0) {
-      const int64_t r = (int64_t)h * T + t;
-      stats[r] = t < live ? make_float2(fmaf(lse[r], kLog2e, (float)e), dl) : make_float2(0.f, 0.f);
-      rowexp[r] = (float)e;
+    for (int k = LR / 2; k > 0; k >>= 1) dl += __shfl_xor_sync(0xFFFFFFFFu, dl, k);
+    if (t < T) {
+      *reinterpret_cast<uint4*>(dos + (t * H + h) * D + col) = make_uint4(p[0], p[1], p[2], p[3]);
+      if (lane % LR == 0) {
+        const int64_t r = (int64_t)h * T + t;
+        stats[r] = make_float2(fmaf(ls[i], kLog2e, (float)e), dl);
+        rowexp[r] = (float)e;
+      }
     }
     emin = fminf(emin, (float)e);
   }
+  emin = warp_min(emin);
   if (lane == 0) low[warp] = emin;
   __syncthreads();
   if (threadIdx.x == 0) {
@@ -715,7 +710,6 @@ __global__ void __launch_bounds__(kFThreads, 1)
   __shared__ uint32_t tmem_sh;
   __shared__ int abort_sh;
   volatile int* abort_flag = &abort_sh;
-  pdl_trigger();
 
   uint8_t* Ks = align1024_p(dkv_raw);
   uint8_t* Vs = Ks + SM::kTile;
@@ -756,6 +750,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
   tc_fence_after();
   const uint32_t tmem = tmem_sh;
   pdl_wait();
+  pdl_trigger();  // behind the wait: the dQ kernel may start, and finds everything it reads
   const int G = H / Hkv, parts = G / nh;
   const int per = Hkv * parts;              // items of a tile
   const int items = idx.head[0] * per;
@@ -1126,7 +1121,8 @@ __global__ void __launch_bounds__(kFThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_sh;
-  pdl_wait();
+  // no wait here: the kernel before is dK, dV, which writes nothing that this one reads and
+  // which let it start only when the kernels before itself had completed
   const int G = H / Hkv;
   const bool heads = G % 2 == 0;
   const int items = heads ? idx.head[0] * (H / 2) : idx.head[1] * H;
@@ -1355,6 +1351,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
          i += (int64_t)gridDim.x * blockDim.x)
       o[i] = make_uint4(0u, 0u, 0u, 0u);
   }
+  pdl_wait();  // this kernel is not done before dK, dV is
   tc_fence_before();
   __syncthreads();
   if (abort_sh) settle_ns(2000000);
@@ -1466,13 +1463,12 @@ struct BwdWs {
 
 // Into how many shares a kv head's query heads are split for dK and dV.  One share
 // needs no partial sums (8 bytes written and read per token, share and dimension) but
-// leaves few items: at least four per SM are wanted, so that they even out.
-// 16,384 tokens, 16/2 heads: see the measured times at the launch.
+// leaves few items: at least two per SM are wanted, so that they even out.
 int dkv_parts(int64_t T, int H, int Hkv) {
   const int G = H / Hkv;
   const int64_t tiles = (T + kPackedTile - 1) / kPackedTile;
   for (int p = 1; p < G; ++p)
-    if (G % p == 0 && tiles * Hkv * p >= 4 * (int64_t)gemm_num_sms()) return p;
+    if (G % p == 0 && tiles * Hkv * p >= 2 * (int64_t)gemm_num_sms()) return p;
   return G;
 }
 
