@@ -460,8 +460,8 @@ int packed_index(const int32_t* lengths, const int32_t* prefix, int32_t n_docs, 
  *          already applied); query head h reads kv head h / (H / Hkv).
  *   H % Hkv == 0;  d is 64 or 128.
  *   index, n_docs  of packed_index with this T and n_docs.
- *   o      device fp16 [T, H d];  lse  device fp32 [H, T]: the log-sum-exp of the
- *          scaled scores.  Padding rows get o = 0 and lse = -inf.
+ *   o      device fp16 [T, H d], 32-byte aligned;  lse  device fp32 [H, T]: the
+ *          log-sum-exp of the scaled scores.  Padding rows get o = 0 and lse = -inf.
  * Products of fp16 operands (the probabilities rounded to fp16), fp32 softmax and
  * sums.  A document's values never reach another's rows, not even as 0 * inf.
  * Asynchronous, deterministic. */
@@ -473,9 +473,10 @@ size_t packed_attention_workspace_bytes(int64_t T, int32_t H, int32_t Hkv, int32
 
 /* packed_attention_bwd - the gradient of packed_attention_fwd.
  *   o, lse  its outputs;  dout  device bf16 [T, H d].
- *   dqkv    device bf16 [T, (H + 2 Hkv) d] (overwritten; 0 in padding rows): dq, and dk
- *           and dv summed in fp32 over the query heads of each kv head.
- *   ws      device workspace of packed_attention_workspace_bytes(T, H, Hkv, d).
+ *   dqkv    device bf16 [T, (H + 2 Hkv) d], 32-byte aligned (overwritten; 0 in padding
+ *           rows): dq, and dk and dv summed in fp32 over the query heads of each kv head.
+ *   ws      device workspace of packed_attention_workspace_bytes(T, H, Hkv, d) bytes,
+ *           32-byte aligned.
  * The score gradients multiply in fp16 after each row of dout is scaled by the power
  * of two that brings its largest magnitude to [1, 2), so their range does not matter; a
  * row of v whose norm is above 1447 latches LSQ_DEV_ERR_NONFINITE (its score gradients may

@@ -40,6 +40,36 @@ __device__ __forceinline__ float ex2(float x) {
   return r;
 }
 
+// Two fp32 operations at a time (each rounded as the single ones are).
+__device__ __forceinline__ uint64_t pack_f32x2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 unpack_f32x2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// 32 bytes of a row (a whole sector) in one store: rows are written by a lane each, and
+// two 16-byte halves of a sector cost two passes of the store path (an output tile of
+// 128 x 128 took 3000 to 6500 cycles to write that way).
+__device__ __forceinline__ void st_global32(void* p, const uint32_t (&v)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
 // ------------------------------------------------------------------ forward
 // A persistent CTA per SM takes work items in turn.  An item is two streams of 128
 // query rows of one document that read the same K and V tiles: two query heads of a kv
@@ -383,11 +413,20 @@ __global__ void __launch_bounds__(kFThreads, 1)
     const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t to = trow + kColO + (uint32_t)s * 128;
     uint32_t ns[2] = {0, 0}, nv = 0, no = 0;  // steps of each buffer, P V products, items
+    const uint64_t sl22 = pack_f32x2(sl2, sl2);
     bool ok = true;
-    for (int k = 0, w; ok && (w = deal(k, items)) >= 0; ++k) {
-      const FwdItem it = fwd_item(idx, w, H, heads, s);
+    int w = deal(0, items);
+    FwdItem it;
+    if (w >= 0) it = fwd_item(idx, w, H, heads, s);
+    for (int k = 1; ok && w >= 0; ++k) {
+      // (the next item is looked up while this one's last product runs)
+      const int w1 = deal(k, items);
       const int n = it.n;
-      if (n == 0) continue;
+      if (n == 0) {
+        w = w1;
+        if (w >= 0) it = fwd_item(idx, w, H, heads, s);
+        continue;
+      }
       const int q = it.row + r;
       const int kmax = min(max(q, it.prompt - 1), it.end - 1);  // the row's last key
       const int kall = min(max(it.row + (warp & 3) * 32, it.prompt - 1), it.end - 1);
@@ -445,22 +484,24 @@ __global__ void __launch_bounds__(kFThreads, 1)
         }
         // P = exp2(s sl2 - m_ref) in fp16 (masked scores are -inf, so their p is 0) over
         // the scores' own columns, and the row sum
-        const float nm = -m_ref;
-        float rs0 = 0.f, rs1 = 0.f;
+        const uint64_t nm2 = pack_f32x2(-m_ref, -m_ref);
+        uint64_t rs = 0;  // (0, 0)
 #pragma unroll
         for (int c = 0; c < kStep / 32; ++c) {
           uint32_t pk[16];
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
-            const float p0 = ex2(fmaf(__uint_as_float(sv[32 * c + e]), sl2, nm));
-            const float p1 = ex2(fmaf(__uint_as_float(sv[32 * c + e + 1]), sl2, nm));
-            rs0 += p0;
-            rs1 += p1;
+            const float2 x = unpack_f32x2(fma_f32x2(
+                pack_f32x2(__uint_as_float(sv[32 * c + e]), __uint_as_float(sv[32 * c + e + 1])),
+                sl22, nm2));
+            const float p0 = ex2(x.x), p1 = ex2(x.y);
+            rs = add_f32x2(rs, pack_f32x2(p0, p1));
             pk[e >> 1] = pack_f16x2(p0, p1);
           }
           tmem_st16(ts + 16 * c, pk);
         }
-        l_run += rs0 + rs1;
+        const float2 rsum = unpack_f32x2(rs);
+        l_run += rsum.x + rsum.y;
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -469,14 +510,17 @@ __global__ void __launch_bounds__(kFThreads, 1)
       // -------------------------------------------------------------- epilogue
       // (a barrier of its own: pv_done may be two phases on, where a wait for the
       // phase before the last would not return)
+      const bool live = q < it.end;
+      uint16_t* orow = out + (int64_t)q * H * D + (int64_t)it.head * D;
+      float* lrow = lse_out + (int64_t)it.head * T + q;
+      w = w1;
+      if (w >= 0) it = fwd_item(idx, w, H, heads, s);
       ok = ok && wait_all(&o_full[s], no);
       if (!ok) break;
       ++no;
       nv += n;
       tc_fence_after();
       const float inv = 1.f / l_run;
-      const bool live = q < it.end;
-      uint16_t* orow = out + (int64_t)q * H * D + (int64_t)it.head * D;
       uint32_t ov[D];
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) tmem_ld32(to + 32 * c, ov + 32 * c);
@@ -486,15 +530,15 @@ __global__ void __launch_bounds__(kFThreads, 1)
       if (lane == 0) mbar_arrive(smem_u32(&o_free[s]));
       if (live) {
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-          uint32_t pk[4];
+        for (int c = 0; c < D / 16; ++c) {
+          uint32_t pk[8];
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            pk[e] = pack_f16x2(__uint_as_float(ov[8 * c + 2 * e]) * inv,
-                               __uint_as_float(ov[8 * c + 2 * e + 1]) * inv);
-          *reinterpret_cast<uint4*>(orow + 8 * c) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+          for (int e = 0; e < 8; ++e)
+            pk[e] = pack_f16x2(__uint_as_float(ov[16 * c + 2 * e]) * inv,
+                               __uint_as_float(ov[16 * c + 2 * e + 1]) * inv);
+          st_global32(orow + 16 * c, pk);
         }
-        lse_out[(int64_t)it.head * T + q] = (m_ref + log2f(l_run)) * 0.69314718055994531f;
+        *lrow = (m_ref + log2f(l_run)) * 0.69314718055994531f;
       }
     }
   }
@@ -641,17 +685,17 @@ template <int D>
 __device__ __forceinline__ void store_grad_row(const uint32_t (&raw)[D], float scale,
                                                const float2* cs, uint16_t* out) {
 #pragma unroll
-  for (int c = 0; c < D / 16; ++c) {
-    float a[8], b[8];
+  for (int c = 0; c < D / 32; ++c) {
+    float a[16], b[16];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      a[e] = __uint_as_float(raw[8 * c + e]) * scale;
-      b[e] = __uint_as_float(raw[D / 2 + 8 * c + e]) * scale;
+    for (int e = 0; e < 16; ++e) {
+      a[e] = __uint_as_float(raw[16 * c + e]) * scale;
+      b[e] = __uint_as_float(raw[D / 2 + 16 * c + e]) * scale;
     }
     if (cs) {
 #pragma unroll
-      for (int e = 0; e < 8; e += 2) {
-        const float4 f = __ldg(reinterpret_cast<const float4*>(cs + 8 * c + e));
+      for (int e = 0; e < 16; e += 2) {
+        const float4 f = __ldg(reinterpret_cast<const float4*>(cs + 16 * c + e));
         const float x0 = a[e], y0 = b[e], x1 = a[e + 1], y1 = b[e + 1];
         a[e] = x0 * f.x + y0 * f.y;
         b[e] = y0 * f.x - x0 * f.y;
@@ -659,12 +703,14 @@ __device__ __forceinline__ void store_grad_row(const uint32_t (&raw)[D], float s
         b[e + 1] = y1 * f.z - x1 * f.w;
       }
     }
-    *reinterpret_cast<uint4*>(out + 8 * c) =
-        make_uint4(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]), pack_bf16x2(a[4], a[5]),
-                   pack_bf16x2(a[6], a[7]));
-    *reinterpret_cast<uint4*>(out + D / 2 + 8 * c) =
-        make_uint4(pack_bf16x2(b[0], b[1]), pack_bf16x2(b[2], b[3]), pack_bf16x2(b[4], b[5]),
-                   pack_bf16x2(b[6], b[7]));
+    uint32_t pa[8], pb[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      pa[e] = pack_bf16x2(a[2 * e], a[2 * e + 1]);
+      pb[e] = pack_bf16x2(b[2 * e], b[2 * e + 1]);
+    }
+    st_global32(out + 16 * c, pa);
+    st_global32(out + D / 2 + 16 * c, pb);
   }
 }
 
@@ -1037,10 +1083,12 @@ __global__ void __launch_bounds__(kFThreads, 1)
         } else {
           float* out = (b ? dk : dv) + ((int64_t)kpos * Hkv * parts + it.h0 / nh) * D;
 #pragma unroll
-          for (int e = 0; e < D; e += 4)
-            *reinterpret_cast<float4*>(out + e) =
-                make_float4(__uint_as_float(acc[e]) * f, __uint_as_float(acc[e + 1]) * f,
-                            __uint_as_float(acc[e + 2]) * f, __uint_as_float(acc[e + 3]) * f);
+          for (int e = 0; e < D; e += 8) {
+            uint32_t v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = __float_as_uint(__uint_as_float(acc[e + i]) * f);
+            st_global32(out + e, v);
+          }
         }
       }
     }
@@ -1532,6 +1580,8 @@ int bwd_t(const uint16_t* qkv, const PackedIndex& x, const uint16_t* o, const fl
   return LSQ_OK;
 }
 
+bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
+
 int check_heads(int64_t T, int32_t H, int32_t Hkv, int32_t d, const char* who) {
   if (H <= 0 || Hkv <= 0 || H % Hkv != 0 || H > 65535)
     return set_error(LSQ_ERR_SHAPE, "%s: H must be a multiple of Hkv, at most 65535", who);
@@ -1587,8 +1637,9 @@ extern "C" int packed_attention_fwd(const uint16_t* qkv, const int32_t* index, i
   LSQ_TRY(check_packed(T, n_docs, index, "packed_attention_fwd"));
   LSQ_TRY(check_heads(T, H, Hkv, d, "packed_attention_fwd"));
   if (!qkv || !o || !lse) return set_error(LSQ_ERR_INVALID, "packed_attention_fwd: null pointer");
-  if (!aligned16(qkv) || !aligned16(o) || !aligned16(lse))
-    return set_error(LSQ_ERR_ALIGN, "packed_attention_fwd: pointers must be 16-byte aligned");
+  if (!aligned16(qkv) || !aligned32(o) || !aligned16(lse))
+    return set_error(LSQ_ERR_ALIGN,
+                     "packed_attention_fwd: pointers must be 16-byte aligned, o 32-byte");
   return launch_packed_attention_fwd(qkv, index, n_docs, T, H, Hkv, d, o, lse,
                                      static_cast<cudaStream_t>(stream));
 }
@@ -1608,12 +1659,14 @@ extern "C" int packed_attention_bwd(const uint16_t* qkv, const int32_t* index, i
   LSQ_TRY(check_heads(T, H, Hkv, d, "packed_attention_bwd"));
   if (!qkv || !o || !lse || !dout || !dqkv)
     return set_error(LSQ_ERR_INVALID, "packed_attention_bwd: null pointer");
-  if (!aligned16(qkv) || !aligned16(o) || !aligned16(lse) || !aligned16(dout) || !aligned16(dqkv))
-    return set_error(LSQ_ERR_ALIGN, "packed_attention_bwd: pointers must be 16-byte aligned");
+  if (!aligned16(qkv) || !aligned16(o) || !aligned16(lse) || !aligned16(dout) || !aligned32(dqkv))
+    return set_error(LSQ_ERR_ALIGN,
+                     "packed_attention_bwd: pointers must be 16-byte aligned, dqkv 32-byte");
   const size_t need = packed_attention_ws_bytes(T, H, Hkv, d);
   if (!ws || ws_bytes < need)
     return set_error(LSQ_ERR_WORKSPACE, "packed_attention_bwd: workspace %zu < %zu", ws_bytes, need);
-  if (!aligned16(ws)) return set_error(LSQ_ERR_ALIGN, "packed_attention_bwd: unaligned workspace");
+  if (!aligned32(ws))
+    return set_error(LSQ_ERR_ALIGN, "packed_attention_bwd: the workspace must be 32-byte aligned");
   return launch_packed_attention_bwd(qkv, index, n_docs, o, lse, dout, T, H, Hkv, d, nullptr, dqkv,
                                      ws, ws_bytes, static_cast<cudaStream_t>(stream));
 }

@@ -20,6 +20,7 @@ def L():
 _raw = np.zeros(4096 + 64, np.uint8)
 P = ctypes.c_void_p((_raw.ctypes.data + 63) // 64 * 64)    # aligned; never dereferenced
 ODD = ctypes.c_void_p(P.value + 4)
+HALF = ctypes.c_void_p(P.value + 16)
 
 
 def _rc(L, name, *args):
@@ -46,7 +47,7 @@ def test_packed_entries(L):
     for at, val, rc in ((0, None, inval), (1, None, inval), (2, 0, shape), (3, 0, shape),
                         (4, 3, shape), (4, 0, shape), (5, 0, shape), (6, 96, shape),
                         (7, None, inval), (8, None, inval), (0, ODD, align), (1, ODD, align),
-                        (7, ODD, align), (8, ODD, align), (3, 1 << 30, shape)):
+                        (7, ODD, align), (7, HALF, align), (8, ODD, align), (3, 1 << 30, shape)):
         args = list(ok)
         args[at] = val
         if (at, val) == (3, 1 << 30):
@@ -59,7 +60,8 @@ def test_packed_entries(L):
     ok = [P, P, 1, P, P, P, 4, 4, 2, 64, P, P, need, None]
     for at, val, rc in ((0, None, inval), (3, None, inval), (4, None, inval), (5, None, inval),
                         (10, None, inval), (11, None, work), (12, need - 1, work),
-                        (11, ODD, align), (5, ODD, align), (10, ODD, align), (9, 80, shape),
+                        (11, ODD, align), (11, HALF, align), (5, ODD, align),
+                        (10, ODD, align), (10, HALF, align), (9, 80, shape),
                         (7, 5, shape)):
         args = list(ok)
         args[at] = val
