@@ -535,6 +535,7 @@ int lora_adamw_step(float* lora, const float* grad, const lsq_adamw* opt, int64_
  *             the codes those of the nearest root, a v > 0 never stored as 0; a
  *             block whose largest magnitude is below 2^-126 is stored as zeros.
  *             All-zero codes and scales are the initial state.
+ *   0 <= beta < 1;  eps at least 2^-126.
  *   grad_bits  32: g fp32;  16: g bf16.
  *   step_dev  device int32 or NULL: read instead of step, so that a captured update
  *             can be replayed as the count advances (below 1 counts as 1).

@@ -11,8 +11,8 @@
 // explode).  The code is that of the nearest root, rint(127 sqrt(|m| / a)) and
 // rint(255 (v / a)^(1/4)), of the moments as fp32 numbers: every product and sum of
 // their update is rounded once (no contraction), so the state is defined bit for bit.
-// The root is taken with the approximate square root, whose error moves it by less
-// than kNear; only next to a border is the choice made again, in fp64.
+// The root is taken with the approximate square root; only next to a border, closer than
+// its error, is the choice made again, in fp64.
 #include <math.h>
 
 #include <algorithm>
@@ -61,41 +61,76 @@ struct MtArgs {
   MtEntry e[N];
 };
 
-__device__ __forceinline__ float sqrt_approx(float x) {
+// Approximate square root and reciprocal (relative errors 2^-23); subnormal inputs count
+// as 0.
+__device__ __forceinline__ float sqrt_ftz(float x) {
   float r;
-  asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float rcp_ftz(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// Pairs of fp32 numbers, an operation on both at once.  A paired product and a paired sum
+// behind it are contracted to one rounding in spite of their modifiers, so where both
+// roundings count (the moments) the sums are single ones.
+__device__ __forceinline__ uint64_t two(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 both(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
 
-// Nearest integer to y = 127 sqrt(x / a), x >= 0, from an approximation of y; within
-// 1e-4 of a border k + 1/2 the choice is x 254^2 against a (2 k + 1)^2 (both exact
-// in fp64), a tie to the even code.
-__device__ __forceinline__ int code_m(float x, float a, float inv_a) {
-  const float y = 127.f * sqrt_approx(x * inv_a);
-  int k = __float2int_rn(y);
-  const float kb = floorf(y);
-  if (fabsf(y - kb - 0.5f) < 1e-4f) {
-    const int b = (int)kb;
-    const double l = (double)x * 64516.0, r = (double)a * (double)((2 * b + 1) * (2 * b + 1));
-    k = l > r ? b + 1 : l < r ? b : b + (b & 1);
-  }
-  return min(k, 127);
+// The codes are rounded by adding 1.5 2^23, which leaves the nearest integer (ties to
+// even) in the low bits without a conversion: those run on the pipe that the square
+// roots need.  y is 127 sqrt(x / a), off by at most 127 (3/2 2^-23) and a rounding, less
+// than 4e-5, or 255 (x / a)^(1/4), off by at most 255 (2.2 2^-23) and a rounding, less
+// than 9e-5.  Where y lies within kNear of a border, the code is taken from the exact
+// comparison: x 254^2 against a (2 b + 1)^2 (both exact in fp64), x 510^4 against
+// a (2 b + 1)^4; a tie goes to the even code.
+constexpr float kRound = 12582912.f;
+constexpr float kNear = 2e-4f;
+__device__ __forceinline__ int exact_m(float x, float a, float y) {
+  const int b = (int)floorf(y);
+  if (fabsf(y - (float)b - 0.5f) > kNear) return (int)rintf(y);
+  const double l = (double)x * 64516.0, r = (double)a * (double)((2 * b + 1) * (2 * b + 1));
+  return l > r ? b + 1 : l < r ? b : b + (b & 1);
 }
-
-// Nearest integer to y = 255 (x / a)^(1/4), as above with x 510^4 against a (2 k + 1)^4.
-__device__ __forceinline__ int code_v(float x, float a, float inv_a) {
-  const float y = 255.f * sqrt_approx(sqrt_approx(x * inv_a));
-  int k = __float2int_rn(y);
-  const float kb = floorf(y);
-  if (fabsf(y - kb - 0.5f) < 2e-4f) {
-    const int b = (int)kb;
+__device__ __forceinline__ int exact_v(float x, float a, float y) {
+  const int b = (int)floorf(y);
+  int k = (int)rintf(y);
+  if (fabsf(y - (float)b - 0.5f) <= kNear) {
     const double o = (double)((2 * b + 1) * (2 * b + 1));
     const double l = (double)x * 67652010000.0, r = (double)a * (o * o);
     k = l > r ? b + 1 : l < r ? b : b + (b & 1);
   }
-  k = min(k, 255);
   return x > 0.f ? max(k, 1) : k;
 }
+__device__ __forceinline__ float inv_root(float a) { return __fdiv_rn(1.f, __fsqrt_rn(a)); }
+// With a scale of at least 2^-86 a subnormal x has code 0 or 1 whatever its root, so the
+// flushing root will do; below that the exact one is taken.
+constexpr float kFlushScale = 1.2924697e-26f;
 
 // The values the codes stand for: fl32(c |c| / 127^2) at c + 128, and fl32(q^4 / 255^4).
 __device__ __forceinline__ float level_m(int c) {
@@ -106,23 +141,51 @@ __device__ __forceinline__ float level_v(int q) {
   return (float)(d * d / 4228250625.0);
 }
 
-__device__ __forceinline__ float warp_max_pos(float x) {  // x >= 0: the bits order as the values
-  return __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(x)));
-}
 // A block's scale: its largest magnitude, or 0 (every code 0) below the normal range.
 __device__ __forceinline__ float scale_of(float top) { return top < 1.17549435e-38f ? 0.f : top; }
 
+// Four elements of a tensor's array at offset o, of which `in` exist.
+template <class T4, class T>
+__device__ __forceinline__ T4 load4(const void* base, int64_t o, int in) {
+  T4 r;
+  if (in >= 4) {
+    r = *reinterpret_cast<const T4*>(static_cast<const T*>(base) + o);
+  } else {
+    T* e = reinterpret_cast<T*>(&r);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) e[i] = i < in ? static_cast<const T*>(base)[o + i] : T(0);
+  }
+  return r;
+}
+template <class T4, class T>
+__device__ __forceinline__ void store4(void* base, int64_t o, int in, T4 v) {
+  if (in >= 4) {
+    *reinterpret_cast<T4*>(static_cast<T*>(base) + o) = v;
+  } else {
+    const T* e = reinterpret_cast<const T*>(&v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < in) static_cast<T*>(base)[o + i] = e[i];
+  }
+}
+struct alignas(8) U16x4 {
+  uint16_t v[4];
+};
+
 // One warp takes a block of 256 elements, lane l elements 4 l .. 4 l + 3 and 128 + 4 l
 // .. 128 + 4 l + 3, so that every load and store of a warp is contiguous.  Memory
-// bound: 28 bytes per element with an fp32 state, 16 and two scales per block with 8 bits.
+// bound by 28 bytes per element with an fp32 state, 16 and two scales per block with 8
+// bits; there the arithmetic comes close behind (a hundred instructions per element took
+// 205 us for 41.9 M parameters, 3.3 TB/s), hence the pairs, the flushing roots and the
+// one branch for all borders of a thread.
 template <int BITS, int GBITS, int N>
-__global__ void __launch_bounds__(kMtThreads)
+__global__ void __launch_bounds__(kMtThreads, 4)
     adamw_multi_kernel(const __grid_constant__ MtArgs<N> a) {
   __shared__ float lm[BITS == 8 ? 256 : 1], lv[BITS == 8 ? 256 : 1];
   __shared__ float bc[2];
   pdl_trigger();
   if (BITS == 8) {
-    lm[threadIdx.x] = level_m((int)threadIdx.x - 128);
+    lm[threadIdx.x] = level_m((int)(int8_t)threadIdx.x);  // by the code's byte
     lv[threadIdx.x] = level_v((int)threadIdx.x);
   }
   pdl_wait();
@@ -139,7 +202,8 @@ __global__ void __launch_bounds__(kMtThreads)
   __syncthreads();
   const float inv_bc1 = bc[0], isb2 = bc[1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  bool bad = false;
+  const uint64_t b1 = two(a.h.b1, a.h.b1), b2 = two(a.h.b2, a.h.b2);
+  const uint64_t c1 = two(a.h.c1, a.h.c1), c2 = two(a.h.c2, a.h.c2);
   for (uint32_t c = blockIdx.x; c < a.h.chunks; c += gridDim.x) {
     int lo = 0, hi = a.h.n - 1;  // the last tensor whose first chunk is at or before c
     while (lo < hi) {
@@ -151,12 +215,12 @@ __global__ void __launch_bounds__(kMtThreads)
     }
     const MtEntry& e = a.e[lo];
     const int64_t base = (int64_t)(c - e.chunk0) * kChunk + warp * kBlk;
-    const int64_t left = e.n - base;
-    if (left <= 0) continue;  // uniform in the warp
+    if (base >= e.n) continue;  // uniform in the warp
+    const int left = (int)min((int64_t)kBlk, e.n - base);
     const float lr = e.lr, decay = 1.f - lr * e.wd, rate = lr * inv_bc1;
-    float* __restrict__ pp = e.p + base;
-    float p[8], g[8], m[8], v[8];
-    const bool whole = left >= kBlk;
+    float4 p4[2];
+    uint64_t g[4], m[4], v[4];  // element pairs
+    uint32_t mc[2], vc[2];
     float am = 0.f, av = 0.f;
     if (BITS == 8) {
       am = e.ms[base / kBlk];
@@ -164,77 +228,146 @@ __global__ void __launch_bounds__(kMtThreads)
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int o = h * 128 + lane * 4;
-      if (whole) {
-        const float4 x = *reinterpret_cast<const float4*>(pp + o);
-        p[4 * h] = x.x; p[4 * h + 1] = x.y; p[4 * h + 2] = x.z; p[4 * h + 3] = x.w;
-        if (GBITS == 32) {
-          const float4 y = *reinterpret_cast<const float4*>(static_cast<const float*>(e.g) + base + o);
-          g[4 * h] = y.x; g[4 * h + 1] = y.y; g[4 * h + 2] = y.z; g[4 * h + 3] = y.w;
-        } else {
-          const uint2 y =
-              *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(e.g) + base + o);
-          const float2 y0 = unpack_bf16x2(y.x), y1 = unpack_bf16x2(y.y);
-          g[4 * h] = y0.x; g[4 * h + 1] = y0.y; g[4 * h + 2] = y1.x; g[4 * h + 3] = y1.y;
-        }
-        if (BITS == 8) {
-          const char4 cm = *reinterpret_cast<const char4*>(static_cast<int8_t*>(e.m) + base + o);
-          const uchar4 cv = *reinterpret_cast<const uchar4*>(static_cast<uint8_t*>(e.v) + base + o);
-          m[4 * h] = am * lm[cm.x + 128]; m[4 * h + 1] = am * lm[cm.y + 128];
-          m[4 * h + 2] = am * lm[cm.z + 128]; m[4 * h + 3] = am * lm[cm.w + 128];
-          v[4 * h] = av * lv[cv.x]; v[4 * h + 1] = av * lv[cv.y];
-          v[4 * h + 2] = av * lv[cv.z]; v[4 * h + 3] = av * lv[cv.w];
-        } else {
-          const float4 y = *reinterpret_cast<const float4*>(static_cast<float*>(e.m) + base + o);
-          const float4 z = *reinterpret_cast<const float4*>(static_cast<float*>(e.v) + base + o);
-          m[4 * h] = y.x; m[4 * h + 1] = y.y; m[4 * h + 2] = y.z; m[4 * h + 3] = y.w;
-          v[4 * h] = z.x; v[4 * h + 1] = z.y; v[4 * h + 2] = z.z; v[4 * h + 3] = z.w;
-        }
+      const int o = h * 128 + lane * 4, in = left - o;
+      p4[h] = load4<float4, float>(e.p, base + o, in);
+      if (GBITS == 32) {
+        const float4 y = load4<float4, float>(e.g, base + o, in);
+        g[2 * h] = two(y.x, y.y);
+        g[2 * h + 1] = two(y.z, y.w);
       } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const bool in = o + i < left;
-          p[4 * h + i] = in ? pp[o + i] : 0.f;
-          g[4 * h + i] = !in ? 0.f
-                         : GBITS == 32
-                             ? static_cast<const float*>(e.g)[base + o + i]
-                             : bf16_bits_to_float(static_cast<const uint16_t*>(e.g)[base + o + i]);
-          if (BITS == 8) {
-            m[4 * h + i] = in ? am * lm[static_cast<int8_t*>(e.m)[base + o + i] + 128] : 0.f;
-            v[4 * h + i] = in ? av * lv[static_cast<uint8_t*>(e.v)[base + o + i]] : 0.f;
-          } else {
-            m[4 * h + i] = in ? static_cast<float*>(e.m)[base + o + i] : 0.f;
-            v[4 * h + i] = in ? static_cast<float*>(e.v)[base + o + i] : 0.f;
-          }
-        }
+        const U16x4 y = load4<U16x4, uint16_t>(e.g, base + o, in);
+        g[2 * h] = two(bf16_bits_to_float(y.v[0]), bf16_bits_to_float(y.v[1]));
+        g[2 * h + 1] = two(bf16_bits_to_float(y.v[2]), bf16_bits_to_float(y.v[3]));
+      }
+      if (BITS == 8) {
+        mc[h] = load4<uint32_t, uint8_t>(e.m, base + o, in);
+        vc[h] = load4<uint32_t, uint8_t>(e.v, base + o, in);
+      } else {
+        const float4 y = load4<float4, float>(e.m, base + o, in);
+        const float4 z = load4<float4, float>(e.v, base + o, in);
+        m[2 * h] = two(y.x, y.y);
+        m[2 * h + 1] = two(y.z, y.w);
+        v[2 * h] = two(z.x, z.y);
+        v[2 * h + 1] = two(z.z, z.w);
       }
     }
-    float tm = 0.f, tv = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float m1 = __fadd_rn(__fmul_rn(a.h.b1, m[i]), __fmul_rn(a.h.c1, g[i]));
-      const float v1 = __fadd_rn(__fmul_rn(a.h.b2, v[i]), __fmul_rn(__fmul_rn(a.h.c2, g[i]), g[i]));
-      // a gradient whose moments leave the finite range changes nothing of its element
-      if (fabsf(m1) <= 3.402823466e38f && v1 <= 3.402823466e38f) {
-        m[i] = m1;
-        v[i] = v1;
-        p[i] = p[i] * decay - rate * __fdividef(m1, sqrt_approx(v1) * isb2 + a.h.eps);
-      } else {
-        bad = true;
-      }
-      tm = fmaxf(tm, fabsf(m[i]));
-      tv = fmaxf(tv, v[i]);
-    }
-    int cm[8], cv[8];
     if (BITS == 8) {
-      am = scale_of(warp_max_pos(tm));
-      av = scale_of(warp_max_pos(tv));
-      const float im = am > 0.f ? __fdiv_rn(1.f, am) : 0.f, iv = av > 0.f ? __fdiv_rn(1.f, av) : 0.f;
 #pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t wm = mc[j >> 1] >> (16 * (j & 1)), wv = vc[j >> 1] >> (16 * (j & 1));
+        m[j] = mul2(two(am, am), two(lm[wm & 255u], lm[(wm >> 8) & 255u]));
+        v[j] = mul2(two(av, av), two(lv[wv & 255u], lv[(wv >> 8) & 255u]));
+      }
+    }
+    // the moments; the bits of their largest magnitudes (NaN and infinity above all) give
+    // the block's scales and tell whether any is not finite
+    uint32_t tm = 0, tv = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 x0 = both(mul2(b1, m[j])), x1 = both(mul2(c1, g[j]));
+      const float2 y0 = both(mul2(b2, v[j])), y1 = both(mul2(mul2(c2, g[j]), g[j]));
+      const float2 x = make_float2(__fadd_rn(x0.x, x1.x), __fadd_rn(x0.y, x1.y));
+      const float2 y = make_float2(__fadd_rn(y0.x, y1.x), __fadd_rn(y0.y, y1.y));
+      m[j] = two(x.x, x.y);
+      v[j] = two(y.x, y.y);
+      tm = max(tm, max(__float_as_uint(x.x) & 0x7FFFFFFFu, __float_as_uint(x.y) & 0x7FFFFFFFu));
+      tv = max(tv, max(__float_as_uint(y.x), __float_as_uint(y.y)));
+    }
+    uint32_t skip = 0;  // elements whose moments leave the finite range keep everything
+    if (max(tm, tv) >= 0x7F800000u) {
+      atomicOr(a.h.dev_err, DEV_ERR_NONFINITE);
+      tm = tv = 0;
       for (int i = 0; i < 8; ++i) {
-        const int k = am > 0.f ? code_m(fabsf(m[i]), am, im) : 0;
-        cm[i] = m[i] < 0.f ? -k : k;
-        cv[i] = av > 0.f ? code_v(v[i], av, iv) : 0;
+        const int64_t at = base + (i >> 2) * 128 + lane * 4 + (i & 3);
+        float2 x = both(m[0]), y = both(v[0]);
+#pragma unroll
+        for (int j = 1; j < 4; ++j)
+          if (j == i / 2) {
+            x = both(m[j]);
+            y = both(v[j]);
+          }
+        float mi = i & 1 ? x.y : x.x, vi = i & 1 ? y.y : y.x;
+        if (!(fabsf(mi) < INFINITY && vi < INFINITY)) {  // (such an element exists: at < n)
+          skip |= 1u << i;
+          mi = BITS == 8 ? am * lm[static_cast<uint8_t*>(e.m)[at]] : static_cast<float*>(e.m)[at];
+          vi = BITS == 8 ? av * lv[static_cast<uint8_t*>(e.v)[at]] : static_cast<float*>(e.v)[at];
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (j == i / 2) {
+            m[j] = i & 1 ? two(x.x, mi) : two(mi, x.y);
+            v[j] = i & 1 ? two(y.x, vi) : two(vi, y.y);
+          }
+        // (a state that already was not finite counts as zero in the scale)
+        const uint32_t bm = __float_as_uint(mi) & 0x7FFFFFFFu, bv = __float_as_uint(vi) & 0x7FFFFFFFu;
+        tm = max(tm, bm < 0x7F800000u ? bm : 0u);
+        tv = max(tv, bv < 0x7F800000u ? bv : 0u);
+      }
+    }
+    float root[8];
+    {
+      const uint64_t is2 = two(isb2, isb2), ep2 = two(a.h.eps, a.h.eps);
+      const uint64_t de2 = two(decay, decay), nr2 = two(-rate, -rate);
+      float* pf = reinterpret_cast<float*>(p4);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 y = both(v[j]);
+        root[2 * j] = sqrt_ftz(y.x);
+        root[2 * j + 1] = sqrt_ftz(y.y);
+        const float2 d = both(fma2(two(root[2 * j], root[2 * j + 1]), is2, ep2));
+        const uint64_t u = mul2(m[j], two(rcp_ftz(d.x), rcp_ftz(d.y)));
+        const float2 q = both(fma2(u, nr2, mul2(two(pf[2 * j], pf[2 * j + 1]), de2)));
+        if (!(skip >> (2 * j) & 1u)) pf[2 * j] = q.x;
+        if (!(skip >> (2 * j) & 2u)) pf[2 * j + 1] = q.y;
+      }
+    }
+    if (BITS == 8) {
+      am = scale_of(__uint_as_float(__reduce_max_sync(0xFFFFFFFFu, tm)));
+      av = scale_of(__uint_as_float(__reduce_max_sync(0xFFFFFFFFu, tv)));
+      const float im = am > 0.f ? __fdiv_rn(1.f, am) : 0.f, iv = av > 0.f ? inv_root(av) : 0.f;
+      const uint64_t r2 = two(kRound, kRound), nr2 = two(-kRound, -kRound);
+      const uint64_t im2 = two(im, im), iv2 = two(iv, iv), s127 = two(127.f, 127.f),
+                     s255 = two(255.f, 255.f), neg = two(-1.f, -1.f);
+      const bool tiny = av < kFlushScale;
+      float worst = 0.f;  // the largest distance from an integer
+      mc[0] = mc[1] = vc[0] = vc[1] = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 x = both(m[j]), z = both(v[j]);
+        float2 q = both(mul2(two(fabsf(x.x), fabsf(x.y)), im2));
+        uint64_t y = mul2(two(sqrt_ftz(q.x), sqrt_ftz(q.y)), s127);
+        float2 s = both(y);
+        y = two(copysignf(s.x, x.x), copysignf(s.y, x.y));
+        uint64_t t = add2(y, r2);
+        float2 d = both(fma2(add2(t, nr2), neg, y));
+        worst = fmaxf(worst, fmaxf(fabsf(d.x), fabsf(d.y)));
+        float2 k = both(t);
+        mc[j >> 1] |= (__byte_perm(__float_as_uint(k.x), __float_as_uint(k.y), 0x0040) & 0xFFFFu)
+                      << (16 * (j & 1));
+        q = both(mul2(two(root[2 * j], root[2 * j + 1]), iv2));
+        y = mul2(two(sqrt_ftz(q.x), sqrt_ftz(q.y)), s255);
+        t = add2(y, r2);
+        d = both(fma2(add2(t, nr2), neg, y));
+        worst = fmaxf(worst, fmaxf(fabsf(d.x), fabsf(d.y)));
+        k = both(t);
+        // (a v above zero is stored as 1 at least; without a scale as 0)
+        const uint32_t k0 = max(__float_as_uint(k.x) & 0xFFFFu, min(__float_as_uint(z.x), 1u));
+        const uint32_t k1 = max(__float_as_uint(k.y) & 0xFFFFu, min(__float_as_uint(z.y), 1u));
+        vc[j >> 1] |= (__byte_perm(k0, k1, 0x0040) & 0xFFFFu) << (16 * (j & 1));
+      }
+      if (worst > 0.5f - kNear || tiny || am == 0.f) {  // a border near by, or no usual scale
+        mc[0] = mc[1] = vc[0] = vc[1] = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float2 x = both(m[i / 2]), z = both(v[i / 2]);
+          const float mi = i & 1 ? x.y : x.x, vi = i & 1 ? z.y : z.x;
+          const float ri = tiny ? __fsqrt_rn(vi) : root[i];
+          int k = am > 0.f ? exact_m(fabsf(mi), am, 127.f * sqrt_ftz(fabsf(mi) * im)) : 0;
+          k = mi < 0.f ? -k : k;
+          mc[i / 4] |= (uint32_t)(k & 255) << (8 * (i & 3));
+          k = av > 0.f ? exact_v(vi, av, 255.f * sqrt_ftz(ri * iv)) : 0;
+          vc[i / 4] |= (uint32_t)(k & 255) << (8 * (i & 3));
+        }
       }
       if (lane == 0) {
         e.ms[base / kBlk] = am;
@@ -243,40 +376,19 @@ __global__ void __launch_bounds__(kMtThreads)
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int o = h * 128 + lane * 4;
-      if (whole) {
-        *reinterpret_cast<float4*>(pp + o) =
-            make_float4(p[4 * h], p[4 * h + 1], p[4 * h + 2], p[4 * h + 3]);
-        if (BITS == 8) {
-          *reinterpret_cast<char4*>(static_cast<int8_t*>(e.m) + base + o) =
-              make_char4((signed char)cm[4 * h], (signed char)cm[4 * h + 1],
-                         (signed char)cm[4 * h + 2], (signed char)cm[4 * h + 3]);
-          *reinterpret_cast<uchar4*>(static_cast<uint8_t*>(e.v) + base + o) =
-              make_uchar4((unsigned char)cv[4 * h], (unsigned char)cv[4 * h + 1],
-                          (unsigned char)cv[4 * h + 2], (unsigned char)cv[4 * h + 3]);
-        } else {
-          *reinterpret_cast<float4*>(static_cast<float*>(e.m) + base + o) =
-              make_float4(m[4 * h], m[4 * h + 1], m[4 * h + 2], m[4 * h + 3]);
-          *reinterpret_cast<float4*>(static_cast<float*>(e.v) + base + o) =
-              make_float4(v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]);
-        }
+      const int o = h * 128 + lane * 4, in = left - o;
+      store4<float4, float>(e.p, base + o, in, p4[h]);
+      if (BITS == 8) {
+        store4<uint32_t, uint8_t>(e.m, base + o, in, mc[h]);
+        store4<uint32_t, uint8_t>(e.v, base + o, in, vc[h]);
       } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (o + i >= left) continue;
-          pp[o + i] = p[4 * h + i];
-          if (BITS == 8) {
-            static_cast<int8_t*>(e.m)[base + o + i] = (int8_t)cm[4 * h + i];
-            static_cast<uint8_t*>(e.v)[base + o + i] = (uint8_t)cv[4 * h + i];
-          } else {
-            static_cast<float*>(e.m)[base + o + i] = m[4 * h + i];
-            static_cast<float*>(e.v)[base + o + i] = v[4 * h + i];
-          }
-        }
+        const float2 x0 = both(m[2 * h]), x1 = both(m[2 * h + 1]);
+        const float2 y0 = both(v[2 * h]), y1 = both(v[2 * h + 1]);
+        store4<float4, float>(e.m, base + o, in, make_float4(x0.x, x0.y, x1.x, x1.y));
+        store4<float4, float>(e.v, base + o, in, make_float4(y0.x, y0.y, y1.x, y1.y));
       }
     }
   }
-  if (bad) atomicOr(a.h.dev_err, DEV_ERR_NONFINITE);
 }
 
 // Codes to values and back, for a state that is saved, loaded or inspected.
@@ -288,21 +400,27 @@ __global__ void __launch_bounds__(256)
   lut[threadIdx.x] = is_signed ? level_m((int)(int8_t)threadIdx.x) : level_v((int)threadIdx.x);
   pdl_wait();
   __syncthreads();
-  const int64_t n16 = n / 16;
-  const int64_t step = (int64_t)gridDim.x * 256;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n16; i += step) {
-    const uint4 c = reinterpret_cast<const uint4*>(codes)[i];
-    const float a = __ldg(scale + (i >> 4));
-    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+  // a warp takes 512 codes, lane l codes 4 l .. 4 l + 3 of each 128, so that loads and
+  // stores of a warp are contiguous (memory bound: 5 bytes per value)
+  const int lane = threadIdx.x & 31;
+  const int64_t warps = (int64_t)gridDim.x * 8;
+  for (int64_t b = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * 512; b < n; b += warps * 512) {
+    if (b + 512 <= n) {
+      uint32_t w[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      reinterpret_cast<float4*>(out)[i * 4 + k] =
-          make_float4(a * lut[w[k] & 255u], a * lut[(w[k] >> 8) & 255u],
-                      a * lut[(w[k] >> 16) & 255u], a * lut[w[k] >> 24]);
-  }
-  if (blockIdx.x == 0 && threadIdx.x < n - n16 * 16) {
-    const int64_t i = n16 * 16 + threadIdx.x;
-    out[i] = scale[i / kBlk] * lut[codes[i]];
+      for (int k = 0; k < 4; ++k)
+        w[k] = __ldg(reinterpret_cast<const uint32_t*>(codes + b + k * 128) + lane);
+      const float a0 = __ldg(scale + b / kBlk), a1 = __ldg(scale + b / kBlk + 1);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float a = k < 2 ? a0 : a1;
+        __stcs(reinterpret_cast<float4*>(out + b + k * 128) + lane,
+               make_float4(a * lut[w[k] & 255u], a * lut[(w[k] >> 8) & 255u],
+                           a * lut[(w[k] >> 16) & 255u], a * lut[w[k] >> 24]));
+      }
+    } else {
+      for (int64_t i = b + lane; i < n; i += 32) out[i] = scale[i / kBlk] * lut[codes[i]];
+    }
   }
 }
 
@@ -328,14 +446,15 @@ __global__ void __launch_bounds__(256)
       }
       top = fmaxf(top, fabsf(f[i]));
     }
-    const float a = scale_of(warp_max_pos(top));
-    const float ia = a > 0.f ? __fdiv_rn(1.f, a) : 0.f;
+    const float a = scale_of(__uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top))));
+    const float ia = a > 0.f ? is_signed ? __fdiv_rn(1.f, a) : inv_root(a) : 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int64_t at = b * kBlk + i * 32 + lane;
       int c = 0;
       if (a > 0.f) {
-        c = is_signed ? code_m(fabsf(f[i]), a, ia) : code_v(f[i], a, ia);
+        c = is_signed ? exact_m(fabsf(f[i]), a, 127.f * sqrt_ftz(fabsf(f[i]) * ia))
+                      : exact_v(f[i], a, 255.f * sqrt_ftz(__fsqrt_rn(f[i]) * ia));
         if (is_signed && f[i] < 0.f) c = -c;
       }
       if (at < n) codes[at] = (uint8_t)c;
@@ -494,9 +613,9 @@ extern "C" int adamw_multi_step(const lsq_adamw_tensor* tensors, int32_t n_tenso
   if (!opt->step_dev && opt->step < 1)
     return set_error(LSQ_ERR_SHAPE, "adamw_multi_step: step counts from 1");
   if (!(opt->beta1 >= 0.f && opt->beta1 < 1.f) || !(opt->beta2 >= 0.f && opt->beta2 < 1.f) ||
-      !(opt->eps > 0.f) || !std::isfinite(opt->eps))
+      !(opt->eps >= 1.17549435e-38f) || !std::isfinite(opt->eps))
     return set_error(LSQ_ERR_INVALID,
-                     "adamw_multi_step: need 0 <= beta < 1 and a positive finite eps");
+                     "adamw_multi_step: need 0 <= beta < 1 and a finite eps of at least 2^-126");
   LSQ_TRY(check_tensors(tensors, n_tensors, opt->state_bits));
   return launch_adamw_multi(tensors, n_tensors, opt, static_cast<cudaStream_t>(stream));
 }
@@ -515,7 +634,7 @@ static int check_state(const void* codes, const void* scale, const void* x, int6
 extern "C" int adamw_state_dequantize(const void* codes, const float* scale, int64_t n,
                                       int32_t is_signed, float* out, void* stream) {
   LSQ_TRY(check_state(codes, scale, out, n, is_signed, "adamw_state_dequantize"));
-  const int64_t want = (n / 16 + 255) / 256;
+  const int64_t want = (n + 4095) / 4096;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)std::max<int64_t>(1, std::min<int64_t>(want, gemm_num_sms() * 8)));
   cfg.blockDim = dim3(256);

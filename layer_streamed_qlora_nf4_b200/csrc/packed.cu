@@ -192,96 +192,247 @@ __global__ void __launch_bounds__(256)
 // ------------------------------------------------------------------ cross-entropy
 constexpr float kLog2e = 1.4426950408889634f;
 
+__device__ __forceinline__ float ex2(float x) {  // 2^x, relative error 2^-22
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 // (max, sum of exp relative to it) of two sets; (-inf, 0) is the empty set.
 __device__ __forceinline__ void join(float& m, float& s, float mo, float so) {
   const float mn = fmaxf(m, mo);
   if (mn == -INFINITY) return;
-  s = s * exp2f((m - mn) * kLog2e) + so * exp2f((mo - mn) * kLog2e);
+  s = s * ex2((m - mn) * kLog2e) + so * ex2((mo - mn) * kLog2e);
   m = mn;
 }
 
-// One CTA per row.  A row is read twice (maximum and sum of exponentials in one pass,
-// then the gradient), the second time from L2 while it still holds it.  Elements are
-// taken eight at a time from the first whose index in the whole array is a multiple of
-// eight, so that any V is read and written in aligned 16-byte pieces.
-template <int THREADS>
-__global__ void __launch_bounds__(THREADS)
-    packed_ce_kernel(const float* __restrict__ logits, const int32_t* __restrict__ targets,
-                     int64_t V, const float* __restrict__ weight, const int32_t* __restrict__ count,
-                     uint16_t* __restrict__ dlogits, float* __restrict__ row_loss, int* dev_err) {
-  __shared__ float red_m[32], red_s[32];
-  pdl_trigger();
-  pdl_wait();
-  const int64_t row = blockIdx.x;
-  const float* __restrict__ x = logits + row * V;
-  uint16_t* __restrict__ dx = dlogits ? dlogits + row * V : nullptr;
-  const int head = (int)min(V, (int64_t)((8 - (int)((row * V) & 7)) & 7));
-  const int64_t n8 = (V - head) / 8;
-  const int64_t tail = head + n8 * 8;
-  const int64_t y = targets[row];
-  const int tid = threadIdx.x;
-  if (y < 0 || y >= V) {
-    if (dx) {
-      for (int64_t i = tid; i < n8; i += THREADS)
-        reinterpret_cast<uint4*>(dx + head)[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (tid < head) dx[tid] = 0;
-      if (tail + tid < V && tid < 8) dx[tail + tid] = 0;
-    }
-    if (tid == 0) {
-      row_loss[row] = 0.f;
-      if (y >= V) atomicOr(dev_err, DEV_ERR_INDEX);
-    }
-    return;
-  }
-  float m = -INFINITY, s = 0.f;
-  auto add = [&](float v) { join(m, s, v, 1.f); };
-  if (tid < head) add(x[tid]);
-  if (tid < 8 && tail + tid < V) add(x[tail + tid]);
-  const float4* x4 = reinterpret_cast<const float4*>(x + head);
-  for (int64_t i = tid; i < n8; i += THREADS) {
-    const float4 a = x4[2 * i], b = x4[2 * i + 1];
-    const float t = fmaxf(fmaxf(fmaxf(a.x, a.y), fmaxf(a.z, a.w)),
-                          fmaxf(fmaxf(b.x, b.y), fmaxf(b.z, b.w)));
-    if (t > m) {
-      s *= exp2f((m - t) * kLog2e);
-      m = t;
-    }
-    const float c = m == -INFINITY ? 0.f : -m * kLog2e;
-    s += ((exp2f(fmaf(a.x, kLog2e, c)) + exp2f(fmaf(a.y, kLog2e, c))) +
-          (exp2f(fmaf(a.z, kLog2e, c)) + exp2f(fmaf(a.w, kLog2e, c)))) +
-         ((exp2f(fmaf(b.x, kLog2e, c)) + exp2f(fmaf(b.y, kLog2e, c))) +
-          (exp2f(fmaf(b.z, kLog2e, c)) + exp2f(fmaf(b.w, kLog2e, c))));
-  }
+constexpr int kCeThreads = 256;
+constexpr int kCeChunks = 2;  // bulk copies of a slice
+
+// The pairs of a warp's lanes joined, the same in every lane.
+__device__ __forceinline__ void warp_join(float& m, float& s) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     const float mo = __shfl_xor_sync(0xFFFFFFFFu, m, o);
     const float so = __shfl_xor_sync(0xFFFFFFFFu, s, o);
     join(m, s, mo, so);
   }
+}
+
+// A cluster of C CTAs per row, each with a slice of the row in shared memory, so that
+// the logits are read once: bulk copies bring the slice in, the online maximum and sum
+// of exponentials follow them, the CTAs exchange their pairs through the cluster's shared
+// memory, and the gradient is formed from the slice.  Memory bound: 4 bytes read and 2
+// written per logit (512 rows of 128,256: 56 us at the measured copy rate).  Measured
+// there: 98 us for one CTA per row that reads it twice (the rows in flight exceed the L2),
+// 84 us for this form, 86 us for persistent clusters that refill a chunk with the next
+// row's as soon as they are done with it, 100 us and more with shares re-read through L2;
+// 2048 rows of 151,936 (40% with a target): 216 us.
+// Elements are taken eight at a time from the first whose index in the whole array is a
+// multiple of eight, so that any V moves in aligned 16-byte pieces; the few before and
+// behind are rank 0's and the last rank's.
+__global__ void __launch_bounds__(kCeThreads)
+    packed_ce_kernel(const float* __restrict__ logits, const int32_t* __restrict__ targets,
+                     int64_t V, const float* __restrict__ weight, const int32_t* __restrict__ count,
+                     uint16_t* __restrict__ dlogits, float* __restrict__ row_loss, int C,
+                     int* dev_err) {
+  extern __shared__ __align__(128) float slice[];
+  __shared__ __align__(8) uint64_t bar[kCeChunks];
+  __shared__ float red_m[kCeThreads / 32], red_s[kCeThreads / 32];
+  __shared__ __align__(16) float pair[4];
+  __shared__ int abort_sh;
+  pdl_trigger();
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int64_t row = blockIdx.x / C;
+  const int rank = blockIdx.x % C;
+  const int head = (int)min(V, (int64_t)((8 - (int)((row * V) & 7)) & 7));
+  const int64_t n8 = (V - head) / 8;             // groups of eight
+  const int64_t per = (n8 + C - 1) / C;
+  const int64_t g0 = min(n8, per * rank);
+  const int ng = (int)(min(n8, g0 + per) - g0);  // groups of this slice
+  const int64_t first = head + g0 * 8;           // its first element
+  const int64_t tail = head + n8 * 8;
+  // the ragged ends: element `odd` of the row, one per thread
+  const int64_t odd = rank == 0 && tid < head ? tid
+                      : rank == C - 1 && tid >= 32 && tail + tid - 32 < V && tid < 40 ? tail + tid - 32
+                                                                                     : -1;
+  const float* __restrict__ x = logits + row * V;
+  uint16_t* __restrict__ dx = dlogits ? dlogits + row * V : nullptr;
+  if (tid == 0) {
+    for (int i = 0; i < kCeChunks; ++i) mbar_init(smem_u32(&bar[i]), 1);
+    abort_sh = 0;
+    fence_mbar_init();
+    fence_proxy_async_smem();
+  }
+  __syncthreads();
+  pdl_wait();
+  const int64_t y = targets[row];
+  if (y < 0 || y >= V) {  // (the same in the whole cluster)
+    if (dx) {
+      for (int i = tid; i < ng; i += kCeThreads)
+        reinterpret_cast<uint4*>(dx + first)[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (odd >= 0) dx[odd] = 0;
+    }
+    if (tid == 0 && rank == 0) {
+      row_loss[row] = 0.f;
+      if (y >= V) atomicOr(dev_err, DEV_ERR_INDEX);
+    }
+    return;
+  }
+  const int cg = (ng + kCeChunks - 1) / kCeChunks;  // groups of a chunk
+  if (tid == 0)
+    for (int i = 0; i < kCeChunks; ++i) {
+      const int a = min(ng, i * cg), n = min(ng, a + cg) - a;
+      if (n == 0) continue;
+      mbar_arrive_expect_tx(smem_u32(&bar[i]), (uint32_t)n * 32u);
+      asm volatile(
+          "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+              "r"(smem_u32(slice + a * 8)),
+          "l"(x + first + (int64_t)a * 8), "r"((uint32_t)n * 32u), "r"(smem_u32(&bar[i]))
+          : "memory");
+    }
+  float m = -INFINITY, s = 0.f;
+  const float xo = odd >= 0 ? x[odd] : -INFINITY;
+  if (odd >= 0) join(m, s, xo, 1.f);
+  const float4* s4 = reinterpret_cast<const float4*>(slice);
+  for (int i = 0; i < kCeChunks; ++i) {
+    const int a = min(ng, i * cg) * 2, e = min(ng, (i + 1) * cg) * 2;  // in float4
+    if (a == e) break;
+    // (one warp polls: all of them would keep the shared-memory pipe from the others)
+    if (tid < 32) mbar_wait_short(smem_u32(&bar[i]), 0u, &abort_sh, dev_err);
+    __syncthreads();
+    for (int k = a + tid; k < e; k += 4 * kCeThreads) {
+      float4 v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        v[j] = k + j * kCeThreads < e ? s4[k + j * kCeThreads]
+                                      : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+      float t = m;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) t = fmaxf(t, fmaxf(fmaxf(v[j].x, v[j].y), fmaxf(v[j].z, v[j].w)));
+      const float c = t == -INFINITY ? 0.f : -t * kLog2e;
+      s *= m == -INFINITY ? 0.f : ex2(fmaf(m, kLog2e, c));
+      m = t;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        s += (ex2(fmaf(v[j].x, kLog2e, c)) + ex2(fmaf(v[j].y, kLog2e, c))) +
+             (ex2(fmaf(v[j].z, kLog2e, c)) + ex2(fmaf(v[j].w, kLog2e, c)));
+    }
+  }
+  warp_join(m, s);
+  if (lane == 0) {
+    red_m[tid >> 5] = m;
+    red_s[tid >> 5] = s;
+  }
+  __syncthreads();
+  // one warp joins the warps' pairs (by all threads, one after the other, this took as
+  // long as the row itself)
+  if (tid < 32) {
+    m = lane < kCeThreads / 32 ? red_m[lane] : -INFINITY;
+    s = lane < kCeThreads / 32 ? red_s[lane] : 0.f;
+    warp_join(m, s);
+    if (lane == 0) {
+      pair[0] = m;
+      pair[1] = s;
+    }
+  }
+  if (C > 1) {
+    // (only warp 0's pair is to be seen by the others: it alone releases)
+    if (tid < 32)
+      asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    else
+      asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    m = -INFINITY;
+    s = 0.f;
+    if (lane < C) {
+      const float4 v = ld_shared_cluster_f4(mapa_shared(smem_u32(pair), (uint32_t)lane));
+      m = v.x;
+      s = v.y;
+    }
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) {
+      const float mo = __shfl_xor_sync(0xFFFFFFFFu, m, o);
+      const float so = __shfl_xor_sync(0xFFFFFFFFu, s, o);
+      join(m, s, mo, so);
+    }
+    m = __shfl_sync(0xFFFFFFFFu, m, 0);
+    s = __shfl_sync(0xFFFFFFFFu, s, 0);
+    // done reading (the operands: not before the pairs have arrived)
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" : "+f"(m), "+f"(s)::"memory");
+  } else {
+    __syncthreads();
+    m = pair[0];
+    s = pair[1];
+  }
+  float c = weight ? weight[row] : 1.f;
+  if (count) c /= (float)max(1, *count);
+  const float k = c / s, off = -m * kLog2e;
+  auto grad = [&](float v, int64_t j) { return k * ex2(fmaf(v, kLog2e, off)) - (j == y ? c : 0.f); };
+  if (dx) {
+    const int yt = (int)min(max(y - first, (int64_t)-1), (int64_t)INT32_MAX);
+    for (int i = tid; i < ng; i += kCeThreads) {
+      const float4 a = s4[2 * i], b = s4[2 * i + 1];
+      float g[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) g[e] = k * ex2(fmaf(g[e], kLog2e, off));
+      if (yt >> 3 == i) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) g[e] -= (yt & 7) == e ? c : 0.f;
+      }
+      __stcs(reinterpret_cast<uint4*>(dx + first) + i,
+             make_uint4(pack_bf16x2(g[0], g[1]), pack_bf16x2(g[2], g[3]), pack_bf16x2(g[4], g[5]),
+                        pack_bf16x2(g[6], g[7])));
+    }
+    if (odd >= 0) dx[odd] = float_to_bf16_bits(grad(xo, odd));
+  }
+  if (tid == 0 && rank == 0) row_loss[row] = m + logf(s) - x[y];
+  if (C > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// The same for rows too long for a cluster's shared memory: one CTA per row, which reads
+// it twice.
+__global__ void __launch_bounds__(1024)
+    packed_ce_long_kernel(const float* __restrict__ logits, const int32_t* __restrict__ targets,
+                          int64_t V, const float* __restrict__ weight,
+                          const int32_t* __restrict__ count, uint16_t* __restrict__ dlogits,
+                          float* __restrict__ row_loss, int* dev_err) {
+  __shared__ float red_m[32], red_s[32];
+  pdl_trigger();
+  pdl_wait();
+  const int tid = threadIdx.x;
+  const int64_t row = blockIdx.x, y = targets[row];
+  const float* __restrict__ x = logits + row * V;
+  uint16_t* __restrict__ dx = dlogits ? dlogits + row * V : nullptr;
+  const bool on = y >= 0 && y < V;
+  float m = -INFINITY, s = 0.f;
+  if (on)
+    for (int64_t i = tid; i < V; i += 1024) {
+      const float v = x[i];
+      if (v > m) {
+        s *= m == -INFINITY ? 0.f : ex2((m - v) * kLog2e);
+        m = v;
+      }
+      s += m == -INFINITY && v == m ? 0.f : ex2((v - m) * kLog2e);
+    }
+  warp_join(m, s);
   if ((tid & 31) == 0) {
     red_m[tid >> 5] = m;
     red_s[tid >> 5] = s;
   }
   __syncthreads();
-  m = red_m[0];
-  s = red_s[0];
-  for (int w = 1; w < THREADS / 32; ++w) join(m, s, red_m[w], red_s[w]);
-  if (tid == 0) row_loss[row] = m + logf(s) - x[y];
-  if (!dx) return;
-  float c = weight ? weight[row] : 1.f;
+  m = red_m[tid & 31];
+  s = red_s[tid & 31];
+  warp_join(m, s);
+  float c = on ? (weight ? weight[row] : 1.f) : 0.f;
   if (count) c /= (float)max(1, *count);
-  const float k = c / s, off = -m * kLog2e;
-  auto grad = [&](float v, int64_t j) { return k * exp2f(fmaf(v, kLog2e, off)) - (j == y ? c : 0.f); };
-  if (tid < head) dx[tid] = float_to_bf16_bits(grad(x[tid], tid));
-  if (tid < 8 && tail + tid < V) dx[tail + tid] = float_to_bf16_bits(grad(x[tail + tid], tail + tid));
-  for (int64_t i = tid; i < n8; i += THREADS) {
-    const float4 a = x4[2 * i], b = x4[2 * i + 1];
-    const int64_t j = head + 8 * i;
-    reinterpret_cast<uint4*>(dx + head)[i] =
-        make_uint4(pack_bf16x2(grad(a.x, j), grad(a.y, j + 1)),
-                   pack_bf16x2(grad(a.z, j + 2), grad(a.w, j + 3)),
-                   pack_bf16x2(grad(b.x, j + 4), grad(b.y, j + 5)),
-                   pack_bf16x2(grad(b.z, j + 6), grad(b.w, j + 7)));
+  if (dx)
+    for (int64_t i = tid; i < V; i += 1024)
+      dx[i] = on ? float_to_bf16_bits(c / s * ex2((x[i] - m) * kLog2e) - (i == y ? c : 0.f))
+                 : (uint16_t)0;
+  if (tid == 0) {
+    row_loss[row] = on ? m + logf(s) - x[y] : 0.f;
+    if (y >= V) atomicOr(dev_err, DEV_ERR_INDEX);
   }
 }
 
@@ -309,6 +460,19 @@ __global__ void __launch_bounds__(1024)
       *loss = (accumulate ? *loss : 0.f) + s;
     }
   }
+}
+
+constexpr int64_t kCeMaxSmem = 220 * 1024;
+
+// CTAs of a row and bytes of shared memory of each: slices of at most 16,384 logits (64
+// KB, three CTAs per SM, so that the copies of one overlap the arithmetic of another),
+// as far as a portable cluster of eight goes; more CTAs for few rows.
+int64_t ce_plan(int64_t T, int64_t V, int* C) {
+  int c = 1;
+  while (c < 8 && (V > 16384 * (int64_t)c || (V > 2048 * (int64_t)c && T * c < gemm_num_sms())))
+    c *= 2;
+  *C = c;
+  return ((V / 8 + c - 1) / c) * 32 + 32;
 }
 
 template <class... P, class... A>
@@ -354,12 +518,37 @@ int launch_packed_ce(const float* logits, int64_t T, int64_t V, const int32_t* t
   int* err = device_status_ptr();
   if (!err) return set_error(LSQ_ERR_CUDA, "device status word unavailable");
   const int prof = prof_begin(st);
-  if (V >= 4096)
-    LSQ_CUDA(launch_dep(packed_ce_kernel<512>, (unsigned)T, 512, st, logits, targets, V, weight,
+  int C = 1;  // CTAs of a row
+  const int64_t smem = ce_plan(T, V, &C);
+  if (smem > kCeMaxSmem || T * C > INT32_MAX) {
+    LSQ_CUDA(launch_dep(packed_ce_long_kernel, (unsigned)T, 1024, st, logits, targets, V, weight,
                         count, dlogits, row_loss, err));
-  else
-    LSQ_CUDA(launch_dep(packed_ce_kernel<128>, (unsigned)T, 128, st, logits, targets, V, weight,
-                        count, dlogits, row_loss, err));
+  } else {
+    static bool attr[64] = {false};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 64 && !attr[dev]) {
+      LSQ_CUDA(cudaFuncSetAttribute(packed_ce_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    (int)kCeMaxSmem));
+      attr[dev] = true;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(T * C));
+    cfg.blockDim = dim3(kCeThreads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = (unsigned)C;
+    at[1].val.clusterDim.y = 1;
+    at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    LSQ_CUDA(::lsq::launched(cudaLaunchKernelEx(&cfg, packed_ce_kernel, logits, targets, V, weight,
+                                                count, dlogits, row_loss, C, err)));
+  }
   if (prof >= 0) prof_end(prof, st, "packed_ce", 0.0, (dlogits ? 6.0 : 4.0) * T * V);
   return LSQ_OK;
 }

@@ -59,4 +59,27 @@ inline PackedIndex packed_index_view(const int32_t* base, int64_t T, int64_t n_d
   return x;
 }
 
+// A bounded wait like mbar_wait_bounded, which reads the clock only after 64 polls have
+// failed: the read takes longer than most waits here.
+#ifdef __CUDACC__
+__device__ __forceinline__ bool mbar_wait_short(uint32_t bar, uint32_t parity,
+                                                volatile int* abort_flag, int* dev_err) {
+  uint64_t t0 = 0;
+  for (uint32_t n = 1;; ++n) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((n & 63u) == 0) {
+      if (*abort_flag) return false;
+      const uint64_t t = globaltimer_ns();
+      if (t0 == 0) {
+        t0 = t;
+      } else if (t - t0 > kWaitLimitNs) {
+        *abort_flag = 1;
+        atomicOr(dev_err, DEV_ERR_WAIT_GEMM);
+        return false;
+      }
+    }
+  }
+}
+#endif
+
 }  // namespace lsq

@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
   pdl_wait();  // the index and q, k, v come from the kernels before
   const int items = heads ? idx.head[0] * (H / 2) : idx.head[1] * H;
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-    return mbar_wait_bounded(smem_u32(bar), parity & 1u, abort_flag, dev_err, DEV_ERR_WAIT_GEMM);
+    return mbar_wait_short(smem_u32(bar), parity & 1u, abort_flag, dev_err);
   };
 
   // the same by a whole warp, which leaves it together: a lane that fell behind could
@@ -801,7 +801,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
   const int per = Hkv * parts;              // items of a tile
   const int items = idx.head[0] * per;
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-    return mbar_wait_bounded(smem_u32(bar), parity & 1u, abort_flag, dev_err, DEV_ERR_WAIT_GEMM);
+    return mbar_wait_short(smem_u32(bar), parity & 1u, abort_flag, dev_err);
   };
   auto wait_all = [&](uint64_t* bar, uint32_t parity) -> bool {
     return __all_sync(0xFFFFFFFFu, wait(bar, parity));
@@ -1175,7 +1175,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
   const bool heads = G % 2 == 0;
   const int items = heads ? idx.head[0] * (H / 2) : idx.head[1] * H;
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-    return mbar_wait_bounded(smem_u32(bar), parity & 1u, abort_flag, dev_err, DEV_ERR_WAIT_GEMM);
+    return mbar_wait_short(smem_u32(bar), parity & 1u, abort_flag, dev_err);
   };
   auto wait_all = [&](uint64_t* bar, uint32_t parity) -> bool {
     return __all_sync(0xFFFFFFFFu, wait(bar, parity));

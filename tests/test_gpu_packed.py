@@ -285,7 +285,8 @@ def test_attention_is_deterministic_on_any_stream_and_in_a_graph(L):
     _check(q2.cpu(), g2.cpu(), op.documents([0, 450]), H, Hkv, *out)
 
 
-LOSS = [(1, 1), (1, 2), (3, 7), (5, 8), (4, 1001), (6, 4096), (2, 5003), (3, 40000), (2, 131075)]
+LOSS = [(1, 1), (1, 2), (3, 7), (5, 8), (4, 1001), (6, 4096), (2, 5003), (3, 40000), (2, 131075),
+        (2, 460003)]
 
 
 @pytest.mark.parametrize("T,V", LOSS)
