@@ -572,6 +572,48 @@ int adamw_state_dequantize(const void* codes, const float* scale, int64_t n, int
 int adamw_state_quantize(const float* x, int64_t n, int32_t is_signed, void* codes, float* scale,
                          void* stream);
 
+/* ------------------------------------------------- packed layers and steps */
+
+/* decoder_layer_packed_fwd / _bwd - decoder_layer_fwd / _bwd of one packed row of
+ * n_tokens tokens: positions restart and attention stays inside each document of the
+ * index (packed_index with n_tokens and n_docs).  Workspace:
+ * decoder_layer_workspace_bytes(cfg, 1, n_tokens), 32-byte aligned; the other arguments
+ * as there, with batch * seq = n_tokens.  Added in ABI 2.2. */
+int decoder_layer_packed_fwd(const lsq_cfg* cfg, const void* blob, const float* lora,
+                             const float* x_in, const int32_t* index, int32_t n_docs,
+                             int32_t n_tokens, float* x_out, void* ws, size_t ws_bytes,
+                             void* stream);
+int decoder_layer_packed_bwd(const lsq_cfg* cfg, const void* blob, const float* lora,
+                             const float* x_in, const float* dx_out, const int32_t* index,
+                             int32_t n_docs, int32_t n_tokens, float* dx_in, float* lora_grad,
+                             int32_t accumulate, void* ws, size_t ws_bytes, void* stream);
+
+/* stream_stack_packed_step - stream_stack_step on packed rows: one row of n_tokens
+ * tokens with n_docs documents per micro-batch.
+ *   tokens     device int32 [micro_batches, n_tokens] (padding: any id).
+ *   lengths, prefix  device int32 [micro_batches, n_docs] (prefix may be NULL), and
+ *   loss_mask  device uint8 [micro_batches, n_tokens] or NULL: as for packed_index and
+ *              packed_targets.
+ *   loss_out   the mean cross-entropy over all targets of the step (0 if there is none);
+ *              lora_grad is its gradient.
+ *   tensors, n_tensors, opt  the update of adamw_multi_step behind the last backward:
+ *              tensors of the caller's choice inside lora and lora_grad, each with its
+ *              own rate and decay, the state in 8 or 32 bits.  opt NULL: none.
+ *   logits_out device fp32 [n_tokens, V] of the last micro-batch, or NULL.
+ *   ws         stream_stack_packed_workspace_bytes(cfg, n_tokens, n_docs), 32-byte
+ *              aligned.
+ * Streaming, graphs, data parallelism, the synchronous return and the other arguments
+ * are those of stream_stack_step; a latched status bit (a length outside its range
+ * among them) is returned as LSQ_ERR_DEVICE.  Added in ABI 2.2. */
+size_t stream_stack_packed_workspace_bytes(const lsq_cfg* cfg, int32_t n_tokens, int32_t n_docs);
+int stream_stack_packed_step(lsq_stack* stack, const int32_t* tokens, int32_t micro_batches,
+                             int32_t n_tokens, const int32_t* lengths, const int32_t* prefix,
+                             int32_t n_docs, const uint8_t* loss_mask, const uint16_t* emb,
+                             const uint16_t* lm_head, const uint16_t* final_norm, float* lora,
+                             float* lora_grad, const lsq_adamw_tensor* tensors, int32_t n_tensors,
+                             const lsq_adamw_hyper* opt, float* loss_out, float* logits_out,
+                             void* ws, size_t ws_bytes, void* stream, int64_t timeout_ms);
+
 /* ------------------------------------------------------------ measurement */
 
 /* Number of kernel launches the library has issued in this process. */

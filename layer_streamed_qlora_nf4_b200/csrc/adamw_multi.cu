@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(kMtThreads, 4)
     const int64_t base = (int64_t)(c - e.chunk0) * kChunk + warp * kBlk;
     if (base >= e.n) continue;  // uniform in the warp
     const int left = (int)min((int64_t)kBlk, e.n - base);
-    const float lr = e.lr, decay = 1.f - lr * e.wd, rate = lr * inv_bc1;
+    const float lr = e.lr, decay = lr * e.wd, rate = lr * inv_bc1;
     float4 p4[2];
     uint64_t g[4], m[4], v[4];  // element pairs
     uint32_t mc[2], vc[2];
@@ -307,7 +307,8 @@ __global__ void __launch_bounds__(kMtThreads, 4)
     float root[8];
     {
       const uint64_t is2 = two(isb2, isb2), ep2 = two(a.h.eps, a.h.eps);
-      const uint64_t de2 = two(decay, decay), nr2 = two(-rate, -rate);
+      // the change of p first, then one sum: p itself is rounded once
+      const uint64_t de2 = two(-decay, -decay), nr2 = two(-rate, -rate);
       float* pf = reinterpret_cast<float*>(p4);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -316,7 +317,8 @@ __global__ void __launch_bounds__(kMtThreads, 4)
         root[2 * j + 1] = sqrt_ftz(y.y);
         const float2 d = both(fma2(two(root[2 * j], root[2 * j + 1]), is2, ep2));
         const uint64_t u = mul2(m[j], two(rcp_ftz(d.x), rcp_ftz(d.y)));
-        const float2 q = both(fma2(u, nr2, mul2(two(pf[2 * j], pf[2 * j + 1]), de2)));
+        const uint64_t p0 = two(pf[2 * j], pf[2 * j + 1]);
+        const float2 q = both(add2(p0, fma2(u, nr2, mul2(p0, de2))));
         if (!(skip >> (2 * j) & 1u)) pf[2 * j] = q.x;
         if (!(skip >> (2 * j) & 2u)) pf[2 * j + 1] = q.y;
       }
@@ -601,8 +603,8 @@ using namespace lsq;
 
 extern "C" int64_t adamw_scale_floats(int64_t n) { return n <= 0 ? 0 : (n + kBlk - 1) / kBlk; }
 
-extern "C" int adamw_multi_step(const lsq_adamw_tensor* tensors, int32_t n_tensors,
-                                const lsq_adamw_hyper* opt, void* stream) {
+int lsq::check_adamw_multi(const lsq_adamw_tensor* tensors, int n_tensors,
+                           const lsq_adamw_hyper* opt) {
   if (!opt || (!tensors && n_tensors > 0))
     return set_error(LSQ_ERR_INVALID, "adamw_multi_step: null pointer");
   if (n_tensors < 0) return set_error(LSQ_ERR_SHAPE, "adamw_multi_step: negative tensor count");
@@ -616,7 +618,12 @@ extern "C" int adamw_multi_step(const lsq_adamw_tensor* tensors, int32_t n_tenso
       !(opt->eps >= 1.17549435e-38f) || !std::isfinite(opt->eps))
     return set_error(LSQ_ERR_INVALID,
                      "adamw_multi_step: need 0 <= beta < 1 and a finite eps of at least 2^-126");
-  LSQ_TRY(check_tensors(tensors, n_tensors, opt->state_bits));
+  return check_tensors(tensors, n_tensors, opt->state_bits);
+}
+
+extern "C" int adamw_multi_step(const lsq_adamw_tensor* tensors, int32_t n_tensors,
+                                const lsq_adamw_hyper* opt, void* stream) {
+  LSQ_TRY(check_adamw_multi(tensors, n_tensors, opt));
   return launch_adamw_multi(tensors, n_tensors, opt, static_cast<cudaStream_t>(stream));
 }
 

@@ -345,8 +345,9 @@ __global__ void rope_table_kernel(int seq, int half, int d, double log_theta, fl
 
 // In-place rotation of the q and k heads of the fused qkv buffer (fp16); a
 // thread rotates 8 pairs (i, i + d/2).
+// (a token's position is t % seq, or, in packed rows, pos[t])
 __global__ void rope_kernel(uint16_t* __restrict__ qkv, int64_t T, int seq, int H, int Hkv, int d,
-                            const float2* __restrict__ cs) {
+                            const float2* __restrict__ cs, const int* __restrict__ pos_of) {
   pdl_trigger();  // the next kernel may launch once all CTAs of this one run
   const int half = d / 2, chunks = half / 8;
   const int64_t ld = (int64_t)(H + 2 * Hkv) * d;
@@ -357,7 +358,7 @@ __global__ void rope_kernel(uint16_t* __restrict__ qkv, int64_t T, int seq, int 
     const int64_t th = i / chunks;
     const int head = (int)(th % (H + Hkv));
     const int64_t t = th / (H + Hkv);
-    const int pos = (int)(t % seq);
+    const int pos = pos_of ? pos_of[t] : (int)(t % seq);
     uint16_t* base = qkv + t * ld + (int64_t)head * d + ch * 8;
     const uint4 a = *reinterpret_cast<const uint4*>(base);
     const uint4 b = *reinterpret_cast<const uint4*>(base + half);
@@ -383,7 +384,7 @@ __global__ void rope_kernel(uint16_t* __restrict__ qkv, int64_t T, int seq, int 
 __global__ void reduce_rope_kernel(const float* __restrict__ parts, int n_parts, int64_t T,
                                    int seq, int H, int Hkv, int d,
                                    const float2* __restrict__ cs, uint16_t* __restrict__ qkv,
-                                   int* dev_err) {
+                                   const int* __restrict__ pos_of, int* dev_err) {
   pdl_trigger();  // the next kernel may launch once all CTAs of this one run
   const int half = d / 2, chunks = half / 8;
   const int64_t ld = (int64_t)(H + 2 * Hkv) * d;
@@ -411,7 +412,7 @@ __global__ void reduce_rope_kernel(const float* __restrict__ parts, int n_parts,
       const int64_t th = i / chunks;
       const int head = (int)(th % (H + Hkv));
       const int64_t t = th / (H + Hkv);
-      const int pos = (int)(t % seq);
+      const int pos = pos_of ? pos_of[t] : (int)(t % seq);
       const int64_t e = t * ld + (int64_t)head * d + ch * 8;
       float f1[8], f2[8];
       sum8(e, f1);
@@ -829,14 +830,14 @@ int launch_rmsnorm_bwd_sum(const float* parts, int n_parts, const float* x, cons
 }
 
 int launch_reduce_rope(const float* parts, int n_parts, int64_t T, int seq, int H, int Hkv, int d,
-                       const float2* cs, uint16_t* qkv, cudaStream_t st) {
+                       const float2* cs, uint16_t* qkv, cudaStream_t st, const int* pos) {
   if (n_parts < 1 || d % 16 != 0) return set_error(LSQ_ERR_SHAPE, "reduce_rope: bad shape");
   int* dev_err = device_status_ptr();
   if (!dev_err) return set_error(LSQ_ERR_CUDA, "device status word unavailable");
   const int64_t n = T * (H + Hkv) * (d / 16) + T * Hkv * (d / 8);
   const int prof = prof_begin(st);
   reduce_rope_kernel<<<grid_for(n, 256), 256, 0, st>>>(parts, n_parts, T, seq, H, Hkv, d, cs, qkv,
-                                                       dev_err);
+                                                       pos, dev_err);
   LSQ_CUDA(::lsq::launched(cudaGetLastError()));
   // the product's output read once (fp32, as if reduced), q|k|v written (fp16), the table
   if (prof >= 0)
@@ -853,10 +854,10 @@ int launch_rope_table(int seq, int d, float theta, float2* cs, cudaStream_t st) 
 }
 
 int launch_rope(uint16_t* qkv, int64_t T, int seq, int H, int Hkv, int d, const float2* cs,
-                cudaStream_t st) {
+                cudaStream_t st, const int* pos) {
   const int64_t n = T * (H + Hkv) * (d / 16);
   const int prof = prof_begin(st);
-  rope_kernel<<<grid_for(n, 256), 256, 0, st>>>(qkv, T, seq, H, Hkv, d, cs);
+  rope_kernel<<<grid_for(n, 256), 256, 0, st>>>(qkv, T, seq, H, Hkv, d, cs, pos);
   LSQ_CUDA(::lsq::launched(cudaGetLastError()));
   // q and k read and written in place (fp16), plus the table rows once
   if (prof >= 0) prof_end(prof, st, "rope", 0.0, 4.0 * T * (H + Hkv) * d + 4.0 * seq * d);

@@ -151,7 +151,8 @@ int launch_rmsnorm_bwd_sum(const float* parts, int n_parts, const float* x, cons
                            const float* rstd, const float* dres, int64_t T, int64_t D, float* dx,
                            uint16_t* dx_bf16, cudaStream_t st);
 int launch_reduce_rope(const float* parts, int n_parts, int64_t T, int seq, int H, int Hkv, int d,
-                       const float2* cs, uint16_t* qkv, cudaStream_t st);
+                       const float2* cs, uint16_t* qkv, cudaStream_t st,
+                       const int* pos = nullptr);
 int launch_splitk_reduce(const float* partial, int splits, int64_t T, int64_t M, void* out,
                          int out_kind, int64_t ldo, const float* residual, int64_t ldr,
                          cudaStream_t st);
@@ -165,9 +166,10 @@ int launch_rmsnorm_bwd(const float* dy, const float* x, const uint16_t* g, const
                        cudaStream_t st);
 // cos/sin table [seq][d/2] for rotate-half RoPE
 int launch_rope_table(int seq, int d, float theta, float2* cs, cudaStream_t st);
-// in place on the fp16 q and k heads of the fused qkv buffer
+// in place on the fp16 q and k heads of the fused qkv buffer; pos (nullable): each
+// token's position, instead of t % seq
 int launch_rope(uint16_t* qkv, int64_t T, int seq, int H, int Hkv, int d, const float2* cs,
-                cudaStream_t st);
+                cudaStream_t st, const int* pos = nullptr);
 // dk, dv are per query head [T, H d] (summed over each kv group here)
 int launch_rope_grad(const float* dq, const float* dk, const float* dv, int64_t T, int seq, int H,
                      int Hkv, int d, const float2* cs, uint16_t* dqkv, cudaStream_t st);
@@ -296,6 +298,7 @@ int launch_packed_attention_bwd(const uint16_t* qkv, const int32_t* index, int n
                                 const uint16_t* o, const float* lse, const uint16_t* dout,
                                 int64_t T, int H, int Hkv, int d, const float2* cs, uint16_t* dqkv,
                                 void* ws, size_t ws_bytes, cudaStream_t st);
+int check_adamw_multi(const lsq_adamw_tensor* tensors, int n_tensors, const lsq_adamw_hyper* opt);
 int launch_adamw_multi(const lsq_adamw_tensor* t, int n, const lsq_adamw_hyper* o,
                        cudaStream_t st);
 
@@ -309,7 +312,13 @@ struct LayerShapes {
 };
 int layer_shapes(const lsq_cfg* cfg, LayerShapes* out);
 size_t layer_ws_bytes(const lsq_cfg* cfg, int64_t T);
+// A packed row's documents (batch 1, seq = its tokens): the index of packed_index.
+struct PackedRow {
+  const int32_t* index;
+  int n_docs;
+};
 // dx_out_bf16 may be null (then converted internally).
+// packed (nullable): attention and positions inside the documents of one packed row
 // rope_cs: the cos/sin table of launch_rope_table for this seq, or null (then the
 // layer builds it in its workspace); lora16: this layer's LoRA operands rounded by
 // prepare_lora16, or null (then the layer rounds its masters in its workspace)
@@ -320,7 +329,8 @@ size_t layer_ws_bytes(const lsq_cfg* cfg, int64_t T);
 int layer_fwd_impl(const lsq_cfg* cfg, const void* blob, const float* lora, const float* x_in,
                    int batch, int seq, float* x_out, void* ws, size_t ws_bytes,
                    cudaStream_t st, const float2* rope_cs = nullptr,
-                   const uint16_t* lora16 = nullptr, void* saved_u = nullptr);
+                   const uint16_t* lora16 = nullptr, void* saved_u = nullptr,
+                   const PackedRow* packed = nullptr);
 size_t layer_saved_u_bytes(const lsq_cfg* cfg, int64_t T);
 // The LoRA operands of one layer in their product types (fp16 A, bf16 block-
 // diagonal B stacks): elements per layer, and the rounding of n_layers
@@ -332,6 +342,7 @@ int layer_bwd_impl(const lsq_cfg* cfg, const void* blob, const float* lora, cons
                    const float* dx_out, const uint16_t* dx_out_bf16, int batch, int seq,
                    float* dx_in, uint16_t* dx_in_bf16, float* lora_grad, int accumulate,
                    void* ws, size_t ws_bytes, cudaStream_t st, const float2* rope_cs = nullptr,
-                   const uint16_t* lora16 = nullptr, const void* saved_u = nullptr);
+                   const uint16_t* lora16 = nullptr, const void* saved_u = nullptr,
+                   const PackedRow* packed = nullptr);
 
 }  // namespace lsq

@@ -14,6 +14,7 @@
 // forward GEMMs; gradients that feed tensor cores are bf16; every accumulation,
 // norm and softmax is fp32.
 #include "common.cuh"
+#include "packed.cuh"
 
 namespace lsq {
 
@@ -389,7 +390,7 @@ size_t plan_buffers(const LayerShapes& s, int64_t T, void* base, Buffers* b) {
   x.dn1 = a.take<float>(T * s.D);
   x.dq = a.take<float>(T * s.qd);
   x.dk = a.take<float>(T * s.qd);   // per query head, summed per kv head in rope_grad
-  x.dv = a.take<float>(T * s.qd);
+  x.dv = a.take<float>(T * s.qd + 1024);  // (with room for a packed row's, which share dq, dk, dv)
   x.delta = a.take<float>(T * s.H);
   x.rope_cs = a.take<float2>(T * s.hd / 2);  // >= seq * d/2 entries
   // LoRA K-split scratch: the largest of every skinny product in the layer
@@ -501,7 +502,9 @@ int check_layer_args(const lsq_cfg* cfg, const void* blob, const float* lora, co
 // when x_out is given, the down projection with its residual.
 int forward_core(const LayerShapes& s, const Views& v, const float* x, int batch, int seq,
                  const float2* rope_cs, float eps, const Buffers& b, float* x_out,
-                 cudaStream_t st, bool have_u = false) {
+                 cudaStream_t st, bool have_u = false, const PackedRow* packed = nullptr) {
+  const int* pos = packed ? packed_index_view(packed->index, (int64_t)batch * seq, packed->n_docs).pos
+                          : nullptr;
   const int64_t T = (int64_t)batch * seq;
   const int r = v.lora_on ? s.r : 0;  // r = 0: no LoRA slab in the GEMMs
   const bool down = v.lora_on && !have_u;  // compute u = x A^T here
@@ -519,10 +522,14 @@ int forward_core(const LayerShapes& s, const Views& v, const float* x, int batch
   g_qkv.splits_out = &np;
   LSQ_TRY(gemm_run(g_qkv, b.gemm, b.gemm_bytes, st));
   if (np > 1)
-    LSQ_TRY(launch_reduce_rope(parts, np, T, seq, s.H, s.Hkv, s.hd, rope_cs, b.qkv, st));
+    LSQ_TRY(launch_reduce_rope(parts, np, T, seq, s.H, s.Hkv, s.hd, rope_cs, b.qkv, st, pos));
   else
-    LSQ_TRY(launch_rope(b.qkv, T, seq, s.H, s.Hkv, s.hd, rope_cs, st));
-  LSQ_TRY(launch_attention_fwd(b.qkv, T, seq, s.H, s.Hkv, s.hd, b.ao, b.lse, st));
+    LSQ_TRY(launch_rope(b.qkv, T, seq, s.H, s.Hkv, s.hd, rope_cs, st, pos));
+  if (packed)
+    LSQ_TRY(launch_packed_attention_fwd(b.qkv, packed->index, packed->n_docs, T, s.H, s.Hkv, s.hd,
+                                        b.ao, b.lse, st));
+  else
+    LSQ_TRY(launch_attention_fwd(b.qkv, T, seq, s.H, s.Hkv, s.hd, b.ao, b.lse, st));
   if (down)
     LSQ_TRY(launch_lora_down16(b.ao, s.qd, v.A16_o, T, s.qd, r, nullptr, b.u16_o, b.lscratch,
                                b.lscratch_bytes, st, b.uh_o));
@@ -588,7 +595,7 @@ size_t layer_ws_bytes(const lsq_cfg* cfg, int64_t T) {
 int layer_fwd_impl(const lsq_cfg* cfg, const void* blob, const float* lora, const float* x_in,
                    int batch, int seq, float* x_out, void* ws, size_t ws_bytes,
                    cudaStream_t st, const float2* rope_cs, const uint16_t* lora16,
-                   void* saved_u) {
+                   void* saved_u, const PackedRow* packed) {
   LayerShapes s;
   LSQ_TRY(check_layer_args(cfg, blob, lora, x_in, batch, seq, x_out, &s, "decoder_layer_fwd",
                            true));
@@ -605,14 +612,14 @@ int layer_fwd_impl(const lsq_cfg* cfg, const void* blob, const float* lora, cons
     LSQ_TRY(launch_rope_table(seq, s.hd, cfg->rope_theta, b.rope_cs, st));
     rope_cs = b.rope_cs;
   }
-  return forward_core(s, v, x_in, batch, seq, rope_cs, cfg->rms_eps, b, x_out, st);
+  return forward_core(s, v, x_in, batch, seq, rope_cs, cfg->rms_eps, b, x_out, st, false, packed);
 }
 
 int layer_bwd_impl(const lsq_cfg* cfg, const void* blob, const float* lora, const float* x_in,
                    const float* dx_out, const uint16_t* dx_out_bf16, int batch, int seq,
                    float* dx_in, uint16_t* dx_in_bf16, float* lora_grad, int accumulate, void* ws,
                    size_t ws_bytes, cudaStream_t st, const float2* rope_cs,
-                   const uint16_t* lora16, const void* saved_u) {
+                   const uint16_t* lora16, const void* saved_u, const PackedRow* packed) {
   LayerShapes s;
   LSQ_TRY(check_layer_args(cfg, blob, lora, x_in, batch, seq, dx_in, &s, "decoder_layer_bwd"));
   if (!dx_out || !lora_grad) return set_error(LSQ_ERR_INVALID, "decoder_layer_bwd: null pointer");
@@ -650,7 +657,7 @@ int layer_bwd_impl(const lsq_cfg* cfg, const void* blob, const float* lora, cons
   // the same kernels on the same inputs would reproduce them bit for bit)
   if (saved_u) carve_saved_u(s, T, const_cast<void*>(saved_u), &b);
   LSQ_TRY(forward_core(s, v, x_in, batch, seq, rope_cs, cfg->rms_eps, b, nullptr, st,
-                       saved_u != nullptr));
+                       saved_u != nullptr, packed));
 
   const uint16_t* dout_b = dx_out_bf16;
   if (!dout_b) {
@@ -695,9 +702,16 @@ int layer_bwd_impl(const lsq_cfg* cfg, const void* blob, const float* lora, cons
   LSQ_TRY(launch_lora_grad_ab16(b.v16_o, b.ao, s.qd, gA_o, b.dh_b, b.u16_o, s.D, r, 1, pe1, T, sc,
                                 accumulate, gB_o, st));
   // attention, RoPE
-  LSQ_TRY(launch_attention_bwd(b.qkv, b.ao, b.da, b.lse, T, seq, s.H, s.Hkv, s.hd, b.delta, b.dq,
-                               b.dk, b.dv, st));
-  LSQ_TRY(launch_rope_grad(b.dq, b.dk, b.dv, T, seq, s.H, s.Hkv, s.hd, rope_cs, b.dqkv, st));
+  if (packed) {
+    const size_t room = (size_t)(reinterpret_cast<uint8_t*>(b.dv + T * s.qd + 1024) -
+                                 reinterpret_cast<uint8_t*>(b.dq));
+    LSQ_TRY(launch_packed_attention_bwd(b.qkv, packed->index, packed->n_docs, b.ao, b.lse, b.da, T,
+                                        s.H, s.Hkv, s.hd, rope_cs, b.dqkv, b.dq, room, st));
+  } else {
+    LSQ_TRY(launch_attention_bwd(b.qkv, b.ao, b.da, b.lse, T, seq, s.H, s.Hkv, s.hd, b.delta, b.dq,
+                                 b.dk, b.dv, st));
+    LSQ_TRY(launch_rope_grad(b.dq, b.dk, b.dv, T, seq, s.H, s.Hkv, s.hd, rope_cs, b.dqkv, st));
+  }
   // q|k|v projections
   LSQ_TRY(launch_lora_vproj16(b.dqkv, T, s.qkv_n, v.B16_qkv, 3 * r, nullptr, b.v16_qkv,
                               b.lscratch, b.lscratch_bytes, st, b.vh_qkv));
@@ -757,4 +771,35 @@ extern "C" int decoder_layer_bwd(const lsq_cfg* cfg, const void* blob, const flo
                                  void* ws, size_t ws_bytes, void* stream) {
   return layer_bwd_impl(cfg, blob, lora, x_in, dx_out, nullptr, batch, seq, dx_in, nullptr,
                         lora_grad, accumulate, ws, ws_bytes, static_cast<cudaStream_t>(stream));
+}
+
+static int check_packed_layer(const lsq_cfg* cfg, const int32_t* index, int32_t n_docs,
+                              int32_t n_tokens, const void* ws, const char* who) {
+  if (!cfg) return set_error(LSQ_ERR_INVALID, "%s: null configuration", who);
+  LSQ_TRY(check_packed(n_tokens, n_docs, index, who));
+  if (reinterpret_cast<uintptr_t>(ws) & 31u)
+    return set_error(LSQ_ERR_ALIGN, "%s: the workspace must be 32-byte aligned", who);
+  return LSQ_OK;
+}
+
+extern "C" int decoder_layer_packed_fwd(const lsq_cfg* cfg, const void* blob, const float* lora,
+                                        const float* x_in, const int32_t* index, int32_t n_docs,
+                                        int32_t n_tokens, float* x_out, void* ws, size_t ws_bytes,
+                                        void* stream) {
+  LSQ_TRY(check_packed_layer(cfg, index, n_docs, n_tokens, ws, "decoder_layer_packed_fwd"));
+  const PackedRow row{index, n_docs};
+  return layer_fwd_impl(cfg, blob, lora, x_in, 1, n_tokens, x_out, ws, ws_bytes,
+                        static_cast<cudaStream_t>(stream), nullptr, nullptr, nullptr, &row);
+}
+
+extern "C" int decoder_layer_packed_bwd(const lsq_cfg* cfg, const void* blob, const float* lora,
+                                        const float* x_in, const float* dx_out,
+                                        const int32_t* index, int32_t n_docs, int32_t n_tokens,
+                                        float* dx_in, float* lora_grad, int32_t accumulate,
+                                        void* ws, size_t ws_bytes, void* stream) {
+  LSQ_TRY(check_packed_layer(cfg, index, n_docs, n_tokens, ws, "decoder_layer_packed_bwd"));
+  const PackedRow row{index, n_docs};
+  return layer_bwd_impl(cfg, blob, lora, x_in, dx_out, nullptr, 1, n_tokens, dx_in, nullptr,
+                        lora_grad, accumulate, ws, ws_bytes, static_cast<cudaStream_t>(stream),
+                        nullptr, nullptr, nullptr, &row);
 }

@@ -49,6 +49,7 @@
 #include <vector>
 
 #include "common.cuh"
+#include "packed.cuh"
 
 struct lsq_stack {
   lsq_cfg cfg;
@@ -131,6 +132,10 @@ struct StackWs {
   float* row_ref;    // [T] reference per-row -log p
   float* seq_scale;  // [2 * pairs] dlogits coefficient per sequence
   float* logps;      // [4 * pairs]
+  // packed step only
+  int32_t* index;    // of the current micro-batch's documents
+  int32_t* targets;  // [T]
+  int32_t* count;    // [2] targets of the whole step, and of the current row
 };
 
 constexpr int kMaxPairs = 32;
@@ -188,8 +193,16 @@ int64_t head_chunk_tokens(const lsq_cfg* cfg, int64_t T, int seq, bool dpo) {
   return std::min<int64_t>(T, seqs * seq);
 }
 
+// Tokens per lm_head chunk of a packed row: as many as keep it within 4 GiB, in tiles of
+// 128 (the head and the loss know no documents).
+int64_t packed_chunk_tokens(const lsq_cfg* cfg, int64_t T) {
+  const int64_t rows = (int64_t(4) << 30) / std::max<int64_t>((int64_t)cfg->vocab * 6, 1);
+  return std::min<int64_t>(T, std::max<int64_t>(128, rows / 128 * 128));
+}
+
+// packed_docs > 0: a packed step of rows with that many documents
 size_t plan_stack_ws(const lsq_cfg* cfg, const LayerShapes& s, int64_t T, int seq, void* base,
-                     StackWs* w, bool dpo = false) {
+                     StackWs* w, bool dpo = false, int packed_docs = 0) {
   Arena a;
   a.base = static_cast<uint8_t*>(base);
   a.cap = SIZE_MAX;
@@ -198,7 +211,7 @@ size_t plan_stack_ws(const lsq_cfg* cfg, const LayerShapes& s, int64_t T, int se
   x.xs = a.take<float>((size_t)(cfg->n_layers + 1) * T * D);
   x.hf = a.take<uint16_t>(T * D);
   x.rstd_f = a.take<float>(T);
-  x.head_T = head_chunk_tokens(cfg, T, seq, dpo);
+  x.head_T = packed_docs ? packed_chunk_tokens(cfg, T) : head_chunk_tokens(cfg, T, seq, dpo);
   x.logits = a.take<float>((size_t)x.head_T * V);
   x.dlogits = a.take<uint16_t>((size_t)x.head_T * V);
   x.row_loss = a.take<float>(T);
@@ -225,6 +238,11 @@ size_t plan_stack_ws(const lsq_cfg* cfg, const LayerShapes& s, int64_t T, int se
     x.row_ref = a.take<float>(T);
     x.seq_scale = a.take<float>(2 * kMaxPairs);
     x.logps = a.take<float>(4 * kMaxPairs);
+  }
+  if (packed_docs) {
+    x.index = a.take<int32_t>((size_t)packed_index_words(T, packed_docs));
+    x.targets = a.take<int32_t>(T);
+    x.count = a.take<int32_t>(2);
   }
   if (w) *w = x;
   return a.used;
@@ -592,7 +610,18 @@ struct DpoArgs {
   float* logps_out;  // host [4 * pairs] or null
 };
 
-// One optimiser step over the streamed stack: SFT (dpo == null) or DPO.  The
+struct PackedArgs {
+  const int32_t* lengths;    // [micro_batches, n_docs]
+  const int32_t* prefix;     // the same, or null
+  int n_docs;
+  const uint8_t* loss_mask;  // [micro_batches, tokens], or null
+  const lsq_adamw_tensor* tensors;
+  int n_tensors;
+  const lsq_adamw_hyper* hyper;  // null: no update
+};
+
+// One optimiser step over the streamed stack: SFT (dpo == null) or DPO, or SFT on
+// packed rows (pk: one row of seq tokens per micro-batch).    The
 // DPO step runs the reference (adapter off) forward of each layer right after
 // the policy forward, from the same resident layer buffer, so it reads the
 // stack as often as an SFT step does.
@@ -600,14 +629,14 @@ int step_impl(lsq_stack* h, const int32_t* tokens, int32_t micro_batches, int32_
               int32_t seq, const uint16_t* emb, const uint16_t* lm_head,
               const uint16_t* final_norm, float* lora, float* lora_grad, const lsq_adamw* opt,
               float* loss_out, float* logits_out, void* ws, size_t ws_bytes, void* stream,
-              int64_t timeout_ms, const DpoArgs* dpo) {
+              int64_t timeout_ms, const DpoArgs* dpo, const PackedArgs* pk = nullptr) {
   if (!h) return set_error(LSQ_ERR_INVALID, "stream_stack_step: null handle");
   if (h->aborted)
     return set_error(LSQ_ERR_INVALID,
                      "stream_stack_step: the stack's communicator was aborted after a timeout");
   if (!tokens || !emb || !lm_head || !final_norm || !lora || !lora_grad || !loss_out)
     return set_error(LSQ_ERR_INVALID, "stream_stack_step: null pointer");
-  if (micro_batches <= 0 || batch <= 0 || seq < 2)
+  if (micro_batches <= 0 || batch <= 0 || seq < (pk ? 1 : 2))
     return set_error(LSQ_ERR_SHAPE, "stream_stack_step: need micro_batches, batch >= 1, seq >= 2");
   if (opt && (!opt->m || !opt->v || opt->step < 1))
     return set_error(LSQ_ERR_INVALID, "stream_stack_step: AdamW needs m, v and step >= 1");
@@ -618,11 +647,14 @@ int step_impl(lsq_stack* h, const int32_t* tokens, int32_t micro_batches, int32_
   const LayerShapes& s = h->shapes;
   const int L = cfg->n_layers;
   const int64_t T = (int64_t)batch * seq, D = s.D, V = cfg->vocab;
-  const size_t need = plan_stack_ws(cfg, s, T, seq, nullptr, nullptr, dpo != nullptr);
+  const int n_docs = pk ? pk->n_docs : 0;
+  const size_t need = plan_stack_ws(cfg, s, T, seq, nullptr, nullptr, dpo != nullptr, n_docs);
   if (!ws || ws_bytes < need)
     return set_error(LSQ_ERR_WORKSPACE, "stream_stack_step: workspace %zu < %zu", ws_bytes, need);
   StackWs w;
-  plan_stack_ws(cfg, s, T, seq, ws, &w, dpo != nullptr);
+  plan_stack_ws(cfg, s, T, seq, ws, &w, dpo != nullptr, n_docs);
+  const PackedRow row{w.index, n_docs};
+  const PackedRow* prow = pk ? &row : nullptr;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   const int64_t layer_floats = h->lora_layout.floats_per_layer;
   const float inv_count = 1.f / (float)((double)micro_batches * batch * (seq - 1));
@@ -662,7 +694,7 @@ int step_impl(lsq_stack* h, const int32_t* tokens, int32_t micro_batches, int32_
     const std::vector<uintptr_t> sig = {
         (uintptr_t)lora, (uintptr_t)lora_grad, (uintptr_t)ws, (uintptr_t)ws_bytes,
         (uintptr_t)batch, (uintptr_t)seq, (uintptr_t)micro_batches, (uintptr_t)profiling,
-        (uintptr_t)(dpo != nullptr), (uintptr_t)w.head_T};  // (head_T moves the layer workspace)
+        (uintptr_t)(dpo != nullptr), (uintptr_t)w.head_T, (uintptr_t)n_docs};  // (head_T moves the layer workspace)
     if (sig != h->graph_sig) {
       drop_graphs(h);
       h->graph_sig = sig;
@@ -722,9 +754,24 @@ int step_impl(lsq_stack* h, const int32_t* tokens, int32_t micro_batches, int32_
   // communicator), so that collectives of the two never run interleaved.
   if (h->shard) LSQ_CUDA(cudaStreamWaitEvent(h->copy_stream, h->t_start, 0));
   if (!h->resident && !visits.empty()) LSQ_TRY(enqueue_copy(0));
+  // the documents and targets of a packed row; the targets' number of the whole step is
+  // needed before its first gradient
+  auto prepare_row = [&](int mb, bool counting) -> int {
+    LSQ_TRY(launch_packed_index(pk->lengths + (int64_t)mb * n_docs,
+                                pk->prefix ? pk->prefix + (int64_t)mb * n_docs : nullptr, n_docs, T,
+                                w.index, cs));
+    // (the second time only the targets count, not their number)
+    return launch_packed_targets(tokens + (int64_t)mb * T, w.index, n_docs, T,
+                                 pk->loss_mask ? pk->loss_mask + (int64_t)mb * T : nullptr,
+                                 w.targets, counting ? w.count : w.count + 1,
+                                 counting && mb > 0 ? 1 : 0, cs);
+  };
+  if (pk)
+    for (int mb = 0; mb < micro_batches; ++mb) LSQ_TRY(prepare_row(mb, true));
   size_t j = 0;
   for (int mb = 0; mb < micro_batches; ++mb) {
     const int32_t* tok = tokens + (int64_t)mb * T;
+    if (pk && micro_batches > 1) LSQ_TRY(prepare_row(mb, false));
     LSQ_TRY(launch_embedding(tok, T, emb, D, V, w.xs, cs));
     const int mbk = profiling ? mb : 0;  // profiled graphs are replayed once per step
     for (int i = 0; i < L; ++i, ++j) {
@@ -735,7 +782,7 @@ int step_impl(lsq_stack* h, const int32_t* tokens, int32_t micro_batches, int32_
         return layer_fwd_impl(cfg, blob, lora + (int64_t)i * layer_floats,
                               w.xs + (size_t)i * T * D, batch, seq, w.xs + (size_t)(i + 1) * T * D,
                               w.layer_ws, w.layer_ws_bytes, s, w.rope_cs, w.lora16 + i * l16,
-                              w.saved_u + (size_t)i * w.saved_u_bytes);
+                              w.saved_u + (size_t)i * w.saved_u_bytes, prow);
       }));
       if (dpo)  // reference model: the same layer with its adapter off
         LSQ_TRY(visit(std::make_tuple(1, i, b, 0, mbk), [&](cudaStream_t s) {
@@ -763,12 +810,20 @@ int step_impl(lsq_stack* h, const int32_t* tokens, int32_t micro_batches, int32_
         if (logits_out && last_mb)
           LSQ_CUDA(cudaMemcpyAsync(logits_out + c0 * V, w.logits, (size_t)tc * V * sizeof(float),
                                    cudaMemcpyDeviceToDevice, cs));
-        LSQ_TRY(launch_cross_entropy(w.logits, tok + c0, tc, seq, V, inv_count, w.dlogits,
-                                     w.row_loss + c0, cs));
+        if (pk)
+          LSQ_TRY(launch_packed_ce(w.logits, tc, V, w.targets + c0, nullptr, w.count, w.dlogits,
+                                   w.row_loss + c0, cs));
+        else
+          LSQ_TRY(launch_cross_entropy(w.logits, tok + c0, tc, seq, V, inv_count, w.dlogits,
+                                       w.row_loss + c0, cs));
         LSQ_TRY(gemm_run(head_dx(lm_head, V, D, w.dlogits, tc, w.dhf + c0 * D), w.gemm,
                          w.gemm_bytes, cs));
       }
-      LSQ_TRY(launch_sum_rows(w.row_loss, T, inv_count, mb > 0 ? 1 : 0, w.loss_dev, cs));
+      if (pk)
+        LSQ_TRY(launch_packed_loss(w.row_loss, w.targets, T, V, nullptr, w.count, mb > 0 ? 1 : 0,
+                                   w.loss_dev, cs));
+      else
+        LSQ_TRY(launch_sum_rows(w.row_loss, T, inv_count, mb > 0 ? 1 : 0, w.loss_dev, cs));
     } else {
       LSQ_TRY(gemm_run(head_fwd(lm_head, V, D, w.hf, T, w.logits), w.gemm, w.gemm_bytes, cs));
       LSQ_TRY(launch_cross_entropy(w.logits, tok, T, seq, V, 0.f, nullptr, w.row_loss, cs));
@@ -793,7 +848,7 @@ int step_impl(lsq_stack* h, const int32_t* tokens, int32_t micro_batches, int32_
                               w.xs + (size_t)i * T * D, w.dh[cur], w.dhb[cur], batch, seq,
                               w.dh[1 - cur], w.dhb[1 - cur], lora_grad + (int64_t)i * layer_floats,
                               acc, w.layer_ws, w.layer_ws_bytes, s, w.rope_cs, w.lora16 + i * l16,
-                              w.saved_u + (size_t)i * w.saved_u_bytes);
+                              w.saved_u + (size_t)i * w.saved_u_bytes, prow);
       }));
       if (!h->resident) LSQ_CUDA(cudaEventRecord(h->freed[visits[j].buf], cs));
       if (h->grad_comm && mb == micro_batches - 1) {
@@ -819,6 +874,8 @@ int step_impl(lsq_stack* h, const int32_t* tokens, int32_t micro_batches, int32_
   if (opt)
     LSQ_TRY(launch_adamw(lora, lora_grad, opt->m, opt->v, layer_floats * L, opt->lr, opt->beta1,
                          opt->beta2, opt->eps, opt->weight_decay, opt->step, cs));
+  if (pk && pk->hyper)
+    LSQ_TRY(launch_adamw_multi(pk->tensors, pk->n_tensors, pk->hyper, cs));
   LSQ_CUDA(cudaMemcpyAsync(h->loss_host, w.loss_dev, sizeof(float), cudaMemcpyDeviceToHost, cs));
   if (dpo)
     LSQ_CUDA(cudaMemcpyAsync(h->loss_host + 1, w.logps, 4 * dpo->pairs * sizeof(float),
@@ -903,4 +960,36 @@ extern "C" int stream_stack_dpo_step(lsq_stack* h, const int32_t* tokens, int32_
   DpoArgs d{pairs, beta, logps_out};
   return step_impl(h, tokens, 1, 2 * pairs, seq, emb, lm_head, final_norm, lora, lora_grad, opt,
                    loss_out, logits_out, ws, ws_bytes, stream, timeout_ms, &d);
+}
+
+extern "C" size_t stream_stack_packed_workspace_bytes(const lsq_cfg* cfg, int32_t n_tokens,
+                                                      int32_t n_docs) {
+  LayerShapes s;
+  if (n_tokens <= 0 || n_tokens > (1 << 30) || n_docs <= 0 || n_docs > (1 << 24) ||
+      layer_shapes(cfg, &s) != LSQ_OK || cfg->n_layers <= 0 || cfg->vocab <= 0)
+    return 0;
+  return plan_stack_ws(cfg, s, n_tokens, n_tokens, nullptr, nullptr, false, n_docs);
+}
+
+extern "C" int stream_stack_packed_step(lsq_stack* h, const int32_t* tokens, int32_t micro_batches,
+                                        int32_t n_tokens, const int32_t* lengths,
+                                        const int32_t* prefix, int32_t n_docs,
+                                        const uint8_t* loss_mask, const uint16_t* emb,
+                                        const uint16_t* lm_head, const uint16_t* final_norm,
+                                        float* lora, float* lora_grad,
+                                        const lsq_adamw_tensor* tensors, int32_t n_tensors,
+                                        const lsq_adamw_hyper* opt, float* loss_out,
+                                        float* logits_out, void* ws, size_t ws_bytes, void* stream,
+                                        int64_t timeout_ms) {
+  if (!lengths) return set_error(LSQ_ERR_INVALID, "stream_stack_packed_step: null lengths");
+  if (n_tokens <= 0 || n_tokens > (1 << 30) || n_docs <= 0 || n_docs > (1 << 24))
+    return set_error(LSQ_ERR_SHAPE, "stream_stack_packed_step: %d tokens, %d documents", n_tokens,
+                     n_docs);
+  if (reinterpret_cast<uintptr_t>(ws) & 31u)
+    return set_error(LSQ_ERR_ALIGN,
+                     "stream_stack_packed_step: the workspace must be 32-byte aligned");
+  if (opt) LSQ_TRY(check_adamw_multi(tensors, n_tensors, opt));
+  const PackedArgs pk{lengths, prefix, n_docs, loss_mask, tensors, n_tensors, opt};
+  return step_impl(h, tokens, micro_batches, 1, n_tokens, emb, lm_head, final_norm, lora, lora_grad,
+                   nullptr, loss_out, logits_out, ws, ws_bytes, stream, timeout_ms, nullptr, &pk);
 }

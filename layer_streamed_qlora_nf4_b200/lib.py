@@ -34,6 +34,8 @@ EXPORTS = (
     "packed_index_ints", "packed_index", "packed_targets", "packed_cross_entropy",
     "packed_attention_fwd", "packed_attention_bwd", "packed_attention_workspace_bytes",
     "adamw_scale_floats", "adamw_multi_step", "adamw_state_dequantize", "adamw_state_quantize",
+    "decoder_layer_packed_fwd", "decoder_layer_packed_bwd",
+    "stream_stack_packed_workspace_bytes", "stream_stack_packed_step",
 )
 LSQ_NCCL_ID_BYTES = 128
 
@@ -175,6 +177,16 @@ _PROTOS = {
                                             _P, _SZ, _P]),
     "packed_targets": (ctypes.c_int, [_P, _P, _I32, _I64, _P, _P, _P, _I32, _P]),
     "packed_cross_entropy": (ctypes.c_int, [_P, _I64, _I64, _P, _P, _P, _P, _P, _P, _I32, _P]),
+    "decoder_layer_packed_fwd": (ctypes.c_int, [ctypes.POINTER(lsq_cfg), _P, _P, _P, _P, _I32, _I32,
+                                                _P, _P, _SZ, _P]),
+    "decoder_layer_packed_bwd": (ctypes.c_int, [ctypes.POINTER(lsq_cfg), _P, _P, _P, _P, _P, _I32,
+                                                _I32, _P, _P, _I32, _P, _SZ, _P]),
+    "stream_stack_packed_workspace_bytes": (_SZ, [ctypes.POINTER(lsq_cfg), _I32, _I32]),
+    "stream_stack_packed_step": (ctypes.c_int, [_P, _P, _I32, _I32, _P, _P, _I32, _P, _P, _P, _P,
+                                                _P, _P, ctypes.POINTER(lsq_adamw_tensor), _I32,
+                                                ctypes.POINTER(lsq_adamw_hyper),
+                                                ctypes.POINTER(ctypes.c_float), _P, _P, _SZ, _P,
+                                                _I64]),
     "adamw_scale_floats": (_I64, [_I64]),
     "adamw_multi_step": (ctypes.c_int, [ctypes.POINTER(lsq_adamw_tensor), _I32,
                                         ctypes.POINTER(lsq_adamw_hyper), _P]),
@@ -761,9 +773,8 @@ class AdamWMulti:
                                       state_bits=bits,
                                       grad_bits=32 if gdt == torch.float32 else 16)
 
-    def step(self, step, stream=None):
-        """One update; step: the count from 1, or an int32 device tensor that holds it
-        (for a captured update that is replayed as the count advances)."""
+    def at(self, step):
+        """The arguments (tensors, n_tensors, opt) of an update; step as for step()."""
         import torch
         h = self._hyper
         if isinstance(step, torch.Tensor):
@@ -771,8 +782,75 @@ class AdamWMulti:
             h.step, h.step_dev = 1, step.data_ptr()
         else:
             h.step, h.step_dev = int(step), None
+        return self._table, self._n, h
+
+    def step(self, step, stream=None):
+        """One update; step: the count from 1, or an int32 device tensor that holds it
+        (for a captured update that is replayed as the count advances)."""
+        import torch
+        h = self.at(step)[2]
         if self._n == 0:
             return
         _call("adamw_multi_step", stream,
               (self._dev, step if isinstance(step, torch.Tensor) else None), self._table, self._n,
               ctypes.byref(h))
+
+
+# ------------------------------------------------------------ packed layers and steps
+def decoder_layer_packed_fwd(cfg, blob, lora, x_in, index, x_out, ws, stream=None):
+    """x_in, x_out: fp32 [n_tokens, D] of one packed row; index: its PackedIndex."""
+    import torch
+    T = index.n_tokens
+    _need("x_in", x_in, torch.float32, (T, cfg["hidden"]))
+    _need("x_out", x_out, torch.float32, (T, cfg["hidden"]))
+    c = cfg_struct(cfg)
+    _call("decoder_layer_packed_fwd", stream, (blob, lora, x_in, index.buf, x_out, ws),
+          ctypes.byref(c), blob.data_ptr(), _addr(lora), x_in.data_ptr(), index.buf.data_ptr(),
+          index.n_docs, T, x_out.data_ptr(), ws.data_ptr(), ws.numel())
+
+
+def decoder_layer_packed_bwd(cfg, blob, lora, x_in, dx_out, index, dx_in, lora_grad, ws,
+                             accumulate=False, stream=None):
+    import torch
+    T = index.n_tokens
+    for name, t in (("x_in", x_in), ("dx_out", dx_out), ("dx_in", dx_in)):
+        _need(name, t, torch.float32, (T, cfg["hidden"]))
+    c = cfg_struct(cfg)
+    _call("decoder_layer_packed_bwd", stream, (blob, lora, x_in, dx_out, index.buf, dx_in,
+                                               lora_grad, ws),
+          ctypes.byref(c), blob.data_ptr(), lora.data_ptr(), x_in.data_ptr(), dx_out.data_ptr(),
+          index.buf.data_ptr(), index.n_docs, T, dx_in.data_ptr(), lora_grad.data_ptr(),
+          1 if accumulate else 0, ws.data_ptr(), ws.numel())
+
+
+def stream_stack_packed_workspace_bytes(cfg, n_tokens, n_docs):
+    c = cfg_struct(cfg)
+    return load().stream_stack_packed_workspace_bytes(ctypes.byref(c), n_tokens, n_docs)
+
+
+def stream_stack_packed_step(stack, tokens, lengths, emb, lm_head, final_norm, lora, lora_grad, ws,
+                             prefix=None, loss_mask=None, opt=None, step=1, logits_out=None,
+                             timeout_ms=600000, stream=None):
+    """One SFT step on packed rows.  tokens: int32 [micro_batches, n_tokens]; lengths, prefix:
+    int32 [micro_batches, n_docs]; loss_mask: uint8 or bool [micro_batches, n_tokens]; opt: an
+    AdamWMulti over views of lora and lora_grad, updated with the count `step`, or None.
+    Returns the mean loss over all targets (host float)."""
+    import torch
+    if tokens.dim() != 2 or lengths.dim() != 2 or lengths.shape[0] != tokens.shape[0]:
+        raise ValueError("tokens must be [micro_batches, n_tokens], lengths [micro_batches, n_docs]")
+    _need("tokens", tokens, torch.int32)
+    _need("lengths", lengths, torch.int32)
+    if prefix is not None:
+        _need("prefix", prefix, torch.int32, lengths.shape)
+    if loss_mask is not None:
+        if loss_mask.dtype == torch.bool:
+            loss_mask = loss_mask.view(torch.uint8)
+        _need("loss_mask", loss_mask, torch.uint8, tokens.shape)
+    loss = ctypes.c_float(0.0)
+    table, n, hyper = opt.at(step) if opt is not None else (None, 0, None)
+    _check(load().stream_stack_packed_step(
+        stack.handle, _ptr(tokens), tokens.shape[0], tokens.shape[1], _ptr(lengths), _ptr(prefix),
+        lengths.shape[1], _ptr(loss_mask), _ptr(emb), _ptr(lm_head), _ptr(final_norm), _ptr(lora),
+        _ptr(lora_grad), table, n, ctypes.byref(hyper) if hyper is not None else None,
+        ctypes.byref(loss), _ptr(logits_out), _ptr(ws), ws.numel(), _stream(stream), timeout_ms))
+    return loss.value

@@ -75,8 +75,8 @@ def _check(x, d, lr, bits, steps=1):
     for i in range(len(x["p"])):
         for k in ("m", "v") + (("ms", "vs") if bits == 8 else ()):
             assert np.array_equal(d[k][i].cpu().numpy(), x[k][i]), (k, i)
-        # p is rounded twice a step (2^-24 each), and the update of at most a few lr is
-        # off by 2^-20 relative
+        # p is rounded once a step (2^-24), and the update of at most a few lr is off by
+        # 2^-20 relative
         tol = steps * (2.0 ** -23 * np.abs(x["p"][i]) + 2.0 ** -20 * 10 * lr[i])
         assert (np.abs(d["p"][i].cpu().numpy() - x["p"][i]) <= tol).all(), i
 
