@@ -535,8 +535,7 @@ def nf4_lora_linear_fwd_noalloc(x, codes, absmax, A, B, scale, y, residual=None,
 # ------------------------------------------------------------ packed documents, AdamW
 def _need(name, t, dtype, shape=None, numel=None):
     """Checks one tensor argument: its type, that it is contiguous, its shape or length."""
-    import torch
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, (_th or _torch()).Tensor):
         raise TypeError("%s must be a torch tensor" % name)
     if t.dtype is not dtype:
         raise TypeError("%s must be %s, not %s" % (name, dtype, t.dtype))
@@ -548,35 +547,48 @@ def _need(name, t, dtype, shape=None, numel=None):
         raise ValueError("%s must have %d elements, not %d" % (name, numel, t.numel()))
 
 
-_current = None   # (current device, its current stream): looked up once, a call of each is cheap
+def _fits(t, dtype, shape):
+    """Whether a tensor argument needs no closer look (_need says what is wrong with it)."""
+    try:
+        return t.dtype is dtype and t.shape == shape and t.is_contiguous()
+    except AttributeError:
+        return False
+
+
+_th = _device = _raw_stream = None   # torch, its current device and stream: looked up once
+
+
+def _torch():
+    global _th, _device, _raw_stream
+    if _th is None:
+        import torch
+        _device = torch.cuda.current_device
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda d: torch.cuda.current_stream(d).cuda_stream)
+        _th = torch
+    return _th
 
 
 def _call(name, stream, tensors, *args):
     """Runs one entry point on the device that holds all the tensors (made current for
     the call) and on its current stream, or the given one.  args: all but the stream."""
-    global _current
-    if _current is None:
-        import torch
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        _current = (torch.cuda.current_device,
-                    raw or (lambda d: torch.cuda.current_stream(d).cuda_stream))
+    th = _th or _torch()
     dev = -2
     for t in tensors:
         if t is not None:
             d = t.get_device()
-            if d < 0:
-                raise ValueError("%s: every tensor must be a CUDA tensor" % name)
             if d != dev:
+                if d < 0:
+                    raise ValueError("%s: every tensor must be a CUDA tensor" % name)
                 if dev != -2:
                     raise ValueError("%s: tensors on cuda:%d and cuda:%d" % (name, dev, d))
                 dev = d
-    fn = getattr(load(), name)
-    if dev == _current[0]():
-        rc = fn(*args, _current[1](dev) if stream is None else stream)
+    fn = getattr(_lib or load(), name)
+    if dev == _device():
+        rc = fn(*args, _raw_stream(dev) if stream is None else stream)
     else:
-        import torch
-        with torch.cuda.device(dev):
-            rc = fn(*args, _current[1](dev) if stream is None else stream)
+        with th.cuda.device(dev):
+            rc = fn(*args, _raw_stream(dev) if stream is None else stream)
     if rc != LSQ_OK:
         _check(rc)
 
@@ -604,32 +616,33 @@ class PackedIndex:
 
 def packed_index(lengths, index, prefix=None, stream=None):
     """lengths, prefix: int32 [n_docs] on the device; index: PackedIndex (filled)."""
-    import torch
-    _need("lengths", lengths, torch.int32, (index.n_docs,))
-    if prefix is not None:
-        _need("prefix", prefix, torch.int32, (index.n_docs,))
+    i32, n = (_th or _torch()).int32, (index.n_docs,)
+    if not _fits(lengths, i32, n):
+        _need("lengths", lengths, i32, n)
+    if prefix is not None and not _fits(prefix, i32, n):
+        _need("prefix", prefix, i32, n)
     _call("packed_index", stream, (lengths, prefix, index.buf), lengths.data_ptr(), _addr(prefix),
           index.n_docs, index.n_tokens, index.buf.data_ptr())
 
 
 def _packed_heads(qkv, index, n_heads, n_kv_heads):
-    import torch
     n = n_heads + 2 * n_kv_heads
     if n_heads <= 0 or n_kv_heads <= 0 or qkv.dim() != 2 or qkv.shape[1] % n:
         raise ValueError("qkv must be [T, (n_heads + 2 n_kv_heads) d]")
-    _need("qkv", qkv, torch.float16, (index.n_tokens, qkv.shape[1]))
     return qkv.shape[1] // n
 
 
 def packed_attention_fwd(qkv, index, n_heads, n_kv_heads, o, lse, stream=None):
     """qkv: fp16 [T, (H + 2 Hkv) d]; o: fp16 [T, H d]; lse: fp32 [H, T]."""
-    import torch
-    d, T = _packed_heads(qkv, index, n_heads, n_kv_heads), index.n_tokens
-    _need("o", o, torch.float16, (T, n_heads * d))
-    _need("lse", lse, torch.float32, (n_heads, T))
-    _call("packed_attention_fwd", stream, (qkv, index.buf, o, lse), qkv.data_ptr(),
-          index.buf.data_ptr(), index.n_docs, T, n_heads, n_kv_heads, d, o.data_ptr(),
-          lse.data_ptr())
+    th, T, buf = _th or _torch(), index.n_tokens, index.buf
+    d = _packed_heads(qkv, index, n_heads, n_kv_heads)
+    for name, t, dtype, shape in (
+            ("qkv", qkv, th.float16, (T, (n_heads + 2 * n_kv_heads) * d)),
+            ("o", o, th.float16, (T, n_heads * d)), ("lse", lse, th.float32, (n_heads, T))):
+        if not _fits(t, dtype, shape):
+            _need(name, t, dtype, shape)
+    _call("packed_attention_fwd", stream, (qkv, buf, o, lse), qkv.data_ptr(), buf.data_ptr(),
+          index.n_docs, T, n_heads, n_kv_heads, d, o.data_ptr(), lse.data_ptr())
 
 
 def packed_attention_workspace_bytes(T, n_heads, n_kv_heads, d):
@@ -639,16 +652,19 @@ def packed_attention_workspace_bytes(T, n_heads, n_kv_heads, d):
 def packed_attention_bwd(qkv, index, o, lse, dout, n_heads, n_kv_heads, dqkv, ws, stream=None):
     """dout: bf16 [T, H d]; dqkv: bf16, the shape of qkv (overwritten); ws: uint8 of
     packed_attention_workspace_bytes."""
-    import torch
-    d, T = _packed_heads(qkv, index, n_heads, n_kv_heads), index.n_tokens
-    _need("o", o, torch.float16, (T, n_heads * d))
-    _need("lse", lse, torch.float32, (n_heads, T))
-    _need("dout", dout, torch.bfloat16, (T, n_heads * d))
-    _need("dqkv", dqkv, torch.bfloat16, qkv.shape)
-    _need("ws", ws, torch.uint8)
-    _call("packed_attention_bwd", stream, (qkv, index.buf, o, lse, dout, dqkv, ws),
-          qkv.data_ptr(), index.buf.data_ptr(), index.n_docs, o.data_ptr(), lse.data_ptr(),
-          dout.data_ptr(), T, n_heads, n_kv_heads, d, dqkv.data_ptr(), ws.data_ptr(), ws.numel())
+    th, T, buf = _th or _torch(), index.n_tokens, index.buf
+    d = _packed_heads(qkv, index, n_heads, n_kv_heads)
+    wide, hd = (T, (n_heads + 2 * n_kv_heads) * d), (T, n_heads * d)
+    for name, t, dtype, shape in (
+            ("qkv", qkv, th.float16, wide), ("o", o, th.float16, hd),
+            ("lse", lse, th.float32, (n_heads, T)), ("dout", dout, th.bfloat16, hd),
+            ("dqkv", dqkv, th.bfloat16, wide)):
+        if not _fits(t, dtype, shape):
+            _need(name, t, dtype, shape)
+    _need("ws", ws, th.uint8)
+    _call("packed_attention_bwd", stream, (qkv, buf, o, lse, dout, dqkv, ws), qkv.data_ptr(),
+          buf.data_ptr(), index.n_docs, o.data_ptr(), lse.data_ptr(), dout.data_ptr(), T, n_heads,
+          n_kv_heads, d, dqkv.data_ptr(), ws.data_ptr(), ws.numel())
 
 
 def packed_targets(tokens, index, targets, count, loss_mask=None, accumulate=False, stream=None):
@@ -671,20 +687,21 @@ def packed_cross_entropy(logits, targets, row_loss, loss, dlogits=None, weight=N
                          accumulate=False, stream=None):
     """logits: fp32 [T, V]; targets: int32 [T]; row_loss: fp32 [T]; loss: fp32 [1];
     dlogits: bf16 [T, V]; weight: fp32 [T]; count: int32 [1]."""
-    import torch
+    th = _th or _torch()
     if logits.dim() != 2:
         raise ValueError("logits must be [T, V]")
     T, V = logits.shape
-    _need("logits", logits, torch.float32, (T, V))
-    _need("targets", targets, torch.int32, numel=T)
-    _need("row_loss", row_loss, torch.float32, numel=T)
-    _need("loss", loss, torch.float32, numel=1)
-    if dlogits is not None:
-        _need("dlogits", dlogits, torch.bfloat16, (T, V))
-    if weight is not None:
-        _need("weight", weight, torch.float32, numel=T)
-    if count is not None:
-        _need("count", count, torch.int32, numel=1)
+    # (targets, row losses and weights may be shaped as their batch is)
+    for name, t, dtype, n, optional in (
+            ("targets", targets, th.int32, T, False), ("row_loss", row_loss, th.float32, T, False),
+            ("loss", loss, th.float32, 1, False), ("weight", weight, th.float32, T, True),
+            ("count", count, th.int32, 1, True)):
+        if not (t is None and optional) and not _fits(t, dtype, (n,)):
+            _need(name, t, dtype, numel=n)
+    if not _fits(logits, th.float32, (T, V)):
+        _need("logits", logits, th.float32, (T, V))
+    if dlogits is not None and not _fits(dlogits, th.bfloat16, (T, V)):
+        _need("dlogits", dlogits, th.bfloat16, (T, V))
     _call("packed_cross_entropy", stream, (logits, targets, row_loss, loss, dlogits, weight, count),
           logits.data_ptr(), T, V, targets.data_ptr(), _addr(weight), _addr(count),
           _addr(dlogits), row_loss.data_ptr(), loss.data_ptr(), 1 if accumulate else 0)
@@ -695,19 +712,21 @@ def adamw_scale_floats(n):
 
 
 def _state_signed(codes):
-    import torch
-    if codes.dtype not in (torch.int8, torch.uint8):
-        raise TypeError("codes must be int8 (m) or uint8 (v)")
-    return 1 if codes.dtype == torch.int8 else 0
+    th = _th or _torch()
+    if codes.dtype is th.int8:
+        return 1
+    if codes.dtype is th.uint8:
+        return 0
+    raise TypeError("codes must be int8 (m) or uint8 (v)")
 
 
 def adamw_state_dequantize(codes, scale, out, stream=None):
     """codes: int8 (m) or uint8 (v); scale: fp32 per 256 codes; out: fp32."""
-    import torch
+    th = _th or _torch()
     signed, n = _state_signed(codes), codes.numel()
     _need("codes", codes, codes.dtype)
-    _need("scale", scale, torch.float32, numel=adamw_scale_floats(n))
-    _need("out", out, torch.float32, numel=n)
+    _need("scale", scale, th.float32, numel=(n + 255) // 256)
+    _need("out", out, th.float32, numel=n)
     _call("adamw_state_dequantize", stream, (codes, scale, out), codes.data_ptr(),
           scale.data_ptr(), n, signed, out.data_ptr())
 
