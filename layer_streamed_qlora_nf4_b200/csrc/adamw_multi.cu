@@ -144,11 +144,11 @@ __device__ __forceinline__ float level_v(int q) {
 // A block's scale: its largest magnitude, or 0 (every code 0) below the normal range.
 __device__ __forceinline__ float scale_of(float top) { return top < 1.17549435e-38f ? 0.f : top; }
 
-// Four elements of a tensor's array at offset o, of which `in` exist.
-template <class T4, class T>
+// Four elements of a tensor's array at offset o, of which `in` exist (all in a whole block).
+template <bool WHOLE, class T4, class T>
 __device__ __forceinline__ T4 load4(const void* base, int64_t o, int in) {
   T4 r;
-  if (in >= 4) {
+  if (WHOLE || in >= 4) {
     r = *reinterpret_cast<const T4*>(static_cast<const T*>(base) + o);
   } else {
     T* e = reinterpret_cast<T*>(&r);
@@ -157,9 +157,9 @@ __device__ __forceinline__ T4 load4(const void* base, int64_t o, int in) {
   }
   return r;
 }
-template <class T4, class T>
+template <bool WHOLE, class T4, class T>
 __device__ __forceinline__ void store4(void* base, int64_t o, int in, T4 v) {
-  if (in >= 4) {
+  if (WHOLE || in >= 4) {
     *reinterpret_cast<T4*>(static_cast<T*>(base) + o) = v;
   } else {
     const T* e = reinterpret_cast<const T*>(&v);
@@ -171,6 +171,196 @@ __device__ __forceinline__ void store4(void* base, int64_t o, int in, T4 v) {
 struct alignas(8) U16x4 {
   uint16_t v[4];
 };
+
+// One block of a tensor (a warp): elements [base, base + left).
+struct MtRates {
+  float inv_bc1, isb2;
+};
+template <int BITS, int GBITS, bool WHOLE>
+__device__ __forceinline__ void adamw_block(const MtHead& h, const MtEntry& e, const MtRates& r,
+                                            const float* lm, const float* lv, int64_t base, int left,
+                                            int lane) {
+  const uint64_t b1 = two(h.b1, h.b1), b2 = two(h.b2, h.b2);
+  const uint64_t c1 = two(h.c1, h.c1), c2 = two(h.c2, h.c2);
+  const float decay = e.lr * e.wd, rate = e.lr * r.inv_bc1;
+  float4 p4[2];
+  uint64_t g[4], m[4], v[4];  // element pairs
+  uint32_t mc[2], vc[2];
+  float am = 0.f, av = 0.f;
+  if (BITS == 8) {
+    am = e.ms[base / kBlk];
+    av = e.vs[base / kBlk];
+  }
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int o = u * 128 + lane * 4, in = left - o;
+    p4[u] = load4<WHOLE, float4, float>(e.p, base + o, in);
+    if (GBITS == 32) {
+      const float4 y = load4<WHOLE, float4, float>(e.g, base + o, in);
+      g[2 * u] = two(y.x, y.y);
+      g[2 * u + 1] = two(y.z, y.w);
+    } else {
+      const U16x4 y = load4<WHOLE, U16x4, uint16_t>(e.g, base + o, in);
+      g[2 * u] = two(bf16_bits_to_float(y.v[0]), bf16_bits_to_float(y.v[1]));
+      g[2 * u + 1] = two(bf16_bits_to_float(y.v[2]), bf16_bits_to_float(y.v[3]));
+    }
+    if (BITS == 8) {
+      mc[u] = load4<WHOLE, uint32_t, uint8_t>(e.m, base + o, in);
+      vc[u] = load4<WHOLE, uint32_t, uint8_t>(e.v, base + o, in);
+    } else {
+      const float4 y = load4<WHOLE, float4, float>(e.m, base + o, in);
+      const float4 z = load4<WHOLE, float4, float>(e.v, base + o, in);
+      m[2 * u] = two(y.x, y.y);
+      m[2 * u + 1] = two(y.z, y.w);
+      v[2 * u] = two(z.x, z.y);
+      v[2 * u + 1] = two(z.z, z.w);
+    }
+  }
+  if (BITS == 8) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t wm = mc[j >> 1] >> (16 * (j & 1)), wv = vc[j >> 1] >> (16 * (j & 1));
+      m[j] = mul2(two(am, am), two(lm[wm & 255u], lm[(wm >> 8) & 255u]));
+      v[j] = mul2(two(av, av), two(lv[wv & 255u], lv[(wv >> 8) & 255u]));
+    }
+  }
+  // the moments; the bits of their largest magnitudes (NaN and infinity above all) give
+  // the block's scales and tell whether any is not finite
+  uint32_t tm = 0, tv = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 x0 = both(mul2(b1, m[j])), x1 = both(mul2(c1, g[j]));
+    const float2 y0 = both(mul2(b2, v[j])), y1 = both(mul2(mul2(c2, g[j]), g[j]));
+    const float2 x = make_float2(__fadd_rn(x0.x, x1.x), __fadd_rn(x0.y, x1.y));
+    const float2 y = make_float2(__fadd_rn(y0.x, y1.x), __fadd_rn(y0.y, y1.y));
+    m[j] = two(x.x, x.y);
+    v[j] = two(y.x, y.y);
+    tm = max(tm, max(__float_as_uint(x.x) & 0x7FFFFFFFu, __float_as_uint(x.y) & 0x7FFFFFFFu));
+    tv = max(tv, max(__float_as_uint(y.x), __float_as_uint(y.y)));
+  }
+  uint32_t skip = 0;  // elements whose moments leave the finite range keep everything
+  if (max(tm, tv) >= 0x7F800000u) {
+    atomicOr(h.dev_err, DEV_ERR_NONFINITE);
+    tm = tv = 0;
+    for (int i = 0; i < 8; ++i) {
+      const int64_t at = base + (i >> 2) * 128 + lane * 4 + (i & 3);
+      float2 x = both(m[0]), y = both(v[0]);
+#pragma unroll
+      for (int j = 1; j < 4; ++j)
+        if (j == i / 2) {
+          x = both(m[j]);
+          y = both(v[j]);
+        }
+      float mi = i & 1 ? x.y : x.x, vi = i & 1 ? y.y : y.x;
+      if (!(fabsf(mi) < INFINITY && vi < INFINITY)) {  // (such an element exists: at < n)
+        skip |= 1u << i;
+        mi = BITS == 8 ? am * lm[static_cast<uint8_t*>(e.m)[at]] : static_cast<float*>(e.m)[at];
+        vi = BITS == 8 ? av * lv[static_cast<uint8_t*>(e.v)[at]] : static_cast<float*>(e.v)[at];
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (j == i / 2) {
+          m[j] = i & 1 ? two(x.x, mi) : two(mi, x.y);
+          v[j] = i & 1 ? two(y.x, vi) : two(vi, y.y);
+        }
+      // (a state that already was not finite counts as zero in the scale)
+      const uint32_t bm = __float_as_uint(mi) & 0x7FFFFFFFu, bv = __float_as_uint(vi) & 0x7FFFFFFFu;
+      tm = max(tm, bm < 0x7F800000u ? bm : 0u);
+      tv = max(tv, bv < 0x7F800000u ? bv : 0u);
+    }
+  }
+  float root[8];
+  {
+    const uint64_t is2 = two(r.isb2, r.isb2), ep2 = two(h.eps, h.eps);
+    // the change of p first, then one sum: p itself is rounded once
+    const uint64_t de2 = two(-decay, -decay), nr2 = two(-rate, -rate);
+    float* pf = reinterpret_cast<float*>(p4);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 y = both(v[j]);
+      root[2 * j] = sqrt_ftz(y.x);
+      root[2 * j + 1] = sqrt_ftz(y.y);
+      const float2 d = both(fma2(two(root[2 * j], root[2 * j + 1]), is2, ep2));
+      const uint64_t u = mul2(m[j], two(rcp_ftz(d.x), rcp_ftz(d.y)));
+      const uint64_t p0 = two(pf[2 * j], pf[2 * j + 1]);
+      const float2 q = both(add2(p0, fma2(u, nr2, mul2(p0, de2))));
+      pf[2 * j] = q.x;
+      pf[2 * j + 1] = q.y;
+    }
+  }
+  if (skip)
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (skip >> i & 1u)
+        reinterpret_cast<float*>(p4)[i] = e.p[base + (i >> 2) * 128 + lane * 4 + (i & 3)];
+  if (BITS == 8) {
+    am = scale_of(__uint_as_float(__reduce_max_sync(0xFFFFFFFFu, tm)));
+    av = scale_of(__uint_as_float(__reduce_max_sync(0xFFFFFFFFu, tv)));
+    const float im = am > 0.f ? __fdiv_rn(1.f, am) : 0.f, iv = av > 0.f ? inv_root(av) : 0.f;
+    const uint64_t r2 = two(kRound, kRound), nr2 = two(-kRound, -kRound);
+    const uint64_t im2 = two(im, im), iv2 = two(iv, iv), s127 = two(127.f, 127.f),
+                   s255 = two(255.f, 255.f), neg = two(-1.f, -1.f);
+    const bool tiny = av < kFlushScale;
+    float worst = 0.f;  // the largest distance from an integer
+    mc[0] = mc[1] = vc[0] = vc[1] = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 x = both(m[j]), z = both(v[j]);
+      float2 q = both(mul2(two(fabsf(x.x), fabsf(x.y)), im2));
+      uint64_t y = mul2(two(sqrt_ftz(q.x), sqrt_ftz(q.y)), s127);
+      float2 s = both(y);
+      y = two(copysignf(s.x, x.x), copysignf(s.y, x.y));
+      uint64_t t = add2(y, r2);
+      float2 d = both(fma2(add2(t, nr2), neg, y));
+      worst = fmaxf(worst, fmaxf(fabsf(d.x), fabsf(d.y)));
+      float2 k = both(t);
+      mc[j >> 1] |= (__byte_perm(__float_as_uint(k.x), __float_as_uint(k.y), 0x0040) & 0xFFFFu)
+                    << (16 * (j & 1));
+      q = both(mul2(two(root[2 * j], root[2 * j + 1]), iv2));
+      y = mul2(two(sqrt_ftz(q.x), sqrt_ftz(q.y)), s255);
+      t = add2(y, r2);
+      d = both(fma2(add2(t, nr2), neg, y));
+      worst = fmaxf(worst, fmaxf(fabsf(d.x), fabsf(d.y)));
+      k = both(t);
+      // (a v above zero is stored as 1 at least; without a scale as 0)
+      const uint32_t k0 = max(__float_as_uint(k.x) & 0xFFFFu, min(__float_as_uint(z.x), 1u));
+      const uint32_t k1 = max(__float_as_uint(k.y) & 0xFFFFu, min(__float_as_uint(z.y), 1u));
+      vc[j >> 1] |= (__byte_perm(k0, k1, 0x0040) & 0xFFFFu) << (16 * (j & 1));
+    }
+    if (worst > 0.5f - kNear || tiny || am == 0.f) {  // a border near by, or no usual scale
+      mc[0] = mc[1] = vc[0] = vc[1] = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float2 x = both(m[i / 2]), z = both(v[i / 2]);
+        const float mi = i & 1 ? x.y : x.x, vi = i & 1 ? z.y : z.x;
+        const float ri = tiny ? __fsqrt_rn(vi) : root[i];
+        int k = am > 0.f ? exact_m(fabsf(mi), am, 127.f * sqrt_ftz(fabsf(mi) * im)) : 0;
+        k = mi < 0.f ? -k : k;
+        mc[i / 4] |= (uint32_t)(k & 255) << (8 * (i & 3));
+        k = av > 0.f ? exact_v(vi, av, 255.f * sqrt_ftz(ri * iv)) : 0;
+        vc[i / 4] |= (uint32_t)(k & 255) << (8 * (i & 3));
+      }
+    }
+    if (lane == 0) {
+      e.ms[base / kBlk] = am;
+      e.vs[base / kBlk] = av;
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int o = u * 128 + lane * 4, in = left - o;
+    store4<WHOLE, float4, float>(e.p, base + o, in, p4[u]);
+    if (BITS == 8) {
+      store4<WHOLE, uint32_t, uint8_t>(e.m, base + o, in, mc[u]);
+      store4<WHOLE, uint32_t, uint8_t>(e.v, base + o, in, vc[u]);
+    } else {
+      const float2 x0 = both(m[2 * u]), x1 = both(m[2 * u + 1]);
+      const float2 y0 = both(v[2 * u]), y1 = both(v[2 * u + 1]);
+      store4<WHOLE, float4, float>(e.m, base + o, in, make_float4(x0.x, x0.y, x1.x, x1.y));
+      store4<WHOLE, float4, float>(e.v, base + o, in, make_float4(y0.x, y0.y, y1.x, y1.y));
+    }
+  }
+}
 
 // One warp takes a block of 256 elements, lane l elements 4 l .. 4 l + 3 and 128 + 4 l
 // .. 128 + 4 l + 3, so that every load and store of a warp is contiguous.  Memory
@@ -200,10 +390,8 @@ __global__ void __launch_bounds__(kMtThreads, 4)
     bc[1] = i2;
   }
   __syncthreads();
-  const float inv_bc1 = bc[0], isb2 = bc[1];
+  const MtRates r{bc[0], bc[1]};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint64_t b1 = two(a.h.b1, a.h.b1), b2 = two(a.h.b2, a.h.b2);
-  const uint64_t c1 = two(a.h.c1, a.h.c1), c2 = two(a.h.c2, a.h.c2);
   for (uint32_t c = blockIdx.x; c < a.h.chunks; c += gridDim.x) {
     int lo = 0, hi = a.h.n - 1;  // the last tensor whose first chunk is at or before c
     while (lo < hi) {
@@ -217,179 +405,10 @@ __global__ void __launch_bounds__(kMtThreads, 4)
     const int64_t base = (int64_t)(c - e.chunk0) * kChunk + warp * kBlk;
     if (base >= e.n) continue;  // uniform in the warp
     const int left = (int)min((int64_t)kBlk, e.n - base);
-    const float lr = e.lr, decay = lr * e.wd, rate = lr * inv_bc1;
-    float4 p4[2];
-    uint64_t g[4], m[4], v[4];  // element pairs
-    uint32_t mc[2], vc[2];
-    float am = 0.f, av = 0.f;
-    if (BITS == 8) {
-      am = e.ms[base / kBlk];
-      av = e.vs[base / kBlk];
-    }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int o = h * 128 + lane * 4, in = left - o;
-      p4[h] = load4<float4, float>(e.p, base + o, in);
-      if (GBITS == 32) {
-        const float4 y = load4<float4, float>(e.g, base + o, in);
-        g[2 * h] = two(y.x, y.y);
-        g[2 * h + 1] = two(y.z, y.w);
-      } else {
-        const U16x4 y = load4<U16x4, uint16_t>(e.g, base + o, in);
-        g[2 * h] = two(bf16_bits_to_float(y.v[0]), bf16_bits_to_float(y.v[1]));
-        g[2 * h + 1] = two(bf16_bits_to_float(y.v[2]), bf16_bits_to_float(y.v[3]));
-      }
-      if (BITS == 8) {
-        mc[h] = load4<uint32_t, uint8_t>(e.m, base + o, in);
-        vc[h] = load4<uint32_t, uint8_t>(e.v, base + o, in);
-      } else {
-        const float4 y = load4<float4, float>(e.m, base + o, in);
-        const float4 z = load4<float4, float>(e.v, base + o, in);
-        m[2 * h] = two(y.x, y.y);
-        m[2 * h + 1] = two(y.z, y.w);
-        v[2 * h] = two(z.x, z.y);
-        v[2 * h + 1] = two(z.z, z.w);
-      }
-    }
-    if (BITS == 8) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t wm = mc[j >> 1] >> (16 * (j & 1)), wv = vc[j >> 1] >> (16 * (j & 1));
-        m[j] = mul2(two(am, am), two(lm[wm & 255u], lm[(wm >> 8) & 255u]));
-        v[j] = mul2(two(av, av), two(lv[wv & 255u], lv[(wv >> 8) & 255u]));
-      }
-    }
-    // the moments; the bits of their largest magnitudes (NaN and infinity above all) give
-    // the block's scales and tell whether any is not finite
-    uint32_t tm = 0, tv = 0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 x0 = both(mul2(b1, m[j])), x1 = both(mul2(c1, g[j]));
-      const float2 y0 = both(mul2(b2, v[j])), y1 = both(mul2(mul2(c2, g[j]), g[j]));
-      const float2 x = make_float2(__fadd_rn(x0.x, x1.x), __fadd_rn(x0.y, x1.y));
-      const float2 y = make_float2(__fadd_rn(y0.x, y1.x), __fadd_rn(y0.y, y1.y));
-      m[j] = two(x.x, x.y);
-      v[j] = two(y.x, y.y);
-      tm = max(tm, max(__float_as_uint(x.x) & 0x7FFFFFFFu, __float_as_uint(x.y) & 0x7FFFFFFFu));
-      tv = max(tv, max(__float_as_uint(y.x), __float_as_uint(y.y)));
-    }
-    uint32_t skip = 0;  // elements whose moments leave the finite range keep everything
-    if (max(tm, tv) >= 0x7F800000u) {
-      atomicOr(a.h.dev_err, DEV_ERR_NONFINITE);
-      tm = tv = 0;
-      for (int i = 0; i < 8; ++i) {
-        const int64_t at = base + (i >> 2) * 128 + lane * 4 + (i & 3);
-        float2 x = both(m[0]), y = both(v[0]);
-#pragma unroll
-        for (int j = 1; j < 4; ++j)
-          if (j == i / 2) {
-            x = both(m[j]);
-            y = both(v[j]);
-          }
-        float mi = i & 1 ? x.y : x.x, vi = i & 1 ? y.y : y.x;
-        if (!(fabsf(mi) < INFINITY && vi < INFINITY)) {  // (such an element exists: at < n)
-          skip |= 1u << i;
-          mi = BITS == 8 ? am * lm[static_cast<uint8_t*>(e.m)[at]] : static_cast<float*>(e.m)[at];
-          vi = BITS == 8 ? av * lv[static_cast<uint8_t*>(e.v)[at]] : static_cast<float*>(e.v)[at];
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (j == i / 2) {
-            m[j] = i & 1 ? two(x.x, mi) : two(mi, x.y);
-            v[j] = i & 1 ? two(y.x, vi) : two(vi, y.y);
-          }
-        // (a state that already was not finite counts as zero in the scale)
-        const uint32_t bm = __float_as_uint(mi) & 0x7FFFFFFFu, bv = __float_as_uint(vi) & 0x7FFFFFFFu;
-        tm = max(tm, bm < 0x7F800000u ? bm : 0u);
-        tv = max(tv, bv < 0x7F800000u ? bv : 0u);
-      }
-    }
-    float root[8];
-    {
-      const uint64_t is2 = two(isb2, isb2), ep2 = two(a.h.eps, a.h.eps);
-      // the change of p first, then one sum: p itself is rounded once
-      const uint64_t de2 = two(-decay, -decay), nr2 = two(-rate, -rate);
-      float* pf = reinterpret_cast<float*>(p4);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 y = both(v[j]);
-        root[2 * j] = sqrt_ftz(y.x);
-        root[2 * j + 1] = sqrt_ftz(y.y);
-        const float2 d = both(fma2(two(root[2 * j], root[2 * j + 1]), is2, ep2));
-        const uint64_t u = mul2(m[j], two(rcp_ftz(d.x), rcp_ftz(d.y)));
-        const uint64_t p0 = two(pf[2 * j], pf[2 * j + 1]);
-        const float2 q = both(add2(p0, fma2(u, nr2, mul2(p0, de2))));
-        if (!(skip >> (2 * j) & 1u)) pf[2 * j] = q.x;
-        if (!(skip >> (2 * j) & 2u)) pf[2 * j + 1] = q.y;
-      }
-    }
-    if (BITS == 8) {
-      am = scale_of(__uint_as_float(__reduce_max_sync(0xFFFFFFFFu, tm)));
-      av = scale_of(__uint_as_float(__reduce_max_sync(0xFFFFFFFFu, tv)));
-      const float im = am > 0.f ? __fdiv_rn(1.f, am) : 0.f, iv = av > 0.f ? inv_root(av) : 0.f;
-      const uint64_t r2 = two(kRound, kRound), nr2 = two(-kRound, -kRound);
-      const uint64_t im2 = two(im, im), iv2 = two(iv, iv), s127 = two(127.f, 127.f),
-                     s255 = two(255.f, 255.f), neg = two(-1.f, -1.f);
-      const bool tiny = av < kFlushScale;
-      float worst = 0.f;  // the largest distance from an integer
-      mc[0] = mc[1] = vc[0] = vc[1] = 0;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 x = both(m[j]), z = both(v[j]);
-        float2 q = both(mul2(two(fabsf(x.x), fabsf(x.y)), im2));
-        uint64_t y = mul2(two(sqrt_ftz(q.x), sqrt_ftz(q.y)), s127);
-        float2 s = both(y);
-        y = two(copysignf(s.x, x.x), copysignf(s.y, x.y));
-        uint64_t t = add2(y, r2);
-        float2 d = both(fma2(add2(t, nr2), neg, y));
-        worst = fmaxf(worst, fmaxf(fabsf(d.x), fabsf(d.y)));
-        float2 k = both(t);
-        mc[j >> 1] |= (__byte_perm(__float_as_uint(k.x), __float_as_uint(k.y), 0x0040) & 0xFFFFu)
-                      << (16 * (j & 1));
-        q = both(mul2(two(root[2 * j], root[2 * j + 1]), iv2));
-        y = mul2(two(sqrt_ftz(q.x), sqrt_ftz(q.y)), s255);
-        t = add2(y, r2);
-        d = both(fma2(add2(t, nr2), neg, y));
-        worst = fmaxf(worst, fmaxf(fabsf(d.x), fabsf(d.y)));
-        k = both(t);
-        // (a v above zero is stored as 1 at least; without a scale as 0)
-        const uint32_t k0 = max(__float_as_uint(k.x) & 0xFFFFu, min(__float_as_uint(z.x), 1u));
-        const uint32_t k1 = max(__float_as_uint(k.y) & 0xFFFFu, min(__float_as_uint(z.y), 1u));
-        vc[j >> 1] |= (__byte_perm(k0, k1, 0x0040) & 0xFFFFu) << (16 * (j & 1));
-      }
-      if (worst > 0.5f - kNear || tiny || am == 0.f) {  // a border near by, or no usual scale
-        mc[0] = mc[1] = vc[0] = vc[1] = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float2 x = both(m[i / 2]), z = both(v[i / 2]);
-          const float mi = i & 1 ? x.y : x.x, vi = i & 1 ? z.y : z.x;
-          const float ri = tiny ? __fsqrt_rn(vi) : root[i];
-          int k = am > 0.f ? exact_m(fabsf(mi), am, 127.f * sqrt_ftz(fabsf(mi) * im)) : 0;
-          k = mi < 0.f ? -k : k;
-          mc[i / 4] |= (uint32_t)(k & 255) << (8 * (i & 3));
-          k = av > 0.f ? exact_v(vi, av, 255.f * sqrt_ftz(ri * iv)) : 0;
-          vc[i / 4] |= (uint32_t)(k & 255) << (8 * (i & 3));
-        }
-      }
-      if (lane == 0) {
-        e.ms[base / kBlk] = am;
-        e.vs[base / kBlk] = av;
-      }
-    }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int o = h * 128 + lane * 4, in = left - o;
-      store4<float4, float>(e.p, base + o, in, p4[h]);
-      if (BITS == 8) {
-        store4<uint32_t, uint8_t>(e.m, base + o, in, mc[h]);
-        store4<uint32_t, uint8_t>(e.v, base + o, in, vc[h]);
-      } else {
-        const float2 x0 = both(m[2 * h]), x1 = both(m[2 * h + 1]);
-        const float2 y0 = both(v[2 * h]), y1 = both(v[2 * h + 1]);
-        store4<float4, float>(e.m, base + o, in, make_float4(x0.x, x0.y, x1.x, x1.y));
-        store4<float4, float>(e.v, base + o, in, make_float4(y0.x, y0.y, y1.x, y1.y));
-      }
-    }
+    if (left == kBlk)
+      adamw_block<BITS, GBITS, true>(a.h, e, r, lm, lv, base, left, lane);
+    else
+      adamw_block<BITS, GBITS, false>(a.h, e, r, lm, lv, base, left, lane);
   }
 }
 
