@@ -61,6 +61,11 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 // 32 bytes of a row (a whole sector) in one store: rows are written by a lane each, and
 // two 16-byte halves of a sector cost two passes of the store path (an output tile of
 // 128 x 128 took 3000 to 6500 cycles to write that way).
@@ -561,12 +566,18 @@ __global__ void __launch_bounds__(kFThreads, 1)
 // Both are persistent, go through the other side in chunks of 64, keep P and dS in TMEM
 // as fp16 A operands over the columns they come from, and split the issuing of products
 // between two warps.
-//   warps 0-3, 4-7: the gradient warps (a TMEM lane per thread)
-//   warp 8 : TMA producer;  warps 9, 10: MMA issuers (warp 9 also allocates TMEM)
-//   warp 11: clears rows behind a document's end, and (dK, dV) stages the queries' values
+//   warps 0-15: the gradient warps, four groups of four (a TMEM lane per thread): groups 0
+//            and 2 take the two halves of the columns of one set (or stream), 1 and 3 of
+//            the other.  (With two groups of whole rows a chunk took a thread 3700 cycles,
+//            latency more than work: the products of two chunks need 2560.)
+//   warp 16: TMA producer;  warps 17, 18: MMA issuers (warp 17 also allocates TMEM)
+//   warp 19: clears rows behind a document's end, and (dK, dV) stages the queries' values
 // The prepared values of a query and head: dO' = 2^e dO in fp16, its largest in [1, 2),
 // e, delta' = 2^e delta and l = lse log2 e + e.
 constexpr int kBC = 64;        // columns of a chunk (queries for dK/dV, keys for dQ)
+constexpr int kBH = kBC / 2;   // columns of a thread
+constexpr int kBThreads = 640;
+constexpr int kBTma = 16, kBMma = 17, kBTail = 19;
 constexpr int kWindow = 64;    // tokens of a window of the exponents' minima
 // |dS'| <= 2 |dO'| |v| with |dO'| < 2 sqrt(128): below fp16's 65504 for these norms of v
 constexpr float kMaxNormV = 1447.f;
@@ -679,39 +690,46 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// Two consecutive fp32 rows' halves to bf16 and out: v[0, D) of one row, scaled, with cs
-// (nullable) the rotation by the row's position undone in the pairs (i, i + D/2).
+// A thread's share of a gradient row, the columns [q, q + D/4) and [D/2 + q, ...): scaled,
+// with cs (nullable; of the row's position, at column q) the rotation of the pairs
+// (i, i + D/2) undone, to bf16 at out + q and out + D/2 + q.
 template <int D>
-__device__ __forceinline__ void store_grad_row(const uint32_t (&raw)[D], float scale,
-                                               const float2* cs, uint16_t* out) {
+__device__ __forceinline__ void store_grad_share(const uint32_t (&lo)[D / 4],
+                                                 const uint32_t (&hi)[D / 4], float scale,
+                                                 const float2* cs, uint16_t* out) {
 #pragma unroll
-  for (int c = 0; c < D / 32; ++c) {
-    float a[16], b[16];
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      a[e] = __uint_as_float(raw[16 * c + e]) * scale;
-      b[e] = __uint_as_float(raw[D / 2 + 16 * c + e]) * scale;
-    }
-    if (cs) {
-#pragma unroll
-      for (int e = 0; e < 16; e += 2) {
-        const float4 f = __ldg(reinterpret_cast<const float4*>(cs + 16 * c + e));
-        const float x0 = a[e], y0 = b[e], x1 = a[e + 1], y1 = b[e + 1];
-        a[e] = x0 * f.x + y0 * f.y;
-        b[e] = y0 * f.x - x0 * f.y;
-        a[e + 1] = x1 * f.z + y1 * f.w;
-        b[e + 1] = y1 * f.z - x1 * f.w;
-      }
-    }
+  for (int c = 0; c < D / 4; c += 16) {
     uint32_t pa[8], pb[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      pa[e] = pack_bf16x2(a[2 * e], a[2 * e + 1]);
-      pb[e] = pack_bf16x2(b[2 * e], b[2 * e + 1]);
+    for (int e = 0; e < 16; e += 2) {
+      float a0 = __uint_as_float(lo[c + e]) * scale, a1 = __uint_as_float(lo[c + e + 1]) * scale;
+      float b0 = __uint_as_float(hi[c + e]) * scale, b1 = __uint_as_float(hi[c + e + 1]) * scale;
+      if (cs) {
+        const float4 f = __ldg(reinterpret_cast<const float4*>(cs + c + e));
+        const float x0 = a0, y0 = b0, x1 = a1, y1 = b1;
+        a0 = x0 * f.x + y0 * f.y;
+        b0 = y0 * f.x - x0 * f.y;
+        a1 = x1 * f.z + y1 * f.w;
+        b1 = y1 * f.z - x1 * f.w;
+      }
+      pa[e / 2] = pack_bf16x2(a0, a1);
+      pb[e / 2] = pack_bf16x2(b0, b1);
     }
-    st_global32(out + 16 * c, pa);
-    st_global32(out + D / 2 + 16 * c, pb);
+    st_global32(out + c, pa);
+    st_global32(out + D / 2 + c, pb);
   }
+}
+// That share of an accumulator row in TMEM.
+template <int D>
+__device__ __forceinline__ void load_share(uint32_t t, uint32_t (&lo)[D / 4], uint32_t (&hi)[D / 4]) {
+  if constexpr (D == 128) {
+    tmem_ld32(t, lo);
+    tmem_ld32(t + D / 2, hi);
+  } else {
+    tmem_ld16(t, lo);
+    tmem_ld16(t + D / 2, hi);
+  }
+  tmem_ld_wait();
 }
 
 // ------------------------------------------------------------------ dK, dV
@@ -735,7 +753,7 @@ struct DkvSmem {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kFThreads, 1)
+__global__ void __launch_bounds__(kBThreads, 1)
     packed_attn_dkdv_kernel(const __grid_constant__ CUtensorMap tm_kv,   // qkv, boxes of 128 rows
                             const __grid_constant__ CUtensorMap tm_q,    // qkv, boxes of 64 rows
                             const __grid_constant__ CUtensorMap tm_do,   // dO', boxes of 64 rows
@@ -761,7 +779,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
   uint8_t* Vs = Ks + SM::kTile;
   uint8_t* Qb = Vs + SM::kTile;             // [NR] chunks of Q
   uint8_t* dOb = Qb + NR * SM::kQc;         // [NR] chunks of dO'
-  float2* st = reinterpret_cast<float2*>(dOb + NR * SM::kQc);  // [NR][64] (emin - l, delta')
+  float* st = reinterpret_cast<float*>(dOb + NR * SM::kQc);  // [NR] 64 x (emin - l), 64 x -delta'
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr uint32_t kColS = 0, kColP = 2 * kBC, kColV = 4 * kBC, kColK = 4 * kBC + 128;
 
@@ -776,18 +794,18 @@ __global__ void __launch_bounds__(kFThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&s_full[i]), 1);
       mbar_init(smem_u32(&dp_full[i]), 1);
-      mbar_init(smem_u32(&p_full[i]), 4);
-      mbar_init(smem_u32(&ds_full[i]), 4);
+      mbar_init(smem_u32(&p_full[i]), 8);
+      mbar_init(smem_u32(&ds_full[i]), 8);
       mbar_init(smem_u32(&s_free[i]), 1);
       mbar_init(smem_u32(&dp_free[i]), 1);
     }
     mbar_init(smem_u32(&acc_full), 1);
-    mbar_init(smem_u32(&acc_free), 8);
+    mbar_init(smem_u32(&acc_free), 16);
     abort_sh = 0;
     fence_mbar_init();
     fence_proxy_async_smem();
   }
-  if (warp == kWarpMma) {
+  if (warp == kBMma) {
     tmem_alloc(smem_u32(&tmem_sh), 512);
     tmem_relinquish();
   }
@@ -823,7 +841,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
     return it;
   };
 
-  if (warp == kWarpTma) {
+  if (warp == kBTma) {
     if (lane == 0) {
       uint32_t c = 0, ni = 0;
       bool ok = true;
@@ -856,7 +874,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp == kWarpMma) {
+  } else if (warp == kBMma) {
     // ---------------------------------------------------------------- S^T and dP'^T
     const uint32_t lead = elect_lane();
     const uint32_t id = umma_idesc_f16(128, kBC);
@@ -895,7 +913,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
       }
       if (ok) mma_commit(lead, smem_u32(&kv_free));
     }
-  } else if (warp == kWarpMma + 1) {
+  } else if (warp == kBMma + 1) {
     // ---------------------------------------------------------------- dV' and dK'
     const uint32_t lead = elect_lane();
     const uint32_t id = umma_idesc_f16(128, D) | (1u << 16);  // B MN-major
@@ -915,7 +933,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
         tc_fence_after();
 #pragma unroll
         for (int kk = 0; kk < kBC / 16; ++kk)
-          mma_ts(lead, tmem + kColV, tmem + kColS + b * kBC + kk * 8, dd + (uint32_t)(kk * 128), id,
+          mma_ts(lead, tmem + kColV, tmem + kColS + b * kBC + (kk >> 1) * kBH + (kk & 1) * 8, dd + (uint32_t)(kk * 128), id,
                  (j > 0 || kk > 0) ? 1u : 0u);
         mma_commit(lead, smem_u32(&s_free[b]));
         ok = wait_all(&ds_full[b], c / 2);
@@ -923,14 +941,14 @@ __global__ void __launch_bounds__(kFThreads, 1)
         tc_fence_after();
 #pragma unroll
         for (int kk = 0; kk < kBC / 16; ++kk)
-          mma_ts(lead, tmem + kColK, tmem + kColP + b * kBC + kk * 8, qd + (uint32_t)(kk * 128), id,
+          mma_ts(lead, tmem + kColK, tmem + kColP + b * kBC + (kk >> 1) * kBH + (kk & 1) * 8, qd + (uint32_t)(kk * 128), id,
                  (j > 0 || kk > 0) ? 1u : 0u);
         mma_commit(lead, smem_u32(&dp_free[b]));
         mma_commit(lead, smem_u32(&r_free[slot]));
       }
       if (ok) mma_commit(lead, smem_u32(&acc_full));
     }
-  } else if (warp == kWarpTail) {
+  } else if (warp == kBTail) {
     // ---------------------------------------------------------------- the queries' values
     uint32_t c = 0, ni = 0;
     bool ok = true;
@@ -941,14 +959,21 @@ __global__ void __launch_bounds__(kFThreads, 1)
       // window that reaches into another document must not count)
       float emin = 127.f;
       const int w0 = (it.qs + kWindow - 1) / kWindow, w1 = it.t.end / kWindow;
+      const int e0 = w0 < w1 ? w0 * kWindow : it.t.end;  // [qs, e0) and [w1 .., end)
+      const int e1 = w0 < w1 ? w1 * kWindow : it.t.end;
+      // (loads of several heads in flight: one after the other they took 8 us an item)
+#pragma unroll 4
       for (int hh = 0; hh < nh; ++hh) {
         const float* we = winexp + (int64_t)(it.h0 + hh) * nw;
         const float* re = rowexp + (int64_t)(it.h0 + hh) * T;
-        for (int i = w0 + lane; i < w1; i += 32) emin = fminf(emin, __ldg(we + i));
-        const int e0 = w0 < w1 ? w0 * kWindow : it.t.end;  // [qs, e0) and [w1 .., end)
-        for (int q = it.qs + lane; q < e0; q += 32) emin = fminf(emin, __ldg(re + q));
-        if (w0 < w1)
-          for (int q = w1 * kWindow + lane; q < it.t.end; q += 32) emin = fminf(emin, __ldg(re + q));
+        const int q = it.qs + lane, u = e1 + lane;
+        const float a = w0 + lane < w1 ? __ldg(we + w0 + lane) : 127.f;
+        const float b = q < e0 ? __ldg(re + q) : 127.f, c = q + 32 < e0 ? __ldg(re + q + 32) : 127.f;
+        const float d = u < it.t.end ? __ldg(re + u) : 127.f;
+        const float e = u + 32 < it.t.end ? __ldg(re + u + 32) : 127.f;
+        emin = fminf(fminf(fminf(emin, a), fminf(b, c)), fminf(d, e));
+        for (int i = w0 + 32 + lane; i < w1; i += 32) emin = fminf(emin, __ldg(we + i));
+        for (int i = q + 64; i < e0; i += 32) emin = fminf(emin, __ldg(re + i));
       }
       emin = warp_min(emin);
       if (lane == 0) emin_sh[ni % kItems] = emin;
@@ -966,8 +991,11 @@ __global__ void __launch_bounds__(kFThreads, 1)
           }
           ok = wait_all(&r_full[slot], c / NR);
           if (!ok) break;
-          st[slot * kBC + lane] = v[0];
-          st[slot * kBC + 32 + lane] = v[1];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            st[slot * 2 * kBC + lane + 32 * i] = v[i].x;
+            st[slot * 2 * kBC + kBC + lane + 32 * i] = -v[i].y;
+          }
           if (q0 + kBC > it.t.end) {
             // queries behind the document: their P and dS are 0, and so must the rows be
             // that those multiply (0 * inf)
@@ -982,9 +1010,12 @@ __global__ void __launch_bounds__(kFThreads, 1)
     }
   } else {
     // ---------------------------------------------------------------- gradient warps
-    const uint32_t b = warp >> 2;              // set: chunks c with c % 2 == b
+    const uint32_t b = (warp >> 2) & 1;        // set: chunks c with c % 2 == b
+    const int hf = warp >> 3;                  // columns 32 hf .. of a chunk
     const int r = (warp & 3) * 32 + lane;      // key of the tile = TMEM lane
     const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t ts = trow + kColS + b * kBC + hf * kBH, tp = trow + kColP + b * kBC + hf * kBH;
+    const uint64_t sl22 = pack_f32x2(sl2, sl2);
     uint32_t c = 0, ni = 0;
     bool ok = true;
     for (int k = 0, w; ok && (w = deal(k, items)) >= 0; ++k) {
@@ -995,39 +1026,52 @@ __global__ void __launch_bounds__(kFThreads, 1)
       const int klast = it.t.row0 + (warp & 3) * 32 + 31;
       const int qall = klast < it.t.prompt ? it.t.begin : klast;
       const int n = nh * it.nc;
-      for (int j = 0; j < n; ++j, ++c) {
+      int q0 = it.qs + hf * kBH;  // first query of this thread's columns
+      for (int j = 0, jc = 0; j < n; ++j, ++c, q0 += kBC) {
+        if (jc == it.nc) {  // the next head
+          jc = 0;
+          q0 = it.qs + hf * kBH;
+        }
+        ++jc;
         if ((c & 1) != b) continue;
         const uint32_t slot = c % NR, ph = c / 2;
-        const int q0 = it.qs + (j % it.nc) * kBC;
-        const float4* sv4 = reinterpret_cast<const float4*>(st + slot * kBC);
+        // pairs of (emin - l), and of -delta'
+        const ulonglong2* l2 = reinterpret_cast<const ulonglong2*>(st + slot * 2 * kBC + hf * kBH);
+        const ulonglong2* dl = l2 + kBC / 4;
         ok = wait_all(&st_full[slot], c / NR) && wait_all(&s_full[b], ph);
         if (!ok) break;
         tc_fence_after();
-        uint32_t p[kBC];
-        tmem_ld32(trow + kColS + b * kBC, p);
-        tmem_ld32(trow + kColS + b * kBC + 32, p + 32);
+        uint32_t sv[kBH];
+        tmem_ld32(ts, sv);
         tmem_ld_wait();
-        const bool whole = q0 >= qall && q0 + kBC <= it.t.end;  // (uniform in the warp)
+        const bool whole = q0 >= qall && q0 + kBH <= it.t.end;  // (uniform in the warp)
+        uint64_t p[kBH / 2];
 #pragma unroll
-        for (int e = 0; e < kBC; e += 2) {
-          const float4 v = sv4[e / 2];
-          p[e] = __float_as_uint(ex2(fmaf(__uint_as_float(p[e]), sl2, v.x)));
-          p[e + 1] = __float_as_uint(ex2(fmaf(__uint_as_float(p[e + 1]), sl2, v.z)));
+        for (int e = 0; e < kBH / 2; e += 2) {
+          const ulonglong2 v = l2[e / 2];
+          const float2 x = unpack_f32x2(fma_f32x2(
+              pack_f32x2(__uint_as_float(sv[2 * e]), __uint_as_float(sv[2 * e + 1])), sl22, v.x));
+          const float2 y = unpack_f32x2(fma_f32x2(
+              pack_f32x2(__uint_as_float(sv[2 * e + 2]), __uint_as_float(sv[2 * e + 3])), sl22, v.y));
+          p[e] = pack_f32x2(ex2(x.x), ex2(x.y));
+          p[e + 1] = pack_f32x2(ex2(y.x), ex2(y.y));
         }
         if (!whole) {
           const int lo = qlo - q0, hi = it.t.end - q0;
 #pragma unroll
-          for (int e = 0; e < kBC; ++e)
-            if (e < lo || e >= hi) p[e] = 0u;
+          for (int e = 0; e < kBH / 2; ++e) {
+            const float2 x = unpack_f32x2(p[e]);
+            p[e] = pack_f32x2(2 * e >= lo && 2 * e < hi ? x.x : 0.f,
+                              2 * e + 1 >= lo && 2 * e + 1 < hi ? x.y : 0.f);
+          }
         }
+        uint32_t pk[kBH / 2];
 #pragma unroll
-        for (int e = 0; e < kBC; e += 32) {
-          uint32_t pk[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            pk[i] = pack_f16x2(__uint_as_float(p[e + 2 * i]), __uint_as_float(p[e + 2 * i + 1]));
-          tmem_st16(trow + kColS + b * kBC + e / 2, pk);
+        for (int e = 0; e < kBH / 2; ++e) {
+          const float2 x = unpack_f32x2(p[e]);
+          pk[e] = pack_f16x2(x.x, x.y);
         }
+        tmem_st16(ts, pk);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -1035,27 +1079,25 @@ __global__ void __launch_bounds__(kFThreads, 1)
         ok = wait_all(&dp_full[b], ph);
         if (!ok) break;
         tc_fence_after();
-        uint32_t dsk[kBC / 2];
+        tmem_ld32(tp, sv);
+        tmem_ld_wait();
 #pragma unroll
-        for (int e = 0; e < kBC; e += 32) {
-          uint32_t d[32];
-          tmem_ld32(trow + kColP + b * kBC + e, d);
-          tmem_ld_wait();
+        for (int e = 0; e < kBH / 2; e += 2) {
+          const ulonglong2 v = dl[e / 2];
 #pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            const float4 v = sv4[(e + i) / 2];
-            float x = __uint_as_float(p[e + i]) * (__uint_as_float(d[i]) - v.y);
-            float y = __uint_as_float(p[e + i + 1]) * (__uint_as_float(d[i + 1]) - v.w);
+          for (int i = 0; i < 2; ++i) {
+            const uint64_t d = pack_f32x2(__uint_as_float(sv[2 * (e + i)]),
+                                          __uint_as_float(sv[2 * (e + i) + 1]));
+            float2 x = unpack_f32x2(mul_f32x2(p[e + i], add_f32x2(d, i ? v.y : v.x)));
             if (!whole) {  // (dp behind the document may be anything)
-              x = p[e + i] ? x : 0.f;
-              y = p[e + i + 1] ? y : 0.f;
+              const float2 q = unpack_f32x2(p[e + i]);
+              x.x = q.x != 0.f ? x.x : 0.f;
+              x.y = q.y != 0.f ? x.y : 0.f;
             }
-            dsk[(e + i) / 2] = pack_f16x2(x, y);
+            pk[e + i] = pack_f16x2(x.x, x.y);
           }
         }
-#pragma unroll
-        for (int e = 0; e < kBC / 2; e += 16)
-          tmem_st16(trow + kColP + b * kBC + e, *reinterpret_cast<uint32_t(*)[16]>(dsk + e));
+        tmem_st16(tp, pk);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -1066,10 +1108,8 @@ __global__ void __launch_bounds__(kFThreads, 1)
       ok = ok && wait_all(&acc_full, ni);
       if (!ok) break;
       tc_fence_after();
-      uint32_t acc[D];
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) tmem_ld32(trow + (b ? kColK : kColV) + 32 * i, acc + 32 * i);
-      tmem_ld_wait();
+      uint32_t lo[D / 4], hi[D / 4];
+      load_share<D>(trow + (b ? kColK : kColV) + hf * (D / 4), lo, hi);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&acc_free));
@@ -1077,17 +1117,22 @@ __global__ void __launch_bounds__(kFThreads, 1)
       ++ni;
       if (kpos < it.t.end) {
         if (parts == 1) {
-          const int col = (b ? H + it.g : H + Hkv + it.g) * D;
-          store_grad_row<D>(acc, f, b && cs ? cs + (int64_t)idx.pos[kpos] * (D / 2) : nullptr,
-                            dqkv + (int64_t)kpos * (H + 2 * Hkv) * D + col);
+          const int col = (b ? H + it.g : H + Hkv + it.g) * D + hf * (D / 4);
+          store_grad_share<D>(lo, hi, f,
+                              b && cs ? cs + (int64_t)idx.pos[kpos] * (D / 2) + hf * (D / 4) : nullptr,
+                              dqkv + (int64_t)kpos * (H + 2 * Hkv) * D + col);
         } else {
-          float* out = (b ? dk : dv) + ((int64_t)kpos * Hkv * parts + it.h0 / nh) * D;
+          float* out = (b ? dk : dv) + ((int64_t)kpos * Hkv * parts + it.h0 / nh) * D + hf * (D / 4);
 #pragma unroll
-          for (int e = 0; e < D; e += 8) {
-            uint32_t v[8];
+          for (int e = 0; e < D / 4; e += 8) {
+            uint32_t x[8], y[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = __float_as_uint(__uint_as_float(acc[e + i]) * f);
-            st_global32(out + e, v);
+            for (int i = 0; i < 8; ++i) {
+              x[i] = __float_as_uint(__uint_as_float(lo[e + i]) * f);
+              y[i] = __float_as_uint(__uint_as_float(hi[e + i]) * f);
+            }
+            st_global32(out + e, x);
+            st_global32(out + D / 2 + e, y);
           }
         }
       }
@@ -1096,7 +1141,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
   tc_fence_before();
   __syncthreads();
   if (abort_sh) settle_ns(2000000);
-  if (warp == kWarpMma) {
+  if (warp == kBMma) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
@@ -1116,7 +1161,7 @@ struct DqSmem {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kFThreads, 1)
+__global__ void __launch_bounds__(kBThreads, 1)
     packed_attn_dq_kernel(const __grid_constant__ CUtensorMap tm_q,    // qkv, boxes of 128 rows
                           const __grid_constant__ CUtensorMap tm_kv,   // qkv, boxes of 64 rows
                           const __grid_constant__ CUtensorMap tm_do,   // dO', boxes of 128 rows
@@ -1146,11 +1191,11 @@ __global__ void __launch_bounds__(kFThreads, 1)
       mbar_init(smem_u32(&q_full[i]), 1);
       mbar_init(smem_u32(&q_free[i]), 1);
       mbar_init(smem_u32(&s_full[i]), 1);
-      mbar_init(smem_u32(&s_free[i]), 4);
+      mbar_init(smem_u32(&s_free[i]), 8);
       mbar_init(smem_u32(&dp_full[i]), 1);
-      mbar_init(smem_u32(&ds_full[i]), 4);
+      mbar_init(smem_u32(&ds_full[i]), 8);
       mbar_init(smem_u32(&dq_full[i]), 1);
-      mbar_init(smem_u32(&dq_free[i]), 4);
+      mbar_init(smem_u32(&dq_free[i]), 8);
     }
     for (int i = 0; i < NR; ++i) {
       mbar_init(smem_u32(&r_full[i]), 1);
@@ -1161,7 +1206,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
     fence_mbar_init();
     fence_proxy_async_smem();
   }
-  if (warp == kWarpMma) {
+  if (warp == kBMma) {
     tmem_alloc(smem_u32(&tmem_sh), 512);
     tmem_relinquish();
   }
@@ -1181,7 +1226,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
     return __all_sync(0xFFFFFFFFu, wait(bar, parity));
   };
 
-  if (warp == kWarpTma) {
+  if (warp == kBTma) {
     if (lane == 0) {
       uint32_t c = 0, nq[2] = {0, 0};
       bool ok = true;
@@ -1219,9 +1264,9 @@ __global__ void __launch_bounds__(kFThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp == kWarpMma || warp == kWarpMma + 1) {
+  } else if (warp == kBMma || warp == kBMma + 1) {
     // ---------------------------------------------------------------- MMA issuers
-    const int s = warp - kWarpMma;
+    const int s = warp - kBMma;
     const uint32_t lead = elect_lane();
     const uint32_t id_s = umma_idesc_f16(128, kBC);
     const uint32_t id_q = umma_idesc_f16(128, D) | (1u << 16);  // B (K) MN-major
@@ -1270,7 +1315,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
           const uint64_t kd = umma_desc_mn_sw128(smem_u32(Kb + slot * SM::kKc), kBC * 128, 1024u);
 #pragma unroll
           for (int kk = 0; kk < kBC / 16; ++kk)
-            mma_ts(lead, tq, tp + kk * 8, kd + (uint32_t)(kk * 128), id_q,
+            mma_ts(lead, tq, tp + (kk >> 1) * kBH + (kk & 1) * 8, kd + (uint32_t)(kk * 128), id_q,
                    (j > 0 || kk > 0) ? 1u : 0u);
           if (more)
             scores(tp, od, Vb + next * SM::kKc, &dp_full[s]);
@@ -1285,7 +1330,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
         mma_commit(lead, smem_u32(&r_free[slot]));
       }
     }
-  } else if (warp == kWarpTail) {
+  } else if (warp == kBTail) {
     // Follows every chunk of the ring; keys behind the document: their dS is 0, and so
     // must the K rows be that those multiply (0 * inf).
     uint32_t c = 0;
@@ -1310,9 +1355,12 @@ __global__ void __launch_bounds__(kFThreads, 1)
     }
   } else {
     // ---------------------------------------------------------------- gradient warps
-    const int s = warp >> 2;
+    const int s = (warp >> 2) & 1;
+    const int hf = warp >> 3;              // keys 32 hf .. of a chunk
     const int r = (warp & 3) * 32 + lane;  // query of the tile = TMEM lane
     const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)s * 128;
+    const uint32_t ts = trow + kColS + hf * kBH, tp = trow + kColP + hf * kBH;
+    const uint64_t sl22 = pack_f32x2(sl2, sl2);
     uint32_t nc = 0, ni = 0;
     bool ok = true;
     for (int k = 0, w; ok && (w = deal(k, items)) >= 0; ++k) {
@@ -1325,51 +1373,44 @@ __global__ void __launch_bounds__(kFThreads, 1)
       const int64_t at = (int64_t)it.head * T + min(q, it.end - 1);
       const float2 sq = __ldg(stats + at);
       const float e = __ldg(rowexp + at);
-      const float nl2 = e - sq.x, dl = sq.y;
+      const uint64_t nl2 = pack_f32x2(e - sq.x, e - sq.x), ndl = pack_f32x2(-sq.y, -sq.y);
       for (int j = 0; j < n; ++j, ++nc) {
         ok = wait_all(&s_full[s], nc);
         if (!ok) break;
         tc_fence_after();
-        uint32_t p[kBC];
-        tmem_ld32(trow + kColS, p);
-        tmem_ld32(trow + kColS + 32, p + 32);
+        uint32_t sv[kBH];
+        tmem_ld32(ts, sv);
         tmem_ld_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&s_free[s]));
+        const int k0 = it.begin + j * kBC + hf * kBH;
+        const int last = kmax - k0;
+        const bool whole = k0 + kBH - 1 <= kall;  // (uniform in the warp)
+        uint64_t p[kBH / 2];
 #pragma unroll
-        for (int i = 0; i < kBC; ++i)
-          p[i] = __float_as_uint(ex2(fmaf(__uint_as_float(p[i]), sl2, nl2)));
-        const int last = kmax - it.begin - j * kBC;
-        const bool whole = it.begin + (j + 1) * kBC - 1 <= kall;  // (uniform in the warp)
-        if (!whole) {
-#pragma unroll
-          for (int i = 0; i < kBC; ++i)
-            if (i > last) p[i] = 0u;
+        for (int i = 0; i < kBH / 2; ++i) {
+          const float2 x = unpack_f32x2(fma_f32x2(
+              pack_f32x2(__uint_as_float(sv[2 * i]), __uint_as_float(sv[2 * i + 1])), sl22, nl2));
+          p[i] = pack_f32x2(ex2(x.x), ex2(x.y));
         }
         ok = wait_all(&dp_full[s], nc);
         if (!ok) break;
         tc_fence_after();
-        uint32_t dsk[kBC / 2];
+        tmem_ld32(tp, sv);
+        tmem_ld_wait();
+        uint32_t dsk[kBH / 2];
 #pragma unroll
-        for (int i = 0; i < kBC; i += 32) {
-          uint32_t d[32];
-          tmem_ld32(trow + kColP + i, d);
-          tmem_ld_wait();
-#pragma unroll
-          for (int u = 0; u < 32; u += 2) {
-            float x = __uint_as_float(p[i + u]) * (__uint_as_float(d[u]) - dl);
-            float y = __uint_as_float(p[i + u + 1]) * (__uint_as_float(d[u + 1]) - dl);
-            if (!whole) {  // (dp behind the document may be anything)
-              x = i + u > last ? 0.f : x;
-              y = i + u + 1 > last ? 0.f : y;
-            }
-            dsk[(i + u) / 2] = pack_f16x2(x, y);
+        for (int i = 0; i < kBH / 2; ++i) {
+          const uint64_t d = pack_f32x2(__uint_as_float(sv[2 * i]), __uint_as_float(sv[2 * i + 1]));
+          float2 x = unpack_f32x2(mul_f32x2(p[i], add_f32x2(d, ndl)));
+          if (!whole) {  // (scores and dp behind the row's last key may be anything)
+            x.x = 2 * i > last ? 0.f : x.x;
+            x.y = 2 * i + 1 > last ? 0.f : x.y;
           }
+          dsk[i] = pack_f16x2(x.x, x.y);
         }
-#pragma unroll
-        for (int i = 0; i < kBC / 2; i += 16)
-          tmem_st16(trow + kColP + i, *reinterpret_cast<uint32_t(*)[16]>(dsk + i));
+        tmem_st16(tp, dsk);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -1380,16 +1421,16 @@ __global__ void __launch_bounds__(kFThreads, 1)
       if (!ok) break;
       ++ni;
       tc_fence_after();
-      uint32_t acc[D];
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) tmem_ld32(trow + kColQ + 32 * i, acc + 32 * i);
-      tmem_ld_wait();
+      uint32_t lo[D / 4], hi[D / 4];
+      load_share<D>(trow + kColQ + hf * (D / 4), lo, hi);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&dq_free[s]));
       if (q < it.end)
-        store_grad_row<D>(acc, scale * ex2(-e), cs ? cs + (int64_t)idx.pos[q] * (D / 2) : nullptr,
-                          dqkv + (int64_t)q * (H + 2 * Hkv) * D + (int64_t)it.head * D);
+        store_grad_share<D>(lo, hi, scale * ex2(-e),
+                            cs ? cs + (int64_t)idx.pos[q] * (D / 2) + hf * (D / 4) : nullptr,
+                            dqkv + (int64_t)q * (H + 2 * Hkv) * D + (int64_t)it.head * D +
+                                hf * (D / 4));
     }
   }
   {  // padding rows have no gradient
@@ -1403,7 +1444,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
   tc_fence_before();
   __syncthreads();
   if (abort_sh) settle_ns(2000000);
-  if (warp == kWarpMma) {
+  if (warp == kBMma) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
@@ -1565,11 +1606,11 @@ int bwd_t(const uint16_t* qkv, const PackedIndex& x, const uint16_t* o, const fl
   const int parts = dkv_parts(T, H, Hkv), sms = gemm_num_sms();
   const int64_t kitems = (int64_t)x.cap * Hkv * parts;
   LSQ_CUDA(launch_dep(packed_attn_dkdv_kernel<D>, dim3((unsigned)std::min<int64_t>(kitems, sms)),
-                      kFThreads, DkvSmem<D>::kBytes, st, qkv128, qkv64, do64, x, w.stats, w.rowexp,
+                      kBThreads, DkvSmem<D>::kBytes, st, qkv128, qkv64, do64, x, w.stats, w.rowexp,
                       w.winexp, T, H, Hkv, H / Hkv / parts, sl2, scale, cs, dqkv, w.dk, w.dv, err));
   const int64_t qitems = (H / Hkv) % 2 == 0 ? (int64_t)x.cap * (H / 2) : (int64_t)x.cap2 * H;
   LSQ_CUDA(launch_dep(packed_attn_dq_kernel<D>, dim3((unsigned)std::min<int64_t>(qitems, sms)),
-                      kFThreads, DqSmem<D>::kBytes, st, qkv128, qkv64, do128, x, w.stats, w.rowexp,
+                      kBThreads, DqSmem<D>::kBytes, st, qkv128, qkv64, do128, x, w.stats, w.rowexp,
                       T, H, Hkv, sl2, scale, cs, dqkv, err));
   if (parts > 1) {
     const int64_t n = T * 2 * Hkv * (D / 8);
