@@ -890,7 +890,7 @@ __global__ void __launch_bounds__(kBThreads, 1)
         const uint32_t slot = c % NR, b = c & 1;
         const uint64_t qd = umma_desc_k_sw128(smem_u32(Qb + slot * SM::kQc));
         const uint64_t dd = umma_desc_k_sw128(smem_u32(dOb + slot * SM::kQc));
-        ok = wait_all(&r_full[slot], c / NR);
+        ok = wait_all(&r_full[slot], c / NR) && wait_all(&st_full[slot], c / NR);
         // dV of the chunk before the last has read the P in this buffer
         if (ok && c >= 2) ok = wait_all(&s_free[b], c / 2 - 1);
         if (!ok) break;
@@ -1038,7 +1038,7 @@ __global__ void __launch_bounds__(kBThreads, 1)
         // pairs of (emin - l), and of -delta'
         const ulonglong2* l2 = reinterpret_cast<const ulonglong2*>(st + slot * 2 * kBC + hf * kBH);
         const ulonglong2* dl = l2 + kBC / 4;
-        ok = wait_all(&st_full[slot], c / NR) && wait_all(&s_full[b], ph);
+        ok = wait_all(&s_full[b], ph);  // (and st: S^T is issued behind it)
         if (!ok) break;
         tc_fence_after();
         uint32_t sv[kBH];
@@ -1072,14 +1072,15 @@ __global__ void __launch_bounds__(kBThreads, 1)
           pk[e] = pack_f16x2(x.x, x.y);
         }
         tmem_st16(ts, pk);
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&p_full[b]));
+        // (dP' is there by now: its load runs while the store of P' does)
         ok = wait_all(&dp_full[b], ph);
         if (!ok) break;
         tc_fence_after();
         tmem_ld32(tp, sv);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&p_full[b]));
         tmem_ld_wait();
 #pragma unroll
         for (int e = 0; e < kBH / 2; e += 2) {
@@ -1552,12 +1553,14 @@ struct BwdWs {
 
 // Into how many shares a kv head's query heads are split for dK and dV.  One share
 // needs no partial sums (8 bytes written and read per token, share and dimension) but
-// leaves few items: at least two per SM are wanted, so that they even out.
+// leaves few items: one per SM is wanted (what is left uneven dQ fills).  One, two and
+// four per SM took 512, 515 and 541 us forward and backward of 16,384 packed tokens with
+// 16/2 heads, 156, 176 and 176 us backward of 2048 tokens with 32/8.
 int dkv_parts(int64_t T, int H, int Hkv) {
   const int G = H / Hkv;
   const int64_t tiles = (T + kPackedTile - 1) / kPackedTile;
   for (int p = 1; p < G; ++p)
-    if (G % p == 0 && tiles * Hkv * p >= 2 * (int64_t)gemm_num_sms()) return p;
+    if (G % p == 0 && tiles * Hkv * p >= (int64_t)gemm_num_sms()) return p;
   return G;
 }
 
