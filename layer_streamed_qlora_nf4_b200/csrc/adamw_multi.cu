@@ -128,9 +128,11 @@ __device__ __forceinline__ int exact_v(float x, float a, float y) {
   return x > 0.f ? max(k, 1) : k;
 }
 __device__ __forceinline__ float inv_root(float a) { return __fdiv_rn(1.f, __fsqrt_rn(a)); }
-// With a scale of at least 2^-86 a subnormal x has code 0 or 1 whatever its root, so the
-// flushing root will do; below that the exact one is taken.
-constexpr float kFlushScale = 1.2924697e-26f;
+// The roots of v are taken of 2^24 v, 2^12 too large: so that a subnormal v keeps its root
+// (with an eps below 2^-63 that is the quotient's whole denominator).  From 2^100 on, where
+// 2^24 v could overflow, by the exact square root.
+constexpr float kRootUp = 16777216.f, kRootDown = 1.f / 4096.f;
+constexpr uint32_t kHugeV = (127u + 100u) << 23;
 
 // The values the codes stand for: fl32(c |c| / 127^2) at c + 128, and fl32(q^4 / 255^4).
 __device__ __forceinline__ float level_m(int c) {
@@ -271,15 +273,21 @@ __device__ __forceinline__ void adamw_block(const MtHead& h, const MtEntry& e, c
   }
   float root[8];
   {
-    const uint64_t is2 = two(r.isb2, r.isb2), ep2 = two(h.eps, h.eps);
+    const float isd = r.isb2 * kRootDown;
+    const uint64_t is2 = two(isd, isd), ep2 = two(h.eps, h.eps), up2 = two(kRootUp, kRootUp);
     // the change of p first, then one sum: p itself is rounded once
     const uint64_t de2 = two(-decay, -decay), nr2 = two(-rate, -rate);
     float* pf = reinterpret_cast<float*>(p4);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float2 y = both(v[j]);
+      const float2 y = both(mul2(v[j], up2));
       root[2 * j] = sqrt_ftz(y.x);
       root[2 * j + 1] = sqrt_ftz(y.y);
+      if (tv >= kHugeV) {
+        const float2 z = both(v[j]);
+        root[2 * j] = __fsqrt_rn(z.x) * 4096.f;
+        root[2 * j + 1] = __fsqrt_rn(z.y) * 4096.f;
+      }
       const float2 d = both(fma2(two(root[2 * j], root[2 * j + 1]), is2, ep2));
       const uint64_t u = mul2(m[j], two(rcp_ftz(d.x), rcp_ftz(d.y)));
       const uint64_t p0 = two(pf[2 * j], pf[2 * j + 1]);
@@ -296,11 +304,10 @@ __device__ __forceinline__ void adamw_block(const MtHead& h, const MtEntry& e, c
   if (BITS == 8) {
     am = scale_of(__uint_as_float(__reduce_max_sync(0xFFFFFFFFu, tm)));
     av = scale_of(__uint_as_float(__reduce_max_sync(0xFFFFFFFFu, tv)));
-    const float im = am > 0.f ? __fdiv_rn(1.f, am) : 0.f, iv = av > 0.f ? inv_root(av) : 0.f;
+    const float im = am > 0.f ? __fdiv_rn(1.f, am) : 0.f, iv = av > 0.f ? inv_root(av) * kRootDown : 0.f;
     const uint64_t r2 = two(kRound, kRound), nr2 = two(-kRound, -kRound);
     const uint64_t im2 = two(im, im), iv2 = two(iv, iv), s127 = two(127.f, 127.f),
                    s255 = two(255.f, 255.f), neg = two(-1.f, -1.f);
-    const bool tiny = av < kFlushScale;
     float worst = 0.f;  // the largest distance from an integer
     mc[0] = mc[1] = vc[0] = vc[1] = 0;
 #pragma unroll
@@ -327,17 +334,16 @@ __device__ __forceinline__ void adamw_block(const MtHead& h, const MtEntry& e, c
       const uint32_t k1 = max(__float_as_uint(k.y) & 0xFFFFu, min(__float_as_uint(z.y), 1u));
       vc[j >> 1] |= (__byte_perm(k0, k1, 0x0040) & 0xFFFFu) << (16 * (j & 1));
     }
-    if (worst > 0.5f - kNear || tiny || am == 0.f) {  // a border near by, or no usual scale
+    if (worst > 0.5f - kNear || fminf(am, av) == 0.f) {  // a border near by, or no scale
       mc[0] = mc[1] = vc[0] = vc[1] = 0;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float2 x = both(m[i / 2]), z = both(v[i / 2]);
         const float mi = i & 1 ? x.y : x.x, vi = i & 1 ? z.y : z.x;
-        const float ri = tiny ? __fsqrt_rn(vi) : root[i];
         int k = am > 0.f ? exact_m(fabsf(mi), am, 127.f * sqrt_ftz(fabsf(mi) * im)) : 0;
         k = mi < 0.f ? -k : k;
         mc[i / 4] |= (uint32_t)(k & 255) << (8 * (i & 3));
-        k = av > 0.f ? exact_v(vi, av, 255.f * sqrt_ftz(ri * iv)) : 0;
+        k = av > 0.f ? exact_v(vi, av, 255.f * sqrt_ftz(root[i] * iv)) : 0;
         vc[i / 4] |= (uint32_t)(k & 255) << (8 * (i & 3));
       }
     }

@@ -138,6 +138,42 @@ def test_tiny_and_huge_moments(L):
 
 
 @pytest.mark.parametrize("bits", [8, 32])
+@pytest.mark.parametrize("eps", [1e-30, 2.0 ** -126])
+def test_denominators_of_subnormal_and_huge_moments(L, bits, eps):
+    """With an eps far below the root of a subnormal v that root is the denominator.  The
+    change of p (from 0) is a product of rate, moment and reciprocal: the rate is rounded
+    twice, the root and the reciprocal are off by 2^-23, the root's factor, the sum, and
+    three products by 2^-24 each, together below 2^-20; its last bits may be subnormal."""
+    import torch
+    n = 2048
+    rng = np.random.default_rng(5)
+    g = (rng.standard_normal(n) * 10.0 ** rng.uniform(-21.5, -16.5, n)).astype(np.float32)
+    g[512:1024:3] = 10.0 ** rng.uniform(14, 17, len(g[512:1024:3]))
+    x = dict(p=[np.zeros(n, np.float32)], g=[g],
+             m=[np.zeros(n, np.int8 if bits == 8 else np.float32)],
+             v=[np.zeros(n, np.uint8 if bits == 8 else np.float32)],
+             ms=[np.zeros(8, np.float32)], vs=[np.zeros(8, np.float32)])
+    d = _device(x, False)
+    L.AdamWMulti(d["p"], d["g"], d["m"], d["v"], lr=1e-3, m_scale=d["ms"] if bits == 8 else None,
+                 v_scale=d["vs"] if bits == 8 else None, eps=eps).step(1)
+    torch.cuda.synchronize()
+    assert L.lsq_device_status(clear=True) == 0
+    zero = np.zeros(n, np.float32)
+    rp, m1, v1 = op.adamw(zero, g, zero, zero, 1, 1e-3, 0.0, eps=eps)
+    assert ((v1 > 0) & (v1 < 2.0 ** -126)).sum() > 100 and (v1 > 2.0 ** 100).sum() > 10
+    got = d["p"][0].cpu().numpy().astype(np.float64)
+    ok = np.abs(rp) < 3e38
+    assert (np.abs(got - rp)[ok] <= 2.0 ** -20 * np.abs(rp[ok]) + 2.0 ** -149).all()
+    for k, s, ref, signed in (("m", "ms", m1, True), ("v", "vs", v1, False)):
+        if bits == 8:
+            c, sc = op.encode(ref, signed)
+            assert np.array_equal(d[k][0].cpu().numpy(), c)
+            assert np.array_equal(d[s][0].cpu().numpy(), sc)
+        else:
+            assert np.array_equal(d[k][0].cpu().numpy(), ref)
+
+
+@pytest.mark.parametrize("bits", [8, 32])
 def test_not_finite_gradients_are_left_out(L, bits):
     import torch
     sizes = [600]
