@@ -458,7 +458,7 @@ int packed_index(const int32_t* lengths, const int32_t* prefix, int32_t n_docs, 
 /* packed_attention_fwd - o = softmax(q k^T / sqrt(d)) v over the keys a token sees.
  *   qkv    device fp16 [T, (H + 2 Hkv) d]: the q heads, then the k and v heads (RoPE
  *          already applied); query head h reads kv head h / (H / Hkv).
- *   H % Hkv == 0;  d is 64 or 128.
+ *   H % Hkv == 0, H at most 32767;  d is 64 or 128;  T (H + 2 Hkv) below 2^31.
  *   index, n_docs  of packed_index with this T and n_docs.
  *   o      device fp16 [T, H d], 32-byte aligned;  lse  device fp32 [H, T]: the
  *          log-sum-exp of the scaled scores.  Padding rows get o = 0 and lse = -inf.
@@ -478,7 +478,9 @@ size_t packed_attention_workspace_bytes(int64_t T, int32_t H, int32_t Hkv, int32
  *   ws      device workspace of packed_attention_workspace_bytes(T, H, Hkv, d) bytes,
  *           32-byte aligned.
  * The score gradients multiply in fp16 after each row of dout is scaled by the power
- * of two that brings its largest magnitude to [1, 2), so their range does not matter; a
+ * of two that brings its largest magnitude to [1, 2), so their range does not matter for
+ * dq.  In dk and dv the rows of a document that see a tile of 128 keys share the factor of
+ * the largest, so a row's part is exact to 2^-25 of the largest row's, not of its own.  A
  * row of v whose norm is above 1447 latches LSQ_DEV_ERR_NONFINITE (its score gradients may
  * overflow).  Asynchronous, deterministic (fixed-order sums, no atomics). */
 int packed_attention_bwd(const uint16_t* qkv, const int32_t* index, int32_t n_docs,
@@ -539,8 +541,8 @@ int lora_adamw_step(float* lora, const float* grad, const lsq_adamw* opt, int64_
  *   grad_bits  32: g fp32;  16: g bf16.
  *   step_dev  device int32 or NULL: read instead of step, so that a captured update
  *             can be replayed as the count advances (below 1 counts as 1).
- * An element whose new moment is not finite keeps its parameter and moments and
- * latches LSQ_DEV_ERR_NONFINITE.  Asynchronous, deterministic. */
+ * An element whose new moment is not finite keeps its parameter and moments (8-bit ones
+ * take the block's new scale) and latches LSQ_DEV_ERR_NONFINITE.  Asynchronous, deterministic. */
 typedef struct lsq_adamw_tensor {
   float* p;
   const void* g;
@@ -603,7 +605,8 @@ int decoder_layer_packed_bwd(const lsq_cfg* cfg, const void* blob, const float* 
  *   ws         stream_stack_packed_workspace_bytes(cfg, n_tokens, n_docs), 32-byte
  *              aligned.
  * Streaming, graphs, data parallelism, the synchronous return and the other arguments
- * are those of stream_stack_step; a latched status bit (a length outside its range
+ * are those of stream_stack_step (averaged gradients are the mean over the ranks of each
+ * rank's mean, whatever its number of targets); a latched status bit (a length outside its range
  * among them) is returned as LSQ_ERR_DEVICE.  Added in ABI 2.2. */
 size_t stream_stack_packed_workspace_bytes(const lsq_cfg* cfg, int32_t n_tokens, int32_t n_docs);
 int stream_stack_packed_step(lsq_stack* stack, const int32_t* tokens, int32_t micro_batches,

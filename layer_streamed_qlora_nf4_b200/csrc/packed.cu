@@ -14,26 +14,24 @@ namespace {
 
 constexpr int kIdxThreads = 1024;
 
-// Inclusive sum over the CTA's 1024 threads (in thread order); sh holds 32 values.
-__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* sh) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// Inclusive sums over a warp, and over the CTA's 1024 threads (in thread order; sh holds
+// 32 values).
+__device__ __forceinline__ int64_t warp_scan(int64_t v) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int64_t u = __shfl_up_sync(0xFFFFFFFFu, v, o);
     if (lane >= o) v += u;
   }
+  return v;
+}
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* sh) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  v = warp_scan(v);
   __syncthreads();  // sh is free
   if (lane == 31) sh[warp] = v;
   __syncthreads();
-  if (warp == 0) {
-    int64_t w = sh[lane];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t u = __shfl_up_sync(0xFFFFFFFFu, w, o);
-      if (lane >= o) w += u;
-    }
-    sh[lane] = w;
-  }
+  if (warp == 0) sh[lane] = warp_scan(sh[lane]);
   __syncthreads();
   return v + (warp > 0 ? sh[warp - 1] : 0);
 }
@@ -70,17 +68,18 @@ __device__ __forceinline__ int ties_before(int kind, int i, int pt) {
   return flat ? i : 0;
 }
 
-// Every CTA scans all lengths, 1024 documents at a time (a few microseconds for the
-// thousands of documents a row holds), and writes its own share of the tokens and
+// Every CTA scans all lengths, 1024 documents at a time (up to 32 of them in one warp,
+// without the barriers of a scan over the block), and writes its own share of the tokens and
 // tiles, each found by a binary search over the 1024 starts in shared memory: a
 // single long document costs no more than many short ones.
 __global__ void __launch_bounds__(kIdxThreads)
     packed_index_kernel(const int32_t* __restrict__ lengths, const int32_t* __restrict__ prefix,
                         int n_docs, int T, PackedIndex x, int* dev_err) {
   __shared__ int64_t sh[32];
+  __shared__ int64_t sums[2];
   __shared__ int tok0[kIdxThreads], t1[kIdxThreads], t2[kIdxThreads], doc_e[kIdxThreads],
       doc_p[kIdxThreads];
-  const bool sorted = n_docs <= kIdxThreads;
+  const bool sorted = n_docs <= kIdxThreads, few = n_docs <= 32;
   pdl_trigger();
   pdl_wait();
   const int tid = threadIdx.x;
@@ -89,26 +88,42 @@ __global__ void __launch_bounds__(kIdxThreads)
   int base1 = 0, base2 = 0;
   bool bad = false;
   for (int d0 = 0; d0 < n_docs; d0 += kIdxThreads) {
-    const int d = d0 + tid;
-    int len = d < n_docs ? lengths[d] : 0;
-    int pre = d < n_docs && prefix ? prefix[d] : 0;
-    if (len < 0 || pre < 0 || pre > len) bad = true;  // such a length counts as 0
-    len = max(len, 0);
-    const int64_t end = base + block_scan(len, sh);
-    const int64_t total = base + sh[31];
-    if (end > T) bad = true;  // documents are cut where the row ends
-    const int s = (int)min((int64_t)T, end - len), e = (int)min((int64_t)T, end);
-    pre = min(max(pre, 0), e - s);
-    const int n1 = (e - s + kPackedTile - 1) / kPackedTile;
-    const int n2 = (e - s + 2 * kPackedTile - 1) / (2 * kPackedTile);
-    const int64_t i12 = block_scan(((int64_t)n1 << 32) | (int64_t)n2, sh);
-    const int64_t all12 = sh[31];
-    tok0[tid] = s;
-    doc_e[tid] = e;
-    doc_p[tid] = s + pre;
-    t1[tid] = base1 + (int)(i12 >> 32) - n1;
-    t2[tid] = base2 + (int)(i12 & 0xFFFFFFFF) - n2;
+    if (!few || tid < 32) {
+      auto scan = [&](int64_t v, int64_t* total) {
+        if (few) {
+          v = warp_scan(v);
+          *total = __shfl_sync(0xFFFFFFFFu, v, 31);
+        } else {
+          v = block_scan(v, sh);
+          *total = sh[31];
+        }
+        return v;
+      };
+      const int d = d0 + tid;
+      int len = d < n_docs ? lengths[d] : 0;
+      int pre = d < n_docs && prefix ? prefix[d] : 0;
+      if (len < 0 || pre < 0 || pre > len) bad = true;  // such a length counts as 0
+      len = max(len, 0);
+      int64_t all, all12;
+      const int64_t end = base + scan(len, &all);
+      if (end > T) bad = true;  // documents are cut where the row ends
+      const int s = (int)min((int64_t)T, end - len), e = (int)min((int64_t)T, end);
+      pre = min(max(pre, 0), e - s);
+      const int n1 = (e - s + kPackedTile - 1) / kPackedTile;
+      const int n2 = (e - s + 2 * kPackedTile - 1) / (2 * kPackedTile);
+      const int64_t i12 = scan(((int64_t)n1 << 32) | (int64_t)n2, &all12);
+      tok0[tid] = s;
+      doc_e[tid] = e;
+      doc_p[tid] = s + pre;
+      t1[tid] = base1 + (int)(i12 >> 32) - n1;
+      t2[tid] = base2 + (int)(i12 & 0xFFFFFFFF) - n2;
+      if (tid == 0) {
+        sums[0] = all;
+        sums[1] = all12;
+      }
+    }
     __syncthreads();
+    const int64_t total = base + sums[0], all12 = sums[1];
     const int nd = min(n_docs - d0, kIdxThreads);
     // documents of no tokens share their start with the next one: the last at or
     // before a token is the one that holds it
@@ -121,33 +136,36 @@ __global__ void __launch_bounds__(kIdxThreads)
       x.doc_end[t] = doc_e[k];
     }
     // a tile's place: by its work, or (with more documents than one chunk) in order
-    auto emit = [&](int kind, const int* first, int n, int before, int size, PackedTile* list,
+    auto emit = [&](int kind, int i, const int* first, int before, int size, PackedTile* list,
                     int cap) {
-      for (int i = gtid >> 5; i < n; i += gsize >> 5) {
-        const int k = find_last(first, nd, before + i);
-        const int at = before + i - first[k];  // tile of its document
-        int place = before + i;
-        if (sorted) {
-          const int lane = tid & 31;
-          auto tiles_of = [&](int len) { return (len + size - 1) / size; };
-          const int pt = (doc_p[k] - tok0[k] + kPackedTile - 1) / kPackedTile;
-          const int w = work_of(kind, at, tiles_of(doc_e[k] - tok0[k]), pt);
-          place = 0;
-          for (int d = lane; d < n_docs; d += 32) {
-            const int nt = tiles_of(doc_e[d] - tok0[d]);
-            const int dpt = (doc_p[d] - tok0[d] + kPackedTile - 1) / kPackedTile;
-            const int above = count_above(kind, nt, dpt, w);
-            place += d < k ? count_above(kind, nt, dpt, w - 1) : above;
-          }
-          place = __reduce_add_sync(0xFFFFFFFFu, place) + ties_before(kind, at, pt);
+      const int k = find_last(first, nd, before + i);
+      const int at = before + i - first[k];  // tile of its document
+      int place = before + i;
+      if (sorted) {
+        const int lane = tid & 31;
+        auto tiles_of = [&](int len) { return (len + size - 1) / size; };
+        const int pt = (doc_p[k] - tok0[k] + kPackedTile - 1) / kPackedTile;
+        const int w = work_of(kind, at, tiles_of(doc_e[k] - tok0[k]), pt);
+        place = 0;
+        for (int d = lane; d < n_docs; d += 32) {
+          const int nt = tiles_of(doc_e[d] - tok0[d]);
+          const int dpt = (doc_p[d] - tok0[d] + kPackedTile - 1) / kPackedTile;
+          const int above = count_above(kind, nt, dpt, w);
+          place += d < k ? count_above(kind, nt, dpt, w - 1) : above;
         }
-        if ((tid & 31) == 0 && place < cap)
-          list[place] = {tok0[k] + at * size, tok0[k], doc_e[k], doc_p[k]};
+        place = __reduce_add_sync(0xFFFFFFFFu, place) + ties_before(kind, at, pt);
       }
+      if ((tid & 31) == 0 && place < cap)
+        list[place] = {tok0[k] + at * size, tok0[k], doc_e[k], doc_p[k]};
     };
-    emit(LIST_Q, t1, c1, base1, kPackedTile, x.tiles, x.cap);
-    emit(LIST_K, t1, c1, base1, kPackedTile, x.ktiles, x.cap);
-    emit(LIST_Q2, t2, c2, base2, 2 * kPackedTile, x.tiles2, x.cap2);
+    for (int i = gtid >> 5; i < 2 * c1 + c2; i += gsize >> 5) {  // (a warp takes a tile)
+      if (i < c1)
+        emit(LIST_Q, i, t1, base1, kPackedTile, x.tiles, x.cap);
+      else if (i < 2 * c1)
+        emit(LIST_K, i - c1, t1, base1, kPackedTile, x.ktiles, x.cap);
+      else
+        emit(LIST_Q2, i - 2 * c1, t2, base2, 2 * kPackedTile, x.tiles2, x.cap2);
+    }
     base = hi;
     base1 += c1;
     base2 += c2;
@@ -495,9 +513,13 @@ int launch_packed_index(const int32_t* lengths, const int32_t* prefix, int n_doc
                         int32_t* index, cudaStream_t st) {
   int* err = device_status_ptr();
   if (!err) return set_error(LSQ_ERR_CUDA, "device status word unavailable");
-  const unsigned grid = (unsigned)std::min<int64_t>(64, (T + kIdxThreads - 1) / kIdxThreads);
+  // a thread per token and a warp per tile, as far as 64 CTAs go: a row of many short
+  // documents has as many tiles, and each looks at all documents
+  const PackedIndex x = packed_index_view(index, T, n_docs);
+  const int64_t work = std::max<int64_t>(T, 32 * (2 * (int64_t)x.cap + x.cap2));
+  const unsigned grid = (unsigned)std::min<int64_t>(64, (work + kIdxThreads - 1) / kIdxThreads);
   LSQ_CUDA(launch_dep(packed_index_kernel, grid, kIdxThreads, st, lengths, prefix, n_docs, (int)T,
-                      packed_index_view(index, T, n_docs), err));
+                      x, err));
   return LSQ_OK;
 }
 

@@ -227,7 +227,6 @@ __global__ void __launch_bounds__(kFThreads, 1)
   __shared__ uint32_t tmem_sh;
   __shared__ int abort_sh;
   volatile int* abort_flag = &abort_sh;
-  pdl_trigger();  // the next kernel may launch once all CTAs of this one run
 
   uint8_t* Qs = align1024_p(attn_raw);   // [2] Q tiles
   uint8_t* KV = Qs + 2 * SM::kTile;      // ring: K and V tiles in turn
@@ -266,7 +265,8 @@ __global__ void __launch_bounds__(kFThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_sh;
-  pdl_wait();  // the index and q, k, v come from the kernels before
+  pdl_trigger();  // the next kernel may launch once all CTAs of this one run and have their TMEM
+  pdl_wait();     // the index and q, k, v come from the kernels before
   const int items = heads ? idx.head[0] * (H / 2) : idx.head[1] * H;
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
     return mbar_wait_short(smem_u32(bar), parity & 1u, abort_flag, dev_err);
@@ -765,7 +765,8 @@ __global__ void __launch_bounds__(kBThreads, 1)
                             int* __restrict__ dev_err) {
   using SM = DkvSmem<D>;
   constexpr int DA = D / 64, NR = SM::kRing, kItems = 8;
-  static_assert(NR % 2 == 0 && kItems > NR, "a ring slot always serves the same set of warps");
+  static_assert(NR % 2 == 0, "a ring slot always serves the same set of warps");
+  static_assert(kItems > NR + 1, "an item's least exponent is kept until all have read it");
   extern __shared__ uint8_t dkv_raw[];
   __shared__ __align__(8) uint64_t kv_full, kv_free, r_full[NR], r_free[NR], st_full[NR];
   __shared__ __align__(8) uint64_t s_full[2], dp_full[2], p_full[2], ds_full[2], s_free[2], dp_free[2];
@@ -1111,10 +1112,10 @@ __global__ void __launch_bounds__(kBThreads, 1)
       tc_fence_after();
       uint32_t lo[D / 4], hi[D / 4];
       load_share<D>(trow + (b ? kColK : kColV) + hf * (D / 4), lo, hi);
+      const float f = ex2(-emin_sh[ni % kItems]) * (b ? scale : 1.f);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&acc_free));
-      const float f = ex2(-emin_sh[ni % kItems]) * (b ? scale : 1.f);
       ++ni;
       if (kpos < it.t.end) {
         if (parts == 1) {
@@ -1178,7 +1179,6 @@ __global__ void __launch_bounds__(kBThreads, 1)
   __shared__ uint32_t tmem_sh;
   __shared__ int abort_sh;
   volatile int* abort_flag = &abort_sh;
-  pdl_trigger();
 
   uint8_t* Qs = align1024_p(dq_raw);        // [2] Q of the streams
   uint8_t* dOs = Qs + 2 * SM::kTile;        // [2] dO'
@@ -1215,6 +1215,7 @@ __global__ void __launch_bounds__(kBThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_sh;
+  pdl_trigger();
   // no wait here: the kernel before is dK, dV, which writes nothing that this one reads and
   // which let it start only when the kernels before itself had completed
   const int G = H / Hkv;
@@ -1624,14 +1625,16 @@ int bwd_t(const uint16_t* qkv, const PackedIndex& x, const uint16_t* o, const fl
   return LSQ_OK;
 }
 
+constexpr int kMaxHeads = 32767;  // (H + Hkv is a grid dimension)
 bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
 
 int check_heads(int64_t T, int32_t H, int32_t Hkv, int32_t d, const char* who) {
-  if (H <= 0 || Hkv <= 0 || H % Hkv != 0 || H > 65535)
-    return set_error(LSQ_ERR_SHAPE, "%s: H must be a multiple of Hkv, at most 65535", who);
+  if (H <= 0 || Hkv <= 0 || H % Hkv != 0 || H > kMaxHeads)
+    return set_error(LSQ_ERR_SHAPE, "%s: H must be a multiple of Hkv, at most %d", who, kMaxHeads);
   if (d != 64 && d != 128) return set_error(LSQ_ERR_SHAPE, "%s: d must be 64 or 128", who);
-  if (T * (H + 2 * (int64_t)Hkv) > (int64_t(1) << 33))
-    return set_error(LSQ_ERR_SHAPE, "%s: too many tokens and heads", who);
+  // (items are counted in 32 bits; such a qkv would take 256 GiB)
+  if (T * (H + 2 * (int64_t)Hkv) >= (int64_t(1) << 31))
+    return set_error(LSQ_ERR_SHAPE, "%s: T (H + 2 Hkv) must be below 2^31", who);
   return LSQ_OK;
 }
 
@@ -1689,8 +1692,7 @@ extern "C" int packed_attention_fwd(const uint16_t* qkv, const int32_t* index, i
 }
 
 extern "C" size_t packed_attention_workspace_bytes(int64_t T, int32_t H, int32_t Hkv, int32_t d) {
-  if (T <= 0 || T > (int64_t(1) << 30) || H <= 0 || Hkv <= 0 || H % Hkv != 0 ||
-      (d != 64 && d != 128))
+  if (T <= 0 || T > (int64_t(1) << 30) || check_heads(T, H, Hkv, d, "packed_attention") != LSQ_OK)
     return 0;
   return packed_attention_ws_bytes(T, H, Hkv, d);
 }

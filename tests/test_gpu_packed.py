@@ -176,6 +176,30 @@ def test_index_of_many_documents(L):
     assert words[0] == (lengths > 0).sum()
 
 
+@pytest.mark.parametrize("n_docs", [32, 33, 1000, 1024, 1025])
+def test_index_around_a_warp_and_a_block_of_documents(L, n_docs):
+    """Short documents in a short row: the tiles outnumber a block's warps."""
+    rng = np.random.default_rng(n_docs)
+    lengths = np.where(rng.random(n_docs) < 0.9, 1, rng.integers(0, 300, n_docs))
+    T = int(lengths.sum()) + 2
+    words = _index(L, lengths.tolist(), None, T).buf.cpu().numpy()
+    docs = op.documents(lengths.tolist(), None)
+    cap, cap2 = min(T, T // 128 + n_docs), min(T, T // 256 + n_docs)
+    for n, size, base in ((words[0], 128, 8), (words[0], 128, 8 + 4 * cap),
+                          (words[1], 256, 8 + 8 * cap)):
+        want = [(r, s, e, pe) for s, e, pe in docs for r in range(s, e, size)]
+        got = words[base:base + 4 * n].reshape(n, 4)
+        assert sorted(map(tuple, got)) == sorted(want)
+        if n_docs <= 1024 and base == 8:
+            seen = np.minimum(got[:, 2], got[:, 0] + 128) - got[:, 1]
+            assert (np.diff((seen + 127) // 128) <= 0).all()
+    pos, _, doc_end = words[-3 * T:].reshape(3, T)
+    ends = np.cumsum(lengths)
+    own = np.repeat(np.arange(n_docs), lengths)
+    assert np.array_equal(pos[:T - 2], np.arange(T - 2) - (ends - lengths)[own])
+    assert np.array_equal(doc_end[:T - 2], ends[own]) and (doc_end[T - 2:] == T - 2).all()
+
+
 def test_index_bad_lengths_are_cut_and_latched(L):
     bad = L.LSQ_DEV_ERR_INDEX
     for lengths, prefix, T, total in (([5, -3, 4], None, 12, 9), ([5, 9], None, 10, 10),

@@ -57,6 +57,13 @@ def test_packed_entries(L):
     assert need > 0
     for bad_shape in ((0, 4, 2, 64), (4, 3, 2, 64), (4, 4, 2, 32), (4, 0, 2, 64), (4, 4, 0, 64)):
         assert L.packed_attention_workspace_bytes(*bad_shape) == 0
+    # sizes that the kernels' grids and counts have no room for
+    for T, H, Hkv in ((1, 32768, 32768), (1 << 25, 32, 16)):
+        assert L.packed_attention_workspace_bytes(T, H, Hkv, 64) == 0
+        assert _rc(L, "packed_attention_fwd", P, P, 1, T, H, Hkv, 64, P, P, None) == shape
+        assert _rc(L, "packed_attention_bwd", P, P, 1, P, P, P, T, H, Hkv, 64, P, P, 1 << 40,
+                   None) == shape
+    assert L.packed_attention_workspace_bytes((1 << 25) - 1, 32, 16, 64) > 0
     ok = [P, P, 1, P, P, P, 4, 4, 2, 64, P, P, need, None]
     for at, val, rc in ((0, None, inval), (3, None, inval), (4, None, inval), (5, None, inval),
                         (10, None, inval), (11, None, work), (12, need - 1, work),
