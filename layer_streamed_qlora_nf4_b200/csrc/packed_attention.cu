@@ -743,7 +743,7 @@ __device__ __forceinline__ void load_share(uint32_t t, uint32_t (&lo)[D / 4], ui
 // emin is the least exponent of the item's queries: P' = 2^(emin - e) P <= 1, so all
 // products carry the same factor 2^emin, taken out at the end.  With all heads of the
 // group in one item (nh = G) the sums are the gradients, written in bf16; otherwise
-// fp32 parts are left for the kernel below.
+// fp32 parts are left for the kernel below to sum.
 template <int D>
 struct DkvSmem {
   static constexpr uint32_t kTile = 128 * D * 2;  // K or V
@@ -1149,6 +1149,51 @@ __global__ void __launch_bounds__(kBThreads, 1)
   }
 }
 
+// dk and dv (bf16, into dqkv) from the fp32 parts of `parts` shares of each kv head's
+// query heads, summed in order; with cs the rotation of k by its position undone.  The
+// whole grid shares the rows, a thread takes 4 pairs (i, i + D/2).
+struct GradParts {
+  const float *dk, *dv;
+  int parts;  // 1: nothing to sum
+};
+template <int D>
+__device__ __forceinline__ void sum_parts(const GradParts& gp, int64_t tokens, const int* pos,
+                                          int Hkv, int64_t ld, int col0, const float2* cs,
+                                          uint16_t* __restrict__ dqkv) {
+  constexpr int half = D / 2, chunks = half / 4;
+  const int64_t n = tokens * 2 * Hkv * chunks;
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n;
+       i += (int64_t)gridDim.x * blockDim.x) {
+    const int ch = (int)(i % chunks);
+    const int64_t th = i / chunks;
+    const int hh = (int)(th % (2 * Hkv));
+    const int64_t t = th / (2 * Hkv);
+    const float* src = (hh < Hkv ? gp.dk : gp.dv) + ((t * Hkv + hh % Hkv) * gp.parts) * D + ch * 4;
+    float a[4] = {0.f, 0.f, 0.f, 0.f}, b[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int k = 0; k < gp.parts; ++k) {
+      const float4 x = __ldcg(reinterpret_cast<const float4*>(src + (int64_t)k * D));
+      const float4 y = __ldcg(reinterpret_cast<const float4*>(src + (int64_t)k * D + half));
+      a[0] += x.x; a[1] += x.y; a[2] += x.z; a[3] += x.w;
+      b[0] += y.x; b[1] += y.y; b[2] += y.z; b[3] += y.w;
+    }
+    if (cs && hh < Hkv) {
+      const float2* c = cs + (int64_t)pos[t] * half + ch * 4;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 f = c[k];
+        const float x = a[k], y = b[k];
+        a[k] = x * f.x + y * f.y;
+        b[k] = y * f.x - x * f.y;
+      }
+    }
+    uint16_t* out = dqkv + t * ld + col0 + hh * D + ch * 4;
+    *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]));
+    *reinterpret_cast<uint2*>(out + half) =
+        make_uint2(pack_bf16x2(b[0], b[1]), pack_bf16x2(b[2], b[3]));
+  }
+}
+
 // ------------------------------------------------------------------ dQ
 // Items and streams as in the forward; a stream's chunk of 64 keys:
 //   its MMA warp: S = Q K^T, dP' = dO' V^T;  its gradient warps: P = exp2(S c - lse log2 e),
@@ -1170,7 +1215,7 @@ __global__ void __launch_bounds__(kBThreads, 1)
                           PackedIndex idx, const float2* __restrict__ stats,
                           const float* __restrict__ rowexp, int64_t T, int H, int Hkv, float sl2,
                           float scale, const float2* __restrict__ cs, uint16_t* __restrict__ dqkv,
-                          int* __restrict__ dev_err) {
+                          GradParts gp, int* __restrict__ dev_err) {
   using SM = DqSmem<D>;
   constexpr int DA = D / 64, NR = SM::kRing;
   extern __shared__ uint8_t dq_raw[];
@@ -1442,57 +1487,15 @@ __global__ void __launch_bounds__(kBThreads, 1)
          i += (int64_t)gridDim.x * blockDim.x)
       o[i] = make_uint4(0u, 0u, 0u, 0u);
   }
-  pdl_wait();  // this kernel is not done before dK, dV is
+  pdl_wait();  // this kernel is not done before dK, dV is, whose shares it sums
+  if (gp.parts > 1)
+    sum_parts<D>(gp, idx.head[2], idx.pos, Hkv, (int64_t)(H + 2 * Hkv) * D, H * D, cs, dqkv);
   tc_fence_before();
   __syncthreads();
   if (abort_sh) settle_ns(2000000);
   if (warp == kBMma) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
-  }
-}
-
-// dk and dv (bf16, into dqkv) from the fp32 parts of `parts` shares of each kv head's
-// query heads, summed in order; with cs the rotation of k by its position undone.  A
-// thread takes 4 pairs (i, i + d/2).
-__global__ void __launch_bounds__(256)
-    packed_grad_kernel(const float* __restrict__ dk, const float* __restrict__ dv,
-                       const int* __restrict__ head, const int* __restrict__ pos, int H, int Hkv,
-                       int parts, int d, const float2* __restrict__ cs,
-                       uint16_t* __restrict__ dqkv) {
-  pdl_trigger();
-  pdl_wait();
-  const int half = d / 2, chunks = half / 4;
-  const int64_t ld = (int64_t)(H + 2 * Hkv) * d;
-  const int64_t n = (int64_t)head[2] * 2 * Hkv * chunks;
-  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n;
-       i += (int64_t)gridDim.x * blockDim.x) {
-    const int ch = (int)(i % chunks);
-    const int64_t th = i / chunks;
-    const int hh = (int)(th % (2 * Hkv));
-    const int64_t t = th / (2 * Hkv);
-    const float* src = (hh < Hkv ? dk : dv) + ((t * Hkv + hh % Hkv) * parts) * d + ch * 4;
-    float a[4] = {0.f, 0.f, 0.f, 0.f}, b[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int k = 0; k < parts; ++k) {
-      const float4 x = *reinterpret_cast<const float4*>(src + (int64_t)k * d);
-      const float4 y = *reinterpret_cast<const float4*>(src + (int64_t)k * d + half);
-      a[0] += x.x; a[1] += x.y; a[2] += x.z; a[3] += x.w;
-      b[0] += y.x; b[1] += y.y; b[2] += y.z; b[3] += y.w;
-    }
-    if (cs && hh < Hkv) {
-      const float2* c = cs + (int64_t)pos[t] * half + ch * 4;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float2 f = c[k];
-        const float x = a[k], y = b[k];
-        a[k] = x * f.x + y * f.y;
-        b[k] = y * f.x - x * f.y;
-      }
-    }
-    uint16_t* out = dqkv + t * ld + (int64_t)(H + hh) * d + ch * 4;
-    *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]));
-    *reinterpret_cast<uint2*>(out + half) =
-        make_uint2(pack_bf16x2(b[0], b[1]), pack_bf16x2(b[2], b[3]));
   }
 }
 
@@ -1554,14 +1557,17 @@ struct BwdWs {
 
 // Into how many shares a kv head's query heads are split for dK and dV.  One share
 // needs no partial sums (8 bytes written and read per token, share and dimension) but
-// leaves few items: one per SM is wanted (what is left uneven dQ fills).  One, two and
-// four per SM took 512, 515 and 541 us forward and backward of 16,384 packed tokens with
-// 16/2 heads, 156, 176 and 176 us backward of 2048 tokens with 32/8.
-int dkv_parts(int64_t T, int H, int Hkv) {
+// leaves few items, and those of one long document are uneven; what a document's last tile
+// lacks of 128 tokens is half a tile on average.  Wanted are nine items for ten SMs (dQ
+// takes the SMs that are left).  Backward in us with one, two and four shares:
+// (32/8 heads, d 128) 512 tokens in 5 documents 32, 29, 30; 1024 in 3: 59, 49, 55; 2048 in
+// one 191, 148, 162, in 4: 77, 88, 99; (16/2) 4096 in 10: 108, 84, 88; 6144 in 15: 133,
+// 118, 121; (8/2, d 64) 1024 in 1000: 179, 197, 264.
+int dkv_parts(int64_t T, int64_t n_docs, int H, int Hkv) {
   const int G = H / Hkv;
-  const int64_t tiles = (T + kPackedTile - 1) / kPackedTile;
+  const int64_t tiles = std::min(T, (T + kPackedTile - 1) / kPackedTile + n_docs / 2);
   for (int p = 1; p < G; ++p)
-    if (G % p == 0 && tiles * Hkv * p >= (int64_t)gemm_num_sms()) return p;
+    if (G % p == 0 && tiles * Hkv * p * 10 >= (int64_t)gemm_num_sms() * 9) return p;
   return G;
 }
 
@@ -1570,7 +1576,7 @@ size_t carve_bwd(int64_t T, int H, int Hkv, int d, void* base, BwdWs* w) {
   a.base = static_cast<uint8_t*>(base);
   a.cap = SIZE_MAX;
   BwdWs x;
-  const int parts = dkv_parts(T, H, Hkv);
+  const int parts = dkv_parts(T, 0, H, Hkv);  // (the most that any number of documents takes)
   x.dos = a.take<uint16_t>((size_t)T * H * d);
   x.stats = a.take<float2>((size_t)T * H);
   x.rowexp = a.take<float>((size_t)T * H);
@@ -1585,7 +1591,7 @@ size_t carve_bwd(int64_t T, int H, int Hkv, int d, void* base, BwdWs* w) {
 template <int D>
 int bwd_t(const uint16_t* qkv, const PackedIndex& x, const uint16_t* o, const float* lse,
           const uint16_t* dout, int64_t T, int H, int Hkv, const float2* cs, uint16_t* dqkv,
-          const BwdWs& w, cudaStream_t st) {
+          int parts, const BwdWs& w, cudaStream_t st) {
   static bool attr_kv[64] = {false}, attr_q[64] = {false};
   LSQ_TRY(allow_smem(packed_attn_dkdv_kernel<D>, (int)DkvSmem<D>::kBytes, attr_kv));
   LSQ_TRY(allow_smem(packed_attn_dq_kernel<D>, (int)DqSmem<D>::kBytes, attr_q));
@@ -1607,7 +1613,7 @@ int bwd_t(const uint16_t* qkv, const PackedIndex& x, const uint16_t* o, const fl
                        (uint64_t)hd, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B));
   LSQ_TRY(make_tmap_2d(&do64, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, w.dos, (uint64_t)hd, (uint64_t)T,
                        (uint64_t)hd, 64, kBC, CU_TENSOR_MAP_SWIZZLE_128B));
-  const int parts = dkv_parts(T, H, Hkv), sms = gemm_num_sms();
+  const int sms = gemm_num_sms();
   const int64_t kitems = (int64_t)x.cap * Hkv * parts;
   LSQ_CUDA(launch_dep(packed_attn_dkdv_kernel<D>, dim3((unsigned)std::min<int64_t>(kitems, sms)),
                       kBThreads, DkvSmem<D>::kBytes, st, qkv128, qkv64, do64, x, w.stats, w.rowexp,
@@ -1615,13 +1621,7 @@ int bwd_t(const uint16_t* qkv, const PackedIndex& x, const uint16_t* o, const fl
   const int64_t qitems = (H / Hkv) % 2 == 0 ? (int64_t)x.cap * (H / 2) : (int64_t)x.cap2 * H;
   LSQ_CUDA(launch_dep(packed_attn_dq_kernel<D>, dim3((unsigned)std::min<int64_t>(qitems, sms)),
                       kBThreads, DqSmem<D>::kBytes, st, qkv128, qkv64, do128, x, w.stats, w.rowexp,
-                      T, H, Hkv, sl2, scale, cs, dqkv, err));
-  if (parts > 1) {
-    const int64_t n = T * 2 * Hkv * (D / 8);
-    LSQ_CUDA(launch_dep(packed_grad_kernel,
-                        dim3((unsigned)std::min<int64_t>((n + 255) / 256, sms * 16)), 256, 0, st,
-                        w.dk, w.dv, x.head, x.pos, H, Hkv, parts, D, cs, dqkv));
-  }
+                      T, H, Hkv, sl2, scale, cs, dqkv, GradParts{w.dk, w.dv, parts}, err));
   return LSQ_OK;
 }
 
@@ -1665,9 +1665,10 @@ int launch_packed_attention_bwd(const uint16_t* qkv, const int32_t* index, int n
   BwdWs w;
   if (carve_bwd(T, H, Hkv, d, ws, &w) > ws_bytes)
     return set_error(LSQ_ERR_WORKSPACE, "packed attention: workspace too small");
+  const int parts = dkv_parts(T, n_docs, H, Hkv);
   const int prof = prof_begin(st);
-  LSQ_TRY(d == 128 ? bwd_t<128>(qkv, x, o, lse, dout, T, H, Hkv, cs, dqkv, w, st)
-                   : bwd_t<64>(qkv, x, o, lse, dout, T, H, Hkv, cs, dqkv, w, st));
+  LSQ_TRY(d == 128 ? bwd_t<128>(qkv, x, o, lse, dout, T, H, Hkv, cs, dqkv, parts, w, st)
+                   : bwd_t<64>(qkv, x, o, lse, dout, T, H, Hkv, cs, dqkv, parts, w, st));
   if (prof >= 0)
     prof_end(prof, st, "packed_attention_bwd", 0.0,
              2.0 * T * (double)(4 * H + 4 * Hkv) * d + 4.0 * T * H);
