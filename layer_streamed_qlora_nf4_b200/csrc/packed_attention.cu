@@ -579,6 +579,13 @@ constexpr int kBH = kBC / 2;   // columns of a thread
 constexpr int kBThreads = 640;
 constexpr int kBTma = 16, kBMma = 17, kBTail = 19;
 constexpr int kWindow = 64;    // tokens of a window of the exponents' minima
+// Items are handed out as CTAs come for them, heaviest first: the TMA producer draws the
+// next one from a counter (zeroed by the kernel that prepares dO') and passes it to the
+// other 19 warps through a ring in shared memory.  What an item computes does not depend
+// on who takes it.  (Dealt out beforehand, the dQ CTAs that start last, behind the longest
+// dK, dV items, kept as large a share as the others.)
+constexpr int kTake = 4;
+constexpr int kTakers = 19;
 // |dS'| <= 2 |dO'| |v| with |dO'| < 2 sqrt(128): below fp16's 65504 for these norms of v
 constexpr float kMaxNormV = 1447.f;
 
@@ -600,7 +607,8 @@ __global__ void __launch_bounds__(256)
                             const uint16_t* __restrict__ dout, const float* __restrict__ lse,
                             const int* __restrict__ head, int64_t T, int H, int Hkv,
                             uint16_t* __restrict__ dos, float2* __restrict__ stats,
-                            float* __restrict__ rowexp, float* __restrict__ winexp, int* dev_err) {
+                            float* __restrict__ rowexp, float* __restrict__ winexp,
+                            int* __restrict__ taken, int* dev_err) {
   constexpr int LR = D / 8, RW = 32 / LR, IT = kWindow / 8 / RW;  // lanes a row, rows a warp, rounds
   __shared__ float low[8];
   pdl_trigger();
@@ -608,6 +616,7 @@ __global__ void __launch_bounds__(256)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int h = blockIdx.y, col = (lane % LR) * 8;
   const int64_t live = head[2];
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 2) taken[threadIdx.x] = 0;
   const int64_t t0 = (int64_t)blockIdx.x * kWindow + warp * (kWindow / 8) + lane / LR;
   if (h >= H) {
     bool big = false;
@@ -761,7 +770,7 @@ __global__ void __launch_bounds__(kBThreads, 1)
                             const float* __restrict__ rowexp, const float* __restrict__ winexp,
                             int64_t T, int H, int Hkv, int nh, float sl2, float scale,
                             const float2* __restrict__ cs, uint16_t* __restrict__ dqkv,
-                            float* __restrict__ dk, float* __restrict__ dv,
+                            float* __restrict__ dk, float* __restrict__ dv, int* taken,
                             int* __restrict__ dev_err) {
   using SM = DkvSmem<D>;
   constexpr int DA = D / 64, NR = SM::kRing, kItems = 8;
@@ -770,7 +779,8 @@ __global__ void __launch_bounds__(kBThreads, 1)
   extern __shared__ uint8_t dkv_raw[];
   __shared__ __align__(8) uint64_t kv_full, kv_free, r_full[NR], r_free[NR], st_full[NR];
   __shared__ __align__(8) uint64_t s_full[2], dp_full[2], p_full[2], ds_full[2], s_free[2], dp_free[2];
-  __shared__ __align__(8) uint64_t acc_full, acc_free;
+  __shared__ __align__(8) uint64_t acc_full, acc_free, item_full[kTake], item_free[kTake];
+  __shared__ int item_sh[kTake];
   __shared__ float emin_sh[kItems];
   __shared__ uint32_t tmem_sh;
   __shared__ int abort_sh;
@@ -802,6 +812,10 @@ __global__ void __launch_bounds__(kBThreads, 1)
     }
     mbar_init(smem_u32(&acc_full), 1);
     mbar_init(smem_u32(&acc_free), 16);
+    for (int i = 0; i < kTake; ++i) {
+      mbar_init(smem_u32(&item_full[i]), 1);
+      mbar_init(smem_u32(&item_free[i]), kTakers);
+    }
     abort_sh = 0;
     fence_mbar_init();
     fence_proxy_async_smem();
@@ -825,6 +839,28 @@ __global__ void __launch_bounds__(kBThreads, 1)
   auto wait_all = [&](uint64_t* bar, uint32_t parity) -> bool {
     return __all_sync(0xFFFFFFFFu, wait(bar, parity));
   };
+  const bool many = items > (int)gridDim.x;  // (else the CTAs have one each)
+  // item k of this CTA (-1: none is left), given and taken; those below `fixed` are known
+  const int fixed = 1;
+  auto give = [&](int k, int w) -> bool {
+    if (many && k >= fixed) {
+      const uint32_t n = (uint32_t)(k - fixed), slot = n % kTake;
+      if (n >= kTake && !wait(&item_free[slot], n / kTake - 1)) return false;
+      item_sh[slot] = w < items ? w : -1;
+      mbar_arrive(smem_u32(&item_full[slot]));
+    }
+    return w < items;
+  };
+  auto take = [&](int k) -> int {
+    if (k < fixed) return (int)blockIdx.x < items ? (int)blockIdx.x : -1;
+    if (!many) return -1;
+    const uint32_t n = (uint32_t)(k - fixed), slot = n % kTake;
+    if (!wait_all(&item_full[slot], n / kTake)) return -1;
+    const int w = item_sh[slot];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&item_free[slot]));
+    return w;
+  };
   // an item's tile, first query head, first query and chunks of a head
   struct Item {
     PackedTile t;
@@ -846,7 +882,7 @@ __global__ void __launch_bounds__(kBThreads, 1)
     if (lane == 0) {
       uint32_t c = 0, ni = 0;
       bool ok = true;
-      for (int k = 0, w; ok && (w = deal(k, items)) >= 0; ++k) {
+      for (int k = 0, w = blockIdx.x; ok && give(k, w); ++k) {
         const Item it = item(w);
         if (ni > 0) ok = wait(&kv_free, ni - 1);
         if (!ok) break;
@@ -872,6 +908,10 @@ __global__ void __launch_bounds__(kBThreads, 1)
                           (it.h0 + hh) * D + 64 * a, it.qs + j * kBC);
             }
           }
+        // (drawn when three chunks are left: any sooner, and a CTA with a long item takes
+        // another one from those that will be done before it)
+        if (ok && c >= 3) ok = wait(&r_free[(c - 3) % NR], (c - 3) / NR);
+        w = many ? (int)gridDim.x + atomicAdd(taken, 1) : items;
       }
     }
     __syncwarp();
@@ -882,7 +922,7 @@ __global__ void __launch_bounds__(kBThreads, 1)
     const uint64_t kd = umma_desc_k_sw128(smem_u32(Ks)), vd = umma_desc_k_sw128(smem_u32(Vs));
     uint32_t c = 0, ni = 0;
     bool ok = true;
-    for (int k = 0, w; ok && (w = deal(k, items)) >= 0; ++k) {
+    for (int k = 0, w; ok && (w = take(k)) >= 0; ++k) {
       const Item it = item(w);
       ok = wait_all(&kv_full, ni);
       ++ni;
@@ -920,7 +960,7 @@ __global__ void __launch_bounds__(kBThreads, 1)
     const uint32_t id = umma_idesc_f16(128, D) | (1u << 16);  // B MN-major
     uint32_t c = 0, ni = 0;
     bool ok = true;
-    for (int k = 0, w; ok && (w = deal(k, items)) >= 0; ++k) {
+    for (int k = 0, w; ok && (w = take(k)) >= 0; ++k) {
       const Item it = item(w);
       if (ni > 0) ok = wait_all(&acc_free, ni - 1);
       ++ni;
@@ -954,7 +994,7 @@ __global__ void __launch_bounds__(kBThreads, 1)
     uint32_t c = 0, ni = 0;
     bool ok = true;
     const int64_t nw = (T + kWindow - 1) / kWindow;
-    for (int k = 0, w; ok && (w = deal(k, items)) >= 0; ++k, ++ni) {
+    for (int k = 0, w; ok && (w = take(k)) >= 0; ++k, ++ni) {
       const Item it = item(w);
       // the least exponent: whole windows by their minima, the edges token by token (a
       // window that reaches into another document must not count)
@@ -1019,7 +1059,7 @@ __global__ void __launch_bounds__(kBThreads, 1)
     const uint64_t sl22 = pack_f32x2(sl2, sl2);
     uint32_t c = 0, ni = 0;
     bool ok = true;
-    for (int k = 0, w; ok && (w = deal(k, items)) >= 0; ++k) {
+    for (int k = 0, w; ok && (w = take(k)) >= 0; ++k) {
       const Item it = item(w);
       const int kpos = it.t.row0 + r;
       // the queries [qlo, end) see this key; all of the warp's keys from qall on
@@ -1215,12 +1255,14 @@ __global__ void __launch_bounds__(kBThreads, 1)
                           PackedIndex idx, const float2* __restrict__ stats,
                           const float* __restrict__ rowexp, int64_t T, int H, int Hkv, float sl2,
                           float scale, const float2* __restrict__ cs, uint16_t* __restrict__ dqkv,
-                          GradParts gp, int* __restrict__ dev_err) {
+                          GradParts gp, int* taken, int* __restrict__ dev_err) {
   using SM = DqSmem<D>;
   constexpr int DA = D / 64, NR = SM::kRing;
   extern __shared__ uint8_t dq_raw[];
   __shared__ __align__(8) uint64_t q_full[2], q_free[2], r_full[NR], r_free[NR], k_clear[NR];
   __shared__ __align__(8) uint64_t s_full[2], s_free[2], dp_full[2], ds_full[2], dq_full[2], dq_free[2];
+  __shared__ __align__(8) uint64_t item_full[kTake], item_free[kTake];
+  __shared__ int item_sh[kTake];
   __shared__ uint32_t tmem_sh;
   __shared__ int abort_sh;
   volatile int* abort_flag = &abort_sh;
@@ -1248,6 +1290,10 @@ __global__ void __launch_bounds__(kBThreads, 1)
       mbar_init(smem_u32(&r_free[i]), 3);  // the two streams' products and warp 11
       mbar_init(smem_u32(&k_clear[i]), 1);
     }
+    for (int i = 0; i < kTake; ++i) {
+      mbar_init(smem_u32(&item_full[i]), 1);
+      mbar_init(smem_u32(&item_free[i]), kTakers);
+    }
     abort_sh = 0;
     fence_mbar_init();
     fence_proxy_async_smem();
@@ -1272,12 +1318,34 @@ __global__ void __launch_bounds__(kBThreads, 1)
   auto wait_all = [&](uint64_t* bar, uint32_t parity) -> bool {
     return __all_sync(0xFFFFFFFFu, wait(bar, parity));
   };
+  const bool many = items > (int)gridDim.x;  // (else the CTAs have one each)
+  // item k of this CTA (-1: none is left), given and taken; those below `fixed` are known
+  const int fixed = many ? 0 : 1;
+  auto give = [&](int k, int w) -> bool {
+    if (many && k >= fixed) {
+      const uint32_t n = (uint32_t)(k - fixed), slot = n % kTake;
+      if (n >= kTake && !wait(&item_free[slot], n / kTake - 1)) return false;
+      item_sh[slot] = w < items ? w : -1;
+      mbar_arrive(smem_u32(&item_full[slot]));
+    }
+    return w < items;
+  };
+  auto take = [&](int k) -> int {
+    if (k < fixed) return (int)blockIdx.x < items ? (int)blockIdx.x : -1;
+    if (!many) return -1;
+    const uint32_t n = (uint32_t)(k - fixed), slot = n % kTake;
+    if (!wait_all(&item_full[slot], n / kTake)) return -1;
+    const int w = item_sh[slot];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&item_free[slot]));
+    return w;
+  };
 
   if (warp == kBTma) {
     if (lane == 0) {
       uint32_t c = 0, nq[2] = {0, 0};
       bool ok = true;
-      for (int k = 0, w; ok && (w = deal(k, items)) >= 0; ++k) {
+      for (int k = 0, w = many ? atomicAdd(taken + 1, 1) : blockIdx.x; ok && give(k, w); ++k) {
         const FwdItem it = fwd_item(idx, w, H, heads, 0), it1 = fwd_item(idx, w, H, heads, 1);
         const int g = it.head / G;
 #pragma unroll
@@ -1308,6 +1376,8 @@ __global__ void __launch_bounds__(kBThreads, 1)
                         (H + Hkv + g) * D + 64 * a, it.begin + j * kBC);
           }
         }
+        if (ok && c >= 3) ok = wait(&r_free[(c - 3) % NR], (c - 3) / NR);  // as there
+        w = many ? atomicAdd(taken + 1, 1) : items;
       }
     }
     __syncwarp();
@@ -1331,7 +1401,7 @@ __global__ void __launch_bounds__(kBThreads, 1)
                bd + (uint32_t)((kk >> 2) * (kBC * 128 / 16) + (kk & 3) * 2), id_s, kk > 0 ? 1u : 0u);
       mma_commit(lead, smem_u32(bar));
     };
-    for (int k = 0, w; ok && (w = deal(k, items)) >= 0; ++k) {
+    for (int k = 0, w; ok && (w = take(k)) >= 0; ++k) {
       const FwdItem it = fwd_item(idx, w, H, heads, s);
       if (it.n > 0) {
         ok = wait_all(&q_full[s], ni) && wait_all(&r_full[c % NR], c / NR);
@@ -1382,7 +1452,7 @@ __global__ void __launch_bounds__(kBThreads, 1)
     // must the K rows be that those multiply (0 * inf).
     uint32_t c = 0;
     bool ok = true;
-    for (int k = 0, w; ok && (w = deal(k, items)) >= 0; ++k) {
+    for (int k = 0, w; ok && (w = take(k)) >= 0; ++k) {
       const FwdItem it = fwd_item(idx, w, H, heads, 0);
       for (int j = 0; j < it.nu && ok; ++j, ++c) {
         const uint32_t slot = c % NR;
@@ -1410,7 +1480,7 @@ __global__ void __launch_bounds__(kBThreads, 1)
     const uint64_t sl22 = pack_f32x2(sl2, sl2);
     uint32_t nc = 0, ni = 0;
     bool ok = true;
-    for (int k = 0, w; ok && (w = deal(k, items)) >= 0; ++k) {
+    for (int k = 0, w; ok && (w = take(k)) >= 0; ++k) {
       const FwdItem it = fwd_item(idx, w, H, heads, s);
       const int n = it.n;
       if (n == 0) continue;
@@ -1552,6 +1622,7 @@ struct BwdWs {
   float2* stats;   // [H, T] (lse log2 e + e, delta')
   float* rowexp;   // [H, T] e
   float* winexp;   // [H, windows] the least e of 64 tokens
+  int* taken;      // [2] items handed out: dK and dV, dQ
   float *dk, *dv;  // [T, Hkv parts, d] fp32
 };
 
@@ -1581,6 +1652,7 @@ size_t carve_bwd(int64_t T, int H, int Hkv, int d, void* base, BwdWs* w) {
   x.stats = a.take<float2>((size_t)T * H);
   x.rowexp = a.take<float>((size_t)T * H);
   x.winexp = a.take<float>((size_t)((T + kWindow - 1) / kWindow) * H);
+  x.taken = a.take<int>(2);
   const size_t n = parts > 1 ? (size_t)T * Hkv * parts * d : 0;
   x.dk = a.take<float>(n);
   x.dv = a.take<float>(n);
@@ -1602,7 +1674,7 @@ int bwd_t(const uint16_t* qkv, const PackedIndex& x, const uint16_t* o, const fl
   const unsigned windows = (unsigned)((T + kWindow - 1) / kWindow);
   LSQ_CUDA(launch_dep(packed_attn_prep_kernel<D>, dim3(windows, (unsigned)(H + Hkv)), 256, 0, st,
                       qkv, o, dout, lse, x.head, T, H, Hkv, w.dos, w.stats, w.rowexp, w.winexp,
-                      err));
+                      w.taken, err));
   const int64_t row = (int64_t)(H + 2 * Hkv) * D, hd = (int64_t)H * D;
   CUtensorMap qkv128, qkv64, do128, do64;
   LSQ_TRY(make_tmap_2d(&qkv128, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, qkv, (uint64_t)row, (uint64_t)T,
@@ -1617,11 +1689,11 @@ int bwd_t(const uint16_t* qkv, const PackedIndex& x, const uint16_t* o, const fl
   const int64_t kitems = (int64_t)x.cap * Hkv * parts;
   LSQ_CUDA(launch_dep(packed_attn_dkdv_kernel<D>, dim3((unsigned)std::min<int64_t>(kitems, sms)),
                       kBThreads, DkvSmem<D>::kBytes, st, qkv128, qkv64, do64, x, w.stats, w.rowexp,
-                      w.winexp, T, H, Hkv, H / Hkv / parts, sl2, scale, cs, dqkv, w.dk, w.dv, err));
+                      w.winexp, T, H, Hkv, H / Hkv / parts, sl2, scale, cs, dqkv, w.dk, w.dv, w.taken, err));
   const int64_t qitems = (H / Hkv) % 2 == 0 ? (int64_t)x.cap * (H / 2) : (int64_t)x.cap2 * H;
   LSQ_CUDA(launch_dep(packed_attn_dq_kernel<D>, dim3((unsigned)std::min<int64_t>(qitems, sms)),
                       kBThreads, DqSmem<D>::kBytes, st, qkv128, qkv64, do128, x, w.stats, w.rowexp,
-                      T, H, Hkv, sl2, scale, cs, dqkv, GradParts{w.dk, w.dv, parts}, err));
+                      T, H, Hkv, sl2, scale, cs, dqkv, GradParts{w.dk, w.dv, parts}, w.taken, err));
   return LSQ_OK;
 }
 
