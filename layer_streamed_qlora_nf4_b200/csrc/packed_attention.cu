@@ -104,8 +104,9 @@ template <int D>
 struct FwdSmem {
   static constexpr int DA = D / 64;                  // 64-element swizzle atoms along d
   static constexpr uint32_t kTile = 128 * D * 2;     // a tile of 128 rows of Q, K or V
-  static constexpr int kRing = D == 128 ? 5 : 8;     // K and V tiles in flight
-  static constexpr uint32_t kBytes = 1024 + (2 + kRing) * kTile;
+  static constexpr int kRing = D == 128 ? 4 : 8;     // K and V tiles in flight
+  static constexpr uint32_t kStage = 32 * 128;       // 32 rows of 64 columns of o, for each warp
+  static constexpr uint32_t kBytes = 1024 + (2 + kRing) * kTile + 8 * kStage;
 };
 
 // Key steps of the rows [row, row + 128) of a tile's document (0: no such rows).
@@ -214,8 +215,9 @@ __device__ __forceinline__ void zero_rows(uint8_t* tile, int rows, int all, int 
 
 template <int D>
 __global__ void __launch_bounds__(kFThreads, 1)
-    packed_attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_qkv, PackedIndex idx, int64_t T,
-                           int H, int Hkv, uint16_t* __restrict__ out,
+    packed_attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_qkv,
+                           const __grid_constant__ CUtensorMap tm_o,  // o, boxes of 32 rows
+                           PackedIndex idx, int64_t T, int H, int Hkv, uint16_t* __restrict__ out,
                            float* __restrict__ lse_out, float sl2, int* __restrict__ dev_err) {
   using SM = FwdSmem<D>;
   constexpr int DA = SM::DA, NR = SM::kRing;
@@ -230,6 +232,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
 
   uint8_t* Qs = align1024_p(attn_raw);   // [2] Q tiles
   uint8_t* KV = Qs + 2 * SM::kTile;      // ring: K and V tiles in turn
+  uint8_t* Os = KV + NR * SM::kTile;     // [8] staging of the softmax warps
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr uint32_t kColS = 0, kColO = 256;  // TMEM: S[stream][buffer] from 0, O at 256 and 384
   const int G = H / Hkv;
@@ -260,7 +263,10 @@ __global__ void __launch_bounds__(kFThreads, 1)
     tmem_alloc(smem_u32(&tmem_sh), 512);
     tmem_relinquish();
   }
-  if (warp == kWarpTma && lane == 0) tma_prefetch_desc(&tm_qkv);
+  if (warp == kWarpTma && lane == 0) {
+    tma_prefetch_desc(&tm_qkv);
+    tma_prefetch_desc(&tm_o);
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -516,6 +522,8 @@ __global__ void __launch_bounds__(kFThreads, 1)
       // (a barrier of its own: pv_done may be two phases on, where a wait for the
       // phase before the last would not return)
       const bool live = q < it.end;
+      const int wrow = it.row + (warp & 3) * 32, ocol = it.head * D;
+      const bool whole = wrow + 32 <= it.end;  // (uniform in the warp)
       uint16_t* orow = out + (int64_t)q * H * D + (int64_t)it.head * D;
       float* lrow = lse_out + (int64_t)it.head * T + q;
       w = w1;
@@ -533,7 +541,35 @@ __global__ void __launch_bounds__(kFThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&o_free[s]));
-      if (live) {
+      // A whole warp's rows go through its slice of shared memory to a bulk store, which
+      // runs while the warp goes on: stored by the threads, each its own row 32 bytes at a
+      // time, a tile took 3000 to 4500 cycles, a quarter of an item of 512 tokens (the
+      // store path takes a request per row and sector).  Rows next to a document's end are
+      // stored that way, since the bulk store would write those behind it.
+      if (whole) {
+        uint8_t* slice = Os + warp * SM::kStage;
+#pragma unroll
+        for (int a = 0; a < DA; ++a) {
+          if (lane == 0) bulk_wait_read<0>();  // the slice's last store has read it
+          __syncwarp();
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            const uint32_t* x = ov + 64 * a + 8 * c;
+            uint32_t pk[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              pk[e] = pack_f16x2(__uint_as_float(x[2 * e]) * inv, __uint_as_float(x[2 * e + 1]) * inv);
+            *reinterpret_cast<uint4*>(slice + lane * 128 + ((c ^ (lane & 7)) << 4)) =
+                make_uint4(pk[0], pk[1], pk[2], pk[3]);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_2d(&tm_o, smem_u32(slice), ocol + 64 * a, wrow);
+            bulk_commit();
+          }
+        }
+      } else if (live) {
 #pragma unroll
         for (int c = 0; c < D / 16; ++c) {
           uint32_t pk[8];
@@ -543,9 +579,10 @@ __global__ void __launch_bounds__(kFThreads, 1)
                                __uint_as_float(ov[16 * c + 2 * e + 1]) * inv);
           st_global32(orow + 16 * c, pk);
         }
-        *lrow = (m_ref + log2f(l_run)) * 0.69314718055994531f;
       }
+      if (live) *lrow = (m_ref + log2f(l_run)) * 0.69314718055994531f;
     }
+    if (lane == 0) bulk_wait_all();
   }
   fill_padding<D>(idx.head[2], T, H, out, lse_out);
 
@@ -1604,7 +1641,9 @@ int fwd_t(const uint16_t* qkv, const PackedIndex& x, int64_t T, int H, int Hkv, 
   static bool attr[64] = {false};
   LSQ_TRY(allow_smem(packed_attn_fwd_kernel<D>, (int)SM::kBytes, attr));
   const int64_t row = (int64_t)(H + 2 * Hkv) * D;
-  CUtensorMap tm;
+  CUtensorMap tm, to;
+  LSQ_TRY(make_tmap_2d(&to, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, o, (uint64_t)H * D, (uint64_t)T,
+                       (uint64_t)H * D, 64, 32, CU_TENSOR_MAP_SWIZZLE_128B));
   LSQ_TRY(make_tmap_2d(&tm, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, qkv, (uint64_t)row, (uint64_t)T,
                        (uint64_t)row, 64, kAQ, CU_TENSOR_MAP_SWIZZLE_128B));
   int* err = device_status_ptr();
@@ -1612,7 +1651,7 @@ int fwd_t(const uint16_t* qkv, const PackedIndex& x, int64_t T, int H, int Hkv, 
   const float sl2 = kLog2e / sqrtf((float)D);
   const int64_t items = (H / Hkv) % 2 == 0 ? (int64_t)x.cap * (H / 2) : (int64_t)x.cap2 * H;
   const unsigned grid = (unsigned)std::min<int64_t>(items, gemm_num_sms());
-  LSQ_CUDA(launch_dep(packed_attn_fwd_kernel<D>, dim3(grid), kFThreads, SM::kBytes, st, tm, x, T, H,
+  LSQ_CUDA(launch_dep(packed_attn_fwd_kernel<D>, dim3(grid), kFThreads, SM::kBytes, st, tm, to, x, T, H,
                       Hkv, o, lse, sl2, err));
   return LSQ_OK;
 }
@@ -1631,9 +1670,9 @@ struct BwdWs {
 // leaves few items, and those of one long document are uneven; what a document's last tile
 // lacks of 128 tokens is half a tile on average.  Wanted are nine items for ten SMs (dQ
 // takes the SMs that are left).  Backward in us with one, two and four shares:
-// (32/8 heads, d 128) 512 tokens in 5 documents 32, 29, 30; 1024 in 3: 59, 49, 55; 2048 in
-// one 191, 148, 162, in 4: 77, 88, 99; (16/2) 4096 in 10: 108, 84, 88; 6144 in 15: 133,
-// 118, 121; (8/2, d 64) 1024 in 1000: 179, 197, 264.
+// (32/8 heads, d 128) 512 tokens in 5 documents 33, 30, 31; 1024 in 3: 47, 47, 55; 2048 in
+// one 167, 154, 171, in 4: 72, 88, 103; (16/2) 4096 in 10: 97, 79, 92; 6144 in 15: 113,
+// 114, 124; (8/2, d 64) 1024 in 1000: 194, 217, 307.
 int dkv_parts(int64_t T, int64_t n_docs, int H, int Hkv) {
   const int G = H / Hkv;
   const int64_t tiles = std::min(T, (T + kPackedTile - 1) / kPackedTile + n_docs / 2);
