@@ -370,10 +370,12 @@ __device__ __forceinline__ void adamw_block(const MtHead& h, const MtEntry& e, c
 
 // One warp takes a block of 256 elements, lane l elements 4 l .. 4 l + 3 and 128 + 4 l
 // .. 128 + 4 l + 3, so that every load and store of a warp is contiguous.  Memory
-// bound by 28 bytes per element with an fp32 state, 16 and two scales per block with 8
-// bits; there the arithmetic comes close behind (a hundred instructions per element took
-// 205 us for 41.9 M parameters, 3.3 TB/s), hence the pairs, the flushing roots and the
-// one branch for all borders of a thread.
+// bound by 28 bytes per element with an fp32 state (41.9 M parameters in 448 tensors: 186
+// us, 6.3 TB/s), 16 and two scales per block with 8 bits; there the arithmetic comes before
+// it, hence the pairs, the flushing roots and the one branch for all borders of a thread:
+// 150 us, 4.5 TB/s, 84 instructions an element at 65% of the issue slots (a hundred took 205
+// us).  The loads are not what is waited for: with the next block brought in ahead, through
+// shared memory, it took 153 us, and longer with one contiguous share of the blocks per CTA.
 template <int BITS, int GBITS, int N>
 __global__ void __launch_bounds__(kMtThreads, 4)
     adamw_multi_kernel(const __grid_constant__ MtArgs<N> a) {
@@ -428,7 +430,8 @@ __global__ void __launch_bounds__(256)
   pdl_wait();
   __syncthreads();
   // a warp takes 512 codes, lane l codes 4 l .. 4 l + 3 of each 128, so that loads and
-  // stores of a warp are contiguous (memory bound: 5 bytes per value)
+  // stores of a warp are contiguous (memory bound: 5 bytes per value; 41.9 M values: 36 us,
+  // 5.8 TB/s)
   const int lane = threadIdx.x & 31;
   const int64_t warps = (int64_t)gridDim.x * 8;
   for (int64_t b = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * 512; b < n; b += warps * 512) {
