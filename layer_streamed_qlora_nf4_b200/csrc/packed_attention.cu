@@ -136,10 +136,12 @@ struct FwdItem {
   int begin, end, prompt;
   int row, head, n, nu;
 };
+// (read through L2: the dQ kernel must not meet a line that another kernel left in L1)
 __device__ __forceinline__ FwdItem fwd_item(const PackedIndex& x, int w, int H, bool heads, int s) {
   FwdItem it;
   const int per = heads ? H / 2 : H;
-  const PackedTile t = heads ? x.tiles[w / per] : x.tiles2[w / per];
+  const int4 v = __ldcg(reinterpret_cast<const int4*>(heads ? x.tiles : x.tiles2) + w / per);
+  const PackedTile t = {v.x, v.y, v.z, v.w};
   it.begin = t.begin;
   it.end = t.end;
   it.prompt = t.prompt;
@@ -760,7 +762,7 @@ __device__ __forceinline__ void store_grad_share(const uint32_t (&lo)[D / 4],
       float a0 = __uint_as_float(lo[c + e]) * scale, a1 = __uint_as_float(lo[c + e + 1]) * scale;
       float b0 = __uint_as_float(hi[c + e]) * scale, b1 = __uint_as_float(hi[c + e + 1]) * scale;
       if (cs) {
-        const float4 f = __ldg(reinterpret_cast<const float4*>(cs + c + e));
+        const float4 f = __ldcg(reinterpret_cast<const float4*>(cs + c + e));
         const float x0 = a0, y0 = b0, x1 = a1, y1 = b1;
         a0 = x0 * f.x + y0 * f.y;
         b0 = y0 * f.x - x0 * f.y;
@@ -1359,10 +1361,12 @@ __global__ void __launch_bounds__(kBThreads, 1)
   const uint32_t tmem = tmem_sh;
   pdl_trigger();
   // no wait here: the kernel before is dK, dV, which writes nothing that this one reads and
-  // which let it start only when the kernels before itself had completed
+  // which let it start only when the kernels before itself had completed.  But without the
+  // wait L1 may still hold lines of an earlier kernel's memory (this SM need not have run any
+  // kernel of this call), so up to the wait below all is read through L2.
   const int G = H / Hkv;
   const bool heads = G % 2 == 0;
-  const int items = heads ? idx.head[0] * (H / 2) : idx.head[1] * H;
+  const int items = heads ? __ldcg(idx.head) * (H / 2) : __ldcg(idx.head + 1) * H;
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
     return mbar_wait_short(smem_u32(bar), parity & 1u, abort_flag, dev_err);
   };
@@ -1539,8 +1543,8 @@ __global__ void __launch_bounds__(kBThreads, 1)
       const int kmax = min(max(q, it.prompt - 1), it.end - 1);  // its last key
       const int kall = min(max(it.row + (warp & 3) * 32, it.prompt - 1), it.end - 1);
       const int64_t at = (int64_t)it.head * T + min(q, it.end - 1);
-      const float2 sq = __ldg(stats + at);
-      const float e = __ldg(rowexp + at);
+      const float2 sq = __ldcg(stats + at);
+      const float e = __ldcg(rowexp + at);
       const uint64_t nl2 = pack_f32x2(e - sq.x, e - sq.x), ndl = pack_f32x2(-sq.y, -sq.y);
       for (int j = 0; j < n; ++j, ++nc) {
         ok = wait_all(&s_full[s], nc);
@@ -1596,13 +1600,13 @@ __global__ void __launch_bounds__(kBThreads, 1)
       if (lane == 0) mbar_arrive(smem_u32(&dq_free[s]));
       if (q < it.end)
         store_grad_share<D>(lo, hi, scale * ex2(-e),
-                            cs ? cs + (int64_t)idx.pos[q] * (D / 2) + hf * (D / 4) : nullptr,
+                            cs ? cs + (int64_t)__ldcg(idx.pos + q) * (D / 2) + hf * (D / 4) : nullptr,
                             dqkv + (int64_t)q * (H + 2 * Hkv) * D + (int64_t)it.head * D +
                                 hf * (D / 4));
     }
   }
   {  // padding rows have no gradient
-    const int64_t row = (int64_t)(H + 2 * Hkv) * (D / 8), first = idx.head[2];
+    const int64_t row = (int64_t)(H + 2 * Hkv) * (D / 8), first = __ldcg(idx.head + 2);
     uint4* o = reinterpret_cast<uint4*>(dqkv) + first * row;
     for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < (T - first) * row;
          i += (int64_t)gridDim.x * blockDim.x)

@@ -313,6 +313,36 @@ LOSS = [(1, 1), (1, 2), (3, 7), (5, 8), (4, 1001), (6, 4096), (2, 5003), (3, 400
         (2, 460003)]
 
 
+@pytest.mark.parametrize("H,Hkv,d", [(4, 2, 64), (4, 1, 128), (3, 1, 128)])
+def test_attention_problems_that_follow_one_another_in_the_same_memory(L, H, Hkv, d):
+    """Two rows alternate over one index, workspace and set of inputs and outputs, with
+    fewer CTAs than SMs: nothing of the row before may be met again in a cache."""
+    import torch
+    T = 300
+    rows = [([100, 200, 0, 0], [0, 50, 0, 0]), ([37, 1, 200, 62], None)]
+    data = [tuple(t.cuda() for t in _inputs(T, H, Hkv, d, seed=9 + i)) for i in range(2)]
+    lens = [torch.tensor(a, dtype=torch.int32, device="cuda") for a, _ in rows]
+    pre = [None if b is None else torch.tensor(b, dtype=torch.int32, device="cuda")
+           for _, b in rows]
+    want = [_run(L, *data[i], _index(L, *rows[i], T), H, Hkv) for i in range(2)]
+    idx = L.PackedIndex(T, 4)
+    qkv, dout = (torch.empty_like(t) for t in data[0])
+    o, lse, dqkv = (torch.empty_like(t) for t in want[0])
+    ws = torch.empty(L.packed_attention_workspace_bytes(T, H, Hkv, d), dtype=torch.uint8,
+                     device="cuda")
+    same = torch.ones(1, dtype=torch.bool, device="cuda")
+    for k in range(40):
+        i = k & 1
+        qkv.copy_(data[i][0])
+        dout.copy_(data[i][1])
+        L.packed_index(lens[i], idx, prefix=pre[i])
+        L.packed_attention_fwd(qkv, idx, H, Hkv, o, lse)
+        L.packed_attention_bwd(qkv, idx, o, lse, dout, H, Hkv, dqkv, ws)
+        for got, ref in zip((o, lse, dqkv), want[i]):
+            same &= (got == ref).all()
+    assert same.item() and L.lsq_device_status(clear=True) == 0
+
+
 @pytest.mark.parametrize("T,V", LOSS)
 @pytest.mark.parametrize("form", ["plain", "weighted", "none"])
 def test_cross_entropy(L, T, V, form):
