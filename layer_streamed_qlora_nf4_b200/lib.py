@@ -767,27 +767,26 @@ class AdamWMulti:
         if len(lrs) != n or len(wds) != n:
             raise ValueError("lr and weight_decay need one number per parameter")
         self._table = (lsq_adamw_tensor * max(n, 1))()
-        self._n, self._keep, self._dev = n, lists, None
+        self._n, self._keep = n, lists
+        self._dev = params[0] if n else None
+        names = ("params", "grads", "m", "v", "m_scale", "v_scale")
+        mdt, vdt = (torch.int8, torch.uint8) if bits == 8 else (torch.float32, torch.float32)
+        dtypes = (torch.float32, gdt, mdt, vdt, torch.float32, torch.float32)
         for i in range(n):
-            k = params[i].numel()
-            _need("params[%d]" % i, params[i], torch.float32)
-            _need("grads[%d]" % i, grads[i], gdt, numel=k)
-            _need("m[%d]" % i, m[i], torch.int8 if bits == 8 else torch.float32, numel=k)
-            _need("v[%d]" % i, v[i], torch.uint8 if bits == 8 else torch.float32, numel=k)
-            if bits == 8:
-                _need("m_scale[%d]" % i, m_scale[i], torch.float32, numel=adamw_scale_floats(k))
-                _need("v_scale[%d]" % i, v_scale[i], torch.float32, numel=adamw_scale_floats(k))
             ts = [x[i] for x in lists]
-            for t in ts:
+            k = ts[0].numel() if isinstance(ts[0], torch.Tensor) else 0
+            sizes = (k, k, k, k, (k + 255) // 256, (k + 255) // 256)
+            for j, t in enumerate(ts):
+                if not (isinstance(t, torch.Tensor) and t.dtype is dtypes[j] and
+                        t.numel() == sizes[j] and t.is_contiguous()):
+                    _need("%s[%d]" % (names[j], i), t, dtypes[j], numel=sizes[j])
                 if not t.is_cuda:
                     raise ValueError("tensor %d is not on a CUDA device" % i)
-                if self._dev is None:
-                    self._dev = t
-                if t.device != self._dev.device:
+                if t.get_device() != self._dev.get_device():
                     raise ValueError("tensor %d is on %s, the first on %s"
                                      % (i, t.device, self._dev.device))
-            ptrs = [t.data_ptr() for t in ts] + [None] * (6 - len(ts))
-            self._table[i] = lsq_adamw_tensor(*ptrs, k, lrs[i], wds[i])
+            self._table[i] = lsq_adamw_tensor(*[t.data_ptr() for t in ts],
+                                              *[None] * (6 - len(ts)), k, lrs[i], wds[i])
         self._hyper = lsq_adamw_hyper(beta1=betas[0], beta2=betas[1], eps=eps, step=1,
                                       state_bits=bits,
                                       grad_bits=32 if gdt == torch.float32 else 16)
