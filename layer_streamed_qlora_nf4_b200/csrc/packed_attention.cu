@@ -648,9 +648,10 @@ __device__ __forceinline__ float warp_min(float x) {
 // blockIdx.y >= H: the norms of the v rows of kv head blockIdx.y - H.  e brings the row's
 // largest magnitude to [1, 2), so its norm is below 2 sqrt(d).  A zero row takes e = 127
 // (it must not lower the least exponent of a tile); a row that is not finite takes e = 0,
-// and its gradients come out not finite.  16,384 tokens of 16 heads, d 128: 40 us, 5 TB/s.
+// and its gradients come out not finite.  16,384 tokens of 16 heads, d 128: 37 us,
+// 5.4 TB/s (40 with the 64 registers a thread that the compiler takes by itself, and spills).
 template <int D>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, 3)
     packed_attn_prep_kernel(const uint16_t* __restrict__ qkv, const uint16_t* __restrict__ o,
                             const uint16_t* __restrict__ dout, const float* __restrict__ lse,
                             const int* __restrict__ head, int64_t T, int H, int Hkv,
