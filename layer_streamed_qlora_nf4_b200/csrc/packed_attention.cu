@@ -1217,7 +1217,10 @@ __global__ void __launch_bounds__(kBThreads, 1)
                               b && cs ? cs + (int64_t)idx.pos[kpos] * (D / 2) + hf * (D / 4) : nullptr,
                               dqkv + (int64_t)kpos * (H + 2 * Hkv) * D + col);
         } else {
-          float* out = (b ? dk : dv) + ((int64_t)kpos * Hkv * parts + it.h0 / nh) * D + hf * (D / 4);
+          // (eight columns of consecutive tokens lie together, so that a warp's store is one
+          // run of 1 KB: by rows a tile took 7000 to 9000 cycles to write)
+          float* out = (b ? dk : dv) +
+                       (((int64_t)(it.h0 / nh) * (D / 8) + hf * (D / 32)) * T + kpos) * 8;
 #pragma unroll
           for (int e = 0; e < D / 4; e += 8) {
             uint32_t x[8], y[8];
@@ -1226,8 +1229,8 @@ __global__ void __launch_bounds__(kBThreads, 1)
               x[i] = __float_as_uint(__uint_as_float(lo[e + i]) * f);
               y[i] = __float_as_uint(__uint_as_float(hi[e + i]) * f);
             }
-            st_global32(out + e, x);
-            st_global32(out + D / 2 + e, y);
+            st_global32(out + (int64_t)(e / 8) * T * 8, x);
+            st_global32(out + (int64_t)(D / 16 + e / 8) * T * 8, y);
           }
         }
       }
@@ -1243,35 +1246,38 @@ __global__ void __launch_bounds__(kBThreads, 1)
 }
 
 // dk and dv (bf16, into dqkv) from the fp32 parts of `parts` shares of each kv head's
-// query heads, summed in order; with cs the rotation of k by its position undone.  The
-// whole grid shares the rows, a thread takes 4 pairs (i, i + D/2).
+// query heads, [share][D / 8][T][8], summed in order; with cs the rotation of k by its
+// position undone.  The whole grid shares the tokens, a thread takes 4 pairs (i, i + D/2),
+// two threads eight columns of a token, a warp 16 consecutive tokens.
 struct GradParts {
   const float *dk, *dv;
   int parts;  // 1: nothing to sum
 };
 template <int D>
-__device__ __forceinline__ void sum_parts(const GradParts& gp, int64_t tokens, const int* pos,
-                                          int Hkv, int64_t ld, int col0, const float2* cs,
-                                          uint16_t* __restrict__ dqkv) {
-  constexpr int half = D / 2, chunks = half / 4;
-  const int64_t n = tokens * 2 * Hkv * chunks;
-  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n;
-       i += (int64_t)gridDim.x * blockDim.x) {
-    const int ch = (int)(i % chunks);
-    const int64_t th = i / chunks;
-    const int hh = (int)(th % (2 * Hkv));
-    const int64_t t = th / (2 * Hkv);
-    const float* src = (hh < Hkv ? gp.dk : gp.dv) + ((t * Hkv + hh % Hkv) * gp.parts) * D + ch * 4;
+__device__ __forceinline__ void sum_parts(const GradParts& gp, int64_t tokens, int64_t T,
+                                          const int* pos, int Hkv, int64_t ld, int col0,
+                                          const float2* cs, uint16_t* __restrict__ dqkv) {
+  constexpr int half = D / 2, chunks = half / 8;
+  // (there are shares only where tokens / 128 Hkv is below the number of SMs: 32 bits do)
+  const uint32_t n = (uint32_t)tokens * 4u * Hkv * chunks;
+  for (uint32_t i = blockIdx.x * blockDim.x + threadIdx.x; i < n; i += gridDim.x * blockDim.x) {
+    const uint32_t rest = (i >> 1) / (uint32_t)tokens;
+    const int64_t t = (i >> 1) - rest * (uint32_t)tokens;
+    const int ch = (int)(rest % chunks), hh = (int)(rest / chunks);
+    const int col = ch * 8 + (int)(i & 1) * 4;
+    const float* src = (hh < Hkv ? gp.dk : gp.dv) +
+                       (((int64_t)(hh % Hkv) * gp.parts * (D / 8) + ch) * T + t) * 8 + (i & 1) * 4;
     float a[4] = {0.f, 0.f, 0.f, 0.f}, b[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
     for (int k = 0; k < gp.parts; ++k) {
-      const float4 x = __ldcg(reinterpret_cast<const float4*>(src + (int64_t)k * D));
-      const float4 y = __ldcg(reinterpret_cast<const float4*>(src + (int64_t)k * D + half));
-      a[0] += x.x; a[1] += x.y; a[2] += x.z; a[3] += x.w;
-      b[0] += y.x; b[1] += y.y; b[2] += y.z; b[3] += y.w;
+      const float* x = src + (int64_t)k * (D / 8) * T * 8;
+      const float4 u = __ldcg(reinterpret_cast<const float4*>(x));
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(x + (int64_t)chunks * T * 8));
+      a[0] += u.x; a[1] += u.y; a[2] += u.z; a[3] += u.w;
+      b[0] += v.x; b[1] += v.y; b[2] += v.z; b[3] += v.w;
     }
     if (cs && hh < Hkv) {
-      const float2* c = cs + (int64_t)pos[t] * half + ch * 4;
+      const float2* c = cs + (int64_t)pos[t] * half + col;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const float2 f = c[k];
@@ -1280,7 +1286,7 @@ __device__ __forceinline__ void sum_parts(const GradParts& gp, int64_t tokens, c
         b[k] = y * f.x - x * f.y;
       }
     }
-    uint16_t* out = dqkv + t * ld + col0 + hh * D + ch * 4;
+    uint16_t* out = dqkv + t * ld + col0 + hh * D + col;
     *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]));
     *reinterpret_cast<uint2*>(out + half) =
         make_uint2(pack_bf16x2(b[0], b[1]), pack_bf16x2(b[2], b[3]));
@@ -1615,7 +1621,7 @@ __global__ void __launch_bounds__(kBThreads, 1)
   }
   pdl_wait();  // this kernel is not done before dK, dV is, whose shares it sums
   if (gp.parts > 1)
-    sum_parts<D>(gp, idx.head[2], idx.pos, Hkv, (int64_t)(H + 2 * Hkv) * D, H * D, cs, dqkv);
+    sum_parts<D>(gp, idx.head[2], T, idx.pos, Hkv, (int64_t)(H + 2 * Hkv) * D, H * D, cs, dqkv);
   tc_fence_before();
   __syncthreads();
   if (abort_sh) settle_ns(2000000);
@@ -1681,7 +1687,7 @@ struct BwdWs {
   float* rowexp;   // [H, T] e
   float* winexp;   // [H, windows] the least e of 64 tokens
   int* taken;      // [2] items handed out: dK and dV, dQ
-  float *dk, *dv;  // [T, Hkv parts, d] fp32
+  float *dk, *dv;  // [Hkv parts, d / 8, T, 8] fp32
 };
 
 // Into how many shares a kv head's query heads are split for dK and dV.  One share
