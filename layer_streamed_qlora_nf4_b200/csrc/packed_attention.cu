@@ -829,6 +829,7 @@ __global__ void __launch_bounds__(kBThreads, 1)
   constexpr int DA = D / 64, NR = SM::kRing, kItems = 8;
   static_assert(NR % 2 == 0, "a ring slot always serves the same set of warps");
   static_assert(kItems > NR + 1, "an item's least exponent is kept until all have read it");
+  static_assert(NR >= 3, "the chunk that an item is drawn behind has not left its slot");
   extern __shared__ uint8_t dkv_raw[];
   __shared__ __align__(8) uint64_t kv_full, kv_free, r_full[NR], r_free[NR], st_full[NR];
   __shared__ __align__(8) uint64_t s_full[2], dp_full[2], p_full[2], ds_full[2], s_free[2], dp_free[2];
@@ -1318,6 +1319,7 @@ __global__ void __launch_bounds__(kBThreads, 1)
                           GradParts gp, int* taken, int* __restrict__ dev_err) {
   using SM = DqSmem<D>;
   constexpr int DA = D / 64, NR = SM::kRing;
+  static_assert(NR >= 3, "the chunk that an item is drawn behind has not left its slot");
   extern __shared__ uint8_t dq_raw[];
   __shared__ __align__(8) uint64_t q_full[2], q_free[2], r_full[NR], r_free[NR], k_clear[NR];
   __shared__ __align__(8) uint64_t s_full[2], s_free[2], dp_full[2], ds_full[2], dq_full[2], dq_free[2];
