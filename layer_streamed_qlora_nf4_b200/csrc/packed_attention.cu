@@ -557,12 +557,18 @@ __global__ void __launch_bounds__(kFThreads, 1)
       // time, a tile took 3000 to 4500 cycles, a quarter of an item of 512 tokens (the
       // store path takes a request per row and sector).  Rows next to a document's end are
       // stored that way, since the bulk store would write those behind it.
+      // Behind the CTA's last item the stream's Q tile is free too, and takes both halves.
       if (whole) {
-        uint8_t* slice = Os + warp * SM::kStage;
+        uint8_t* slice = w1 < 0 ? Qs + s * SM::kTile + (warp & 3) * DA * SM::kStage
+                                : Os + warp * SM::kStage;
 #pragma unroll
         for (int a = 0; a < DA; ++a) {
-          if (lane == 0) bulk_wait_read<0>();  // the slice's last store has read it
-          __syncwarp();
+          if (w1 >= 0) {
+            if (lane == 0) bulk_wait_read<0>();  // the slice's last store has read it
+            __syncwarp();
+          } else if (a > 0) {
+            slice += SM::kStage;
+          }
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
             const uint32_t* x = ov + 64 * a + 8 * c;
