@@ -217,10 +217,14 @@ __device__ __forceinline__ float ex2(float x) {  // 2^x, relative error 2^-22
   return r;
 }
 
-// (max, sum of exp relative to it) of two sets; (-inf, 0) is the empty set.
+// (max, sum of exp relative to it) of two sets; (-inf, 0) is the empty set.  The maximum
+// passes over NaN, the sum does not: of a set with a NaN it is NaN, whatever the maximum.
 __device__ __forceinline__ void join(float& m, float& s, float mo, float so) {
   const float mn = fmaxf(m, mo);
-  if (mn == -INFINITY) return;
+  if (mn == -INFINITY) {
+    s += so;
+    return;
+  }
   s = s * ex2((m - mn) * kLog2e) + so * ex2((mo - mn) * kLog2e);
   m = mn;
 }
@@ -312,7 +316,12 @@ __global__ void __launch_bounds__(kCeThreads)
     }
   float m = -INFINITY, s = 0.f;
   const float xo = odd >= 0 ? x[odd] : -INFINITY;
-  if (odd >= 0) join(m, s, xo, 1.f);
+  if (xo > -INFINITY) {
+    m = xo;
+    s = 1.f;
+  } else if (isnan(xo)) {
+    s = xo;
+  }
   const float4* s4 = reinterpret_cast<const float4*>(slice);
   for (int i = 0; i < kCeChunks; ++i) {
     const int a = min(ng, i * cg) * 2, e = min(ng, (i + 1) * cg) * 2;  // in float4

@@ -407,6 +407,38 @@ def test_cross_entropy_not_finite_rows_are_the_formulas(L):
     assert torch.isnan(rl[0]) and torch.isnan(rl[1]) and rl[2].item() == float("inf")
 
 
+@pytest.mark.parametrize("T,V", [(4, 1), (4, 7), (5, 300), (5, 1001), (5, 40003), (4, 131075),
+                                 (4, 460003)])
+def test_cross_entropy_a_nan_anywhere_reaches_the_whole_row(L, T, V):
+    """Also among the few logits before and behind those that are taken eight at a time, and
+    in a row that holds nothing else; the other rows do not change."""
+    import torch
+    nan, inf = float("nan"), float("inf")
+    g = torch.Generator().manual_seed(V)
+    clean = torch.randn(T, V, generator=g).cuda()
+    y = torch.full((T,), V // 2, dtype=torch.int32, device="cuda")
+
+    def run(x):
+        rl, tot = torch.empty(T, device="cuda"), torch.empty(1, device="cuda")
+        dl = torch.empty(T, V, dtype=torch.bfloat16, device="cuda")
+        L.packed_cross_entropy(x, y, rl, tot, dlogits=dl)
+        return rl, tot, dl
+    rl0, _, dl0 = run(clean)
+    for row in range(T):
+        for at in sorted({0, 1, 7, 8, V // 2, V - 9, V - 8, V - 2, V - 1} & set(range(V))):
+            for rest in (False, True):
+                x = clean.clone()
+                if rest:
+                    x[row] = -inf       # nothing finite to take a maximum of
+                x[row, at] = nan
+                rl, tot, dl = run(x)
+                assert torch.isnan(rl[row]) and torch.isnan(tot[0]), (row, at, rest)
+                assert torch.isnan(dl[row]).all(), (row, at, rest)
+                keep = torch.arange(T, device="cuda") != row
+                assert torch.equal(rl[keep], rl0[keep]) and torch.equal(dl[keep], dl0[keep])
+    assert L.lsq_device_status(clear=True) == 0
+
+
 def test_attention_of_many_short_documents(L):
     """More work items than a GPU has SMs, each with a cleared tail: every CTA takes
     several in turn."""
