@@ -245,7 +245,8 @@ __device__ __forceinline__ void adamw_block(const MtHead& h, const MtEntry& e, c
     atomicOr(h.dev_err, DEV_ERR_NONFINITE);
     tm = tv = 0;
     for (int i = 0; i < 8; ++i) {
-      const int64_t at = base + (i >> 2) * 128 + lane * 4 + (i & 3);
+      const int off = (i >> 2) * 128 + lane * 4 + (i & 3);
+      const int64_t at = base + off;
       float2 x = both(m[0]), y = both(v[0]);
 #pragma unroll
       for (int j = 1; j < 4; ++j)
@@ -254,7 +255,9 @@ __device__ __forceinline__ void adamw_block(const MtHead& h, const MtEntry& e, c
           y = both(v[j]);
         }
       float mi = i & 1 ? x.y : x.x, vi = i & 1 ? y.y : y.x;
-      if (!(fabsf(mi) < INFINITY && vi < INFINITY)) {  // (such an element exists: at < n)
+      if (!WHOLE && off >= left) {
+        mi = vi = 0.f;  // no such element (its code 0 times a scale that is not finite)
+      } else if (!(fabsf(mi) < INFINITY && vi < INFINITY)) {
         skip |= 1u << i;
         mi = BITS == 8 ? am * lm[static_cast<uint8_t*>(e.m)[at]] : static_cast<float*>(e.m)[at];
         vi = BITS == 8 ? av * lv[static_cast<uint8_t*>(e.v)[at]] : static_cast<float*>(e.v)[at];
