@@ -425,8 +425,8 @@ __global__ void __launch_bounds__(kMtThreads, 4)
 
 // Codes to values and back, for a state that is saved, loaded or inspected.
 __global__ void __launch_bounds__(256)
-    state_decode_kernel(const uint8_t* __restrict__ codes, const float* __restrict__ scale,
-                        int64_t n, int is_signed, float* __restrict__ out) {
+    state_decode_kernel(const uint8_t* codes, const float* scale,
+                        int64_t n, int is_signed, float* out) {
   __shared__ float lut[256];
   pdl_trigger();
   lut[threadIdx.x] = is_signed ? level_m((int)(int8_t)threadIdx.x) : level_v((int)threadIdx.x);
@@ -442,8 +442,8 @@ __global__ void __launch_bounds__(256)
       uint32_t w[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        w[k] = __ldg(reinterpret_cast<const uint32_t*>(codes + b + k * 128) + lane);
-      const float a0 = __ldg(scale + b / kBlk), a1 = __ldg(scale + b / kBlk + 1);
+        w[k] = reinterpret_cast<const uint32_t*>(codes + b + k * 128)[lane];
+      const float a0 = scale[b / kBlk], a1 = scale[b / kBlk + 1];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const float a = k < 2 ? a0 : a1;
@@ -458,8 +458,8 @@ __global__ void __launch_bounds__(256)
 }
 
 __global__ void __launch_bounds__(256)
-    state_encode_kernel(const float* __restrict__ x, int64_t n, int is_signed,
-                        uint8_t* __restrict__ codes, float* __restrict__ scale, int* dev_err) {
+    state_encode_kernel(const float* x, int64_t n, int is_signed,
+                        uint8_t* codes, float* scale, int* dev_err) {
   pdl_trigger();
   pdl_wait();
   const int lane = threadIdx.x & 31;

@@ -74,7 +74,7 @@ __device__ __forceinline__ int ties_before(int kind, int i, int pt) {
 // single long document costs no more than many short ones.  Latency throughout: 2.4 us for
 // 512 tokens in 5 documents, 4.1 for 16,384 in 40, 14 for 1024 in 1000.
 __global__ void __launch_bounds__(kIdxThreads, 1)
-    packed_index_kernel(const int32_t* __restrict__ lengths, const int32_t* __restrict__ prefix,
+    packed_index_kernel(const int32_t* lengths, const int32_t* prefix,
                         int n_docs, int T, PackedIndex x, int* dev_err) {
   __shared__ int64_t sh[32];
   __shared__ int64_t sums[2];
@@ -193,9 +193,9 @@ __global__ void __launch_bounds__(kIdxThreads, 1)
 // in loss_mask (if given); -1 elsewhere.  count: the integer sum over CTAs, the same
 // in any order.  Memory bound (17 bytes a token), in practice the latency of a launch.
 __global__ void __launch_bounds__(256)
-    packed_targets_kernel(const int32_t* __restrict__ tokens, const int* __restrict__ key_end,
-                          const int* __restrict__ doc_end, const uint8_t* __restrict__ loss_mask,
-                          int T, int32_t* __restrict__ targets, int32_t* __restrict__ count) {
+    packed_targets_kernel(const int32_t* tokens, const int* key_end,
+                          const int* doc_end, const uint8_t* loss_mask,
+                          int T, int32_t* targets, int32_t* count) {
   pdl_trigger();
   pdl_wait();
   int n = 0;
@@ -255,9 +255,9 @@ __device__ __forceinline__ void warp_join(float& m, float& s) {
 // multiple of eight, so that any V moves in aligned 16-byte pieces; the few before and
 // behind are rank 0's and the last rank's.
 __global__ void __launch_bounds__(kCeThreads)
-    packed_ce_kernel(const float* __restrict__ logits, const int32_t* __restrict__ targets,
-                     int64_t V, const float* __restrict__ weight, const int32_t* __restrict__ count,
-                     uint16_t* __restrict__ dlogits, float* __restrict__ row_loss, int C,
+    packed_ce_kernel(const float* logits, const int32_t* targets,
+                     int64_t V, const float* weight, const int32_t* count,
+                     uint16_t* dlogits, float* row_loss, int C,
                      int* dev_err) {
   extern __shared__ __align__(128) float slice[];
   __shared__ __align__(8) uint64_t bar[kCeChunks];
@@ -279,8 +279,8 @@ __global__ void __launch_bounds__(kCeThreads)
   const int64_t odd = rank == 0 && tid < head ? tid
                       : rank == C - 1 && tid >= 32 && tail + tid - 32 < V && tid < 40 ? tail + tid - 32
                                                                                      : -1;
-  const float* __restrict__ x = logits + row * V;
-  uint16_t* __restrict__ dx = dlogits ? dlogits + row * V : nullptr;
+  const float* x = logits + row * V;
+  uint16_t* dx = dlogits ? dlogits + row * V : nullptr;
   if (tid == 0) {
     for (int i = 0; i < kCeChunks; ++i) mbar_init(smem_u32(&bar[i]), 1);
     abort_sh = 0;
@@ -422,17 +422,17 @@ __global__ void __launch_bounds__(kCeThreads)
 // per row, which reads it twice.  256 rows of 500,001: 256 us, 3.0 TB/s of the bytes that
 // the other form would move.
 __global__ void __launch_bounds__(1024, 1)
-    packed_ce_long_kernel(const float* __restrict__ logits, const int32_t* __restrict__ targets,
-                          int64_t V, const float* __restrict__ weight,
-                          const int32_t* __restrict__ count, uint16_t* __restrict__ dlogits,
-                          float* __restrict__ row_loss, int* dev_err) {
+    packed_ce_long_kernel(const float* logits, const int32_t* targets,
+                          int64_t V, const float* weight,
+                          const int32_t* count, uint16_t* dlogits,
+                          float* row_loss, int* dev_err) {
   __shared__ float red_m[32], red_s[32];
   pdl_trigger();
   pdl_wait();
   const int tid = threadIdx.x;
   const int64_t row = blockIdx.x, y = targets[row];
-  const float* __restrict__ x = logits + row * V;
-  uint16_t* __restrict__ dx = dlogits ? dlogits + row * V : nullptr;
+  const float* x = logits + row * V;
+  uint16_t* dx = dlogits ? dlogits + row * V : nullptr;
   const bool on = y >= 0 && y < V;
   float m = -INFINITY, s = 0.f;
   if (on)
@@ -467,9 +467,9 @@ __global__ void __launch_bounds__(1024, 1)
 
 // loss (+)= sum over rows with a target of c_t row_loss[t], in a fixed order.
 __global__ void __launch_bounds__(1024, 1)
-    packed_loss_kernel(const float* __restrict__ row_loss, const int32_t* __restrict__ targets,
-                       int64_t T, int64_t V, const float* __restrict__ weight,
-                       const int32_t* __restrict__ count, int accumulate, float* __restrict__ loss) {
+    packed_loss_kernel(const float* row_loss, const int32_t* targets,
+                       int64_t T, int64_t V, const float* weight,
+                       const int32_t* count, int accumulate, float* loss) {
   __shared__ float red[32];
   pdl_trigger();
   pdl_wait();

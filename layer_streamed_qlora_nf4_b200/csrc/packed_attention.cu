@@ -136,12 +136,10 @@ struct FwdItem {
   int begin, end, prompt;
   int row, head, n, nu;
 };
-// (read through L2: the dQ kernel must not meet a line that another kernel left in L1)
 __device__ __forceinline__ FwdItem fwd_item(const PackedIndex& x, int w, int H, bool heads, int s) {
   FwdItem it;
   const int per = heads ? H / 2 : H;
-  const int4 v = __ldcg(reinterpret_cast<const int4*>(heads ? x.tiles : x.tiles2) + w / per);
-  const PackedTile t = {v.x, v.y, v.z, v.w};
+  const PackedTile t = (heads ? x.tiles : x.tiles2)[w / per];
   it.begin = t.begin;
   it.end = t.end;
   it.prompt = t.prompt;
@@ -228,8 +226,8 @@ template <int D>
 __global__ void __launch_bounds__(kFThreads, 1)
     packed_attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_qkv,
                            const __grid_constant__ CUtensorMap tm_o,  // o, boxes of 32 rows
-                           PackedIndex idx, int64_t T, int H, int Hkv, uint16_t* __restrict__ out,
-                           float* __restrict__ lse_out, float sl2, int* __restrict__ dev_err) {
+                           PackedIndex idx, int64_t T, int H, int Hkv, uint16_t* out,
+                           float* lse_out, float sl2, int* dev_err) {
   using SM = FwdSmem<D>;
   constexpr int DA = SM::DA, NR = SM::kRing;
   extern __shared__ uint8_t attn_raw[];
@@ -658,12 +656,12 @@ __device__ __forceinline__ float warp_min(float x) {
 // 5.4 TB/s (40 with the 64 registers a thread that the compiler takes by itself, and spills).
 template <int D>
 __global__ void __launch_bounds__(256, 3)
-    packed_attn_prep_kernel(const uint16_t* __restrict__ qkv, const uint16_t* __restrict__ o,
-                            const uint16_t* __restrict__ dout, const float* __restrict__ lse,
-                            const int* __restrict__ head, int64_t T, int H, int Hkv,
-                            uint16_t* __restrict__ dos, float2* __restrict__ stats,
-                            float* __restrict__ rowexp, float* __restrict__ winexp,
-                            int* __restrict__ taken, int* dev_err) {
+    packed_attn_prep_kernel(const uint16_t* qkv, const uint16_t* o,
+                            const uint16_t* dout, const float* lse,
+                            const int* head, int64_t T, int H, int Hkv,
+                            uint16_t* dos, float2* stats,
+                            float* rowexp, float* winexp,
+                            int* taken, int* dev_err) {
   constexpr int LR = D / 8, RW = 32 / LR, IT = kWindow / 8 / RW;  // lanes a row, rows a warp, rounds
   __shared__ float low[8];
   pdl_trigger();
@@ -769,7 +767,7 @@ __device__ __forceinline__ void store_grad_share(const uint32_t (&lo)[D / 4],
       float a0 = __uint_as_float(lo[c + e]) * scale, a1 = __uint_as_float(lo[c + e + 1]) * scale;
       float b0 = __uint_as_float(hi[c + e]) * scale, b1 = __uint_as_float(hi[c + e + 1]) * scale;
       if (cs) {
-        const float4 f = __ldcg(reinterpret_cast<const float4*>(cs + c + e));
+        const float4 f = *reinterpret_cast<const float4*>(cs + c + e);
         const float x0 = a0, y0 = b0, x1 = a1, y1 = b1;
         a0 = x0 * f.x + y0 * f.y;
         b0 = y0 * f.x - x0 * f.y;
@@ -825,12 +823,12 @@ __global__ void __launch_bounds__(kBThreads, 1)
     packed_attn_dkdv_kernel(const __grid_constant__ CUtensorMap tm_kv,   // qkv, boxes of 128 rows
                             const __grid_constant__ CUtensorMap tm_q,    // qkv, boxes of 64 rows
                             const __grid_constant__ CUtensorMap tm_do,   // dO', boxes of 64 rows
-                            PackedIndex idx, const float2* __restrict__ stats,
-                            const float* __restrict__ rowexp, const float* __restrict__ winexp,
+                            PackedIndex idx, const float2* stats,
+                            const float* rowexp, const float* winexp,
                             int64_t T, int H, int Hkv, int nh, float sl2, float scale,
-                            const float2* __restrict__ cs, uint16_t* __restrict__ dqkv,
-                            float* __restrict__ dk, float* __restrict__ dv, int* taken,
-                            int* __restrict__ dev_err) {
+                            const float2* cs, uint16_t* dqkv,
+                            float* dk, float* dv, int* taken,
+                            int* dev_err) {
   using SM = DkvSmem<D>;
   constexpr int DA = D / 64, NR = SM::kRing, kItems = 8;
   static_assert(NR % 2 == 0, "a ring slot always serves the same set of warps");
@@ -888,8 +886,8 @@ __global__ void __launch_bounds__(kBThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_sh;
-  pdl_wait();
-  pdl_trigger();  // behind the wait: the dQ kernel may start, and finds everything it reads
+  pdl_trigger();
+  pdl_wait();  // dO', its values and the counter come from the kernels before
   const int G = H / Hkv, parts = G / nh;
   const int per = Hkv * parts;              // items of a tile
   const int items = idx.head[0] * per;
@@ -1068,13 +1066,13 @@ __global__ void __launch_bounds__(kBThreads, 1)
         const float* we = winexp + (int64_t)(it.h0 + hh) * nw;
         const float* re = rowexp + (int64_t)(it.h0 + hh) * T;
         const int q = it.qs + lane, u = e1 + lane;
-        const float a = w0 + lane < w1 ? __ldg(we + w0 + lane) : 127.f;
-        const float b = q < e0 ? __ldg(re + q) : 127.f, c = q + 32 < e0 ? __ldg(re + q + 32) : 127.f;
-        const float d = u < it.t.end ? __ldg(re + u) : 127.f;
-        const float e = u + 32 < it.t.end ? __ldg(re + u + 32) : 127.f;
+        const float a = w0 + lane < w1 ? we[w0 + lane] : 127.f;
+        const float b = q < e0 ? re[q] : 127.f, c = q + 32 < e0 ? re[q + 32] : 127.f;
+        const float d = u < it.t.end ? re[u] : 127.f;
+        const float e = u + 32 < it.t.end ? re[u + 32] : 127.f;
         emin = fminf(fminf(fminf(emin, a), fminf(b, c)), fminf(d, e));
-        for (int i = w0 + 32 + lane; i < w1; i += 32) emin = fminf(emin, __ldg(we + i));
-        for (int i = q + 64; i < e0; i += 32) emin = fminf(emin, __ldg(re + i));
+        for (int i = w0 + 32 + lane; i < w1; i += 32) emin = fminf(emin, we[i]);
+        for (int i = q + 64; i < e0; i += 32) emin = fminf(emin, re[i]);
       }
       emin = warp_min(emin);
       if (lane == 0) emin_sh[ni % kItems] = emin;
@@ -1087,7 +1085,7 @@ __global__ void __launch_bounds__(kBThreads, 1)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const int q = q0 + lane + 32 * i;
-            v[i] = q < it.t.end ? __ldg(sh + q) : make_float2(INFINITY, 0.f);
+            v[i] = q < it.t.end ? sh[q] : make_float2(INFINITY, 0.f);
             v[i].x = emin - v[i].x;
           }
           ok = wait_all(&r_full[slot], c / NR);
@@ -1263,7 +1261,7 @@ struct GradParts {
 template <int D>
 __device__ __forceinline__ void sum_parts(const GradParts& gp, int64_t tokens, int64_t T,
                                           const int* pos, int Hkv, int64_t ld, int col0,
-                                          const float2* cs, uint16_t* __restrict__ dqkv) {
+                                          const float2* cs, uint16_t* dqkv) {
   constexpr int half = D / 2, chunks = half / 8;
   // (there are shares only where tokens / 128 Hkv is below the number of SMs: 32 bits do)
   const uint32_t n = (uint32_t)tokens * 4u * Hkv * chunks;
@@ -1278,8 +1276,8 @@ __device__ __forceinline__ void sum_parts(const GradParts& gp, int64_t tokens, i
 #pragma unroll 4
     for (int k = 0; k < gp.parts; ++k) {
       const float* x = src + (int64_t)k * (D / 8) * T * 8;
-      const float4 u = __ldcg(reinterpret_cast<const float4*>(x));
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(x + (int64_t)chunks * T * 8));
+      const float4 u = *reinterpret_cast<const float4*>(x);
+      const float4 v = *reinterpret_cast<const float4*>(x + (int64_t)chunks * T * 8);
       a[0] += u.x; a[1] += u.y; a[2] += u.z; a[3] += u.w;
       b[0] += v.x; b[1] += v.y; b[2] += v.z; b[3] += v.w;
     }
@@ -1319,10 +1317,10 @@ __global__ void __launch_bounds__(kBThreads, 1)
     packed_attn_dq_kernel(const __grid_constant__ CUtensorMap tm_q,    // qkv, boxes of 128 rows
                           const __grid_constant__ CUtensorMap tm_kv,   // qkv, boxes of 64 rows
                           const __grid_constant__ CUtensorMap tm_do,   // dO', boxes of 128 rows
-                          PackedIndex idx, const float2* __restrict__ stats,
-                          const float* __restrict__ rowexp, int64_t T, int H, int Hkv, float sl2,
-                          float scale, const float2* __restrict__ cs, uint16_t* __restrict__ dqkv,
-                          GradParts gp, int* taken, int* __restrict__ dev_err) {
+                          PackedIndex idx, const float2* stats,
+                          const float* rowexp, int64_t T, int H, int Hkv, float sl2,
+                          float scale, const float2* cs, uint16_t* dqkv,
+                          GradParts gp, int* taken, int* dev_err) {
   using SM = DqSmem<D>;
   constexpr int DA = D / 64, NR = SM::kRing;
   static_assert(NR >= 3, "the chunk that an item is drawn behind has not left its slot");
@@ -1375,13 +1373,10 @@ __global__ void __launch_bounds__(kBThreads, 1)
   tc_fence_after();
   const uint32_t tmem = tmem_sh;
   pdl_trigger();
-  // no wait here: the kernel before is dK, dV, which writes nothing that this one reads and
-  // which let it start only when the kernels before itself had completed.  But without the
-  // wait L1 may still hold lines of an earlier kernel's memory (this SM need not have run any
-  // kernel of this call), so up to the wait below all is read through L2.
+  pdl_wait();  // dO', its values and the counter come from the kernels before
   const int G = H / Hkv;
   const bool heads = G % 2 == 0;
-  const int items = heads ? __ldcg(idx.head) * (H / 2) : __ldcg(idx.head + 1) * H;
+  const int items = heads ? idx.head[0] * (H / 2) : idx.head[1] * H;
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
     return mbar_wait_short(smem_u32(bar), parity & 1u, abort_flag, dev_err);
   };
@@ -1558,8 +1553,8 @@ __global__ void __launch_bounds__(kBThreads, 1)
       const int kmax = min(max(q, it.prompt - 1), it.end - 1);  // its last key
       const int kall = min(max(it.row + (warp & 3) * 32, it.prompt - 1), it.end - 1);
       const int64_t at = (int64_t)it.head * T + min(q, it.end - 1);
-      const float2 sq = __ldcg(stats + at);
-      const float e = __ldcg(rowexp + at);
+      const float2 sq = stats[at];
+      const float e = rowexp[at];
       const uint64_t nl2 = pack_f32x2(e - sq.x, e - sq.x), ndl = pack_f32x2(-sq.y, -sq.y);
       for (int j = 0; j < n; ++j, ++nc) {
         ok = wait_all(&s_full[s], nc);
@@ -1615,19 +1610,18 @@ __global__ void __launch_bounds__(kBThreads, 1)
       if (lane == 0) mbar_arrive(smem_u32(&dq_free[s]));
       if (q < it.end)
         store_grad_share<D>(lo, hi, scale * ex2(-e),
-                            cs ? cs + (int64_t)__ldcg(idx.pos + q) * (D / 2) + hf * (D / 4) : nullptr,
+                            cs ? cs + (int64_t)idx.pos[q] * (D / 2) + hf * (D / 4) : nullptr,
                             dqkv + (int64_t)q * (H + 2 * Hkv) * D + (int64_t)it.head * D +
                                 hf * (D / 4));
     }
   }
   {  // padding rows have no gradient
-    const int64_t row = (int64_t)(H + 2 * Hkv) * (D / 8), first = __ldcg(idx.head + 2);
+    const int64_t row = (int64_t)(H + 2 * Hkv) * (D / 8), first = idx.head[2];
     uint4* o = reinterpret_cast<uint4*>(dqkv) + first * row;
     for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < (T - first) * row;
          i += (int64_t)gridDim.x * blockDim.x)
       o[i] = make_uint4(0u, 0u, 0u, 0u);
   }
-  pdl_wait();  // this kernel is not done before dK, dV is, whose shares it sums
   if (gp.parts > 1)
     sum_parts<D>(gp, idx.head[2], T, idx.pos, Hkv, (int64_t)(H + 2 * Hkv) * D, H * D, cs, dqkv);
   tc_fence_before();
