@@ -612,12 +612,16 @@ __global__ void __launch_bounds__(kFThreads, 1)
 }
 
 // ------------------------------------------------------------------ backward
-// Two kernels recompute the probabilities, p = exp2(s c - lse log2 e), and form
-// ds = p (dp - delta) with delta = rowsum(dO o O): one owns the keys (dK, dV), one the
+// Items of two kinds recompute the probabilities, p = exp2(s c - lse log2 e), and form
+// ds = p (dp - delta) with delta = rowsum(dO o O): one kind owns keys (dK, dV), the other
 // queries (dQ), so that no sum is shared between CTAs and none depends on their order.
-// Both are persistent, go through the other side in chunks of 64, keep P and dS in TMEM
-// as fp16 A operands over the columns they come from, and split the issuing of products
-// between two warps.
+// Both go through the other side in chunks of 64, keep P and dS in TMEM as fp16 A operands
+// over the columns they come from, and split the issuing of products between two warps.
+// One persistent kernel takes them all, a CTA its dK, dV items first, so that SMs that
+// find none left go on with dQ while others still work on theirs.  (As two kernels, the
+// second may read what the preparation wrote only when the first is done: backward of 512
+// tokens in 5 documents (32/8 heads, d 128) took 36 us so, 30 now; of 16,384 in 34 (16/2)
+// 268 and 257.)
 //   warps 0-15: the gradient warps, four groups of four (a TMEM lane per thread): groups 0
 //            and 2 take the two halves of the columns of one set (or stream), 1 and 3 of
 //            the other.  (With two groups of whole rows a chunk took a thread 3700 cycles,
@@ -631,11 +635,11 @@ constexpr int kBH = kBC / 2;   // columns of a thread
 constexpr int kBThreads = 640;
 constexpr int kBTma = 16, kBMma = 17, kBTail = 19;
 constexpr int kWindow = 64;    // tokens of a window of the exponents' minima
-// Items are handed out as CTAs come for them, heaviest first: the TMA producer draws the
-// next one from a counter (zeroed by the kernel that prepares dO') and passes it to the
-// other 19 warps through a ring in shared memory.  What an item computes does not depend
-// on who takes it.  (Dealt out beforehand, the dQ CTAs that start last, behind the longest
-// dK, dV items, kept as large a share as the others.)
+// Items are handed out as CTAs come for them, heaviest first, the dQ items behind those of
+// dK and dV: the TMA producer draws the next one from a counter (zeroed by the kernel that
+// prepares dO') and passes it to the other 19 warps through a ring in shared memory.  What
+// an item computes does not depend on who takes it.  (Dealt out beforehand, CTAs that come
+// to dQ last, behind the longest dK, dV items, kept as large a share as the others.)
 constexpr int kTake = 4;
 constexpr int kTakers = 19;
 // |dS'| <= 2 |dO'| |v| with |dO'| < 2 sqrt(128): below fp16's 65504 for these norms of v
@@ -661,7 +665,7 @@ __global__ void __launch_bounds__(256, 3)
                             const int* head, int64_t T, int H, int Hkv,
                             uint16_t* dos, float2* stats,
                             float* rowexp, float* winexp,
-                            int* taken, int* dev_err) {
+                            uint32_t* taken, int* dev_err) {
   constexpr int LR = D / 8, RW = 32 / LR, IT = kWindow / 8 / RW;  // lanes a row, rows a warp, rounds
   __shared__ float low[8];
   pdl_trigger();
@@ -669,7 +673,7 @@ __global__ void __launch_bounds__(256, 3)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int h = blockIdx.y, col = (lane % LR) * 8;
   const int64_t live = head[2];
-  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 2) taken[threadIdx.x] = 0;
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *taken = 0;
   const int64_t t0 = (int64_t)blockIdx.x * kWindow + warp * (kWindow / 8) + lane / LR;
   if (h >= H) {
     bool big = false;
@@ -805,11 +809,10 @@ __device__ __forceinline__ void load_share(uint32_t t, uint32_t (&lo)[D / 4], ui
 // emin is the least exponent of the item's queries: P' = 2^(emin - e) P <= 1, so all
 // products carry the same factor 2^emin, taken out at the end.  With all heads of the
 // group in one item (nh = G) the sums are the gradients, written in bf16; otherwise
-// fp32 parts are left for the kernel below to sum.
+// fp32 parts are left for packed_attn_sum_kernel.
 // Tensor bound: 1280 cycles of products a chunk, which takes about 1760 (the chain from a
-// chunk's scores to its dS' and on; two sets of warps hide one behind the other).  16,384
-// packed tokens (16/2 heads, d 128): 218 us of the 400 that the backward takes; backward of
-// one document of 16,384 tokens (32/8): 6.8 to 7.2 ms, 770 to 810 TFLOP/s over both kernels.
+// chunk's scores to its dS' and on; two sets of warps hide one behind the other).  The whole
+// backward of one document of 16,384 tokens (32/8 heads, d 128): 7.4 ms, 740 TFLOP/s.
 template <int D>
 struct DkvSmem {
   static constexpr uint32_t kTile = 128 * D * 2;  // K or V
@@ -818,33 +821,60 @@ struct DkvSmem {
   static constexpr uint32_t kBytes = 1024 + 2 * kTile + 2 * kRing * kQc + kRing * kBC * 8;
 };
 
+// Hands out the items of one part of the kernel: `first` is this CTA's, known to all its
+// warps (none when it is `items` or more); the others are drawn by the TMA producer, which
+// gives each to the other warps.
+struct ItemRing {
+  uint64_t full[kTake], free[kTake];
+  int item[kTake];
+};
+
+// What both parts of the kernel read and write, and how they wait.
+struct BwdArgs {
+  PackedIndex idx;
+  const float2* stats;
+  const float *rowexp, *winexp;
+  int64_t T;
+  int H, Hkv, nh;
+  float sl2, scale;
+  const float2* cs;
+  uint16_t* dqkv;
+  float *dk, *dv;
+  uint32_t* taken;
+  int* dev_err;
+};
+
+// The CTA's dK, dV items: w0 is its first; -> the first number drawn that is none of them.
 template <int D>
-__global__ void __launch_bounds__(kBThreads, 1)
-    packed_attn_dkdv_kernel(const __grid_constant__ CUtensorMap tm_kv,   // qkv, boxes of 128 rows
-                            const __grid_constant__ CUtensorMap tm_q,    // qkv, boxes of 64 rows
-                            const __grid_constant__ CUtensorMap tm_do,   // dO', boxes of 64 rows
-                            PackedIndex idx, const float2* stats,
-                            const float* rowexp, const float* winexp,
-                            int64_t T, int H, int Hkv, int nh, float sl2, float scale,
-                            const float2* cs, uint16_t* dqkv,
-                            float* dk, float* dv, int* taken,
-                            int* dev_err) {
+__device__ __forceinline__ uint32_t dkdv_part(const BwdArgs& a_, const CUtensorMap& tm_kv,  // qkv, boxes of 128 rows
+                                              const CUtensorMap& tm_q,   // qkv, boxes of 64 rows
+                                              const CUtensorMap& tm_do,  // dO', boxes of 64 rows
+                                              uint8_t* dyn, uint32_t tmem, int items, bool many,
+                                              uint32_t w0, int* abort_sh) {
+  const PackedIndex& idx = a_.idx;
+  const float2* stats = a_.stats;
+  const float *rowexp = a_.rowexp, *winexp = a_.winexp;
+  const int64_t T = a_.T;
+  const int H = a_.H, Hkv = a_.Hkv, nh = a_.nh;
+  const float sl2 = a_.sl2, scale = a_.scale;
+  const float2* cs = a_.cs;
+  uint16_t* dqkv = a_.dqkv;
+  float *dk = a_.dk, *dv = a_.dv;
+  int* dev_err = a_.dev_err;
   using SM = DkvSmem<D>;
   constexpr int DA = D / 64, NR = SM::kRing, kItems = 8;
   static_assert(NR % 2 == 0, "a ring slot always serves the same set of warps");
   static_assert(kItems > NR + 1, "an item's least exponent is kept until all have read it");
   static_assert(NR >= 3, "the chunk that an item is drawn behind has not left its slot");
-  extern __shared__ uint8_t dkv_raw[];
   __shared__ __align__(8) uint64_t kv_full, kv_free, r_full[NR], r_free[NR], st_full[NR];
   __shared__ __align__(8) uint64_t s_full[2], dp_full[2], p_full[2], ds_full[2], s_free[2], dp_free[2];
-  __shared__ __align__(8) uint64_t acc_full, acc_free, item_full[kTake], item_free[kTake];
-  __shared__ int item_sh[kTake];
+  __shared__ __align__(8) uint64_t acc_full, acc_free;
+  __shared__ __align__(8) ItemRing ring;
   __shared__ float emin_sh[kItems];
-  __shared__ uint32_t tmem_sh;
-  __shared__ int abort_sh;
-  volatile int* abort_flag = &abort_sh;
+  __shared__ uint32_t next_sh;
+  volatile int* abort_flag = abort_sh;
 
-  uint8_t* Ks = align1024_p(dkv_raw);
+  uint8_t* Ks = dyn;
   uint8_t* Vs = Ks + SM::kTile;
   uint8_t* Qb = Vs + SM::kTile;             // [NR] chunks of Q
   uint8_t* dOb = Qb + NR * SM::kQc;         // [NR] chunks of dO'
@@ -871,52 +901,40 @@ __global__ void __launch_bounds__(kBThreads, 1)
     mbar_init(smem_u32(&acc_full), 1);
     mbar_init(smem_u32(&acc_free), 16);
     for (int i = 0; i < kTake; ++i) {
-      mbar_init(smem_u32(&item_full[i]), 1);
-      mbar_init(smem_u32(&item_free[i]), kTakers);
+      mbar_init(smem_u32(&ring.full[i]), 1);
+      mbar_init(smem_u32(&ring.free[i]), kTakers);
     }
-    abort_sh = 0;
+    next_sh = UINT32_MAX;
     fence_mbar_init();
     fence_proxy_async_smem();
   }
-  if (warp == kBMma) {
-    tmem_alloc(smem_u32(&tmem_sh), 512);
-    tmem_relinquish();
-  }
-  tc_fence_before();
   __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = tmem_sh;
-  pdl_trigger();
-  pdl_wait();  // dO', its values and the counter come from the kernels before
   const int G = H / Hkv, parts = G / nh;
   const int per = Hkv * parts;              // items of a tile
-  const int items = idx.head[0] * per;
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
     return mbar_wait_short(smem_u32(bar), parity & 1u, abort_flag, dev_err);
   };
   auto wait_all = [&](uint64_t* bar, uint32_t parity) -> bool {
     return __all_sync(0xFFFFFFFFu, wait(bar, parity));
   };
-  const bool many = items > (int)gridDim.x;  // (else the CTAs have one each)
-  // item k of this CTA (-1: none is left), given and taken; those below `fixed` are known
-  const int fixed = 1;
-  auto give = [&](int k, int w) -> bool {
-    if (many && k >= fixed) {
-      const uint32_t n = (uint32_t)(k - fixed), slot = n % kTake;
-      if (n >= kTake && !wait(&item_free[slot], n / kTake - 1)) return false;
-      item_sh[slot] = w < items ? w : -1;
-      mbar_arrive(smem_u32(&item_full[slot]));
+  // item k of this CTA (-1: none is left), given and taken; the first is known
+  auto give = [&](int k, uint32_t w) -> bool {
+    if (many && k > 0) {
+      const uint32_t n = (uint32_t)(k - 1), slot = n % kTake;
+      if (n >= kTake && !wait(&ring.free[slot], n / kTake - 1)) return false;
+      ring.item[slot] = w < (uint32_t)items ? (int)w : -1;
+      mbar_arrive(smem_u32(&ring.full[slot]));
     }
-    return w < items;
+    return w < (uint32_t)items;
   };
   auto take = [&](int k) -> int {
-    if (k < fixed) return (int)blockIdx.x < items ? (int)blockIdx.x : -1;
+    if (k == 0) return w0 < (uint32_t)items ? (int)w0 : -1;
     if (!many) return -1;
-    const uint32_t n = (uint32_t)(k - fixed), slot = n % kTake;
-    if (!wait_all(&item_full[slot], n / kTake)) return -1;
-    const int w = item_sh[slot];
+    const uint32_t n = (uint32_t)(k - 1), slot = n % kTake;
+    if (!wait_all(&ring.full[slot], n / kTake)) return -1;
+    const int w = ring.item[slot];
     __syncwarp();
-    if (lane == 0) mbar_arrive(smem_u32(&item_free[slot]));
+    if (lane == 0) mbar_arrive(smem_u32(&ring.free[slot]));
     return w;
   };
   // an item's tile, first query head, first query and chunks of a head
@@ -940,8 +958,9 @@ __global__ void __launch_bounds__(kBThreads, 1)
     if (lane == 0) {
       uint32_t c = 0, ni = 0;
       bool ok = true;
-      for (int k = 0, w = blockIdx.x; ok && give(k, w); ++k) {
-        const Item it = item(w);
+      uint32_t w = w0;
+      for (int k = 0; ok && give(k, w); ++k) {
+        const Item it = item((int)w);
         if (ni > 0) ok = wait(&kv_free, ni - 1);
         if (!ok) break;
         ++ni;
@@ -969,8 +988,9 @@ __global__ void __launch_bounds__(kBThreads, 1)
         // (drawn when three chunks are left: any sooner, and a CTA with a long item takes
         // another one from those that will be done before it)
         if (ok && c >= 3) ok = wait(&r_free[(c - 3) % NR], (c - 3) / NR);
-        w = many ? (int)gridDim.x + atomicAdd(taken, 1) : items;
+        w = many ? gridDim.x + atomicAdd(a_.taken, 1u) : UINT32_MAX;
       }
+      if (ok) next_sh = w;
     }
     __syncwarp();
   } else if (warp == kBMma) {
@@ -1243,26 +1263,23 @@ __global__ void __launch_bounds__(kBThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (abort_sh) settle_ns(2000000);
-  if (warp == kBMma) {
-    tc_fence_after();
-    tmem_dealloc(tmem, 512);
-  }
+  tc_fence_after();
+  return next_sh;
 }
 
 // dk and dv (bf16, into dqkv) from the fp32 parts of `parts` shares of each kv head's
 // query heads, [share][D / 8][T][8], summed in order; with cs the rotation of k by its
 // position undone.  The whole grid shares the tokens, a thread takes 4 pairs (i, i + D/2),
 // two threads eight columns of a token, a warp 16 consecutive tokens.
-struct GradParts {
-  const float *dk, *dv;
-  int parts;  // 1: nothing to sum
-};
 template <int D>
-__device__ __forceinline__ void sum_parts(const GradParts& gp, int64_t tokens, int64_t T,
-                                          const int* pos, int Hkv, int64_t ld, int col0,
-                                          const float2* cs, uint16_t* dqkv) {
+__global__ void __launch_bounds__(256)
+    packed_attn_sum_kernel(const float* dk, const float* dv, int parts, const int* head,
+                           int64_t T, const int* pos, int Hkv, int64_t ld, int col0,
+                           const float2* cs, uint16_t* dqkv) {
   constexpr int half = D / 2, chunks = half / 8;
+  pdl_trigger();
+  pdl_wait();
+  const int64_t tokens = head[2];
   // (there are shares only where tokens / 128 Hkv is below the number of SMs: 32 bits do)
   const uint32_t n = (uint32_t)tokens * 4u * Hkv * chunks;
   for (uint32_t i = blockIdx.x * blockDim.x + threadIdx.x; i < n; i += gridDim.x * blockDim.x) {
@@ -1270,11 +1287,11 @@ __device__ __forceinline__ void sum_parts(const GradParts& gp, int64_t tokens, i
     const int64_t t = (i >> 1) - rest * (uint32_t)tokens;
     const int ch = (int)(rest % chunks), hh = (int)(rest / chunks);
     const int col = ch * 8 + (int)(i & 1) * 4;
-    const float* src = (hh < Hkv ? gp.dk : gp.dv) +
-                       (((int64_t)(hh % Hkv) * gp.parts * (D / 8) + ch) * T + t) * 8 + (i & 1) * 4;
+    const float* src = (hh < Hkv ? dk : dv) +
+                       (((int64_t)(hh % Hkv) * parts * (D / 8) + ch) * T + t) * 8 + (i & 1) * 4;
     float a[4] = {0.f, 0.f, 0.f, 0.f}, b[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
-    for (int k = 0; k < gp.parts; ++k) {
+    for (int k = 0; k < parts; ++k) {
       const float* x = src + (int64_t)k * (D / 8) * T * 8;
       const float4 u = *reinterpret_cast<const float4*>(x);
       const float4 v = *reinterpret_cast<const float4*>(x + (int64_t)chunks * T * 8);
@@ -1302,8 +1319,7 @@ __device__ __forceinline__ void sum_parts(const GradParts& gp, int64_t tokens, i
 // Items and streams as in the forward; a stream's chunk of 64 keys:
 //   its MMA warp: S = Q K^T, dP' = dO' V^T;  its gradient warps: P = exp2(S c - lse log2 e),
 //   dS' = P (dP' - delta') as fp16 over dP' in TMEM;  the MMA warp: dQ' += dS' K.
-// S of the next chunk is computed while dS of this one is formed.  16,384 packed tokens
-// (16/2 heads, d 128): 153 us, some of it while dK and dV drain.
+// S of the next chunk is computed while dS of this one is formed.
 template <int D>
 struct DqSmem {
   static constexpr uint32_t kTile = 128 * D * 2;  // Q or dO' of a stream
@@ -1312,28 +1328,32 @@ struct DqSmem {
   static constexpr uint32_t kBytes = 1024 + 4 * kTile + 2 * kRing * kKc;
 };
 
+// The CTA's dQ items: w0 is its first (or behind the last); `done` drawn numbers are none
+// of them but lie before theirs.
 template <int D>
-__global__ void __launch_bounds__(kBThreads, 1)
-    packed_attn_dq_kernel(const __grid_constant__ CUtensorMap tm_q,    // qkv, boxes of 128 rows
-                          const __grid_constant__ CUtensorMap tm_kv,   // qkv, boxes of 64 rows
-                          const __grid_constant__ CUtensorMap tm_do,   // dO', boxes of 128 rows
-                          PackedIndex idx, const float2* stats,
-                          const float* rowexp, int64_t T, int H, int Hkv, float sl2,
-                          float scale, const float2* cs, uint16_t* dqkv,
-                          GradParts gp, int* taken, int* dev_err) {
+__device__ __forceinline__ void dq_part(const BwdArgs& a_, const CUtensorMap& tm_q,   // qkv, boxes of 128 rows
+                                        const CUtensorMap& tm_kv,  // qkv, boxes of 64 rows
+                                        const CUtensorMap& tm_do,  // dO', boxes of 128 rows
+                                        uint8_t* dyn, uint32_t tmem, int items, uint32_t done,
+                                        bool many, uint32_t w0, int* abort_sh) {
+  const PackedIndex& idx = a_.idx;
+  const float2* stats = a_.stats;
+  const float* rowexp = a_.rowexp;
+  const int64_t T = a_.T;
+  const int H = a_.H, Hkv = a_.Hkv;
+  const float sl2 = a_.sl2, scale = a_.scale;
+  const float2* cs = a_.cs;
+  uint16_t* dqkv = a_.dqkv;
+  int* dev_err = a_.dev_err;
   using SM = DqSmem<D>;
   constexpr int DA = D / 64, NR = SM::kRing;
   static_assert(NR >= 3, "the chunk that an item is drawn behind has not left its slot");
-  extern __shared__ uint8_t dq_raw[];
   __shared__ __align__(8) uint64_t q_full[2], q_free[2], r_full[NR], r_free[NR], k_clear[NR];
   __shared__ __align__(8) uint64_t s_full[2], s_free[2], dp_full[2], ds_full[2], dq_full[2], dq_free[2];
-  __shared__ __align__(8) uint64_t item_full[kTake], item_free[kTake];
-  __shared__ int item_sh[kTake];
-  __shared__ uint32_t tmem_sh;
-  __shared__ int abort_sh;
-  volatile int* abort_flag = &abort_sh;
+  __shared__ __align__(8) ItemRing ring;
+  volatile int* abort_flag = abort_sh;
 
-  uint8_t* Qs = align1024_p(dq_raw);        // [2] Q of the streams
+  uint8_t* Qs = dyn;                        // [2] Q of the streams
   uint8_t* dOs = Qs + 2 * SM::kTile;        // [2] dO'
   uint8_t* Kb = dOs + 2 * SM::kTile;        // [NR] chunks of K
   uint8_t* Vb = Kb + NR * SM::kKc;          // [NR] chunks of V
@@ -1357,52 +1377,39 @@ __global__ void __launch_bounds__(kBThreads, 1)
       mbar_init(smem_u32(&k_clear[i]), 1);
     }
     for (int i = 0; i < kTake; ++i) {
-      mbar_init(smem_u32(&item_full[i]), 1);
-      mbar_init(smem_u32(&item_free[i]), kTakers);
+      mbar_init(smem_u32(&ring.full[i]), 1);
+      mbar_init(smem_u32(&ring.free[i]), kTakers);
     }
-    abort_sh = 0;
     fence_mbar_init();
     fence_proxy_async_smem();
   }
-  if (warp == kBMma) {
-    tmem_alloc(smem_u32(&tmem_sh), 512);
-    tmem_relinquish();
-  }
-  tc_fence_before();
   __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = tmem_sh;
-  pdl_trigger();
-  pdl_wait();  // dO', its values and the counter come from the kernels before
   const int G = H / Hkv;
   const bool heads = G % 2 == 0;
-  const int items = heads ? idx.head[0] * (H / 2) : idx.head[1] * H;
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
     return mbar_wait_short(smem_u32(bar), parity & 1u, abort_flag, dev_err);
   };
   auto wait_all = [&](uint64_t* bar, uint32_t parity) -> bool {
     return __all_sync(0xFFFFFFFFu, wait(bar, parity));
   };
-  const bool many = items > (int)gridDim.x;  // (else the CTAs have one each)
-  // item k of this CTA (-1: none is left), given and taken; those below `fixed` are known
-  const int fixed = many ? 0 : 1;
-  auto give = [&](int k, int w) -> bool {
-    if (many && k >= fixed) {
-      const uint32_t n = (uint32_t)(k - fixed), slot = n % kTake;
-      if (n >= kTake && !wait(&item_free[slot], n / kTake - 1)) return false;
-      item_sh[slot] = w < items ? w : -1;
-      mbar_arrive(smem_u32(&item_full[slot]));
+  // item k of this CTA (-1: none is left), given and taken; the first is known
+  auto give = [&](int k, uint32_t w) -> bool {
+    if (many && k > 0) {
+      const uint32_t n = (uint32_t)(k - 1), slot = n % kTake;
+      if (n >= kTake && !wait(&ring.free[slot], n / kTake - 1)) return false;
+      ring.item[slot] = w < (uint32_t)items ? (int)w : -1;
+      mbar_arrive(smem_u32(&ring.full[slot]));
     }
-    return w < items;
+    return w < (uint32_t)items;
   };
   auto take = [&](int k) -> int {
-    if (k < fixed) return (int)blockIdx.x < items ? (int)blockIdx.x : -1;
+    if (k == 0) return w0 < (uint32_t)items ? (int)w0 : -1;
     if (!many) return -1;
-    const uint32_t n = (uint32_t)(k - fixed), slot = n % kTake;
-    if (!wait_all(&item_full[slot], n / kTake)) return -1;
-    const int w = item_sh[slot];
+    const uint32_t n = (uint32_t)(k - 1), slot = n % kTake;
+    if (!wait_all(&ring.full[slot], n / kTake)) return -1;
+    const int w = ring.item[slot];
     __syncwarp();
-    if (lane == 0) mbar_arrive(smem_u32(&item_free[slot]));
+    if (lane == 0) mbar_arrive(smem_u32(&ring.free[slot]));
     return w;
   };
 
@@ -1410,8 +1417,10 @@ __global__ void __launch_bounds__(kBThreads, 1)
     if (lane == 0) {
       uint32_t c = 0, nq[2] = {0, 0};
       bool ok = true;
-      for (int k = 0, w = many ? atomicAdd(taken + 1, 1) : blockIdx.x; ok && give(k, w); ++k) {
-        const FwdItem it = fwd_item(idx, w, H, heads, 0), it1 = fwd_item(idx, w, H, heads, 1);
+      uint32_t w = w0;
+      for (int k = 0; ok && give(k, w); ++k) {
+        const FwdItem it = fwd_item(idx, (int)w, H, heads, 0),
+                      it1 = fwd_item(idx, (int)w, H, heads, 1);
         const int g = it.head / G;
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
@@ -1442,7 +1451,7 @@ __global__ void __launch_bounds__(kBThreads, 1)
           }
         }
         if (ok && c >= 3) ok = wait(&r_free[(c - 3) % NR], (c - 3) / NR);  // as there
-        w = many ? atomicAdd(taken + 1, 1) : items;
+        w = many ? gridDim.x + atomicAdd(a_.taken, 1u) - done : UINT32_MAX;
       }
     }
     __syncwarp();
@@ -1615,15 +1624,52 @@ __global__ void __launch_bounds__(kBThreads, 1)
                                 hf * (D / 4));
     }
   }
+  tc_fence_before();
+  __syncthreads();
+}
+
+template <int D>
+__global__ void __launch_bounds__(kBThreads, 1)
+    packed_attn_bwd_kernel(const __grid_constant__ CUtensorMap tm_128,    // qkv, boxes of 128 rows
+                           const __grid_constant__ CUtensorMap tm_64,     // qkv, boxes of 64 rows
+                           const __grid_constant__ CUtensorMap tm_do128,  // dO', boxes of 128 rows
+                           const __grid_constant__ CUtensorMap tm_do64,   // dO', boxes of 64 rows
+                           const __grid_constant__ BwdArgs a) {
+  extern __shared__ uint8_t bwd_raw[];
+  __shared__ uint32_t tmem_sh;
+  __shared__ int abort_sh;
+  uint8_t* dyn = align1024_p(bwd_raw);
+  const int warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) abort_sh = 0;
+  if (warp == kBMma) {
+    tmem_alloc(smem_u32(&tmem_sh), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_sh;
+  pdl_trigger();
+  pdl_wait();  // dO', its values, the index and the counter come from the kernels before
+  const int G = a.H / a.Hkv;
+  const int kitems = a.idx.head[0] * a.Hkv * (G / a.nh);
+  const int qitems = G % 2 == 0 ? a.idx.head[0] * (a.H / 2) : a.idx.head[1] * a.H;
+  // (both are below 2^31, their sum and what is drawn behind it below 2^32)
+  const bool many = (uint32_t)kitems + (uint32_t)qitems > gridDim.x;  // (else one for each CTA)
+  uint32_t w = blockIdx.x;
+  if (w < (uint32_t)kitems)
+    w = dkdv_part<D>(a, tm_128, tm_64, tm_do64, dyn, tmem, kitems, many, w, &abort_sh);
+  // (every product and copy of the first part has been waited for, unless a wait gave up)
+  if (w >= (uint32_t)kitems && w - (uint32_t)kitems < (uint32_t)qitems && !abort_sh)
+    dq_part<D>(a, tm_128, tm_64, tm_do128, dyn, tmem, qitems, (uint32_t)kitems, many,
+               w - (uint32_t)kitems, &abort_sh);
   {  // padding rows have no gradient
-    const int64_t row = (int64_t)(H + 2 * Hkv) * (D / 8), first = idx.head[2];
-    uint4* o = reinterpret_cast<uint4*>(dqkv) + first * row;
-    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < (T - first) * row;
+    const int64_t row = (int64_t)(a.H + 2 * a.Hkv) * (D / 8), first = a.idx.head[2];
+    uint4* o = reinterpret_cast<uint4*>(a.dqkv) + first * row;
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < (a.T - first) * row;
          i += (int64_t)gridDim.x * blockDim.x)
       o[i] = make_uint4(0u, 0u, 0u, 0u);
   }
-  if (gp.parts > 1)
-    sum_parts<D>(gp, idx.head[2], T, idx.pos, Hkv, (int64_t)(H + 2 * Hkv) * D, H * D, cs, dqkv);
   tc_fence_before();
   __syncthreads();
   if (abort_sh) settle_ns(2000000);
@@ -1688,23 +1734,27 @@ struct BwdWs {
   float2* stats;   // [H, T] (lse log2 e + e, delta')
   float* rowexp;   // [H, T] e
   float* winexp;   // [H, windows] the least e of 64 tokens
-  int* taken;      // [2] items handed out: dK and dV, dQ
+  uint32_t* taken; // items handed out behind each CTA's first
   float *dk, *dv;  // [Hkv parts, d / 8, T, 8] fp32
 };
 
 // Into how many shares a kv head's query heads are split for dK and dV.  One share
-// needs no partial sums (8 bytes written and read per token, share and dimension) but
-// leaves few items, and those of one long document are uneven; what a document's last tile
-// lacks of 128 tokens is half a tile on average.  Wanted are nine items for ten SMs (dQ
-// takes the SMs that are left).  Backward in us with one, two and four shares:
-// (32/8 heads, d 128) 512 tokens in 5 documents 33, 30, 31; 1024 in 3: 47, 47, 55; 2048 in
-// one 167, 154, 171, in 4: 72, 88, 103; (16/2) 4096 in 10: 97, 79, 92; 6144 in 15: 113,
-// 114, 124; (8/2, d 64) 1024 in 1000: 194, 217, 307.
+// needs no partial sums (8 bytes written and read per token, share and dimension, and a
+// launch) but leaves few items, and those of one long document are uneven; what a document's
+// last tile lacks of 128 tokens is half a tile on average.  Wanted is more than an item for
+// 16 tokens, since longer rows have longer items, up to nine items for ten SMs (dQ takes
+// the SMs that are left).  Backward in us with one, two, four and eight shares:
+// (32/8 heads, d 128) 512 tokens in 5 documents 30, 30, 33; in one 45, 35, 36; 1024 in 3:
+// 43, 45, 53; 2048 in one 160, 152, 171; in 5: 77, 94, 112; (16/2) 512 in 5: 39, 30, 26, 30;
+// 1024 in 20: 36, 32, 34, 39; 4096 in one 521, 302, 246, 284; in 10: 109, 84, 94, 114;
+// (8/2, d 64) 1024 in 1000: 187, 205, 301.
 int dkv_parts(int64_t T, int64_t n_docs, int H, int Hkv) {
   const int G = H / Hkv;
   const int64_t tiles = std::min(T, (T + kPackedTile - 1) / kPackedTile + n_docs / 2);
-  for (int p = 1; p < G; ++p)
-    if (G % p == 0 && tiles * Hkv * p * 10 >= (int64_t)gemm_num_sms() * 9) return p;
+  for (int p = 1; p < G; ++p) {
+    const int64_t items = tiles * Hkv * p;
+    if (G % p == 0 && (items * 16 > T || items * 10 >= (int64_t)gemm_num_sms() * 9)) return p;
+  }
   return G;
 }
 
@@ -1718,7 +1768,7 @@ size_t carve_bwd(int64_t T, int H, int Hkv, int d, void* base, BwdWs* w) {
   x.stats = a.take<float2>((size_t)T * H);
   x.rowexp = a.take<float>((size_t)T * H);
   x.winexp = a.take<float>((size_t)((T + kWindow - 1) / kWindow) * H);
-  x.taken = a.take<int>(2);
+  x.taken = a.take<uint32_t>(1);
   const size_t n = parts > 1 ? (size_t)T * Hkv * parts * d : 0;
   x.dk = a.take<float>(n);
   x.dv = a.take<float>(n);
@@ -1730,9 +1780,9 @@ template <int D>
 int bwd_t(const uint16_t* qkv, const PackedIndex& x, const uint16_t* o, const float* lse,
           const uint16_t* dout, int64_t T, int H, int Hkv, const float2* cs, uint16_t* dqkv,
           int parts, const BwdWs& w, cudaStream_t st) {
-  static bool attr_kv[64] = {false}, attr_q[64] = {false};
-  LSQ_TRY(allow_smem(packed_attn_dkdv_kernel<D>, (int)DkvSmem<D>::kBytes, attr_kv));
-  LSQ_TRY(allow_smem(packed_attn_dq_kernel<D>, (int)DqSmem<D>::kBytes, attr_q));
+  static bool attr[64] = {false};
+  constexpr uint32_t smem = std::max(DkvSmem<D>::kBytes, DqSmem<D>::kBytes);
+  LSQ_TRY(allow_smem(packed_attn_bwd_kernel<D>, (int)smem, attr));
   int* err = device_status_ptr();
   if (!err) return set_error(LSQ_ERR_CUDA, "device status word unavailable");
   const float scale = 1.f / sqrtf((float)D);
@@ -1752,14 +1802,20 @@ int bwd_t(const uint16_t* qkv, const PackedIndex& x, const uint16_t* o, const fl
   LSQ_TRY(make_tmap_2d(&do64, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, w.dos, (uint64_t)hd, (uint64_t)T,
                        (uint64_t)hd, 64, kBC, CU_TENSOR_MAP_SWIZZLE_128B));
   const int sms = gemm_num_sms();
+  // (at most: the documents' tiles are known on the device)
   const int64_t kitems = (int64_t)x.cap * Hkv * parts;
-  LSQ_CUDA(launch_dep(packed_attn_dkdv_kernel<D>, dim3((unsigned)std::min<int64_t>(kitems, sms)),
-                      kBThreads, DkvSmem<D>::kBytes, st, qkv128, qkv64, do64, x, w.stats, w.rowexp,
-                      w.winexp, T, H, Hkv, H / Hkv / parts, sl2, scale, cs, dqkv, w.dk, w.dv, w.taken, err));
   const int64_t qitems = (H / Hkv) % 2 == 0 ? (int64_t)x.cap * (H / 2) : (int64_t)x.cap2 * H;
-  LSQ_CUDA(launch_dep(packed_attn_dq_kernel<D>, dim3((unsigned)std::min<int64_t>(qitems, sms)),
-                      kBThreads, DqSmem<D>::kBytes, st, qkv128, qkv64, do128, x, w.stats, w.rowexp,
-                      T, H, Hkv, sl2, scale, cs, dqkv, GradParts{w.dk, w.dv, parts}, w.taken, err));
+  const BwdArgs args{x, w.stats, w.rowexp, w.winexp, T, H, Hkv, H / Hkv / parts, sl2, scale, cs,
+                     dqkv, w.dk, w.dv, w.taken, err};
+  LSQ_CUDA(launch_dep(packed_attn_bwd_kernel<D>, dim3((unsigned)std::min<int64_t>(kitems + qitems, sms)),
+                      kBThreads, smem, st, qkv128, qkv64, do128, do64, args));
+  if (parts > 1) {
+    // a thread for four pairs of columns of a token
+    const int64_t n = T * 4 * Hkv * (D / 16);
+    const unsigned grid = (unsigned)std::min<int64_t>((n + 255) / 256, (int64_t)sms * 8);
+    LSQ_CUDA(launch_dep(packed_attn_sum_kernel<D>, dim3(grid), 256, 0, st, w.dk, w.dv, parts, x.head,
+                        T, x.pos, Hkv, row, H * D, cs, dqkv));
+  }
   return LSQ_OK;
 }
 
