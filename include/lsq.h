@@ -477,12 +477,16 @@ size_t packed_attention_workspace_bytes(int64_t T, int32_t H, int32_t Hkv, int32
  *           rows): dq, and dk and dv summed in fp32 over the query heads of each kv head.
  *   ws      device workspace of packed_attention_workspace_bytes(T, H, Hkv, d) bytes,
  *           32-byte aligned.
- * The score gradients multiply in fp16 after each row of dout is scaled by the power
- * of two that brings its largest magnitude to [1, 2), so their range does not matter for
- * dq.  In dk and dv the rows of a document that see a tile of 128 keys share the factor of
- * the largest, so a row's part is exact to 2^-25 of the largest row's, not of its own.  A
- * row of v whose norm is above 1447 latches LSQ_DEV_ERR_NONFINITE (its score gradients may
- * overflow).  Asynchronous, deterministic (fixed-order sums, no atomics). */
+ * The products take fp16 operands, scaled by powers of two that are taken out in fp32:
+ *  - a row of dout so that its largest magnitude is in [1, 2): elements below 2^-17 of it are
+ *    off by up to 2^-25 of it;
+ *  - the score gradients by the row of dout and the largest norm of v among the document's
+ *    keys, so that neither's size matters: one of 2^-29 of the largest possible is still
+ *    rounded to 11 bits.  In dk and dv the rows of a document that see a tile of 128 keys share
+ *    the factor of the largest: a row's part is off by 2^-40 of the largest possible at most,
+ *    beside its rounding to 11 bits.
+ * A row of v that is not finite latches LSQ_DEV_ERR_NONFINITE.  Asynchronous, deterministic
+ * (fixed-order sums, no atomics). */
 int packed_attention_bwd(const uint16_t* qkv, const int32_t* index, int32_t n_docs,
                          const uint16_t* o, const float* lse, const uint16_t* dout, int64_t T,
                          int32_t H, int32_t Hkv, int32_t d, uint16_t* dqkv, void* ws,

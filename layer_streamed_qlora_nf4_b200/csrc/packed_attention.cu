@@ -12,9 +12,11 @@
 // All products run as tcgen05.mma from 128-byte-swizzled shared-memory tiles (TMA)
 // into TMEM accumulators, fp16 operands and fp32 sums throughout.  The gradient of the
 // output arrives in bf16, whose range fp16 lacks: its rows are scaled by powers of two
-// first (dO' = 2^e dO with a largest magnitude in [1, 2)), which loses none of bf16's 8 bits,
-// and the factors are taken out again in fp32.  Every sum has a fixed order, so the
-// results are deterministic.
+// first (dO' = 2^e dO with a largest magnitude in [1, 2); exact down to 2^-17 of it, and off
+// by 2^-25 at most below), and the factors are taken out again in fp32.  The probabilities and
+// score gradients that the backward rounds to fp16 are scaled towards the top of its range,
+// the latter by what the norms of v allow, so that small ones keep their bits.  Every sum has
+// a fixed order, so the results are deterministic.
 #include <cuda.h>
 #include <math.h>
 
@@ -629,7 +631,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
 //   warp 16: TMA producer;  warps 17, 18: MMA issuers (warp 17 also allocates TMEM)
 //   warp 19: clears rows behind a document's end, and (dK, dV) stages the queries' values
 // The prepared values of a query and head: dO' = 2^e dO in fp16, its largest in [1, 2),
-// e, delta' = 2^e delta and l = lse log2 e + e.
+// e, delta' = 2^e delta and l = lse log2 e + e; of a key and kv head: |v|^2.
 constexpr int kBC = 64;        // columns of a chunk (queries for dK/dV, keys for dQ)
 constexpr int kBH = kBC / 2;   // columns of a thread
 constexpr int kBThreads = 640;
@@ -642,18 +644,45 @@ constexpr int kWindow = 64;    // tokens of a window of the exponents' minima
 // to dQ last, behind the longest dK, dV items, kept as large a share as the others.)
 constexpr int kTake = 4;
 constexpr int kTakers = 19;
-// |dS'| <= 2 |dO'| |v| with |dO'| < 2 sqrt(128): below fp16's 65504 for these norms of v
-constexpr float kMaxNormV = 1447.f;
-
+// The exponent a for which |dP' - delta'| 2^a stays below 2^15, half of fp16's range, given
+// the largest |v|^2 among the keys: |dP' - delta'| <= 2 |dO'| |v| < 4 sqrt(d) |v|.  Held where
+// 2^(-e - a), which takes it out again beside 2^e, is a normal number.
+constexpr int kUp = 15;
+__device__ __forceinline__ int ds_exponent(float nv, int d, int e) {
+  const int x = (int)(__float_as_uint(16.f * (float)d * nv) >> 23) - 126;  // 16 d |v|^2 < 2^x
+  return max(min(kUp - ((x + 1) >> 1), 126 - e), -127 - e);
+}
+__device__ __forceinline__ float pow2i(int x) { return __int_as_float((127 + x) << 23); }
 __device__ __forceinline__ float warp_min(float x) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) x = fminf(x, __shfl_xor_sync(0xFFFFFFFFu, x, o));
   return x;
 }
 
+// The largest |v|^2 of the keys [begin, end): whole windows by their maxima, the edges row by
+// row (a window that reaches into another document must not count).  A lane's share; most
+// documents take one round of loads.
+__device__ __forceinline__ float largest_norm(const float* winnorm, const float* rownorm, int begin,
+                                              int end, int lane) {
+  const int w0 = (begin + kWindow - 1) / kWindow, w1 = end / kWindow;
+  const int e0 = w0 < w1 ? w0 * kWindow : end, e1 = w0 < w1 ? w1 * kWindow : end;
+  const int q = begin + lane, u = e1 + lane;
+  const float a = w0 + lane < w1 ? winnorm[w0 + lane] : 0.f;
+  const float b = q < e0 ? rownorm[q] : 0.f, c = q + 32 < e0 ? rownorm[q + 32] : 0.f;
+  const float d = u < end ? rownorm[u] : 0.f, e = u + 32 < end ? rownorm[u + 32] : 0.f;
+  float n = fmaxf(fmaxf(fmaxf(a, b), fmaxf(c, d)), e);
+  for (int i = w0 + 32 + lane; i < w1; i += 32) n = fmaxf(n, winnorm[i]);
+  for (int i = q + 64; i < e0; i += 32) n = fmaxf(n, rownorm[i]);
+  return n;
+}
+__device__ __forceinline__ float warp_most(float x) {  // (of numbers that are not negative)
+  return __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(x)));
+}
+
 // One CTA per window of 64 tokens and head; D / 8 lanes take a row, 16 bytes each, and a
 // warp its eight tokens with all loads in flight (memory bound: 6 bytes per element).
-// blockIdx.y >= H: the norms of the v rows of kv head blockIdx.y - H.  e brings the row's
+// blockIdx.y >= H: the squared norms of the v rows of kv head blockIdx.y - H (0 for one that is
+// not finite, which is latched: what it reaches is not finite whatever the scale).  e brings the row's
 // largest magnitude to [1, 2), so its norm is below 2 sqrt(d).  A zero row takes e = 127
 // (it must not lower the least exponent of a tile); a row that is not finite takes e = 0,
 // and its gradients come out not finite.  16,384 tokens of 16 heads, d 128: 37 us,
@@ -664,7 +693,7 @@ __global__ void __launch_bounds__(256, 3)
                             const uint16_t* dout, const float* lse,
                             const int* head, int64_t T, int H, int Hkv,
                             uint16_t* dos, float2* stats,
-                            float* rowexp, float* winexp,
+                            float* rowexp, float* winexp, float* rownorm, float* winnorm,
                             uint32_t* taken, int* dev_err) {
   constexpr int LR = D / 8, RW = 32 / LR, IT = kWindow / 8 / RW;  // lanes a row, rows a warp, rounds
   __shared__ float low[8];
@@ -676,7 +705,8 @@ __global__ void __launch_bounds__(256, 3)
   if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *taken = 0;
   const int64_t t0 = (int64_t)blockIdx.x * kWindow + warp * (kWindow / 8) + lane / LR;
   if (h >= H) {
-    bool big = false;
+    bool bad = false;
+    float most = 0.f;
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
       const int64_t t = t0 + i * RW;
@@ -693,9 +723,21 @@ __global__ void __launch_bounds__(256, 3)
       }
 #pragma unroll
       for (int k = LR / 2; k > 0; k >>= 1) n += __shfl_xor_sync(0xFFFFFFFFu, n, k);
-      big |= !(n <= kMaxNormV * kMaxNormV);
+      if (!(n < INFINITY)) {
+        bad = true;
+        n = 0.f;
+      }
+      most = fmaxf(most, n);
+      if (t < T && lane % LR == 0) rownorm[(int64_t)(h - H) * T + t] = n;
     }
-    if (big) atomicOr(dev_err, DEV_ERR_NONFINITE);
+    if (bad) atomicOr(dev_err, DEV_ERR_NONFINITE);
+    most = warp_most(most);
+    if (lane == 0) low[warp] = most;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      for (int i = 1; i < 8; ++i) most = fmaxf(most, low[i]);
+      winnorm[(int64_t)(h - H) * gridDim.x + blockIdx.x] = most;
+    }
     return;
   }
   uint4 gr[IT], orow[IT];
@@ -803,11 +845,13 @@ __device__ __forceinline__ void load_share(uint32_t t, uint32_t (&lo)[D / 4], ui
 // those heads the chunks of 64 queries that see some of the keys go by; chunk c is the
 // gradient warps' set c % 2, so that one set's arithmetic runs while the products of the
 // other's chunk do:
-//   warp 9 : S^T = K Q^T, dP'^T = V dO'^T          (buffers c % 2, 64 columns each)
-//   sets   : P' = exp2(S^T c - l + emin) -> TMEM;  dS' = P' (dP' - delta') -> TMEM
-//   warp 10: dV' += P' dO', dK' += dS' Q           (in order, so the sums are fixed)
-// emin is the least exponent of the item's queries: P' = 2^(emin - e) P <= 1, so all
-// products carry the same factor 2^emin, taken out at the end.  With all heads of the
+//   warp 17: S^T = K Q^T, dP'^T = V dO'^T          (buffers c % 2, 64 columns each)
+//   sets   : P' = 2^u exp2(S^T c - l + emin) -> TMEM;  dS' = P' (dP' - delta') 2^(a - u) -> TMEM
+//   warp 18: dV' += P' dO', dK' += dS' Q           (in order, so the sums are fixed)
+// emin is the least exponent of the item's queries: 2^(emin - e) P <= 1, so all products
+// carry the same factor 2^emin, taken out at the end with 2^u and 2^a.  Those bring P' and
+// dS' to 2^15 at most (ds_exponent), so that a P or dS of 2^-29 of the largest possible is
+// still a normal fp16 number and one of 2^-39 not yet 0.  With all heads of the
 // group in one item (nh = G) the sums are the gradients, written in bf16; otherwise
 // fp32 parts are left for packed_attn_sum_kernel.
 // Tensor bound: 1280 cycles of products a chunk, which takes about 1760 (the chain from a
@@ -833,7 +877,7 @@ struct ItemRing {
 struct BwdArgs {
   PackedIndex idx;
   const float2* stats;
-  const float *rowexp, *winexp;
+  const float *rowexp, *winexp, *rownorm, *winnorm;
   int64_t T;
   int H, Hkv, nh;
   float sl2, scale;
@@ -854,6 +898,7 @@ __device__ __forceinline__ uint32_t dkdv_part(const BwdArgs& a_, const CUtensorM
   const PackedIndex& idx = a_.idx;
   const float2* stats = a_.stats;
   const float *rowexp = a_.rowexp, *winexp = a_.winexp;
+  const float *rownorm = a_.rownorm, *winnorm = a_.winnorm;
   const int64_t T = a_.T;
   const int H = a_.H, Hkv = a_.Hkv, nh = a_.nh;
   const float sl2 = a_.sl2, scale = a_.scale;
@@ -864,13 +909,13 @@ __device__ __forceinline__ uint32_t dkdv_part(const BwdArgs& a_, const CUtensorM
   using SM = DkvSmem<D>;
   constexpr int DA = D / 64, NR = SM::kRing, kItems = 8;
   static_assert(NR % 2 == 0, "a ring slot always serves the same set of warps");
-  static_assert(kItems > NR + 1, "an item's least exponent is kept until all have read it");
+  static_assert(kItems > NR + 1, "an item's factors are kept until all have read them");
   static_assert(NR >= 3, "the chunk that an item is drawn behind has not left its slot");
   __shared__ __align__(8) uint64_t kv_full, kv_free, r_full[NR], r_free[NR], st_full[NR];
   __shared__ __align__(8) uint64_t s_full[2], dp_full[2], p_full[2], ds_full[2], s_free[2], dp_free[2];
   __shared__ __align__(8) uint64_t acc_full, acc_free;
   __shared__ __align__(8) ItemRing ring;
-  __shared__ float emin_sh[kItems];
+  __shared__ float factor_sh[kItems][3];  // 2^(a - u); of dV 2^(-emin - u); of dK
   __shared__ uint32_t next_sh;
   volatile int* abort_flag = abort_sh;
 
@@ -878,7 +923,8 @@ __device__ __forceinline__ uint32_t dkdv_part(const BwdArgs& a_, const CUtensorM
   uint8_t* Vs = Ks + SM::kTile;
   uint8_t* Qb = Vs + SM::kTile;             // [NR] chunks of Q
   uint8_t* dOb = Qb + NR * SM::kQc;         // [NR] chunks of dO'
-  float* st = reinterpret_cast<float*>(dOb + NR * SM::kQc);  // [NR] 64 x (emin - l), 64 x -delta'
+  // [NR] 64 x (emin + u - l), 64 x -delta' 2^(a - u)
+  float* st = reinterpret_cast<float*>(dOb + NR * SM::kQc);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr uint32_t kColS = 0, kColP = 2 * kBC, kColV = 4 * kBC, kColK = 4 * kBC + 128;
 
@@ -1076,6 +1122,8 @@ __device__ __forceinline__ uint32_t dkdv_part(const BwdArgs& a_, const CUtensorM
       const Item it = item(w);
       // the least exponent: whole windows by their minima, the edges token by token (a
       // window that reaches into another document must not count)
+      const float nv = largest_norm(winnorm + it.g * nw, rownorm + it.g * T, it.t.begin, it.t.end,
+                                    lane);
       float emin = 127.f;
       const int w0 = (it.qs + kWindow - 1) / kWindow, w1 = it.t.end / kWindow;
       const int e0 = w0 < w1 ? w0 * kWindow : it.t.end;  // [qs, e0) and [w1 .., end)
@@ -1095,7 +1143,14 @@ __device__ __forceinline__ uint32_t dkdv_part(const BwdArgs& a_, const CUtensorM
         for (int i = q + 64; i < e0; i += 32) emin = fminf(emin, re[i]);
       }
       emin = warp_min(emin);
-      if (lane == 0) emin_sh[ni % kItems] = emin;
+      const int e_min = (int)emin, u = min(kUp, 126 - e_min);
+      const int a = ds_exponent(warp_most(nv), D, e_min);
+      const float mul = pow2i(a - u), lift = emin + (float)u;
+      if (lane == 0) {
+        factor_sh[ni % kItems][0] = mul;
+        factor_sh[ni % kItems][1] = ex2(-lift);
+        factor_sh[ni % kItems][2] = ex2(-(float)(e_min + a)) * scale;
+      }
       for (int hh = 0; hh < nh && ok; ++hh) {
         const float2* sh = stats + (int64_t)(it.h0 + hh) * T;
         for (int j = 0; j < it.nc; ++j, ++c) {
@@ -1106,14 +1161,14 @@ __device__ __forceinline__ uint32_t dkdv_part(const BwdArgs& a_, const CUtensorM
           for (int i = 0; i < 2; ++i) {
             const int q = q0 + lane + 32 * i;
             v[i] = q < it.t.end ? sh[q] : make_float2(INFINITY, 0.f);
-            v[i].x = emin - v[i].x;
+            v[i].x = lift - v[i].x;
           }
           ok = wait_all(&r_full[slot], c / NR);
           if (!ok) break;
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             st[slot * 2 * kBC + lane + 32 * i] = v[i].x;
-            st[slot * 2 * kBC + kBC + lane + 32 * i] = -v[i].y;
+            st[slot * 2 * kBC + kBC + lane + 32 * i] = -v[i].y * mul;
           }
           if (q0 + kBC > it.t.end) {
             // queries behind the document: their P and dS are 0, and so must the rows be
@@ -1154,7 +1209,7 @@ __device__ __forceinline__ uint32_t dkdv_part(const BwdArgs& a_, const CUtensorM
         ++jc;
         if ((c & 1) != b) continue;
         const uint32_t slot = c % NR, ph = c / 2;
-        // pairs of (emin - l), and of -delta'
+        // pairs of (emin + u - l), and of -delta' 2^(a - u)
         const ulonglong2* l2 = reinterpret_cast<const ulonglong2*>(st + slot * 2 * kBC + hf * kBH);
         const ulonglong2* dl = l2 + kBC / 4;
         ok = wait_all(&s_full[b], ph);  // (and st: S^T is issued behind it)
@@ -1200,6 +1255,8 @@ __device__ __forceinline__ uint32_t dkdv_part(const BwdArgs& a_, const CUtensorM
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&p_full[b]));
+        const float mul = factor_sh[ni % kItems][0];
+        const uint64_t mul2 = pack_f32x2(mul, mul);
         tmem_ld_wait();
 #pragma unroll
         for (int e = 0; e < kBH / 2; e += 2) {
@@ -1208,7 +1265,7 @@ __device__ __forceinline__ uint32_t dkdv_part(const BwdArgs& a_, const CUtensorM
           for (int i = 0; i < 2; ++i) {
             const uint64_t d = pack_f32x2(__uint_as_float(sv[2 * (e + i)]),
                                           __uint_as_float(sv[2 * (e + i) + 1]));
-            float2 x = unpack_f32x2(mul_f32x2(p[e + i], add_f32x2(d, i ? v.y : v.x)));
+            float2 x = unpack_f32x2(mul_f32x2(p[e + i], fma_f32x2(d, mul2, i ? v.y : v.x)));
             if (!whole) {  // (dp behind the document may be anything)
               const float2 q = unpack_f32x2(p[e + i]);
               x.x = q.x != 0.f ? x.x : 0.f;
@@ -1230,7 +1287,7 @@ __device__ __forceinline__ uint32_t dkdv_part(const BwdArgs& a_, const CUtensorM
       tc_fence_after();
       uint32_t lo[D / 4], hi[D / 4];
       load_share<D>(trow + (b ? kColK : kColV) + hf * (D / 4), lo, hi);
-      const float f = ex2(-emin_sh[ni % kItems]) * (b ? scale : 1.f);
+      const float f = factor_sh[ni % kItems][b ? 2 : 1];
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&acc_free));
@@ -1317,8 +1374,9 @@ __global__ void __launch_bounds__(256)
 
 // ------------------------------------------------------------------ dQ
 // Items and streams as in the forward; a stream's chunk of 64 keys:
-//   its MMA warp: S = Q K^T, dP' = dO' V^T;  its gradient warps: P = exp2(S c - lse log2 e),
-//   dS' = P (dP' - delta') as fp16 over dP' in TMEM;  the MMA warp: dQ' += dS' K.
+//   its MMA warp: S = Q K^T, dP' = dO' V^T;  its gradient warps: P' = 2^a exp2(S c - lse
+//   log2 e), dS' = P' (dP' - delta') as fp16 over dP' in TMEM, a of each query (ds_exponent) by the
+//   norms of v among the item's keys;  the MMA warp: dQ' += dS' K.
 // S of the next chunk is computed while dS of this one is formed.
 template <int D>
 struct DqSmem {
@@ -1338,8 +1396,8 @@ __device__ __forceinline__ void dq_part(const BwdArgs& a_, const CUtensorMap& tm
                                         bool many, uint32_t w0, int* abort_sh) {
   const PackedIndex& idx = a_.idx;
   const float2* stats = a_.stats;
-  const float* rowexp = a_.rowexp;
-  const int64_t T = a_.T;
+  const float *rowexp = a_.rowexp, *rownorm = a_.rownorm, *winnorm = a_.winnorm;
+  const int64_t T = a_.T, nw = (T + kWindow - 1) / kWindow;
   const int H = a_.H, Hkv = a_.Hkv;
   const float sl2 = a_.sl2, scale = a_.scale;
   const float2* cs = a_.cs;
@@ -1564,7 +1622,12 @@ __device__ __forceinline__ void dq_part(const BwdArgs& a_, const CUtensorMap& tm
       const int64_t at = (int64_t)it.head * T + min(q, it.end - 1);
       const float2 sq = stats[at];
       const float e = rowexp[at];
-      const uint64_t nl2 = pack_f32x2(e - sq.x, e - sq.x), ndl = pack_f32x2(-sq.y, -sq.y);
+      const int g = it.head / G;
+      const float nv = largest_norm(winnorm + g * nw, rownorm + g * T, it.begin,
+                                    min(it.end, it.begin + n * kBC), lane);
+      const int a = ds_exponent(warp_most(nv), D, (int)e);
+      const float nl = e - sq.x + (float)a;  // (P is not stored here: it takes the factor)
+      const uint64_t nl2 = pack_f32x2(nl, nl), ndl = pack_f32x2(-sq.y, -sq.y);
       for (int j = 0; j < n; ++j, ++nc) {
         ok = wait_all(&s_full[s], nc);
         if (!ok) break;
@@ -1618,7 +1681,7 @@ __device__ __forceinline__ void dq_part(const BwdArgs& a_, const CUtensorMap& tm
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&dq_free[s]));
       if (q < it.end)
-        store_grad_share<D>(lo, hi, scale * ex2(-e),
+        store_grad_share<D>(lo, hi, scale * ex2(-e - (float)a),
                             cs ? cs + (int64_t)idx.pos[q] * (D / 2) + hf * (D / 4) : nullptr,
                             dqkv + (int64_t)q * (H + 2 * Hkv) * D + (int64_t)it.head * D +
                                 hf * (D / 4));
@@ -1734,6 +1797,8 @@ struct BwdWs {
   float2* stats;   // [H, T] (lse log2 e + e, delta')
   float* rowexp;   // [H, T] e
   float* winexp;   // [H, windows] the least e of 64 tokens
+  float* rownorm;  // [Hkv, T] |v|^2
+  float* winnorm;  // [Hkv, windows] the largest |v|^2 of 64 tokens
   uint32_t* taken; // items handed out behind each CTA's first
   float *dk, *dv;  // [Hkv parts, d / 8, T, 8] fp32
 };
@@ -1768,6 +1833,8 @@ size_t carve_bwd(int64_t T, int H, int Hkv, int d, void* base, BwdWs* w) {
   x.stats = a.take<float2>((size_t)T * H);
   x.rowexp = a.take<float>((size_t)T * H);
   x.winexp = a.take<float>((size_t)((T + kWindow - 1) / kWindow) * H);
+  x.rownorm = a.take<float>((size_t)T * Hkv);
+  x.winnorm = a.take<float>((size_t)((T + kWindow - 1) / kWindow) * Hkv);
   x.taken = a.take<uint32_t>(1);
   const size_t n = parts > 1 ? (size_t)T * Hkv * parts * d : 0;
   x.dk = a.take<float>(n);
@@ -1790,7 +1857,7 @@ int bwd_t(const uint16_t* qkv, const PackedIndex& x, const uint16_t* o, const fl
   const unsigned windows = (unsigned)((T + kWindow - 1) / kWindow);
   LSQ_CUDA(launch_dep(packed_attn_prep_kernel<D>, dim3(windows, (unsigned)(H + Hkv)), 256, 0, st,
                       qkv, o, dout, lse, x.head, T, H, Hkv, w.dos, w.stats, w.rowexp, w.winexp,
-                      w.taken, err));
+                      w.rownorm, w.winnorm, w.taken, err));
   const int64_t row = (int64_t)(H + 2 * Hkv) * D, hd = (int64_t)H * D;
   CUtensorMap qkv128, qkv64, do128, do64;
   LSQ_TRY(make_tmap_2d(&qkv128, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, qkv, (uint64_t)row, (uint64_t)T,
@@ -1805,7 +1872,7 @@ int bwd_t(const uint16_t* qkv, const PackedIndex& x, const uint16_t* o, const fl
   // (at most: the documents' tiles are known on the device)
   const int64_t kitems = (int64_t)x.cap * Hkv * parts;
   const int64_t qitems = (H / Hkv) % 2 == 0 ? (int64_t)x.cap * (H / 2) : (int64_t)x.cap2 * H;
-  const BwdArgs args{x, w.stats, w.rowexp, w.winexp, T, H, Hkv, H / Hkv / parts, sl2, scale, cs,
+  const BwdArgs args{x, w.stats, w.rowexp, w.winexp, w.rownorm, w.winnorm, T, H, Hkv, H / Hkv / parts, sl2, scale, cs,
                      dqkv, w.dk, w.dv, w.taken, err};
   LSQ_CUDA(launch_dep(packed_attn_bwd_kernel<D>, dim3((unsigned)std::min<int64_t>(kitems + qitems, sms)),
                       kBThreads, smem, st, qkv128, qkv64, do128, do64, args));

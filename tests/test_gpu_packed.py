@@ -271,6 +271,68 @@ def test_nothing_crosses_a_document(L, H, Hkv, d):
         assert torch.equal(dqkv[keep], clean[2][keep])
 
 
+@pytest.mark.parametrize("H,Hkv,d", [(2, 1, 64), (1, 1, 128), (4, 1, 128)])
+@pytest.mark.parametrize("vstd,outlier", [(1.0, 1), (0.03, 256), (0.003, 1), (0.0003, 1),
+                                          (1.0, 4096), (1e-6, 64), (300.0, 1)])
+def test_gradients_of_a_long_diffuse_document(L, H, Hkv, d, vstd, outlier):
+    """Thousands of small probabilities, small or large v, one query whose gradient is far
+    above the others': no row of dq, dk and dv may lose its small parts in fp16.  Of each
+    row's norm: the result's rounding to bf16 (2^-8), and those of P, dS and dO's products to
+    fp16, 2^-11 each, of terms that add up as the terms themselves do.  delta takes o rounded
+    to fp16, off by 2^-11 |dO| |o| or 2^-25 |dO| at most, whatever is left of dP - delta."""
+    import torch
+    lengths, T = [700, 4096, 100], 4900
+    g = torch.Generator().manual_seed(int(1e6 * vstd) + outlier)
+    qkv = torch.randn(T, H + 2 * Hkv, d, generator=g)
+    qkv[:, :H + Hkv] *= 0.3
+    qkv[:, H + Hkv:] *= vstd
+    dout = torch.randn(T, H, d, generator=g) * 1e-5
+    dout[2900] *= outlier              # in the middle of the long document
+    qkv, dout = qkv.reshape(T, -1).half().cuda(), dout.reshape(T, -1).bfloat16().cuda()
+    o, lse, dqkv = _run(L, qkv, dout, _index(L, lengths, None, T), H, Hkv)
+    got = dqkv.double().view(T, H + 2 * Hkv, d)
+    x, do = qkv.double().view(T, H + 2 * Hkv, d), dout.double().view(T, H, d)
+    tol, h11 = 2.0 ** -8 + 3 * 2.0 ** -11, 2.0 ** -11 + F32
+    for s, e, _ in op.documents(lengths):
+        dk, dv = (torch.zeros(e - s, Hkv, d, dtype=torch.float64, device="cuda") for _ in "kv")
+        low_k = torch.zeros(e - s, Hkv, dtype=torch.float64, device="cuda")
+        for h in range(H):
+            n = h // (H // Hkv)
+            q, k, v = x[s:e, h], x[s:e, H + n], x[s:e, H + Hkv + n]
+            p = torch.softmax((q @ k.T / d ** 0.5).masked_fill(
+                torch.ones(e - s, e - s, dtype=torch.bool, device="cuda").triu(1), -float("inf")), 1)
+            ro = p @ v
+            ds = p * (do[s:e, h] @ v.T - (do[s:e, h] * ro).sum(1)[:, None]) / d ** 0.5
+            dq = ds @ k
+            off = p * ((do[s:e, h].abs() * (h11 * ro.abs() + 2.0 ** -25)).sum(1) / d ** 0.5)[:, None]
+            err = (got[s:e, h] - dq).norm(dim=1)
+            assert (err <= tol * dq.norm(dim=1) + off @ k.norm(dim=1)).all(), ("dq", h, s)
+            dk[:, n] += ds.T @ q
+            dv[:, n] += p.T @ do[s:e, h]
+            low_k[:, n] += off.T @ q.norm(dim=1)
+        err = (got[s:e, H:H + Hkv] - dk).norm(dim=2)
+        assert (err <= tol * dk.norm(dim=2) + low_k).all(), ("dk", s)
+        err = (got[s:e, H + Hkv:] - dv).norm(dim=2)
+        assert (err <= tol * dv.norm(dim=2)).all(), ("dv", s)
+
+
+def test_large_values_keep_finite_gradients(L):
+    """Rows of v up to fp16's largest numbers: the score gradients are scaled before they are
+    rounded, and nothing is latched."""
+    import torch
+    H, Hkv, d, T, lengths = 4, 2, 64, 300, [200, 90]
+    qkv, dout = _inputs(T, H, Hkv, d, 6)
+    qkv[:, (H + Hkv) * d:] = (qkv[:, (H + Hkv) * d:].float() * 12000).clamp(-65504, 65504).half()
+    _, _, dqkv = _run(L, qkv.cuda(), dout.cuda(), _index(L, lengths, None, T), H, Hkv)
+    want = op.attention_bwd(qkv.float().numpy(), H, Hkv, op.documents(lengths), dout.float().numpy())
+    got = dqkv.float().cpu().numpy()
+    assert np.isfinite(got).all()
+    for lo, hi in ((0, H * d), (H * d, (H + Hkv) * d), ((H + Hkv) * d, None)):
+        a, b = got[:, lo:hi], want[:, lo:hi]
+        # the worst row's roundings of 300 terms of one sign, 2^-11 each, then bf16's
+        assert np.abs(a - b).max() <= 2.0 ** -7 * np.abs(b).max()
+
+
 def test_attention_is_deterministic_on_any_stream_and_in_a_graph(L):
     import torch
     H, Hkv, d, T, lengths = 8, 2, 64, 500, [300, 190]
