@@ -107,8 +107,9 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 // roots need.  y is 127 sqrt(x / a), off by at most 127 (3/2 2^-23) and a rounding, less
 // than 4e-5, or 255 (x / a)^(1/4), off by at most 255 (2.2 2^-23) and a rounding, less
 // than 9e-5.  Where y lies within kNear of a border, the code is taken from the exact
-// comparison: x 254^2 against a (2 b + 1)^2 (both exact in fp64), x 510^4 against
-// a (2 b + 1)^4; a tie goes to the even code.
+// comparison: x 254^2 against a (2 b + 1)^2 (both exact in fp64, 40 bits), x 510^4 against
+// a (2 b + 1)^4 (up to 60 bits: where the rounded products are equal, by what their rounding
+// left, which one fused operation gives exactly); a tie goes to the even code.
 constexpr float kRound = 12582912.f;
 constexpr float kNear = 2e-4f;
 __device__ __forceinline__ int exact_m(float x, float a, float y) {
@@ -121,9 +122,11 @@ __device__ __forceinline__ int exact_v(float x, float a, float y) {
   const int b = (int)floorf(y);
   int k = (int)rintf(y);
   if (fabsf(y - (float)b - 0.5f) <= kNear) {
-    const double o = (double)((2 * b + 1) * (2 * b + 1));
-    const double l = (double)x * 67652010000.0, r = (double)a * (o * o);
-    k = l > r ? b + 1 : l < r ? b : b + (b & 1);
+    const double o = (double)((2 * b + 1) * (2 * b + 1)), xd = (double)x, ad = (double)a;
+    constexpr double kTop = 67652010000.0;  // 510^4
+    const double l = xd * kTop, r = ad * (o * o);
+    const double le = fma(xd, kTop, -l), re = fma(ad, o * o, -r);
+    k = l > r || (l == r && le > re) ? b + 1 : l < r || le < re ? b : b + (b & 1);
   }
   return x > 0.f ? max(k, 1) : k;
 }

@@ -114,21 +114,34 @@ def decode(codes, scale):
     return a * level.astype(np.float32)
 
 
+def _above(v, a, c, top, power):
+    """Is v / a above, at or below the border ((2 c + 1) / (2 top))^power?  1, 0 or -1, in
+    whole numbers: an fp32 number is a whole number of 2^-149."""
+    l = int(v * 2.0 ** 149) * (2 * top) ** power
+    r = int(a * 2.0 ** 149) * (2 * c + 1) ** power
+    return (l > r) - (l < r)
+
+
 def encode(x, signed):
-    """fp32 values to (codes, scale): the nearest root, by trying every level's border."""
+    """fp32 values to (codes, scale): the nearest root (a tie: the even one).  Next to a border
+    between two codes the choice is made in whole numbers."""
     x = np.asarray(x, np.float32)
     n = len(x)
     scale = np.zeros((n + BLOCK - 1) // BLOCK, np.float32)
     codes = np.zeros(n, np.int8 if signed else np.uint8)
-    top = 127 if signed else 255
+    top, power = (127, 2) if signed else (255, 4)
     for b in range(len(scale)):
         v = x[b * BLOCK:(b + 1) * BLOCK].astype(np.float64)
         a = np.abs(v).max()
         if a < TINY:
             continue
         scale[b] = a
-        r = top * (np.abs(v) / a) ** (0.5 if signed else 0.25)
+        r = top * (np.abs(v) / a) ** (1.0 / power)
         c = np.minimum(np.rint(r), top)
+        low = np.floor(r)
+        for i in np.nonzero(np.abs(r - low - 0.5) < 1e-9)[0]:
+            k = int(low[i])
+            c[i] = k + (1, k & 1, 0)[1 - _above(abs(v[i]), a, k, top, power)]
         if signed:
             c = np.sign(v) * c
         else:

@@ -297,3 +297,40 @@ def test_every_code_and_its_borders(L):
             s = torch.empty(len(scale), device="cuda")
             L.adamw_state_quantize(torch.from_numpy(x).cuda(), c, s)
             assert np.array_equal(c.cpu().numpy(), codes)
+
+
+def test_borders_closer_than_fp64_products_tell(L):
+    """x 510^4 and a (2 b + 1)^4 have up to 60 bits: where their fp64 products are equal, the
+    code is still that of the exact comparison.  In the update, and in the conversion."""
+    import torch
+    pairs = np.array([[10322846, 665658.125], [8629209, 3499999], [15995371, 7.3828125],
+                      [16777215, 16646655]], np.float32)
+    # 665658.125 510^4 - 10322846 257^4 = 4, 3499999 510^4 - 8629209 407^4 = -72
+    want = [129, 203]
+    x = np.zeros((len(pairs), 256), np.float32)
+    x[:, 0], x[:, 1:3] = pairs[:, 0], pairs[:, 1:]
+    # a few fp32 steps to both sides of every border, for scales of 24 bits
+    rng = np.random.default_rng(0)
+    a = (rng.integers(1 << 23, 1 << 24, 300) * 2.0 ** rng.integers(-60, 60, 300)).astype(np.float32)
+    near = a[:, None].astype(np.float64) * ((2 * np.arange(255) + 1) / 510.0) ** 4
+    for step in (-1, 0, 1):
+        e = near.astype(np.float32)
+        e = e if step == 0 else np.nextafter(e, np.float32(0 if step < 0 else np.inf))
+        x = np.concatenate([x, np.concatenate([a[:, None], e], 1)])
+    x = x.reshape(-1)
+    codes, scale = op.encode(x, False)
+    assert [codes[256 * i + 1] for i in (0, 1)] == want
+    c = torch.empty(len(x), dtype=torch.uint8, device="cuda")
+    s = torch.empty(len(scale), device="cuda")
+    L.adamw_state_quantize(torch.from_numpy(x).cuda(), c, s)
+    assert np.array_equal(c.cpu().numpy(), codes) and np.array_equal(s.cpu().numpy(), scale)
+    # the update: v = (g - 0 g) g with beta2 = 0 and a zero state is g^2, rounded once
+    g = np.sqrt(x.astype(np.float64)).astype(np.float32)
+    d = dict(p=[torch.zeros(len(x), device="cuda")], g=[torch.from_numpy(g).cuda()],
+             m=[torch.zeros(len(x), dtype=torch.int8, device="cuda")], v=[c.zero_()],
+             ms=[torch.zeros(len(scale), device="cuda")], vs=[s.zero_()])
+    L.AdamWMulti(d["p"], d["g"], d["m"], d["v"], lr=0.0, m_scale=d["ms"], v_scale=d["vs"],
+                 betas=(0.0, 0.0)).step(1)
+    codes, scale = op.encode(g * g, False)
+    assert np.array_equal(c.cpu().numpy(), codes) and np.array_equal(s.cpu().numpy(), scale)
+    assert L.lsq_device_status(clear=True) == 0

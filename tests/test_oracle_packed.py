@@ -103,3 +103,15 @@ def test_adamw_matches_torch():
         p, m, v = op.adamw(p, g, m, v, step, 1e-2, 0.1)
     # the fp32 moments and betas: a few 2^-24 of updates of size lr
     assert np.abs(p - t.detach().numpy()).max() < 4 * 1e-2 * 2.0 ** -20
+
+
+@pytest.mark.parametrize("a,v,code", [(10322846.0, 665658.125, 129),   # 128.5 and 203.5 are the
+                                      (8629209.0, 3499999.0, 203)])    # borders next to them
+def test_a_code_next_to_a_border_is_chosen_in_whole_numbers(a, v, code):
+    """The products that are compared differ by less than a step of fp64."""
+    border = int(np.rint(255 * (v / a) ** 0.25 - 0.5))
+    diff = int(8 * v) * 510 ** 4 - int(8 * a) * (2 * border + 1) ** 4
+    assert abs(diff) < 1000 and code == border + (diff > 0)
+    x = np.zeros(256, np.float32)
+    x[:2] = a, v
+    assert op.encode(x, False)[0][1] == code
