@@ -610,8 +610,9 @@ int decoder_layer_packed_bwd(const lsq_cfg* cfg, const void* blob, const float* 
  *              aligned.
  * Streaming, graphs, data parallelism, the synchronous return and the other arguments
  * are those of stream_stack_step (averaged gradients are the mean over the ranks of each
- * rank's mean, whatever its number of targets); a latched status bit (a length outside its range
- * among them) is returned as LSQ_ERR_DEVICE.  Added in ABI 2.2. */
+ * rank's mean, whatever its number of targets); a latched status bit is returned as
+ * LSQ_ERR_DEVICE.  With LSQ_DEV_ERR_INDEX (a length, a prompt or a target outside its range)
+ * parameters and state are left as they were.  Added in ABI 2.2. */
 size_t stream_stack_packed_workspace_bytes(const lsq_cfg* cfg, int32_t n_tokens, int32_t n_docs);
 int stream_stack_packed_step(lsq_stack* stack, const int32_t* tokens, int32_t micro_batches,
                              int32_t n_tokens, const int32_t* lengths, const int32_t* prefix,

@@ -47,6 +47,7 @@ struct MtHead {
   int n;                  // tensors in this launch
   uint32_t chunks;        // chunks in this launch
   const int32_t* step;    // device step count, or null
+  const int* gate;        // status word that keeps all as it is with a bad index, or null
   int* dev_err;
 };
 
@@ -387,6 +388,7 @@ __global__ void __launch_bounds__(kMtThreads, 4)
     adamw_multi_kernel(const __grid_constant__ MtArgs<N> a) {
   __shared__ float lm[BITS == 8 ? 256 : 1], lv[BITS == 8 ? 256 : 1];
   __shared__ float bc[2];
+  __shared__ int off;
   pdl_trigger();
   if (BITS == 8) {
     lm[threadIdx.x] = level_m((int)(int8_t)threadIdx.x);  // by the code's byte
@@ -402,8 +404,10 @@ __global__ void __launch_bounds__(kMtThreads, 4)
     }
     bc[0] = i1;
     bc[1] = i2;
+    off = a.h.gate ? *a.h.gate & DEV_ERR_INDEX : 0;
   }
   __syncthreads();
+  if (off) return;
   const MtRates r{bc[0], bc[1]};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (uint32_t c = blockIdx.x; c < a.h.chunks; c += gridDim.x) {
@@ -594,7 +598,7 @@ int check_tensors(const lsq_adamw_tensor* t, int n, int bits) {
 }  // namespace
 
 int launch_adamw_multi(const lsq_adamw_tensor* t, int n, const lsq_adamw_hyper* o,
-                       cudaStream_t st) {
+                       cudaStream_t st, const int* gate) {
   MtHead h = {};
   h.b1 = o->beta1;
   h.b2 = o->beta2;
@@ -602,6 +606,7 @@ int launch_adamw_multi(const lsq_adamw_tensor* t, int n, const lsq_adamw_hyper* 
   h.c2 = (float)(1.0 - (double)o->beta2);
   h.eps = o->eps;
   h.step = o->step_dev;
+  h.gate = gate;
   if (!o->step_dev) {
     h.inv_bc1 = (float)(1.0 / (1.0 - pow((double)o->beta1, (double)o->step)));
     h.inv_sqrt_bc2 = (float)(1.0 / sqrt(1.0 - pow((double)o->beta2, (double)o->step)));

@@ -299,8 +299,9 @@ int launch_packed_attention_bwd(const uint16_t* qkv, const int32_t* index, int n
                                 int64_t T, int H, int Hkv, int d, const float2* cs, uint16_t* dqkv,
                                 void* ws, size_t ws_bytes, cudaStream_t st);
 int check_adamw_multi(const lsq_adamw_tensor* tensors, int n_tensors, const lsq_adamw_hyper* opt);
+// gate (nullable): a status word; with DEV_ERR_INDEX in it nothing is updated
 int launch_adamw_multi(const lsq_adamw_tensor* t, int n, const lsq_adamw_hyper* o,
-                       cudaStream_t st);
+                       cudaStream_t st, const int* gate = nullptr);
 
 // ---------------------------------------------------------------- layer internals
 struct LayerShapes {

@@ -875,7 +875,8 @@ int step_impl(lsq_stack* h, const int32_t* tokens, int32_t micro_batches, int32_
     LSQ_TRY(launch_adamw(lora, lora_grad, opt->m, opt->v, layer_floats * L, opt->lr, opt->beta1,
                          opt->beta2, opt->eps, opt->weight_decay, opt->step, cs));
   if (pk && pk->hyper)
-    LSQ_TRY(launch_adamw_multi(pk->tensors, pk->n_tensors, pk->hyper, cs));
+    // (not behind documents that were cut or a target that was left out: the step is refused)
+    LSQ_TRY(launch_adamw_multi(pk->tensors, pk->n_tensors, pk->hyper, cs, device_status_ptr()));
   LSQ_CUDA(cudaMemcpyAsync(h->loss_host, w.loss_dev, sizeof(float), cudaMemcpyDeviceToHost, cs));
   if (dpo)
     LSQ_CUDA(cudaMemcpyAsync(h->loss_host + 1, w.logps, 4 * dpo->pairs * sizeof(float),

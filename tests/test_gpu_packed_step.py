@@ -232,6 +232,42 @@ def test_step_without_targets(L, small):
     assert loss == 0.0 and not grad.any()
 
 
+@pytest.mark.parametrize("what", ["length", "prompt", "token"])
+def test_a_step_with_bad_documents_updates_nothing(L, small, what):
+    """Parameters, moments and scales are bit for bit as before the refused step, and the step
+    that follows with sound documents is the one that would have been without it."""
+    import torch
+    runs = []
+    for bad_first in (False, True):
+        h = small.handle(L, resident=False)
+        lora = small.lora.clone()
+        grad = torch.full_like(lora, float("nan"))
+        opt, parts = _optimiser(L, small.cfg, lora, grad)
+        _run(L, small, h, _batch(21, True, False)[2], opt=opt, step=1, lora=lora, grad=grad)
+
+        def state():
+            return [t.clone() for k in (0, 2, 3, 4, 5) for t in parts[k]]
+        if bad_first:
+            _, _, d = _batch(22, True, False)
+            if what == "length":
+                d["lengths"][1, 1] = 60
+            elif what == "prompt":
+                d["prefix"][0, 0] = 41
+            else:
+                d["tokens"][1, 30] = small.cfg["vocab"]   # a target: this document has no prompt
+            before = state()
+            with pytest.raises(L.LsqError) as e:
+                _run(L, small, h, d, opt=opt, step=2, lora=lora, grad=grad)
+            assert e.value.code == L.LSQ_ERR_DEVICE
+            assert all(torch.equal(a, b) for a, b in zip(before, state()))
+            assert L.lsq_device_status(clear=True) == L.LSQ_DEV_ERR_INDEX
+        loss, _, _, _ = _run(L, small, h, _batch(22, True, False)[2], opt=opt, step=2, lora=lora,
+                             grad=grad)
+        runs.append([torch.tensor(loss)] + state())
+        h.close()
+    assert all(torch.equal(a, b) for a, b in zip(*runs))
+
+
 def test_step_refusals(L, small):
     import torch
     _, _, d = _batch(1, False, False)
