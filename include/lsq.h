@@ -600,7 +600,8 @@ int decoder_layer_packed_bwd(const lsq_cfg* cfg, const void* blob, const float* 
  *   lengths, prefix  device int32 [micro_batches, n_docs] (prefix may be NULL), and
  *   loss_mask  device uint8 [micro_batches, n_tokens] or NULL: as for packed_index and
  *              packed_targets.
- *   loss_out   the mean cross-entropy over all targets of the step (0 if there is none);
+ *   loss_out   the mean cross-entropy over all targets of the step (0 if there is none; over
+ *              several ranks see below);
  *              lora_grad is its gradient.
  *   tensors, n_tensors, opt  the update of adamw_multi_step behind the last backward:
  *              tensors of the caller's choice inside lora and lora_grad, each with its
@@ -609,8 +610,9 @@ int decoder_layer_packed_bwd(const lsq_cfg* cfg, const void* blob, const float* 
  *   ws         stream_stack_packed_workspace_bytes(cfg, n_tokens, n_docs), 32-byte
  *              aligned.
  * Streaming, graphs, data parallelism, the synchronous return and the other arguments
- * are those of stream_stack_step (averaged gradients are the mean over the ranks of each
- * rank's mean, whatever its number of targets); a latched status bit is returned as
+ * are those of stream_stack_step.  With stream_stack_reduce_grads the mean is over the targets
+ * of all ranks, however they are spread: lora_grad is its gradient, and the mean of the ranks'
+ * loss_out its value; a rank without targets takes part.  A latched status bit is returned as
  * LSQ_ERR_DEVICE.  With LSQ_DEV_ERR_INDEX (a length, a prompt or a target outside its range)
  * parameters and state are left as they were.  Added in ABI 2.2. */
 size_t stream_stack_packed_workspace_bytes(const lsq_cfg* cfg, int32_t n_tokens, int32_t n_docs);

@@ -279,14 +279,15 @@ int launch_packed_targets(const int32_t* tokens, const int32_t* index, int n_doc
                           const uint8_t* loss_mask, int32_t* targets, int32_t* count,
                           int accumulate, cudaStream_t st);
 // row losses and, when dlogits is given, c_t (softmax - onehot) in bf16 with
-// c_t = weight[t] / max(*count, 1) (1 for a null weight or count); rows whose target is
-// negative get zeros
+// c_t = weight[t] ranks / max(*count, 1) (1 for a null weight, or for a null count); rows whose
+// target is negative get zeros.  ranks: over which the gradients will be averaged, count the
+// number of targets of all of them
 int launch_packed_ce(const float* logits, int64_t T, int64_t V, const int32_t* targets,
                      const float* weight, const int32_t* count, uint16_t* dlogits,
-                     float* row_loss, cudaStream_t st);
+                     float* row_loss, cudaStream_t st, int ranks = 1);
 int launch_packed_loss(const float* row_loss, const int32_t* targets, int64_t T, int64_t V,
                        const float* weight, const int32_t* count, int accumulate, float* loss,
-                       cudaStream_t st);
+                       cudaStream_t st, int ranks = 1);
 // attention inside the documents of an index: as launch_attention_fwd / _bwd, with o
 // and the gradients 0 and lse -inf in the padding
 int launch_packed_attention_fwd(const uint16_t* qkv, const int32_t* index, int n_docs, int64_t T,

@@ -256,7 +256,7 @@ __device__ __forceinline__ void warp_join(float& m, float& s) {
 // behind are rank 0's and the last rank's.
 __global__ void __launch_bounds__(kCeThreads)
     packed_ce_kernel(const float* logits, const int32_t* targets,
-                     int64_t V, const float* weight, const int32_t* count,
+                     int64_t V, const float* weight, const int32_t* count, float ranks,
                      uint16_t* dlogits, float* row_loss, int C,
                      int* dev_err) {
   extern __shared__ __align__(128) float slice[];
@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(kCeThreads)
     s = pair[1];
   }
   float c = weight ? weight[row] : 1.f;
-  if (count) c /= (float)max(1, *count);
+  if (count) c = c * ranks / (float)max(1, *count);
   const float k = c / s, off = -m * kLog2e;
   auto grad = [&](float v, int64_t j) { return k * ex2(fmaf(v, kLog2e, off)) - (j == y ? c : 0.f); };
   if (dx) {
@@ -424,7 +424,7 @@ __global__ void __launch_bounds__(kCeThreads)
 __global__ void __launch_bounds__(1024, 1)
     packed_ce_long_kernel(const float* logits, const int32_t* targets,
                           int64_t V, const float* weight,
-                          const int32_t* count, uint16_t* dlogits,
+                          const int32_t* count, float ranks, uint16_t* dlogits,
                           float* row_loss, int* dev_err) {
   __shared__ float red_m[32], red_s[32];
   pdl_trigger();
@@ -454,7 +454,7 @@ __global__ void __launch_bounds__(1024, 1)
   s = red_s[tid & 31];
   warp_join(m, s);
   float c = on ? (weight ? weight[row] : 1.f) : 0.f;
-  if (count) c /= (float)max(1, *count);
+  if (count) c = c * ranks / (float)max(1, *count);
   if (dx)
     for (int64_t i = tid; i < V; i += 1024)
       dx[i] = on ? float_to_bf16_bits(c / s * ex2((x[i] - m) * kLog2e) - (i == y ? c : 0.f))
@@ -469,7 +469,7 @@ __global__ void __launch_bounds__(1024, 1)
 __global__ void __launch_bounds__(1024, 1)
     packed_loss_kernel(const float* row_loss, const int32_t* targets,
                        int64_t T, int64_t V, const float* weight,
-                       const int32_t* count, int accumulate, float* loss) {
+                       const int32_t* count, float ranks, int accumulate, float* loss) {
   __shared__ float red[32];
   pdl_trigger();
   pdl_wait();
@@ -485,7 +485,7 @@ __global__ void __launch_bounds__(1024, 1)
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
     if (threadIdx.x == 0) {
-      if (count) s /= (float)max(1, *count);
+      if (count) s = s * ranks / (float)max(1, *count);
       *loss = (accumulate ? *loss : 0.f) + s;
     }
   }
@@ -547,7 +547,7 @@ int launch_packed_targets(const int32_t* tokens, const int32_t* index, int n_doc
 
 int launch_packed_ce(const float* logits, int64_t T, int64_t V, const int32_t* targets,
                      const float* weight, const int32_t* count, uint16_t* dlogits,
-                     float* row_loss, cudaStream_t st) {
+                     float* row_loss, cudaStream_t st, int ranks) {
   int* err = device_status_ptr();
   if (!err) return set_error(LSQ_ERR_CUDA, "device status word unavailable");
   const int prof = prof_begin(st);
@@ -555,7 +555,7 @@ int launch_packed_ce(const float* logits, int64_t T, int64_t V, const int32_t* t
   const int64_t smem = ce_plan(T, V, &C);
   if (smem > kCeMaxSmem || T * C > INT32_MAX) {
     LSQ_CUDA(launch_dep(packed_ce_long_kernel, (unsigned)T, 1024, st, logits, targets, V, weight,
-                        count, dlogits, row_loss, err));
+                        count, (float)ranks, dlogits, row_loss, err));
   } else {
     static bool attr[64] = {false};
     int dev = 0;
@@ -580,7 +580,7 @@ int launch_packed_ce(const float* logits, int64_t T, int64_t V, const int32_t* t
     cfg.attrs = at;
     cfg.numAttrs = 2;
     LSQ_CUDA(::lsq::launched(cudaLaunchKernelEx(&cfg, packed_ce_kernel, logits, targets, V, weight,
-                                                count, dlogits, row_loss, C, err)));
+                                                count, (float)ranks, dlogits, row_loss, C, err)));
   }
   if (prof >= 0) prof_end(prof, st, "packed_ce", 0.0, (dlogits ? 6.0 : 4.0) * T * V);
   return LSQ_OK;
@@ -588,9 +588,9 @@ int launch_packed_ce(const float* logits, int64_t T, int64_t V, const int32_t* t
 
 int launch_packed_loss(const float* row_loss, const int32_t* targets, int64_t T, int64_t V,
                        const float* weight, const int32_t* count, int accumulate, float* loss,
-                       cudaStream_t st) {
+                       cudaStream_t st, int ranks) {
   LSQ_CUDA(launch_dep(packed_loss_kernel, 1, 1024, st, row_loss, targets, T, V, weight, count,
-                      accumulate, loss));
+                      (float)ranks, accumulate, loss));
   return LSQ_OK;
 }
 

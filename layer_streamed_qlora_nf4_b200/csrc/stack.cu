@@ -752,8 +752,11 @@ int step_impl(lsq_stack* h, const int32_t* tokens, int32_t micro_batches, int32_
   // Sharded: the step's first all-gather waits for everything the caller put on
   // the compute stream before the step (e.g. a gradient all-reduce on another
   // communicator), so that collectives of the two never run interleaved.
-  if (h->shard) LSQ_CUDA(cudaStreamWaitEvent(h->copy_stream, h->t_start, 0));
-  if (!h->resident && !visits.empty()) LSQ_TRY(enqueue_copy(0));
+  // (The sum of a packed step's targets below belongs to the other communicator too: the
+  // all-gather waits for it.)
+  const bool sum_counts = pk && h->grad_comm;
+  if (h->shard && !sum_counts) LSQ_CUDA(cudaStreamWaitEvent(h->copy_stream, h->t_start, 0));
+  if (!h->resident && !visits.empty() && !(h->shard && sum_counts)) LSQ_TRY(enqueue_copy(0));
   // the documents and targets of a packed row; the targets' number of the whole step is
   // needed before its first gradient
   auto prepare_row = [&](int mb, bool counting) -> int {
@@ -768,6 +771,24 @@ int step_impl(lsq_stack* h, const int32_t* tokens, int32_t micro_batches, int32_
   };
   if (pk)
     for (int mb = 0; mb < micro_batches; ++mb) LSQ_TRY(prepare_row(mb, true));
+  const int ranks = sum_counts ? h->grad_world : 1;
+  if (sum_counts) {
+    // the mean is over the targets of all ranks: each divides by their number and multiplies
+    // by the number of ranks, which the average of the gradients takes out again
+    const NcclFns* f = nullptr;
+    LSQ_TRY(nccl_fns(&f));
+    LSQ_CUDA(cudaEventRecord(h->red_ev, cs));
+    LSQ_CUDA(cudaStreamWaitEvent(h->red_stream, h->red_ev, 0));
+    const ncclResult_t r = f->all_reduce(w.count, w.count, 1, ncclInt32, ncclSum,
+                                         static_cast<ncclComm_t>(h->grad_comm), h->red_stream);
+    if (r != ncclSuccess) return set_error(LSQ_ERR_CUDA, "ncclAllReduce: %s", f->error_string(r));
+    LSQ_CUDA(cudaEventRecord(h->red_done, h->red_stream));
+    LSQ_CUDA(cudaStreamWaitEvent(cs, h->red_done, 0));
+    if (h->shard) {
+      LSQ_CUDA(cudaStreamWaitEvent(h->copy_stream, h->red_done, 0));
+      if (!visits.empty()) LSQ_TRY(enqueue_copy(0));
+    }
+  }
   size_t j = 0;
   for (int mb = 0; mb < micro_batches; ++mb) {
     const int32_t* tok = tokens + (int64_t)mb * T;
@@ -812,7 +833,7 @@ int step_impl(lsq_stack* h, const int32_t* tokens, int32_t micro_batches, int32_
                                    cudaMemcpyDeviceToDevice, cs));
         if (pk)
           LSQ_TRY(launch_packed_ce(w.logits, tc, V, w.targets + c0, nullptr, w.count, w.dlogits,
-                                   w.row_loss + c0, cs));
+                                   w.row_loss + c0, cs, ranks));
         else
           LSQ_TRY(launch_cross_entropy(w.logits, tok + c0, tc, seq, V, inv_count, w.dlogits,
                                        w.row_loss + c0, cs));
@@ -821,7 +842,7 @@ int step_impl(lsq_stack* h, const int32_t* tokens, int32_t micro_batches, int32_
       }
       if (pk)
         LSQ_TRY(launch_packed_loss(w.row_loss, w.targets, T, V, nullptr, w.count, mb > 0 ? 1 : 0,
-                                   w.loss_dev, cs));
+                                   w.loss_dev, cs, ranks));
       else
         LSQ_TRY(launch_sum_rows(w.row_loss, T, inv_count, mb > 0 ? 1 : 0, w.loss_dev, cs));
     } else {
