@@ -569,9 +569,10 @@ def _torch():
     return _th
 
 
-def _call(name, stream, tensors, *args):
+def _call(name, stream, tensors, *args, last=()):
     """Runs one entry point on the device that holds all the tensors (made current for
-    the call) and on its current stream, or the given one.  args: all but the stream."""
+    the call) and on its current stream, or the given one.  args: those before the stream;
+    last: those behind it."""
     th = _th or _torch()
     dev = -2
     for t in tensors:
@@ -585,10 +586,10 @@ def _call(name, stream, tensors, *args):
                 dev = d
     fn = getattr(_lib or load(), name)
     if dev == _device():
-        rc = fn(*args, _raw_stream(dev) if stream is None else stream)
+        rc = fn(*args, _raw_stream(dev) if stream is None else stream, *last)
     else:
         with th.cuda.device(dev):
-            rc = fn(*args, _raw_stream(dev) if stream is None else stream)
+            rc = fn(*args, _raw_stream(dev) if stream is None else stream, *last)
     if rc != LSQ_OK:
         _check(rc)
 
@@ -815,12 +816,28 @@ class AdamWMulti:
 
 
 # ------------------------------------------------------------ packed layers and steps
+def _need_layer(cfg, blob, loras, ws):
+    """The arguments of a packed layer that are sized by the configuration: the blob (uint8, at
+    least the layout's bytes), LoRA buffers (fp32, one layer's; None passes), the workspace."""
+    import torch
+    _need("ws", ws, torch.uint8)
+    _need("blob", blob, torch.uint8)
+    size = lsq_layer_layout_get(cfg).bytes
+    if blob.numel() < size:
+        raise ValueError("blob has %d bytes, the layer %d" % (blob.numel(), size))
+    for name, t in loras:
+        if t is not None:
+            _need(name, t, torch.float32, numel=lsq_lora_layout_get(cfg).floats_per_layer)
+
+
 def decoder_layer_packed_fwd(cfg, blob, lora, x_in, index, x_out, ws, stream=None):
-    """x_in, x_out: fp32 [n_tokens, D] of one packed row; index: its PackedIndex."""
+    """x_in, x_out: fp32 [n_tokens, D] of one packed row; index: its PackedIndex; lora: fp32 of
+    one layer, or None (adapter off); ws: uint8."""
     import torch
     T = index.n_tokens
     _need("x_in", x_in, torch.float32, (T, cfg["hidden"]))
     _need("x_out", x_out, torch.float32, (T, cfg["hidden"]))
+    _need_layer(cfg, blob, (("lora", lora),), ws)
     c = cfg_struct(cfg)
     _call("decoder_layer_packed_fwd", stream, (blob, lora, x_in, index.buf, x_out, ws),
           ctypes.byref(c), blob.data_ptr(), _addr(lora), x_in.data_ptr(), index.buf.data_ptr(),
@@ -833,6 +850,9 @@ def decoder_layer_packed_bwd(cfg, blob, lora, x_in, dx_out, index, dx_in, lora_g
     T = index.n_tokens
     for name, t in (("x_in", x_in), ("dx_out", dx_out), ("dx_in", dx_in)):
         _need(name, t, torch.float32, (T, cfg["hidden"]))
+    if lora is None or lora_grad is None:
+        raise TypeError("the backward needs lora and lora_grad")
+    _need_layer(cfg, blob, (("lora", lora), ("lora_grad", lora_grad)), ws)
     c = cfg_struct(cfg)
     _call("decoder_layer_packed_bwd", stream, (blob, lora, x_in, dx_out, index.buf, dx_in,
                                                lora_grad, ws),
@@ -850,9 +870,10 @@ def stream_stack_packed_step(stack, tokens, lengths, emb, lm_head, final_norm, l
                              prefix=None, loss_mask=None, opt=None, step=1, logits_out=None,
                              timeout_ms=600000, stream=None):
     """One SFT step on packed rows.  tokens: int32 [micro_batches, n_tokens]; lengths, prefix:
-    int32 [micro_batches, n_docs]; loss_mask: uint8 or bool [micro_batches, n_tokens]; opt: an
-    AdamWMulti over views of lora and lora_grad, updated with the count `step`, or None.
-    Returns the mean loss over all targets (host float)."""
+    int32 [micro_batches, n_docs]; loss_mask: uint8 or bool [micro_batches, n_tokens]; emb,
+    lm_head: bf16 [V, D]; final_norm: bf16 [D]; lora, lora_grad: fp32 of all layers; ws: uint8;
+    opt: an AdamWMulti over views of lora and lora_grad, updated with the count `step`, or None;
+    logits_out: fp32 [n_tokens, V] or None.  Returns the mean loss over all targets (host float)."""
     import torch
     if tokens.dim() != 2 or lengths.dim() != 2 or lengths.shape[0] != tokens.shape[0]:
         raise ValueError("tokens must be [micro_batches, n_tokens], lengths [micro_batches, n_docs]")
@@ -864,11 +885,26 @@ def stream_stack_packed_step(stack, tokens, lengths, emb, lm_head, final_norm, l
         if loss_mask.dtype == torch.bool:
             loss_mask = loss_mask.view(torch.uint8)
         _need("loss_mask", loss_mask, torch.uint8, tokens.shape)
+    c, bf16 = stack.cfg, torch.bfloat16
+    layout = lsq_lora_layout()
+    _check(load().lsq_lora_layout_get(ctypes.byref(c), ctypes.byref(layout)))
+    _need("emb", emb, bf16, (c.vocab, c.hidden))
+    _need("lm_head", lm_head, bf16, (c.vocab, c.hidden))
+    _need("final_norm", final_norm, bf16, numel=c.hidden)
+    _need("lora", lora, torch.float32, numel=layout.floats_per_layer * c.n_layers)
+    _need("lora_grad", lora_grad, torch.float32, numel=lora.numel())
+    if logits_out is not None:
+        _need("logits_out", logits_out, torch.float32, (tokens.shape[1], c.vocab))
+    _need("ws", ws, torch.uint8)
     loss = ctypes.c_float(0.0)
     table, n, hyper = opt.at(step) if opt is not None else (None, 0, None)
-    _check(load().stream_stack_packed_step(
-        stack.handle, _ptr(tokens), tokens.shape[0], tokens.shape[1], _ptr(lengths), _ptr(prefix),
-        lengths.shape[1], _ptr(loss_mask), _ptr(emb), _ptr(lm_head), _ptr(final_norm), _ptr(lora),
-        _ptr(lora_grad), table, n, ctypes.byref(hyper) if hyper is not None else None,
-        ctypes.byref(loss), _ptr(logits_out), _ptr(ws), ws.numel(), _stream(stream), timeout_ms))
+    _call("stream_stack_packed_step", stream,
+          (tokens, lengths, prefix, loss_mask, emb, lm_head, final_norm, lora, lora_grad, logits_out,
+           ws, opt._dev if opt is not None else None,
+           step if opt is not None and isinstance(step, torch.Tensor) else None),
+          stack.handle, tokens.data_ptr(), tokens.shape[0], tokens.shape[1], lengths.data_ptr(),
+          _addr(prefix), lengths.shape[1], _addr(loss_mask), emb.data_ptr(), lm_head.data_ptr(),
+          final_norm.data_ptr(), lora.data_ptr(), lora_grad.data_ptr(), table, n,
+          ctypes.byref(hyper) if hyper is not None else None, ctypes.byref(loss),
+          _addr(logits_out), ws.data_ptr(), ws.numel(), last=(timeout_ms,))
     return loss.value

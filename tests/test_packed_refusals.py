@@ -184,3 +184,85 @@ def test_binding_checks(L):
     with pytest.raises(TypeError):
         L.adamw_state_dequantize(p[0], p[0], p[0])
     assert L.AdamWMulti([], [], [], [], lr=1.0).step(1) is None
+
+
+def _step_args(L, cfg):
+    """Arguments of a packed step, right but for their device."""
+    import torch
+    n = L.lsq_lora_layout_get(cfg).floats_per_layer * cfg["n_layers"]
+    V, D, T = cfg["vocab"], cfg["hidden"], 16
+    return dict(tokens=torch.zeros(2, T, dtype=torch.int32),
+                lengths=torch.zeros(2, 3, dtype=torch.int32),
+                emb=torch.zeros(V, D, dtype=torch.bfloat16),
+                lm_head=torch.zeros(V, D, dtype=torch.bfloat16),
+                final_norm=torch.zeros(D, dtype=torch.bfloat16), lora=torch.zeros(n),
+                lora_grad=torch.zeros(n), ws=torch.zeros(256, dtype=torch.uint8),
+                logits_out=torch.zeros(T, V), prefix=torch.zeros(2, 3, dtype=torch.int32),
+                loss_mask=torch.zeros(2, T, dtype=torch.bool))
+
+
+def test_packed_step_binding(L):
+    """Every tensor is checked for type, size and device before the library sees it."""
+    from types import SimpleNamespace
+    from layer_streamed_qlora_nf4_b200 import synth
+    cfg = synth.SMALL
+    stack = SimpleNamespace(cfg=L.cfg_struct(cfg), handle=None)
+    ok = _step_args(L, cfg)
+    with pytest.raises(ValueError, match="CUDA"):
+        L.stream_stack_packed_step(stack, **ok)
+    for name in ok:
+        t = ok[name]
+        wrong = [t.double(), t.reshape(-1)[:-1], [0]]
+        if t.dim() == 2:
+            wrong += [t[:, :-1], t.t().contiguous().t()]
+        for w in wrong:
+            if name == "ws" and w is wrong[1]:
+                continue                 # (its length is the library's to judge)
+            with pytest.raises((TypeError, ValueError, AttributeError)) as e:
+                L.stream_stack_packed_step(stack, **dict(ok, **{name: w}))
+            assert "CUDA" not in str(e.value), (name, str(e.value))
+
+
+def test_packed_layer_binding(L):
+    import torch
+    from layer_streamed_qlora_nf4_b200 import synth
+    cfg, T = synth.SMALL, 8
+    idx = L.PackedIndex(T, 2, device="cpu")
+    x = torch.zeros(T, cfg["hidden"])
+    n = L.lsq_lora_layout_get(cfg).floats_per_layer
+    blob = torch.zeros(L.lsq_layer_layout_get(cfg).bytes, dtype=torch.uint8)
+    lora, ws = torch.zeros(n), torch.zeros(256, dtype=torch.uint8)
+    for b, l, w in ((blob[:-1], lora, ws), (blob.int(), lora, ws), (blob, lora[:-1], ws),
+                    (blob, lora.half(), ws), (blob, lora, ws.float()), (blob, lora, None),
+                    (None, lora, ws)):
+        with pytest.raises((TypeError, ValueError)) as e:
+            L.decoder_layer_packed_fwd(cfg, b, l, x, idx, x, w)
+        assert "CUDA" not in str(e.value)
+        with pytest.raises((TypeError, ValueError)) as e:
+            L.decoder_layer_packed_bwd(cfg, b, l, x, x, idx, x, lora, w)
+        assert "CUDA" not in str(e.value)
+    for l, g in ((None, lora), (lora, None), (lora, lora[1:])):
+        with pytest.raises((TypeError, ValueError)) as e:
+            L.decoder_layer_packed_bwd(cfg, blob, l, x, x, idx, x, g, ws)
+        assert "CUDA" not in str(e.value)
+    for l in (lora, None):               # (no adapter: the forward takes it)
+        with pytest.raises(ValueError, match="CUDA"):
+            L.decoder_layer_packed_fwd(cfg, blob, l, x, idx, x, ws)
+
+
+def test_a_step_count_on_the_host_is_refused(L):
+    """A count that the device is to read must lie on it."""
+    import torch
+    from types import SimpleNamespace
+    from layer_streamed_qlora_nf4_b200 import synth
+    opt = L.AdamWMulti([], [], [], [], lr=1.0)
+    seen = []
+    keep = L._call
+    L._call = lambda name, stream, tensors, *a, **k: seen.append(tensors)
+    try:
+        count = torch.ones(1, dtype=torch.int32)
+        L.stream_stack_packed_step(SimpleNamespace(cfg=L.cfg_struct(synth.SMALL), handle=None),
+                                   opt=opt, step=count, **_step_args(L, synth.SMALL))
+    finally:
+        L._call = keep
+    assert any(t is count for t in seen[0])
