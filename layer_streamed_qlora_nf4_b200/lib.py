@@ -748,8 +748,9 @@ class AdamWMulti:
 
     params: fp32; grads: all fp32 or all bf16; m, v: fp32 (32-bit state), or int8 and
     uint8 with m_scale, v_scale (8-bit state, fp32 scales of adamw_scale_floats(numel)).
-    lr, weight_decay: one number or one per tensor.  The tensors are checked and their
-    addresses taken here; they must stay allocated while the object is used."""
+    lr, weight_decay: one number or one per tensor (set_rates changes them between steps).
+    The tensors are checked and their addresses taken here; they must stay allocated while the
+    object is used."""
 
     def __init__(self, params, grads, m, v, lr, weight_decay=0.0, m_scale=None, v_scale=None,
                  betas=(0.9, 0.999), eps=1e-8):
@@ -763,12 +764,9 @@ class AdamWMulti:
         if any(x is None or len(x) != n for x in lists):
             raise ValueError("params, grads, m, v%s need one tensor each per parameter"
                              % (", m_scale, v_scale" if bits == 8 else ""))
-        lrs = list(lr) if hasattr(lr, "__len__") else [lr] * n
-        wds = list(weight_decay) if hasattr(weight_decay, "__len__") else [weight_decay] * n
-        if len(lrs) != n or len(wds) != n:
-            raise ValueError("lr and weight_decay need one number per parameter")
         self._table = (lsq_adamw_tensor * max(n, 1))()
         self._n, self._keep = n, lists
+        rates = self._per_tensor("lr", lr), self._per_tensor("weight_decay", weight_decay)
         self._dev = params[0] if n else None
         names = ("params", "grads", "m", "v", "m_scale", "v_scale")
         mdt, vdt = (torch.int8, torch.uint8) if bits == 8 else (torch.float32, torch.float32)
@@ -787,10 +785,27 @@ class AdamWMulti:
                     raise ValueError("tensor %d is on %s, the first on %s"
                                      % (i, t.device, self._dev.device))
             self._table[i] = lsq_adamw_tensor(*[t.data_ptr() for t in ts],
-                                              *[None] * (6 - len(ts)), k, lrs[i], wds[i])
+                                              *[None] * (6 - len(ts)), k)
         self._hyper = lsq_adamw_hyper(beta1=betas[0], beta2=betas[1], eps=eps, step=1,
                                       state_bits=bits,
                                       grad_bits=32 if gdt == torch.float32 else 16)
+        self.set_rates(*rates)
+
+    def _per_tensor(self, name, x):
+        x = [float(v) for v in x] if hasattr(x, "__len__") else [float(x)] * self._n
+        if len(x) != self._n:
+            raise ValueError("%s needs one number per parameter" % name)
+        return x
+
+    def set_rates(self, lr, weight_decay=None):
+        """The rates of the steps that follow (a schedule's): one number or one per tensor;
+        weight_decay None: as it was.  A captured step keeps the rates it was captured with."""
+        lr = self._per_tensor("lr", lr)
+        if weight_decay is not None:
+            for e, x in zip(self._table, self._per_tensor("weight_decay", weight_decay)):
+                e.weight_decay = x
+        for e, x in zip(self._table, lr):
+            e.lr = x
 
     def at(self, step):
         """The arguments (tensors, n_tensors, opt) of an update; step as for step()."""

@@ -334,3 +334,41 @@ def test_borders_closer_than_fp64_products_tell(L):
     codes, scale = op.encode(g * g, False)
     assert np.array_equal(c.cpu().numpy(), codes) and np.array_equal(s.cpu().numpy(), scale)
     assert L.lsq_device_status(clear=True) == 0
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_rates_follow_a_schedule(L, bits):
+    """Warm-up and decay, by one number and by one per tensor; a bad rate is refused at the step
+    and changes nothing."""
+    import torch
+    x = _problem([700, 300, 1], bits, False, 21)
+    d = _device(x, False)
+    o = _opt(L, d, 1e-3, 0.01, bits)
+    wd = [0.01] * 3
+    for step, lr in ((1, 0.0), (2, [1e-4, 2e-4, 0.0]), (3, 1e-3), (4, [5e-4, 1e-4, 2e-4])):
+        if step == 3:
+            wd = [0.0, 0.1, 0.02]
+        o.set_rates(lr, weight_decay=wd if step == 3 else None)
+        o.step(step)
+        lrs = lr if isinstance(lr, list) else [lr] * 3
+        before = [p.copy() for p in x["p"]]
+        _reference(x, step, lrs, wd, bits)
+        # the parameters are compared step by step, each from the device's own
+        for i in range(3):
+            got = d["p"][i].cpu().numpy()
+            decay = lrs[i] * wd[i] * np.abs(before[i].astype(np.float64))
+            tol = (2.0 ** -23 * np.abs(x["p"][i]) +
+                   2.0 ** -20 * (np.abs(x["p"][i] - before[i]) + 2 * decay))
+            assert (np.abs(got - x["p"][i]) <= tol).all(), (step, i)
+            x["p"][i] = got
+            for k in ("m", "v") + (("ms", "vs") if bits == 8 else ()):
+                assert np.array_equal(d[k][i].cpu().numpy(), x[k][i]), (k, i)
+    kept = [t.clone() for k in ("p", "m", "v") for t in d[k]]
+    for bad in (-1.0, float("nan"), float("inf")):
+        o.set_rates([1e-3, bad, 1e-3])
+        with pytest.raises(L.LsqError) as e:
+            o.step(5)
+        assert e.value.code == L.LSQ_ERR_INVALID
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(kept, [t for k in ("p", "m", "v") for t in d[k]]))
+    assert L.lsq_device_status(clear=True) == 0

@@ -266,3 +266,14 @@ def test_a_step_count_on_the_host_is_refused(L):
     finally:
         L._call = keep
     assert any(t is count for t in seen[0])
+
+
+def test_rates_need_one_number_per_tensor(L):
+    o = L.AdamWMulti([], [], [], [], lr=1.0)
+    o.set_rates(0.5)
+    o.set_rates([], weight_decay=[])
+    for bad in (dict(lr=[1.0]), dict(lr=1.0, weight_decay=[1.0])):
+        with pytest.raises(ValueError):
+            o.set_rates(**bad)
+        with pytest.raises(ValueError):
+            L.AdamWMulti([], [], [], [], **bad)
