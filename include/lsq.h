@@ -497,8 +497,8 @@ int packed_attention_bwd(const uint16_t* qkv, const int32_t* index, int32_t n_do
  *   loss_mask  device uint8 [T] or NULL: nonzero where a token is to be predicted
  *              (the answers of a chat); NULL: all.
  *   targets    device int32 [T] (output): tokens[t + 1] where that token belongs to t's
- *              document, is marked, and is not part of a prompt that t itself sees;
- *              -1 elsewhere.
+ *              document, is marked, is not part of a prompt that t itself sees, and is
+ *              not below 0; -1 elsewhere.
  *   count      device int32: the number of targets, added to it (accumulate = 1, over
  *              the micro-batches of a step) or written to it (0).
  * Asynchronous, deterministic. */

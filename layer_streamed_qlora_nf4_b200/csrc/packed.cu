@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(kIdxThreads, 1)
 
 // Target of token t: the next token, where that belongs to the same document, is not
 // seen by t itself (a prompt read in both directions is not predicted), and is marked
-// in loss_mask (if given); -1 elsewhere.  count: the integer sum over CTAs, the same
+// in loss_mask (if given); -1 elsewhere, and where the next token is below 0.  count: the integer sum over CTAs, the same
 // in any order.  Memory bound (17 bytes a token), in practice the latency of a launch.
 __global__ void __launch_bounds__(256)
     packed_targets_kernel(const int32_t* tokens, const int* key_end,
@@ -201,8 +201,9 @@ __global__ void __launch_bounds__(256)
   int n = 0;
   for (int t = blockIdx.x * 256 + threadIdx.x; t < T; t += gridDim.x * 256) {
     const bool on = t + 1 < doc_end[t] && key_end[t] == t + 1 && (!loss_mask || loss_mask[t + 1]);
-    targets[t] = on ? tokens[t + 1] : -1;
-    n += on;
+    const int y = on ? max(tokens[t + 1], -1) : -1;  // (the loss takes none below 0 either)
+    targets[t] = y;
+    n += y >= 0;
   }
   n = __reduce_add_sync(0xFFFFFFFFu, n);
   if ((threadIdx.x & 31) == 0 && n) atomicAdd(count, n);

@@ -79,7 +79,7 @@ def targets(tokens, docs, loss_mask=None):
     y = np.full(T, -1, np.int64)
     for s, e, pe in docs:
         for t in range(s, e - 1):
-            if t + 1 >= pe and (loss_mask is None or loss_mask[t + 1]):
+            if t + 1 >= pe and tokens[t + 1] >= 0 and (loss_mask is None or loss_mask[t + 1]):
                 y[t] = tokens[t + 1]
     return y
 

@@ -159,6 +159,28 @@ def test_index_and_targets(L, lengths, prefix, T):
     assert L.lsq_device_status(clear=True) == 0
 
 
+def test_tokens_below_zero_are_no_targets_and_are_not_counted(L):
+    """Ids such as -100 mark what is not to be predicted: the mean is over the others."""
+    import torch
+    T, V, lengths = 300, 50, [120, 150]
+    rng = np.random.default_rng(4)
+    tok = rng.integers(0, V, T).astype(np.int32)
+    tok[rng.random(T) < 0.4] = -100
+    tok[5:8] = -1, -2, -2 ** 31
+    idx = _index(L, lengths, None, T)
+    want = op.targets(tok, op.documents(lengths))
+    y = torch.full((T,), -9, dtype=torch.int32, device="cuda")
+    n = torch.zeros(1, dtype=torch.int32, device="cuda")
+    L.packed_targets(torch.from_numpy(tok).cuda(), idx, y, n)
+    assert np.array_equal(y.cpu().numpy(), want) and n.item() == (want >= 0).sum() < 200
+    x = rng.standard_normal((T, V)).astype(np.float32)
+    rl, tot = torch.empty(T, device="cuda"), torch.empty(1, device="cuda")
+    L.packed_cross_entropy(torch.from_numpy(x).cuda(), y, rl, tot, count=n)
+    _, loss, _ = op.cross_entropy(x, want, None, int((want >= 0).sum()))
+    # sums of 50 exponentials and of 160 rows in fp32
+    assert abs(tot.item() - loss) <= 2.0 ** -16 * loss
+
+
 def test_index_of_many_documents(L):
     """More documents than a pass of the scan takes, and a long row."""
     rng = np.random.default_rng(0)
