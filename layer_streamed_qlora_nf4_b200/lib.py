@@ -604,7 +604,7 @@ def packed_index_ints(T, n_docs):
 
 class PackedIndex:
     """The buffer of a packed row's index: n_tokens tokens holding n_docs documents
-    (filled by packed_index, once per batch)."""
+    (filled by packed_index, once per batch; until then it is that of a row of padding)."""
 
     def __init__(self, n_tokens, n_docs, device="cuda"):
         import torch
@@ -612,7 +612,8 @@ class PackedIndex:
         if words <= 0:
             raise ValueError("a packed row has at least one token and one document")
         self.n_tokens, self.n_docs = int(n_tokens), int(n_docs)
-        self.buf = torch.empty(words, dtype=torch.int32, device=device)
+        # (zeros: the operators take rows and places to write from it)
+        self.buf = torch.zeros(words, dtype=torch.int32, device=device)
 
 
 def packed_index(lengths, index, prefix=None, stream=None):

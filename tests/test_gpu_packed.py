@@ -222,6 +222,17 @@ def test_index_around_a_warp_and_a_block_of_documents(L, n_docs):
     assert np.array_equal(doc_end[:T - 2], ends[own]) and (doc_end[T - 2:] == T - 2).all()
 
 
+def test_a_new_index_is_a_row_of_padding(L):
+    import torch
+    H, Hkv, d, T = 4, 2, 64, 200
+    qkv, dout = _inputs(T, H, Hkv, d, 1)
+    o, lse, dqkv = _run(L, qkv.cuda(), dout.cuda(), L.PackedIndex(T, 3), H, Hkv)
+    assert not o.any() and not dqkv.any() and torch.isneginf(lse).all()
+    y, n = torch.zeros(T, dtype=torch.int32, device="cuda"), torch.ones(1, dtype=torch.int32, device="cuda")
+    L.packed_targets(y, L.PackedIndex(T, 3), y.clone(), n)
+    assert n.item() == 0
+
+
 def test_index_bad_lengths_are_cut_and_latched(L):
     bad = L.LSQ_DEV_ERR_INDEX
     for lengths, prefix, T, total in (([5, -3, 4], None, 12, 9), ([5, 9], None, 10, 10),

@@ -277,3 +277,12 @@ def test_rates_need_one_number_per_tensor(L):
             o.set_rates(**bad)
         with pytest.raises(ValueError):
             L.AdamWMulti([], [], [], [], **bad)
+
+
+def test_a_new_index_holds_no_documents(L):
+    """What the operators take their rows from is never unwritten memory."""
+    import torch
+    junk = [torch.full((L.packed_index_ints(5000, 7),), -1, dtype=torch.int32) for _ in range(4)]
+    del junk                                       # (memory that the next buffers may reuse)
+    for _ in range(4):
+        assert not L.PackedIndex(5000, 7, device="cpu").buf.any()
