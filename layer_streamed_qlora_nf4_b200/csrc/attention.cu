@@ -62,8 +62,8 @@ __device__ __forceinline__ uint8_t* align1024_a(uint8_t* p) {
 template <int D>
 __global__ void __launch_bounds__(kAThreads, 1)
     attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tm_qkv, int64_t T, int seq, int H,
-                       int Hkv, uint16_t* __restrict__ out, float* __restrict__ lse_out, float sl2,
-                       int* __restrict__ dev_err) {
+                       int Hkv, uint16_t* out, float* lse_out, float sl2,
+                       int* dev_err) {
   using SM = AttnSmem<D>;
   constexpr int DA = SM::DA;
   extern __shared__ uint8_t attn_raw[];
@@ -411,9 +411,9 @@ __global__ void __launch_bounds__(kAThreads, 1)
     attn_bwd_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tm_kv,   // qkv, boxes of 128 rows
                             const __grid_constant__ CUtensorMap tm_q,    // qkv, boxes of 64 rows
                             const __grid_constant__ CUtensorMap tm_do,   // dO, boxes of 64 rows
-                            const float* __restrict__ lse, const float* __restrict__ delta,
+                            const float* lse, const float* delta,
                             int64_t T, int seq, int H, int Hkv, float sl2, float scale,
-                            float* __restrict__ dk, float* __restrict__ dv, int* __restrict__ dev_err) {
+                            float* dk, float* dv, int* dev_err) {
   using SM = DkvSmem<D>;
   constexpr int DA = D / 64;
   extern __shared__ uint8_t dkv_raw[];
@@ -561,8 +561,8 @@ __global__ void __launch_bounds__(kAThreads, 1)
     // query i's, fetched one chunk ahead, and the lanes read them by shuffle
     auto fetch = [&](int c, float* l2v, float* dlv) {
       const int qq = min(k0 + c * kBC + 32 * hf + lane, seq - 1);
-      *l2v = __ldg(lse + (int64_t)h * T + tok0 + qq) * 1.4426950408889634f;
-      *dlv = __ldg(delta + (int64_t)h * T + tok0 + qq);
+      *l2v = lse[(int64_t)h * T + tok0 + qq] * 1.4426950408889634f;
+      *dlv = delta[(int64_t)h * T + tok0 + qq];
     };
     float l2_own = 0.f, dl_own = 0.f;
     if (nc > 0) fetch(0, &l2_own, &dl_own);
@@ -680,9 +680,9 @@ __global__ void __launch_bounds__(kAThreads, 1)
     attn_bwd_dq_tc_kernel(const __grid_constant__ CUtensorMap tm_q,    // qkv, boxes of 128 rows
                           const __grid_constant__ CUtensorMap tm_kv,   // qkv, boxes of 64 rows
                           const __grid_constant__ CUtensorMap tm_do,   // dO, boxes of 128 rows
-                          const float* __restrict__ lse, const float* __restrict__ delta,
+                          const float* lse, const float* delta,
                           int64_t T, int seq, int H, int Hkv, float sl2, float scale,
-                          float* __restrict__ dq, int* __restrict__ dev_err) {
+                          float* dq, int* dev_err) {
   using SM = DqSmem<D>;
   constexpr int DA = D / 64;
   extern __shared__ uint8_t dq_raw[];
@@ -815,8 +815,8 @@ __global__ void __launch_bounds__(kAThreads, 1)
     const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     pdl_wait();  // delta comes from the kernels before
     const int qq = min(q, seq - 1);
-    const float l2 = __ldg(lse + (int64_t)h * T + tok0 + qq) * 1.4426950408889634f;
-    const float dl = __ldg(delta + (int64_t)h * T + tok0 + qq);
+    const float l2 = lse[(int64_t)h * T + tok0 + qq] * 1.4426950408889634f;
+    const float dl = delta[(int64_t)h * T + tok0 + qq];
     bool ok = true;
     // V of chunk c becomes bf16 (dP's operand) as soon as it lands
     auto convert_v = [&](int c) -> bool {

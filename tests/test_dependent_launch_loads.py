@@ -78,3 +78,10 @@ def test_the_check_sees_an_early_read():
                        ("const int x = idx.pos[n]; // nothing", ["idx.pos"])):
         (name, params, body), = kernels(src % early)
         assert name == "k" and early_reads(params, body) == bad, early
+
+
+def test_the_attention_of_equal_sequences_too():
+    text = open(os.path.join(CSRC, "attention.cu")).read()
+    found = [k for k, params, body in kernels(text) if "pdl_wait();" in body and
+             "__restrict__" not in params and not early_reads(params, body)]
+    assert len(found) == 3 and not re.search(r"__ldg\b|ld\.global\.nc", _bare(text))
