@@ -707,14 +707,18 @@ __global__ void __launch_bounds__(256, 3)
   if (h >= H) {
     bool bad = false;
     float most = 0.f;
+    uint4 x[IT];
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
       const int64_t t = t0 + i * RW;
-      uint4 x = make_uint4(0u, 0u, 0u, 0u);
-      if (t < live)
-        x = *reinterpret_cast<const uint4*>(qkv + t * (int64_t)(H + 2 * Hkv) * D +
-                                            (int64_t)(Hkv + h) * D + col);
-      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+      x[i] = t < live ? *reinterpret_cast<const uint4*>(qkv + t * (int64_t)(H + 2 * Hkv) * D +
+                                                        (int64_t)(Hkv + h) * D + col)
+                      : make_uint4(0u, 0u, 0u, 0u);
+    }
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+      const int64_t t = t0 + i * RW;
+      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
       float n = 0.f;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
