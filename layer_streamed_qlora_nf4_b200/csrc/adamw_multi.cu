@@ -377,8 +377,8 @@ __device__ __forceinline__ void adamw_block(const MtHead& h, const MtEntry& e, c
 
 // One warp takes a block of 256 elements, lane l elements 4 l .. 4 l + 3 and 128 + 4 l
 // .. 128 + 4 l + 3, so that every load and store of a warp is contiguous.  Memory
-// bound by 28 bytes per element with an fp32 state (41.9 M parameters in 448 tensors: 186
-// us, 6.3 TB/s), 16 and two scales per block with 8 bits; there the arithmetic comes before
+// bound by 28 bytes per element with an fp32 state (41.9 M parameters in 448 tensors: 190
+// us, 6.2 TB/s), 16 and two scales per block with 8 bits; there the arithmetic comes before
 // it, hence the pairs, the flushing roots and the one branch for all borders of a thread:
 // 150 us, 4.5 TB/s, 84 instructions an element at 65% of the issue slots (a hundred took 205
 // us).  The loads are not what is waited for: with the next block brought in ahead, through
@@ -506,7 +506,9 @@ __global__ void __launch_bounds__(256)
 
 template <int BITS, int GBITS, int N>
 int mt_launch(const MtArgs<N>& a, cudaStream_t st) {
-  // eight CTAs of 256 threads fill an SM; more chunks than that are taken in turn
+  // four CTAs of 256 threads are resident on an SM (64 registers a thread with 8 bits); twice
+  // as many are launched, so that those of the second half take over as the first end, and
+  // more chunks than that are taken in turn
   const uint32_t grid = std::min<uint32_t>(a.h.chunks, (uint32_t)gemm_num_sms() * 8);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);

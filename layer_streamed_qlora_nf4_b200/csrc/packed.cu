@@ -222,11 +222,8 @@ __device__ __forceinline__ float ex2(float x) {  // 2^x, relative error 2^-22
 // passes over NaN, the sum does not: of a set with a NaN it is NaN, whatever the maximum.
 __device__ __forceinline__ void join(float& m, float& s, float mo, float so) {
   const float mn = fmaxf(m, mo);
-  if (mn == -INFINITY) {
-    s += so;
-    return;
-  }
-  s = s * ex2((m - mn) * kLog2e) + so * ex2((mo - mn) * kLog2e);
+  const float at = mn == -INFINITY ? 0.f : mn;  // (without a branch: with one 84 -> 88 us below)
+  s = s * ex2((m - at) * kLog2e) + so * ex2((mo - at) * kLog2e);
   m = mn;
 }
 

@@ -99,8 +99,9 @@ __device__ __forceinline__ void st_global32(void* p, const uint32_t (&v)[8]) {
 // cycles of products (measured alone: 48 cycles for a 128 x 64 x 16 product from shared
 // memory, 64 for a 128 x 128 x 16 one with A from TMEM) and 1024 of exponentials, and takes
 // 1770, in which the softmax threads are busy throughout.  One document of 16,384 tokens
-// (32/8 heads, d 128): 1.89 ms, 1160 TFLOP/s, the clock at 1.65 to 1.75 GHz under the power
-// limit; 16,384 tokens in 32 documents with prompts (16/2): 109 us; 512 tokens: 10 us.
+// (32/8 heads, d 128): 2.25 ms in repeated calls, 980 TFLOP/s, the power limit holding the
+// clock down (1.9 ms and 1150 for a few calls of a cool chip); 16,384 tokens in 34 documents
+// (16/2): 108 us; 512 tokens: 10 us.
 // Measured and set aside: polynomials for part of the exponentials (slower by 7%), steps of
 // 128 keys with one buffer, the streams' exponentials made to alternate (1830 cycles), and
 // the row maximum taken from the probabilities behind them (no change).
@@ -1435,7 +1436,7 @@ __device__ __forceinline__ void dq_part(const BwdArgs& a_, const CUtensorMap& tm
     }
     for (int i = 0; i < NR; ++i) {
       mbar_init(smem_u32(&r_full[i]), 1);
-      mbar_init(smem_u32(&r_free[i]), 3);  // the two streams' products and warp 11
+      mbar_init(smem_u32(&r_free[i]), 3);  // the two streams' products and warp 19
       mbar_init(smem_u32(&k_clear[i]), 1);
     }
     for (int i = 0; i < kTake; ++i) {
