@@ -623,8 +623,8 @@ __global__ void __launch_bounds__(kFThreads, 1)
 // One persistent kernel takes them all, a CTA its dK, dV items first, so that SMs that
 // find none left go on with dQ while others still work on theirs.  (As two kernels, the
 // second may read what the preparation wrote only when the first is done: backward of 512
-// tokens in 5 documents (32/8 heads, d 128) took 36 us so, 30 now; of 16,384 in 34 (16/2)
-// 268 and 257.)
+// tokens in 5 documents (32/8 heads, d 128) took 36 us so against 30, of 16,384 in 34 (16/2)
+// 268 against 257.)
 //   warps 0-15: the gradient warps, four groups of four (a TMEM lane per thread): groups 0
 //            and 2 take the two halves of the columns of one set (or stream), 1 and 3 of
 //            the other.  (With two groups of whole rows a chunk took a thread 3700 cycles,
@@ -682,12 +682,13 @@ __device__ __forceinline__ float warp_most(float x) {  // (of numbers that are n
 
 // One CTA per window of 64 tokens and head; D / 8 lanes take a row, 16 bytes each, and a
 // warp its eight tokens with all loads in flight (memory bound: 6 bytes per element).
-// blockIdx.y >= H: the squared norms of the v rows of kv head blockIdx.y - H (0 for one that is
-// not finite, which is latched: what it reaches is not finite whatever the scale).  e brings the row's
-// largest magnitude to [1, 2), so its norm is below 2 sqrt(d).  A zero row takes e = 127
-// (it must not lower the least exponent of a tile); a row that is not finite takes e = 0,
-// and its gradients come out not finite.  16,384 tokens of 16 heads, d 128: 37 us,
-// 5.4 TB/s (40 with the 64 registers a thread that the compiler takes by itself, and spills).
+// blockIdx.y >= H: the squared norms of the v rows of kv head blockIdx.y - H (0 for one that
+// is not finite, which is latched: what it reaches is not finite whatever the scale).  e
+// brings the row's largest magnitude to [1, 2), so its norm is below 2 sqrt(d).  A zero row
+// takes e = 127 (it must not lower the least exponent of a tile); a row that is not finite
+// takes e = 0, and its gradients come out not finite.  16,384 tokens of 16 heads, d 128: 38
+// us, 5.3 TB/s (41 with the 64 registers a thread that the compiler takes by itself, and
+// spills).
 template <int D>
 __global__ void __launch_bounds__(256, 3)
     packed_attn_prep_kernel(const uint16_t* qkv, const uint16_t* o,
@@ -870,15 +871,14 @@ struct DkvSmem {
   static constexpr uint32_t kBytes = 1024 + 2 * kTile + 2 * kRing * kQc + kRing * kBC * 8;
 };
 
-// Hands out the items of one part of the kernel: `first` is this CTA's, known to all its
-// warps (none when it is `items` or more); the others are drawn by the TMA producer, which
-// gives each to the other warps.
+// Passes the items of one part of the kernel from the TMA producer, which draws them, to the
+// other warps; the CTA's first one is known to all.
 struct ItemRing {
   uint64_t full[kTake], free[kTake];
   int item[kTake];
 };
 
-// What both parts of the kernel read and write, and how they wait.
+// What both parts of the kernel read and write.
 struct BwdArgs {
   PackedIndex idx;
   const float2* stats;
